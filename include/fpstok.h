@@ -101,7 +101,12 @@ typedef enum { FPSTOK_VORONOI = 0, FPSTOK_KNN = 1 } fpstok_assign_mode;
  * thread on the FPS precision argument settles that FPS runs in float32 on
  * both backends whatever the input dtype.)  Gradients (fpstok_pool_backward)
  * are float32 whatever the features' dtype. */
-typedef enum { FPSTOK_F32 = 0, FPSTOK_F16 = 1, FPSTOK_BF16 = 2 } fpstok_dtype;
+typedef enum {
+    FPSTOK_F32 = 0,
+    FPSTOK_F16 = 1,
+    FPSTOK_BF16 = 2,
+    FPSTOK_I32 = 3 /* positions of fpstok_rope only */
+} fpstok_dtype;
 
 /* One CSR batch of events.  All pointers are device pointers. */
 typedef struct {
@@ -318,6 +323,158 @@ fpstok_status fpstok_pool_backward(const fpstok_batch* batch, const fpstok_param
  * Errors: EINVAL (NULL pointers, num_events < 0), EHIP. */
 fpstok_status fpstok_random_start(const int64_t* offsets, int64_t num_events, uint64_t seed,
                                   uint64_t step, int32_t* start_idx, void* stream);
+
+/* ------------------------------------------- attention over the tokens -- */
+
+/* The rows of a batch of B variable-length sequences (events) in a buffer of
+ * num_rows rows, in one of two forms; exactly one of cu_seqlens and
+ * token_count is given:
+ *   packed (cu_seqlens, as fpstok_pack writes it): sequence b is rows
+ *     cu_seqlens[b] .. cu_seqlens[b+1]-1.  Rows behind the last sequence are
+ *     neither read nor written.
+ *   padded (token_count, as fpstok_tokenize writes it): sequence b is the
+ *     first token_count[b] of the rows b*capacity .. (b+1)*capacity-1, and
+ *     num_rows = B*capacity.  The other slots are not read; outputs get 0
+ *     there.
+ * Lengths are device data: a call never waits for them.  Values out of range
+ * are clamped into the buffer (a sequence whose end lies before its start is
+ * empty), so they give wrong results but no access outside it. */
+typedef struct {
+    int64_t num_seqs;          /* B: 0 .. 2^24                                      */
+    int64_t num_rows;          /* rows of the buffers, < 2^31                       */
+    const int32_t* cu_seqlens; /* [B+1] (device), or NULL                           */
+    const int32_t* token_count;/* [B] (device), or NULL                             */
+    int32_t capacity;          /* padded form: slots per sequence                   */
+    int32_t max_len;           /* optional host-side bound on any length, 0 if      */
+                               /* unknown.  It only chooses how the work is split:  */
+                               /* a bound that is too small stays correct           */
+} fpstok_seqs;
+
+/* A [num_rows][heads][head_dim] view: head h of row r starts at
+ * data + r*row_stride + h*head_stride, its elements are adjacent.  Strides in
+ * elements; inputs may use any stride >= 0 (0: the same row or head again),
+ * outputs' rows and heads must not overlap. */
+typedef struct {
+    void* data;
+    int64_t row_stride;
+    int64_t head_stride;
+} fpstok_heads;
+
+#define FPSTOK_MAX_HEAD_DIM 128 /* largest head_dim of the attention             */
+#define FPSTOK_MAX_SINKS 64     /* largest num_sinks accepted                      */
+#define FPSTOK_MAX_AXES 4       /* largest num_axes of fpstok_rope                 */
+
+typedef struct {
+    int32_t num_heads;       /* query heads H >= 1                                 */
+    int32_t num_kv_heads;    /* key/value heads: a divisor of H; query head h       */
+                             /* reads key head h / (H / num_kv_heads)               */
+    int32_t head_dim;        /* D: a multiple of 8 in [8, FPSTOK_MAX_HEAD_DIM]      */
+    int32_t dtype;           /* fpstok_dtype of every view of the call              */
+    int32_t window_left;     /* keys visible before a query's own place, -1: all    */
+    int32_t window_right;    /* keys visible behind it, -1: all; 0: causal          */
+    int32_t num_sinks;       /* first keys of each sequence that window_left does   */
+                             /* not hide: 0 .. FPSTOK_MAX_SINKS                     */
+    float scale;             /* of the scores; finite and > 0                       */
+} fpstok_attn_params;
+
+/* Attention inside every sequence (graphnet PR #923, "What is added":
+ * packed block-diagonal attention over the events' tokens, padded attention
+ * otherwise, and AttentionPool, one query per event).  With Tq queries and Tk
+ * keys in a sequence, query i has its place at p = i + Tk - Tq (the last query
+ * beside the last key) and sees key j if
+ *   (window_right < 0 or j <= p + window_right) and
+ *   (window_left  < 0 or j >= p - window_left or j < num_sinks).
+ * Per query head, over the visible keys:
+ *   s_ij = scale * sum_d q_i[d] k_j[d],  lse_i = log sum_j exp(s_ij),
+ *   out_i = sum_j exp(s_ij - lse_i) v_j.
+ * A query that sees no key gets out = 0 and lse = -inf.  What a query does not
+ * see never reaches its result, not-a-number and infinite values included.
+ *   q_seqs, k_seqs  the queries' and the keys' sequences (k_seqs NULL: the
+ *                   queries'); as many of one as of the other
+ *   q   [q rows][H][D] in;  k, v [k rows][num_kv_heads][D] in
+ *   out [q rows][H][D] out
+ *   lse [q rows][H] f32 out, contiguous, or NULL
+ * Scores, softmax and sums are held in float32; with a 16-bit dtype the
+ * weights exp(s - max) are rounded to it for the product with v.  Results are
+ * bit-identical from run to run.
+ *   ws  fpstok_attention_workspace_size(q_seqs, k_seqs, params, 0) bytes,
+ *       256-byte aligned (NULL if that is 0)
+ * data pointers are 16-byte aligned, and so are the strides in bytes.
+ * Errors: EINVAL (NULL or misaligned pointers, strides, sizes or parameters
+ * out of range), EWORKSPACE, EUNSUPPORTED (more than 2^31 - 1 rows, or rows
+ * times heads too many for one launch), EHIP. */
+fpstok_status fpstok_attention(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
+                               const fpstok_attn_params* params, const fpstok_heads* q,
+                               const fpstok_heads* k, const fpstok_heads* v,
+                               const fpstok_heads* out, float* lse, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Gradients of fpstok_attention with respect to q, k and v (for training
+ * through the tokens, as fpstok_pool_backward): with w_ij = exp(s_ij - lse_i),
+ * g = grad_out and delta_i = sum_d g_i[d] out_i[d], over the visible pairs and,
+ * for k and v, over every query head that reads the key head,
+ *   grad_v_j = sum_i w_ij g_i
+ *   ds_ij    = w_ij (sum_d g_i[d] v_j[d] - delta_i)
+ *   grad_q_i = scale * sum_j ds_ij k_j,   grad_k_j = scale * sum_i ds_ij q_i.
+ * Rows no query sees, and queries that see no key, get 0.  Sums are held in
+ * float32 in a fixed order (no floating-point atomics); with a 16-bit dtype w
+ * and ds are rounded to it for the products.  In float16 a ds below 2^-24
+ * vanishes: scale the loss as for any float16 gradient.
+ *   out, lse  as fpstok_attention wrote them
+ *   grad_q [q rows][H][D], grad_k, grad_v [k rows][num_kv_heads][D] out; they
+ *   may not overlap one another or any input
+ *   ws  fpstok_attention_workspace_size(q_seqs, k_seqs, params, 1) bytes
+ * Errors: as fpstok_attention. */
+fpstok_status fpstok_attention_backward(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
+                                        const fpstok_attn_params* params, const fpstok_heads* q,
+                                        const fpstok_heads* k, const fpstok_heads* v,
+                                        const fpstok_heads* out, const float* lse,
+                                        const fpstok_heads* grad_out, const fpstok_heads* grad_q,
+                                        const fpstok_heads* grad_k, const fpstok_heads* grad_v,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace of fpstok_attention (backward = 0) or
+ * fpstok_attention_backward (backward = 1) for these shapes.  Host-only; 0
+ * for arguments those calls refuse. */
+size_t fpstok_attention_workspace_size(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
+                                       const fpstok_attn_params* params, int32_t backward);
+
+typedef struct {
+    int32_t num_heads;       /* heads of q                                         */
+    int32_t num_kv_heads;    /* heads of k (>= 1 where k is given)                 */
+    int32_t head_dim;        /* D: even, 2 .. 1024                                 */
+    int32_t dtype;           /* fpstok_dtype of q and k                            */
+    int32_t positions_dtype; /* FPSTOK_F32 or FPSTOK_I32                           */
+    int32_t num_axes;        /* A: 1 .. FPSTOK_MAX_AXES                            */
+    int32_t pairs[FPSTOK_MAX_AXES]; /* element pairs each axis rotates, >= 0; R,   */
+                             /* their sum over the axes, in [1, D/2]               */
+    int32_t interleaved;     /* 0: pair p is elements p and p + R of a head;        */
+                             /* 1: elements 2p and 2p + 1                           */
+    int32_t inverse;         /* 1: rotate by the negated angle                      */
+} fpstok_rope_params;
+
+/* Rotary position encoding over several axes (graphnet PR #923, "What is
+ * added": RoPE4D, the four axes x, y, z and t of the tokens' centroids; a time
+ * axis and the two of an image are another use).  The first pairs[0] pairs
+ * turn with axis 0, the next pairs[1] with axis 1, and so on: on row r, pair p
+ * of axis a turns by angle = positions[r][a] * freqs[p],
+ *   y1 = x1 cos - x2 sin,  y2 = x1 sin + x2 cos,
+ * elements in no pair are copied.  Angles are formed and reduced in float64
+ * (exact for |angle| < 2^40), the turn is float32, rounded once.  The gradient
+ * with respect to the input is the same call with inverse = 1.
+ *   seqs       the rows (one form for q and k); padded slots get 0
+ *   positions  [num_rows][A] in, contiguous
+ *   freqs      [R] f32 in
+ *   q_in, q_out [num_rows][num_heads][D]; k_in, k_out
+ *   [num_rows][num_kv_heads][D], or both NULL.  q_out may be q_in (same
+ *   pointer and strides), k_out may be k_in; no other overlap.
+ * Pointers and strides need the alignment of one element; heads aligned to 16
+ * bytes are moved 16 bytes at a time.  No workspace.  Errors: EINVAL,
+ * EUNSUPPORTED, EHIP. */
+fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_params* params,
+                          const void* positions, const float* freqs, const fpstok_heads* q_in,
+                          const fpstok_heads* q_out, const fpstok_heads* k_in,
+                          const fpstok_heads* k_out, void* stream);
 
 /* Device-side status of the last fpstok_sample or fpstok_tokenize call on
  * the workspace `ws` (its first ws_bytes bytes; at least the 256-byte

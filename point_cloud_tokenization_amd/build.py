@@ -4,13 +4,17 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfpstok.so")
-SOURCES = [os.path.join(CSRC, "fpstok_kernels.hip"), os.path.join(CSRC, "fpstok_api.cpp")]
-HEADERS = [os.path.join(ROOT, "include", "fpstok.h"), os.path.join(CSRC, "fpstok_internal.h")]
+SOURCES = [os.path.join(CSRC, f) for f in (
+    "fpstok_kernels.hip", "fpstok_api.cpp", "fpstok_attention.hip", "fpstok_rope.hip",
+    "fpstok_attention_api.cpp")]
+HEADERS = [os.path.join(ROOT, "include", "fpstok.h")] + [os.path.join(CSRC, f) for f in (
+    "fpstok_internal.h", "fpstok_host.h", "fpstok_attention.h", "fpstok_seqs.h")]
 
 ARCH = "gfx950"
 # -ffp-contract=off: the squared distance is the exact float32 sequence
@@ -34,13 +38,27 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    """Compile every HIP source for gfx950 into libfpstok.so (always rebuilds)."""
+    """Compile every HIP source for gfx950 into libfpstok.so (always rebuilds);
+    the sources are compiled side by side, then linked."""
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory() as objs:
+        jobs, linked = [], []
+        for src in SOURCES:
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f != "-shared"], *extra, "-c",
+                   "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", obj, src]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append((cmd, subprocess.Popen(cmd)))
+            linked.append(obj)
+        codes = [job.wait() for _, job in jobs]
+        for (cmd, _), rc in zip(jobs, codes):
+            if rc != 0:
+                raise subprocess.CalledProcessError(rc, cmd)
+        cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *linked]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     return LIB
 

@@ -12,18 +12,14 @@
 #include <cstring>
 #include <vector>
 
+#include "fpstok_host.h"
 #include "fpstok_internal.h"
-
-#define FPSTOK_API extern "C" __attribute__((visibility("default")))
 
 namespace fpstok {
 
 static thread_local char g_last_error[512] = "";
 
-static fpstok_status fail(fpstok_status st, const char* fmt, ...)
-    __attribute__((format(printf, 2, 3)));
-
-static fpstok_status fail(fpstok_status st, const char* fmt, ...) {
+fpstok_status fail(fpstok_status st, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
@@ -31,12 +27,12 @@ static fpstok_status fail(fpstok_status st, const char* fmt, ...) {
     return st;
 }
 
-static fpstok_status ok() {
+fpstok_status ok() {
     g_last_error[0] = '\0';
     return FPSTOK_OK;
 }
 
-static fpstok_status hip_fail(hipError_t e, const char* what) {
+fpstok_status hip_fail(hipError_t e, const char* what) {
     return fail(FPSTOK_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 

@@ -1,0 +1,52 @@
+// Internal interface between the C ABI (fpstok_attention_api.cpp) and the
+// gfx950 kernels of attention (fpstok_attention.hip) and rotary positions
+// (fpstok_rope.hip).  Not installed; not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace fpstok {
+
+constexpr int kMaxAxes = 4;
+
+// Rows of the sequences of a batch (fpstok_seqs).
+struct SeqArgs {
+    const int32_t* cu;     // packed: [B+1], or null
+    const int32_t* count;  // padded: [B], or null
+    int64_t rows;
+    int32_t B;
+    int32_t cap;
+};
+
+struct HeadsArg {
+    void* data;
+    int64_t row, head;  // strides in elements
+};
+
+struct AttnArgs {
+    SeqArgs qs, ks;
+    HeadsArg q, k, v, out, grad_out, grad_q, grad_k, grad_v;
+    float* lse;    // [q rows][H], or null (forward)
+    float* delta;  // [q rows][H] (backward)
+    int32_t H, Hk, D, dtype;
+    int32_t left, right, sinks;
+    float scale;
+};
+
+struct RopeArgs {
+    SeqArgs seqs;
+    HeadsArg in[2], out[2];
+    int32_t heads[2];
+    const void* positions;
+    const float* freqs;
+    int32_t D, dtype, int_positions, axes, R, interleaved, inverse;
+    int32_t first_pair[kMaxAxes + 1];  // pairs of axis a: first_pair[a] .. first_pair[a+1]-1
+};
+
+hipError_t launch_attention(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+
+}  // namespace fpstok

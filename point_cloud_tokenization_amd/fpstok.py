@@ -17,9 +17,10 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "fpstok.h")
 
 OK, EINVAL, EWORKSPACE, EUNSUPPORTED, EHIP, EDEVICE = 0, 1, 2, 3, 4, 5
 VORONOI, KNN = 0, 1
-F32, F16, BF16 = 0, 1, 2  # fpstok_dtype
+F32, F16, BF16, I32 = 0, 1, 2, 3  # fpstok_dtype
 MAX_PATCHES, MAX_K, MAX_LLOYD = 1024, 64, 1000
 NOALLOC_MAX_WORKSPACE = 64 << 20  # FPSTOK_NOALLOC_MAX_WORKSPACE
+MAX_HEAD_DIM, MAX_SINKS, MAX_AXES = 128, 64, 4
 
 
 class FpstokError(RuntimeError):
@@ -45,6 +46,32 @@ class Params(ctypes.Structure):
     _fields_ = [("num_patches", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("lloyd_iters", ctypes.c_int32), ("assign_mode", ctypes.c_int32),
                 ("pool_weighted", ctypes.c_int32)]
+
+
+class Seqs(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int64), ("num_rows", ctypes.c_int64),
+                ("cu_seqlens", ctypes.c_void_p), ("token_count", ctypes.c_void_p),
+                ("capacity", ctypes.c_int32), ("max_len", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class AttnParams(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("window_left", ctypes.c_int32), ("window_right", ctypes.c_int32),
+                ("num_sinks", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("positions_dtype", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("pairs", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32)]
 
 
 _lib = None
@@ -79,7 +106,16 @@ def lib():
         L.fpstok_debug_set_spin_limit.argtypes = [ctypes.c_uint32]
         L.fpstok_debug_set_spin_limit.restype = None
         L.fpstok_upcast.argtypes = [vp, i64, i32, vp, vp]
-        for f in ("fpstok_sample", "fpstok_assign", "fpstok_knn", "fpstok_lloyd",
+        S, A = ctypes.POINTER(Seqs), ctypes.POINTER(AttnParams)
+        L.fpstok_attention.argtypes = [S, S, A] + [ctypes.POINTER(Heads)] * 4 + [vp, vp, sz, vp]
+        L.fpstok_attention_backward.argtypes = [S, S, A] + [ctypes.POINTER(Heads)] * 4 + [vp] + \
+            [ctypes.POINTER(Heads)] * 4 + [vp, sz, vp]
+        L.fpstok_attention_workspace_size.argtypes = [S, S, A, i32]
+        L.fpstok_attention_workspace_size.restype = sz
+        L.fpstok_rope.argtypes = [S, ctypes.POINTER(RopeParams), vp, vp] + \
+            [ctypes.POINTER(Heads)] * 4 + [vp]
+        for f in ("fpstok_attention", "fpstok_attention_backward", "fpstok_rope",
+                  "fpstok_sample", "fpstok_assign", "fpstok_knn", "fpstok_lloyd",
                   "fpstok_pool", "fpstok_tokenize", "fpstok_validate", "fpstok_pack",
                   "fpstok_unpack", "fpstok_pool_backward", "fpstok_random_start",
                   "fpstok_device_status", "fpstok_tokenize_noalloc", "fpstok_upcast"):
@@ -430,3 +466,200 @@ def tokenize(coords, features, offsets=None, batch_ids=None, num_events=None, nu
     t = Tokenizer(coords, features, offsets, num_patches, assign_mode, k, lloyd_iters, pool,
                   charge_col)
     return t(start_idx, stream)
+
+
+# --------------------------------------------- attention over the tokens
+
+def make_seqs(num_rows, cu_seqlens=None, token_count=None, capacity=0, max_len=0):
+    """A Seqs struct (fpstok_seqs): the rows of a batch of sequences, packed
+    (cu_seqlens [B+1] int32, as pack writes it) or padded (token_count [B]
+    int32 with `capacity` slots per sequence).  max_len: optional host-side
+    bound on any length (0: unknown).  The struct keeps its tensor alive."""
+    import torch
+
+    if (cu_seqlens is None) == (token_count is None):
+        raise ValueError("give cu_seqlens or token_count")
+    t = cu_seqlens if token_count is None else token_count
+    _need(t, torch.int32, "cu_seqlens" if token_count is None else "token_count")
+    if t.dim() != 1 or (token_count is None and t.numel() < 1):
+        raise ValueError("cu_seqlens must be [B+1], token_count [B]")
+    if token_count is None:
+        s = Seqs(t.numel() - 1, int(num_rows), t.data_ptr(), None, 0, int(max_len))
+    else:
+        s = Seqs(t.numel(), int(num_rows), None, t.data_ptr(), int(capacity), int(max_len))
+    s.tensor = t
+    return s
+
+
+def make_heads(t, name, heads=None, rows=None, like=None):
+    """A Heads struct over a [rows, heads, D] device tensor (any row and head
+    stride, adjacent elements), which the caller keeps alive."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError("%s must be [rows, heads, D] with adjacent elements" % name)
+    if (heads is not None and t.shape[1] != heads) or (rows is not None and t.shape[0] != rows):
+        raise ValueError("%s must hold %s rows of %s heads, got %s" % (name, rows, heads,
+                                                                     tuple(t.shape)))
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+        if t.device != like.device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
+        if t.shape[2] != like.shape[2]:
+            raise ValueError("%s must have heads of %d elements" % (name, like.shape[2]))
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+class _DeviceCall:
+    """Calls a library function on the stream of one device."""
+
+    def __init__(self, device):
+        import torch
+
+        self.device = device
+        self._index = device.index if device.index is not None else torch.cuda.current_device()
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def _call(self, fn, where, args, stream):
+        import torch
+
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._call(fn, where, args, stream)
+        if stream is not None:
+            s = stream.cuda_stream
+        elif self._raw_stream is not None:
+            s = self._raw_stream(self._index)
+        else:
+            s = torch.cuda.current_stream(self.device).cuda_stream
+        rc = fn(*args, ctypes.c_void_p(s))
+        if rc != OK:
+            _check(rc, where)
+
+
+class Attention(_DeviceCall):
+    """fpstok_attention on given tensors, with its outputs and workspace
+    allocated once, and with training=True fpstok_attention_backward.
+
+    q [q rows, H, D]; k, v [k rows, Hk, D] (float32, float16 or bfloat16, any
+    row and head stride); q_seqs, k_seqs: make_seqs (k_seqs None: q_seqs).
+    window = (left, right), -1 for unbounded; right = 0 is causal.  A call
+    takes what the tensors hold by then; it returns (out, lse), the same
+    buffers each time, and rows behind the last packed sequence keep what they
+    held (0 after construction)."""
+
+    def __init__(self, q, k, v, q_seqs, k_seqs=None, window=(-1, -1), num_sinks=0, scale=None,
+                 training=False, out=None):
+        import torch
+
+        super().__init__(q.device)
+        qh = make_heads(q, "q", rows=q_seqs.num_rows)
+        ks = q_seqs if k_seqs is None else k_seqs
+        kh = make_heads(k, "k", rows=ks.num_rows, like=q)
+        vh = make_heads(v, "v", rows=ks.num_rows, heads=k.shape[1], like=q)
+        for s in (q_seqs, ks):
+            if s.tensor.device != q.device:
+                raise ValueError("the sequences are on %s, expected %s" % (s.tensor.device,
+                                                                        q.device))
+        D = q.shape[2]
+        self.q, self.k, self.v, self.q_seqs, self.k_seqs = q, k, v, q_seqs, k_seqs
+        self.params = AttnParams(q.shape[1], k.shape[1], D, _dtype_code(q, "q"), int(window[0]),
+                                 int(window[1]), int(num_sinks),
+                                 1.0 / D ** 0.5 if scale is None else float(scale))
+        self.out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        self.lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+        oh = make_heads(self.out, "out", rows=q.shape[0], heads=q.shape[1], like=q)
+        self._head = (ctypes.byref(q_seqs), None if k_seqs is None else ctypes.byref(k_seqs),
+                      ctypes.byref(self.params), ctypes.byref(qh), ctypes.byref(kh),
+                      ctypes.byref(vh), ctypes.byref(oh), _ptr(self.lse))
+        need = [lib().fpstok_attention_workspace_size(*self._head[:3], b)
+                for b in ((0, 1) if training else (0,))]
+        self.ws = torch.empty(max(need), dtype=torch.uint8, device=q.device) if max(need) else None
+        self._ws = (_ptr(self.ws), 0 if self.ws is None else self.ws.numel())
+        self._fwd, self._bwd = lib().fpstok_attention, lib().fpstok_attention_backward
+        self.grads = None
+        if training:
+            self.grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
+                               for t in (q, k, v))
+            gh = [make_heads(g, "gradient") for g in self.grads]
+            self._tail = tuple(ctypes.byref(h) for h in gh) + self._ws
+
+    def __call__(self, stream=None):
+        """fpstok_attention: (out, lse)."""
+        self._call(self._fwd, "fpstok_attention", self._head + self._ws, stream)
+        return self.out, self.lse
+
+    def backward(self, grad_out, stream=None):
+        """fpstok_attention_backward after a call on the same inputs:
+        (grad_q, grad_k, grad_v)."""
+        if self.grads is None:
+            raise ValueError("construct with training=True")
+        gh = make_heads(grad_out, "grad_out", rows=self.q.shape[0], heads=self.q.shape[1],
+                        like=self.q)
+        self._call(self._bwd, "fpstok_attention_backward",
+                   self._head + (ctypes.byref(gh),) + self._tail, stream)
+        return self.grads
+
+
+def rope_frequencies(pairs, base=10000.0, top=1.0, device=None):
+    """[sum(pairs)] float32 frequencies: on every axis a geometric row from
+    `top` down to top / base (excluded)."""
+    import torch
+
+    f = [top * float(base) ** (-torch.arange(n, dtype=torch.float64) / max(n, 1)) for n in pairs]
+    return torch.cat(f).to(torch.float32).to(device)
+
+
+class Rope(_DeviceCall):
+    """fpstok_rope on given tensors: q [rows, H, D] and, unless None, k
+    [rows, Hk, D] turned by positions [rows, A] (float32 or int32), pairs[a]
+    pairs by axis a with freqs [sum(pairs)] float32.  Outputs are allocated
+    once unless given (q_out=q, k_out=k turn in place); a call returns
+    (q_out, k_out)."""
+
+    def __init__(self, q, k, positions, freqs, pairs, seqs, interleaved=False, q_out=None,
+                 k_out=None):
+        import torch
+
+        super().__init__(q.device)
+        pairs = [int(x) for x in pairs]
+        A = len(pairs)
+        if not 1 <= A <= MAX_AXES:
+            raise ValueError("pairs must name 1 to %d axes" % MAX_AXES)
+        if positions.dtype not in (torch.float32, torch.int32):
+            raise TypeError("positions must be float32 or int32, got %s" % positions.dtype)
+        _need(positions, positions.dtype, "positions", q.device)
+        _need(freqs, torch.float32, "freqs", q.device)
+        if tuple(positions.shape) != (q.shape[0], A):
+            raise ValueError("positions must be [%d, %d]" % (q.shape[0], A))
+        if freqs.numel() != sum(pairs):
+            raise ValueError("freqs must hold %d values" % sum(pairs))
+        if seqs.tensor.device != q.device:
+            raise ValueError("the sequences are on %s, expected %s" % (seqs.tensor.device, q.device))
+        qh = make_heads(q, "q", rows=seqs.num_rows)
+        self.q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        qo = make_heads(self.q_out, "q_out", rows=q.shape[0], heads=q.shape[1], like=q)
+        kh = ko = self.k_out = None
+        if k is not None:
+            kh = make_heads(k, "k", rows=seqs.num_rows, like=q)
+            self.k_out = torch.zeros(k.shape, dtype=k.dtype, device=k.device) if k_out is None \
+                else k_out
+            ko = make_heads(self.k_out, "k_out", rows=k.shape[0], heads=k.shape[1], like=q)
+        self._keep = (q, k, positions, freqs, seqs)
+        code = I32 if positions.dtype == torch.int32 else F32
+        views = tuple(None if h is None else ctypes.byref(h) for h in (qh, qo, kh, ko))
+        self._args = []
+        for inverse in (0, 1):
+            pr = RopeParams(q.shape[1], 0 if k is None else k.shape[1], q.shape[2],
+                            _dtype_code(q, "q"), code, A,
+                            (ctypes.c_int32 * 4)(*(pairs + [0] * (4 - A))),
+                            1 if interleaved else 0, inverse)
+            self._args.append((ctypes.byref(seqs), ctypes.byref(pr), _ptr(positions), _ptr(freqs))
+                              + views)
+        self._fn = lib().fpstok_rope
+
+    def __call__(self, inverse=False, stream=None):
+        """fpstok_rope; inverse=True turns back (the gradient)."""
+        self._call(self._fn, "fpstok_rope", self._args[1 if inverse else 0], stream)
+        return self.q_out, self.k_out
