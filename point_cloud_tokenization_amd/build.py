@@ -14,7 +14,7 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "fpstok_kernels.hip", "fpstok_api.cpp", "fpstok_attention.hip", "fpstok_rope.hip",
     "fpstok_attention_api.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "fpstok.h")] + [os.path.join(CSRC, f) for f in (
-    "fpstok_internal.h", "fpstok_host.h", "fpstok_attention.h", "fpstok_seqs.h")]
+    "fpstok_internal.h", "fpstok_host.h", "fpstok_attention.h", "fpstok_seqs.h", "fpstok_mma.h")]
 
 ARCH = "gfx950"
 # -ffp-contract=off: the squared distance is the exact float32 sequence

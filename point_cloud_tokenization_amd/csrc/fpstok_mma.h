@@ -1,0 +1,258 @@
+// Matrix-product pieces of the attention kernels: 32 x 32 tiles by the matrix
+// instructions of gfx950, their operands as fragments of 8 elements per lane,
+// and the tiles of rows in LDS they are read from.
+//
+// One product step contracts 16 elements: lane l holds 8 of them (half
+// l >> 5) for row (A) or column (B) l & 31; the 32 x 32 float32 result has
+// column l & 31 and, in register r, row 8 (r / 4) + 4 (l >> 5) + r % 4.  Which
+// 8 of the 16 a half holds is free as long as A and B agree:
+//   natural  half h holds elements 8 h .. 8 h + 7 (16 adjacent bytes of a row
+//            of a 16-bit type);
+//   folded   half h holds 4 h .. 4 h + 3 and 8 + 4 h .. 8 + 4 h + 3: what
+//            registers 0-7 (8-15) of a result hold, so the result of one
+//            product is the operand of the next without moving between lanes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fpstok {
+
+using f32x16 = float __attribute__((ext_vector_type(16)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+#define FPSTOK_LDS __attribute__((address_space(3)))
+
+template <class T>
+struct Elem;
+
+template <>
+struct Elem<__bf16> {
+    using Frag = __bf16 __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kExp = 0x7f807f80u;  // exponent bits of two elements
+    static constexpr uint32_t kOne = 0x00800080u;
+    static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Elem<_Float16> {
+    using Frag = _Float16 __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kExp = 0x7c007c00u;
+    static constexpr uint32_t kOne = 0x04000400u;
+    static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Elem<float> {
+    using Frag = float __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kExp = 0x7f800000u;
+    static constexpr uint32_t kOne = 0x00800000u;
+    static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Eight float32 registers of a result, rounded to the type, as the operand of
+// the next product (folded order).
+template <class T>
+__device__ __forceinline__ typename Elem<T>::Frag to_frag(const float* x) {
+    using f32x8 = float __attribute__((ext_vector_type(8)));
+    f32x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[j];
+    return __builtin_convertvector(v, typename Elem<T>::Frag);
+}
+
+// A tile of rows of DP elements in LDS, in 16-byte chunks.  Chunk c of a row
+// is stored at place c ^ swz(row): reading one chunk of 8 adjacent rows, and
+// the 32 bytes of 4 adjacent rows that one transposing read of 16 lanes
+// takes, then falls on different banks.
+template <class T, int DP>
+struct Tile {
+    static constexpr int kElems = 16 / (int)sizeof(T);  // per chunk
+    static constexpr int kChunks = DP / kElems;         // per row
+    static constexpr int kPitch = DP * (int)sizeof(T);  // bytes
+    using Frag = typename Elem<T>::Frag;
+
+    static __device__ __forceinline__ int swz(int row) {
+        return ((row & 3) << 1) | ((row >> 2) & 1);
+    }
+    static __device__ __forceinline__ int place(int row, int chunk) {
+        return row * kPitch + ((chunk ^ swz(row)) << 4);
+    }
+
+    // Row fragment of row `row` (lane-dependent), elements 16 step + 8 h ..
+    // + 7 (natural order).
+    static __device__ __forceinline__ Frag row_frag(const FPSTOK_LDS char* t, int row, int step,
+                                                    int half) {
+        if constexpr (sizeof(T) == 2) {
+            return *(const FPSTOK_LDS Frag*)(t + place(row, 2 * step + half));
+        } else {
+            using f4 = float __attribute__((ext_vector_type(4)));
+            const f4 a = *(const FPSTOK_LDS f4*)(t + place(row, 4 * step + 2 * half));
+            const f4 b = *(const FPSTOK_LDS f4*)(t + place(row, 4 * step + 2 * half + 1));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+
+    // Transposed fragment: elements `32 db + (lane & 31)` of the 16 rows from
+    // row0 on, in folded order.  16-bit types read 4 rows x 16 elements per 16
+    // lanes with one transposing read (lane i of the 16 addresses 4 elements
+    // of row i / 4 and receives element i of the 4 rows).
+    static __device__ __forceinline__ Frag col_frag(const FPSTOK_LDS char* t, int row0, int db,
+                                                    int lane) {
+        if constexpr (sizeof(T) == 2) {
+            using s4 = short __attribute__((ext_vector_type(4)));
+            using s8 = short __attribute__((ext_vector_type(8)));
+            const int i = lane & 15, r = ((lane >> 5) << 2) + (i >> 2);
+            const int c = db * 4 + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
+            const FPSTOK_LDS char* p = t + row0 * kPitch + place(r, c) + (i & 1) * 8;
+            const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FPSTOK_LDS s4*)p);
+            const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (FPSTOK_LDS s4*)(p + 8 * kPitch));
+            return __builtin_bit_cast(Frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int d = db * 32 + (lane & 31), h4 = (lane >> 5) << 2;
+            Frag f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = (j >> 2) * 8 + h4 + (j & 3);
+                f[j] = *(const FPSTOK_LDS float*)(t + row0 * kPitch + place(r, d >> 2) +
+                                                 (d & 3) * 4);
+            }
+            return f;
+        }
+    }
+};
+
+// True if a chunk holds an infinite or not-a-number element: the exponent
+// bits of such an element carry into the bit above them when one is added.
+template <class T>
+__device__ __forceinline__ bool chunk_bad(u32x4 x) {
+    uint32_t acc = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc |= (x[i] & Elem<T>::kExp) + Elem<T>::kOne;
+    return (acc & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u)) != 0;
+}
+
+// The chunk with its infinite and not-a-number elements replaced by zero.
+template <class T>
+__device__ __forceinline__ u32x4 chunk_clean(u32x4 x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = (x[i] & Elem<T>::kExp) + Elem<T>::kOne;
+        if constexpr (sizeof(T) == 2) {
+            if (c & 0x80000000u) x[i] &= 0x0000ffffu;
+            if (c & 0x00008000u) x[i] &= 0xffff0000u;
+        } else {
+            if (c & 0x80000000u) x[i] = 0;
+        }
+    }
+    return x;
+}
+
+// Rows of a tile on their way from memory to LDS, by THREADS threads: load()
+// issues the loads, store() writes them.  Rows at or past `rows` and elements
+// at or past D read as zero and nothing of them is touched in memory.
+template <class T, int DP, int ROWS, int THREADS>
+struct Stage {
+    using Tl = Tile<T, DP>;
+    static constexpr int kPer = ROWS * Tl::kChunks / THREADS;
+    static_assert(ROWS * Tl::kChunks % THREADS == 0, "whole chunks per thread");
+    u32x4 x[kPer];
+
+    __device__ __forceinline__ void load(const T* base, int64_t stride, int rows, int D, int tid) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = i * THREADS + tid, r = at / Tl::kChunks, c = at % Tl::kChunks;
+            u32x4 v = {0, 0, 0, 0};
+            if (r < rows && c * Tl::kElems < D)
+                v = *(const u32x4*)(base + r * stride + c * Tl::kElems);
+            x[i] = v;
+        }
+    }
+    __device__ __forceinline__ void store(FPSTOK_LDS char* t, int tid) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = i * THREADS + tid, r = at / Tl::kChunks, c = at % Tl::kChunks;
+            *(FPSTOK_LDS u32x4*)(t + Tl::place(r, c)) = x[i];
+        }
+    }
+    // Infinite and not-a-number elements become zero; true if there were any.
+    __device__ __forceinline__ bool clean() {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (chunk_bad<T>(x[i])) {
+                x[i] = chunk_clean<T>(x[i]);
+                bad = true;
+            }
+        return bad;
+    }
+};
+
+// max / sum of a value over the two lanes l and l ^ 32.
+__device__ __forceinline__ float pair_max(float x) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
+__device__ __forceinline__ float pair_sum(float x) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Writes a transposed result (lane l: row l & 31 of the output, registers:
+// elements of it) times `f` to `row`, D elements of it: 16 bytes per lane
+// and store.
+template <class T, int DB>
+__device__ __forceinline__ void store_row(const f32x16* acc, float f, T* row, int D, int lane) {
+    const int half = lane >> 5;
+    if constexpr (sizeof(T) == 2) {
+        using T4 = T __attribute__((ext_vector_type(4)));
+        using f4 = float __attribute__((ext_vector_type(4)));
+        using u2 = uint32_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                u2 p[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[db][(g + k) * 4 + e] * f;
+                    p[k] = __builtin_bit_cast(u2, __builtin_convertvector(v, T4));
+                }
+                // half 0 collects elements 8g .. 8g+7, half 1 the next 8
+                const auto a = __builtin_amdgcn_permlane32_swap(p[0][0], p[1][0], false, false);
+                const auto b = __builtin_amdgcn_permlane32_swap(p[0][1], p[1][1], false, false);
+                const u32x4 o = {a[0], b[0], a[1], b[1]};
+                const int d = db * 32 + g * 8 + half * 8;
+                if (row && d < D) *(u32x4*)(row + d) = o;
+            }
+    } else {
+        using f4 = float __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[db][g * 4 + e] * f;
+                const int d = db * 32 + g * 8 + half * 4;
+                if (row && d < D) *(f4*)(row + d) = v;
+            }
+    }
+}
+
+}  // namespace fpstok
