@@ -4,6 +4,7 @@
 #pragma once
 
 #include <hip/hip_runtime_api.h>
+#include <hip/hip_vector_types.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -29,7 +30,7 @@ struct AttnArgs {
     SeqArgs qs, ks;
     HeadsArg q, k, v, out, grad_out, grad_q, grad_k, grad_v;
     float* lse;    // [q rows][H], or null (forward)
-    float* delta;  // [q rows][H] (backward)
+    float2* stat;  // [Hk][q rows * H / Hk] log2(e) lse, delta (backward)
     int32_t H, Hk, D, dtype;
     int32_t left, right, sinks;
     float scale;

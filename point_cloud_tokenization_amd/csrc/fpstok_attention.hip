@@ -4,54 +4,6 @@
 
 namespace fpstok {
 
-// Keys a query at place p sees: [0, ns) and [lo, hi].
-__device__ __forceinline__ void key_range(const AttnArgs& a, int64_t p, int tk, int& ns, int& lo,
-                                          int& hi) {
-    int64_t h = tk - 1, l = 0;
-    if (a.right >= 0 && p + a.right < h) h = p + a.right;
-    if (a.left >= 0 && p - a.left > 0) l = p - a.left;
-    int64_t n = l < a.sinks ? l : a.sinks;
-    if (n > h + 1) n = h + 1;
-    if (n < 0) n = 0;
-    if (l > h) { l = 1; h = 0; }
-    ns = (int)n;
-    lo = (int)l;
-    hi = (int)h;
-}
-
-// Sequence and place in it of buffer row r; false if no sequence holds it.
-__device__ __forceinline__ bool row_seq(const SeqArgs& s, int64_t r, int& b, int64_t& start,
-                                        int& len) {
-    b = s.cu ? 0 : (int)(r / s.cap);
-    if (s.cu) {
-        int lo = 0, n = s.B;  // largest b with cu[b] <= r
-        while (n > 1) {
-            const int m = n >> 1;
-            if (cu_at(s, lo + m) <= r) { lo += m; n -= m; } else n = m;
-        }
-        b = lo;
-    }
-    seq_rows(s, b, start, len);
-    return r >= start && r < start + len;
-}
-
-template <class T>
-__device__ __forceinline__ float dot(const T* x, const T* y, int D) {
-    float s = 0.0f;
-    for (int d = 0; d < D; ++d) s = __builtin_fmaf((float)x[d], (float)y[d], s);
-    return s;
-}
-
-__device__ __forceinline__ float wave_max(float x) {
-    for (int o = 32; o; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-    return x;
-}
-
-__device__ __forceinline__ float wave_sum(float x) {
-    for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
-    return x;
-}
-
 // The rows of one workgroup's tile.  A row is a (query, head of the group) pair
 // of one key head, numbered query * G + head: every row of a tile reads the
 // same keys, so one query of 8 heads is 8 rows of a tile, and K and V are read
@@ -128,6 +80,27 @@ __device__ __forceinline__ int tile_view(const AttnArgs& a, int64_t pa, int64_t 
     const bool right_all = j1 < tk && (a.right < 0 || j1 <= pa + a.right);
     const bool right_none = j0 >= tk || (a.right >= 0 && j0 > pb + a.right);
     return left_none || right_none ? 0 : left_all && right_all ? 2 : 1;
+}
+
+// Adds the infinite and not-a-number values of rows [j0, j1) that this lane
+// sees (`sees`) to its transposed result.  Rare: only for tiles that hold such
+// values and that some row's mask hides in part.
+template <class T, int DB, class Sees>
+__device__ __forceinline__ void add_bad(f32x16* acc, const T* base, int64_t stride, int j0, int j1,
+                                        int D, int half, Sees sees) {
+    for (int j = j0; j < j1; ++j) {
+        if (!sees(j)) continue;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int d = db * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                if (d < D) {
+                    const float x = (float)base[j * stride + d];
+                    if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) acc[db][e] += x;
+                }
+            }
+    }
 }
 
 // Forward.  A workgroup of 4 waves takes 128 rows (32 per wave) of one key
@@ -263,23 +236,9 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
                 for (int db = 0; db < DB; ++db)
                     o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, o[db]);
             }
-            if (bad_tag[i & 1] == i + 1) {
-                // rare: the rows that see an infinite value get it here
-                for (int j = j0; j < j0 + BN && j <= hi; ++j) {
-                    if (j < lo && j >= a.sinks) continue;
-#pragma unroll
-                    for (int db = 0; db < DB; ++db)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int d = db * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                            if (d < a.D) {
-                                const float x = (float)vb[(int64_t)j * a.v.row + d];
-                                if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u)
-                                    o[db][e] += x;
-                            }
-                        }
-                }
-            }
+            if (bad_tag[i & 1] == i + 1)
+                add_bad<T, DB>(o, vb, a.v.row, j0, j0 + BN < hi + 1 ? j0 + BN : hi + 1, a.D, half,
+                               [&](int j) { return j >= lo || j < a.sinks; });
         }
         if (i + 1 < n) store(i + 1);
         __syncthreads();
@@ -299,105 +258,331 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
                   : some ? (mc + __builtin_amdgcn_logf(l)) * 0.693147180559945f : -INFINITY;
 }
 
-// One wave per (query, head): grad_q, and delta for the kernel below.
-template <class T>
+// grad_q, and the rows' statistics for the kernel below.  Rows and key tiles as
+// in the forward kernel; per 32 keys a wave forms S^T = K Q^T and
+// dP^T = V dO^T, and dS^T = P^T (dP^T - delta), rounded to the type, is the
+// operand of dQ^T += K^T dS^T.
+template <class T, int DP, int BN>
 __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t r = w / a.H;
-    const int h = (int)(w % a.H), hk = h / (a.H / a.Hk);
-    if (r >= a.qs.rows) return;
-    int b, tq, tk;
-    int64_t q0, k0;
-    const bool in = row_seq(a.qs, r, b, q0, tq);
-    if (!in && a.qs.cu) return;
-    float acc[2] = {0.0f, 0.0f}, delta = 0.0f, lse = 0.0f;
-    const T* q = (const T*)a.q.data + r * a.q.row + h * a.q.head;
-    const T* g = (const T*)a.grad_out.data + r * a.grad_out.row + h * a.grad_out.head;
-    const T* o = (const T*)a.out.data + r * a.out.row + h * a.out.head;
-    const T* kb = (const T*)a.k.data + hk * a.k.head;
-    const T* vb = (const T*)a.v.data + hk * a.v.head;
-    int ns = 0, lo = 1, hi = 0;
-    if (in) {
-        seq_rows(a.ks, b, k0, tk);
-        key_range(a, (r - q0) + tk - tq, tk, ns, lo, hi);
-        delta = dot(g, o, a.D);
-        lse = a.lse[r * a.H + h];
-    }
-    if (in && lane == 0) a.delta[r * a.H + h] = delta;
-    const int n = ns + hi - lo + 1;
-    for (int c = 0; c < n; c += 64) {
-        const int t = c + lane;
-        const int64_t j = k0 + (t < ns ? t : lo + t - ns);
-        float ds = 0.0f;
-        if (t < n) {
-            const float p = expf(dot(q, kb + j * a.k.row, a.D) * a.scale - lse);
-            ds = p * (dot(g, vb + j * a.v.row, a.D) - delta);
+    constexpr int BM = 128, DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
+    using Tl = Tile<T, DP>;
+    using Frag = typename Elem<T>::Frag;
+    __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
+    __shared__ int bad_tag[2];
+    FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = a.H / a.Hk;
+    RowTile t;
+    if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
+
+    const int r = wave * 32 + (lane & 31);
+    const int qi = (t.row0 + r) / G, h = t.hk * G + (t.row0 + r) - qi * G;
+    const bool live = r < t.rows;
+    const int64_t qrow = t.q0 + qi;
+    Frag qf[STEPS], gf[STEPS];
+    float delta = 0.0f, lse2 = 0.0f;
+    {
+        const T* q = (const T*)a.q.data + qrow * a.q.row + h * a.q.head;
+        const T* g = (const T*)a.grad_out.data + qrow * a.grad_out.row + h * a.grad_out.head;
+        const T* o = (const T*)a.out.data + qrow * a.out.row + h * a.out.head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = s * 16 + half * 8;
+            Frag fq = {}, fg = {}, fo = {};
+            if (live && d < a.D) {
+                fq = *(const Frag*)(q + d);
+                fg = *(const Frag*)(g + d);
+                fo = *(const Frag*)(o + d);
+            }
+            qf[s] = fq;
+            gf[s] = fg;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                delta = __builtin_fmaf((float)fg[e], (float)fo[e], delta);
         }
-        for (int u = 0; u < 64 && c + u < n; ++u) {
-            const float x = __shfl(ds, u);
-            const T* k = kb + (k0 + (c + u < ns ? c + u : lo + c + u - ns)) * a.k.row;
-            for (int e = 0; e < 2; ++e)
-                if (lane + 64 * e < a.D) acc[e] = __builtin_fmaf(x, (float)k[lane + 64 * e], acc[e]);
+        delta = pair_sum(delta);
+        if (live) {
+            // a row that sees nothing: every weight is masked, the value
+            // only has to be finite
+            const float v = a.lse[qrow * a.H + h];
+            lse2 = v == -INFINITY ? 0.0f : v * 1.44269504088896f;
+            if (half == 0)
+                a.stat[((int64_t)t.hk * a.qs.rows + t.q0) * G + t.row0 + r] =
+                    make_float2(lse2, delta);
         }
     }
-    T* out = (T*)a.grad_q.data + r * a.grad_q.row + h * a.grad_q.head;
-    for (int e = 0; e < 2; ++e)
-        if (lane + 64 * e < a.D) out[lane + 64 * e] = (T)(acc[e] * a.scale);
+    const int64_t off = (int64_t)t.tk - t.tq;
+    const int last = t.rows > 0 ? t.rows - 1 : 0;
+    const int64_t pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
+    const int wl = wave * 32 + 31 < last ? wave * 32 + 31 : last;
+    const int64_t wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
+    const bool wave_live = wave * 32 < t.rows;
+    const int64_t p = qi + off;
+    const int hi = (int)(a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1);
+    const int lo = (int)(a.left >= 0 && p - a.left > 0 ? p - a.left : 0);
+
+    KeyTiles<BN> kt(a, pa, pb, t.tk);
+    const int n = t.rows > 0 ? kt.count : 0;
+    const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
+    const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
+    Stage<T, DP, BN, 256> sk, sv;
+    if (tid < 2) bad_tag[tid] = 0;
+
+    auto load = [&](int i) {
+        const int64_t j0 = (int64_t)kt.tile(i) * BN;
+        sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, tid);
+        sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, tid);
+    };
+    auto store = [&](int i) {
+        FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
+        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sk.clean())
+            bad_tag[i & 1] = i + 1;
+        sk.store(buf, tid);
+        sv.store(buf + BN * Tl::kPitch, tid);
+    };
+
+    f32x16 dq[DB];
+#pragma unroll
+    for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
+    const float c = a.scale * 1.44269504088896f;
+
+    if (n > 0) {
+        load(0);
+        __syncthreads();
+        store(0);
+    }
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+        const int j0 = kt.tile(i) * BN;
+        if (i + 1 < n) load(i + 1);
+        const int view = wave_live ? tile_view<BN>(a, wa, wb, t.tk, j0) : 0;
+        if (view != 0) {
+            const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
+            const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                f32x16 x = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int st = 0; st < STEPS; ++st) {
+                    x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
+                    y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
+                }
+                float ds[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2));
+                    ds[e] = w * (y[e] - delta);
+                }
+                if (view == 1) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = j0 + b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                        if (j > hi || (j < lo && j >= a.sinks)) ds[e] = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const Frag f = to_frag<T>(ds + k * 8);
+#pragma unroll
+                    for (int db = 0; db < DB; ++db)
+                        dq[db] =
+                            Elem<T>::mma(Tl::col_frag(kbuf, b * 32 + k * 16, db, lane), f, dq[db]);
+                }
+            }
+            if (bad_tag[i & 1] == i + 1)
+                add_bad<T, DB>(dq, kb, a.k.row, j0, j0 + BN < hi + 1 ? j0 + BN : hi + 1, a.D, half,
+                               [&](int j) { return j >= lo || j < a.sinks; });
+        }
+        if (i + 1 < n) store(i + 1);
+        __syncthreads();
+    }
+    T* out = (T*)a.grad_q.data + qrow * a.grad_q.row + h * a.grad_q.head;
+    if (!live) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
+    }
+    store_row<T, DB>(dq, a.scale, live || r < t.pad ? out : nullptr, a.D, lane);
 }
 
-// One wave per (key, key head): grad_k and grad_v over every query that sees
-// the key, heads of the group one after another.
-template <class T>
+// grad_k and grad_v.  A workgroup takes 128 keys of one key head (32 per wave,
+// across the lanes) and walks the rows (query, head of the group) that see
+// them, BQ at a time: S = Q K^T and dP = dO V^T have the rows in registers, so P
+// and dS = P (dP - delta), rounded to the type, are the operands of
+// dV^T += dO^T P and dK^T += Q^T dS.  The heads of the group are rows of the same
+// walk: their gradients add up in the accumulators, in a fixed order.
+template <class T, int DP, int BQ>
 __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t r = w / a.Hk;
-    const int hk = (int)(w % a.Hk), G = a.H / a.Hk;
-    if (r >= a.ks.rows) return;
-    int b, tq = 0, tk;
-    int64_t q0 = 0, k0;
-    const bool in = row_seq(a.ks, r, b, k0, tk);
-    if (!in && a.ks.cu) return;
-    float dk[2] = {0.0f, 0.0f}, dv[2] = {0.0f, 0.0f};
-    const T* k = (const T*)a.k.data + r * a.k.row + hk * a.k.head;
-    const T* v = (const T*)a.v.data + r * a.v.row + hk * a.v.head;
-    int64_t i0 = 0, i1 = -1;
-    if (in) {
-        seq_rows(a.qs, b, q0, tq);
-        const int64_t j = r - k0, off = (int64_t)tk - tq;
-        i1 = tq - 1;
-        if (a.right >= 0 && j - a.right - off > 0) i0 = j - a.right - off;
-        if (a.left >= 0 && j >= a.sinks && j + a.left - off < i1) i1 = j + a.left - off;
+    constexpr int BM = 128, DB = DP / 32, QB = BQ / 32, STEPS = DP / 16;
+    using Tl = Tile<T, DP>;
+    using Frag = typename Elem<T>::Frag;
+    __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BQ * Tl::kPitch];
+    __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];
+    __shared__ int bad_tag[2];
+    FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = a.H / a.Hk;
+    RowTile t;
+    if (!row_tile<BM>(a, a.ks, blockIdx.x, 1, t)) return;
+
+    const int r = wave * 32 + (lane & 31);
+    const bool live = r < t.rows;
+    const int64_t krow = t.k0 + t.row0 + r;
+    Frag kf[STEPS], vf[STEPS];
+    {
+        const T* k = (const T*)a.k.data + krow * a.k.row + t.hk * a.k.head;
+        const T* v = (const T*)a.v.data + krow * a.v.row + t.hk * a.v.head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = s * 16 + half * 8;
+            Frag fk = {}, fv = {};
+            if (live && d < a.D) {
+                fk = *(const Frag*)(k + d);
+                fv = *(const Frag*)(v + d);
+            }
+            kf[s] = fk;
+            vf[s] = fv;
+        }
     }
-    for (int h = hk * G; h < (hk + 1) * G; ++h)
-        for (int64_t c = i0; c <= i1; c += 64) {
-            const int64_t i = q0 + c + lane;
-            const T* q = (const T*)a.q.data + h * a.q.head;
-            const T* g = (const T*)a.grad_out.data + h * a.grad_out.head;
-            float p = 0.0f, ds = 0.0f;
-            if (c + lane <= i1) {
-                p = expf(dot(q + i * a.q.row, k, a.D) * a.scale - a.lse[i * a.H + h]);
-                ds = p * (dot(g + i * a.grad_out.row, v, a.D) - a.delta[i * a.H + h]);
-            }
-            for (int u = 0; u < 64 && c + u <= i1; ++u) {
-                const float pu = __shfl(p, u), du = __shfl(ds, u);
-                const T* qu = q + (q0 + c + u) * a.q.row;
-                const T* gu = g + (q0 + c + u) * a.grad_out.row;
-                for (int e = 0; e < 2; ++e)
-                    if (lane + 64 * e < a.D) {
-                        dv[e] = __builtin_fmaf(pu, (float)gu[lane + 64 * e], dv[e]);
-                        dk[e] = __builtin_fmaf(du, (float)qu[lane + 64 * e], dk[e]);
+    // rows that see some key of the tile, and those that see this lane's key
+    const int64_t off = (int64_t)t.tk - t.tq;
+    const int j = t.row0 + r;
+    int64_t i0 = 0, i1 = t.tq - 1, e0 = 0, e1 = t.tq - 1;
+    if (a.right >= 0) {
+        if (t.row0 - a.right - off > 0) i0 = t.row0 - a.right - off;
+        if (j - a.right - off > 0) e0 = j - a.right - off;
+    }
+    if (a.left >= 0) {
+        const int64_t jl = t.row0 + t.rows - 1;
+        if (t.row0 >= a.sinks && jl + a.left - off < i1) i1 = jl + a.left - off;
+        if (j >= a.sinks && j + a.left - off < e1) e1 = j + a.left - off;
+    }
+    const int64_t n_rows = t.rows > 0 && i1 >= i0 ? (i1 - i0 + 1) * G : 0;
+    const int n = (int)((n_rows + BQ - 1) / BQ);
+    const int64_t first = i0 * G;  // row (query * G + head) of the walk's start
+    // this lane's rows, counted from there
+    const int64_t see0 = e0 * G - first, see1 = (e1 + 1) * G - first;
+
+    const T* qb = (const T*)a.q.data + t.q0 * a.q.row + (int64_t)t.hk * G * a.q.head;
+    const T* gb = (const T*)a.grad_out.data + t.q0 * a.grad_out.row +
+                  (int64_t)t.hk * G * a.grad_out.head;
+    const float2* sb = a.stat + ((int64_t)t.hk * a.qs.rows + t.q0) * G + first;
+    if (tid < 2) bad_tag[tid] = 0;
+
+    StageRows<T, DP, BQ, 256> sq, sg;
+    float2 sst = make_float2(0.0f, 0.0f);
+    auto load = [&](int i) {
+        const int64_t at = first + (int64_t)i * BQ;
+        const int64_t left = n_rows - (int64_t)i * BQ;
+        const int rows = left < BQ ? (int)left : BQ;
+        sq.load(qb, a.q.row, a.q.head, at, G, rows, a.D, tid);
+        sg.load(gb, a.grad_out.row, a.grad_out.head, at, G, rows, a.D, tid);
+        sst = make_float2(0.0f, 0.0f);
+        if (tid < rows) sst = sb[(int64_t)i * BQ + tid];
+    };
+    auto view_of = [&](int i, int k0) {  // the tile's rows against 32 keys
+        const int64_t at = first + (int64_t)i * BQ;
+        const int64_t end = first + n_rows < at + BQ ? first + n_rows : at + BQ;
+        return tile_view<32>(a, at / G + off, (end - 1) / G + off, t.tk, t.row0 + k0);
+    };
+    auto store = [&](int i) {
+        FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
+        bool part = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(i, w * 32) != 2;
+        if (part) {
+            const bool bq = sq.clean(), bg = sg.clean();
+            if (bq || bg) bad_tag[i & 1] = i + 1;
+        }
+        sq.store(buf, tid);
+        sg.store(buf + BQ * Tl::kPitch, tid);
+        if (tid < BQ) {
+            stat[i & 1][0][tid] = sst.x;
+            stat[i & 1][1][tid] = sst.y;
+        }
+    };
+
+    f32x16 dk[DB], dv[DB];
+#pragma unroll
+    for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
+    const float c = a.scale * 1.44269504088896f;
+
+    if (n > 0) {
+        load(0);
+        __syncthreads();
+        store(0);
+    }
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+        if (i + 1 < n) load(i + 1);
+        const int view = wave * 32 < t.rows ? view_of(i, wave * 32) : 0;
+        if (view != 0) {
+            const FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
+            const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                f32x16 x = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int st = 0; st < STEPS; ++st) {
+                    x = Elem<T>::mma(Tl::row_frag(qbuf, b * 32 + (lane & 31), st, half), kf[st], x);
+                    y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), vf[st], y);
+                }
+                float w[16], ds[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int q = b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                    w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -stat[i & 1][0][q]));
+                    ds[e] = w[e] * (y[e] - stat[i & 1][1][q]);
+                }
+                if (view == 1) {
+                    // rows of the walk as 32-bit distances from the tile's start
+                    const int64_t at = (int64_t)i * BQ + b * 32 + half * 4;
+                    const int s0 = (int)(see0 - at < -64 ? -64 : see0 - at > 64 ? 64 : see0 - at);
+                    const int s1 = (int)(see1 - at < -64 ? -64 : see1 - at > 64 ? 64 : see1 - at);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int q = (e >> 2) * 8 + (e & 3);
+                        if (q < s0 || q >= s1) w[e] = 0.0f, ds[e] = 0.0f;
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const Frag fw = to_frag<T>(w + k * 8), fs = to_frag<T>(ds + k * 8);
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) {
+                        dv[db] =
+                            Elem<T>::mma(Tl::col_frag(gbuf, b * 32 + k * 16, db, lane), fw, dv[db]);
+                        dk[db] =
+                            Elem<T>::mma(Tl::col_frag(qbuf, b * 32 + k * 16, db, lane), fs, dk[db]);
+                    }
+                }
+            }
+            if (bad_tag[i & 1] == i + 1) {
+                int64_t b0 = (int64_t)i * BQ, b1 = b0 + BQ < n_rows ? b0 + BQ : n_rows;
+                if (b0 < see0) b0 = see0;
+                if (b1 > see1) b1 = see1;
+                for (int64_t x = first + b0; x < first + b1; ++x) {
+                    const int64_t qi = x / G, g = x - qi * G;
+                    const auto all = [](int) { return true; };
+                    add_bad<T, DB>(dk, qb + qi * a.q.row + g * a.q.head, 0, 0, 1, a.D, half, all);
+                    add_bad<T, DB>(dv, gb + qi * a.grad_out.row + g * a.grad_out.head, 0, 0, 1,
+                                   a.D, half, all);
+                }
             }
         }
-    T* ok = (T*)a.grad_k.data + r * a.grad_k.row + hk * a.grad_k.head;
-    T* ov = (T*)a.grad_v.data + r * a.grad_v.row + hk * a.grad_v.head;
-    for (int e = 0; e < 2; ++e)
-        if (lane + 64 * e < a.D) {
-            ok[lane + 64 * e] = (T)(dk[e] * a.scale);
-            ov[lane + 64 * e] = (T)dv[e];
-        }
+        if (i + 1 < n) store(i + 1);
+        __syncthreads();
+    }
+    T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
+    T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
+    if (!live) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
+    }
+    const bool write = live || r < t.pad;
+    store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane);
+    store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane);
 }
 
 // Slots of a grid that covers every tile of BM rows of every sequence.
@@ -418,10 +603,21 @@ static hipError_t forward(const AttnArgs& a, hipStream_t s) {
 
 template <class T>
 static hipError_t backward(const AttnArgs& a, hipStream_t s) {
-    if (a.qs.rows > 0)
-        attention_dq_kernel<T><<<dim3((unsigned)((a.qs.rows * a.H + 3) / 4)), 256, 0, s>>>(a);
-    if (a.ks.rows > 0)
-        attention_dkv_kernel<T><<<dim3((unsigned)((a.ks.rows * a.Hk + 3) / 4)), 256, 0, s>>>(a);
+    constexpr bool k16 = sizeof(T) == 2;
+    const dim3 q((unsigned)(row_slots(a.qs, a.H / a.Hk, 128) * a.Hk));
+    const dim3 k((unsigned)(row_slots(a.ks, 1, 128) * a.Hk));
+    if (a.qs.rows > 0) {
+        if (a.D <= 64)
+            attention_dq_kernel<T, 64, 64><<<q, 256, 0, s>>>(a);
+        else
+            attention_dq_kernel<T, 128, k16 ? 64 : 32><<<q, 256, 0, s>>>(a);
+    }
+    if (a.ks.rows > 0) {
+        if (a.D <= 64)
+            attention_dkv_kernel<T, 64, k16 ? 64 : 32><<<k, 256, 0, s>>>(a);
+        else
+            attention_dkv_kernel<T, 128, 32><<<k, 256, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 

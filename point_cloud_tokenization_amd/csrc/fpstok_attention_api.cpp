@@ -126,7 +126,7 @@ static AttnArgs attn_args(const fpstok_seqs* qs, const fpstok_seqs* ks,
 static size_t attn_workspace(const fpstok_seqs* qs, const fpstok_seqs*,
                              const fpstok_attn_params* p, bool backward) {
     if (!backward) return 0;
-    return ((size_t)qs->num_rows * p->num_heads * sizeof(float) + 255) & ~(size_t)255;
+    return ((size_t)qs->num_rows * p->num_heads * sizeof(float2) + 255) & ~(size_t)255;
 }
 
 static fpstok_status check_attn_ws(size_t need, void* ws, size_t ws_bytes) {
@@ -215,7 +215,7 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
     a.grad_k = heads_arg(grad_k);
     a.grad_v = heads_arg(grad_v);
     a.lse = const_cast<float*>(lse);
-    a.delta = (float*)ws;
+    a.stat = (float2*)ws;
     const hipError_t e = launch_attention_backward(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "attention gradient kernel launch");
     return ok();

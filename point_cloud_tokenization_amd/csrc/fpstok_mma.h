@@ -110,7 +110,6 @@ struct Tile {
                                                     int lane) {
         if constexpr (sizeof(T) == 2) {
             using s4 = short __attribute__((ext_vector_type(4)));
-            using s8 = short __attribute__((ext_vector_type(8)));
             const int i = lane & 15, r = ((lane >> 5) << 2) + (i >> 2);
             const int c = db * 4 + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
             const FPSTOK_LDS char* p = t + row0 * kPitch + place(r, c) + (i & 1) * 8;
@@ -195,6 +194,27 @@ struct Stage {
                 bad = true;
             }
         return bad;
+    }
+};
+
+// The same for rows numbered query * G + head of a group of heads: row `at` +
+// i of the tile starts at base + (row / G) * stride + (row % G) * head.
+template <class T, int DP, int ROWS, int THREADS>
+struct StageRows : Stage<T, DP, ROWS, THREADS> {
+    using Base = Stage<T, DP, ROWS, THREADS>;
+    __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t head, int64_t at,
+                                         int G, int rows, int D, int tid) {
+        using Tl = Tile<T, DP>;
+#pragma unroll
+        for (int i = 0; i < Base::kPer; ++i) {
+            const int n = i * THREADS + tid, r = n / Tl::kChunks, c = n % Tl::kChunks;
+            u32x4 v = {0, 0, 0, 0};
+            if (r < rows && c * Tl::kElems < D) {
+                const int64_t q = (at + r) / G, g = (at + r) - q * G;
+                v = *(const u32x4*)(base + q * stride + g * head + c * Tl::kElems);
+            }
+            this->x[i] = v;
+        }
     }
 };
 
