@@ -401,8 +401,8 @@ typedef struct {
  *       256-byte aligned (NULL if that is 0)
  * data pointers are 16-byte aligned, and so are the strides in bytes.
  * Errors: EINVAL (NULL or misaligned pointers, strides, sizes or parameters
- * out of range), EWORKSPACE, EUNSUPPORTED (more than 2^31 - 1 rows, or rows
- * times heads too many for one launch), EHIP. */
+ * out of range), EWORKSPACE, EUNSUPPORTED (2^30 rows or more, or 2^31 rows
+ * times heads or more), EHIP. */
 fpstok_status fpstok_attention(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
                                const fpstok_attn_params* params, const fpstok_heads* q,
                                const fpstok_heads* k, const fpstok_heads* v,

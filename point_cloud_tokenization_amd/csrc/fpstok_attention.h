@@ -34,6 +34,17 @@ struct AttnArgs {
     int32_t H, Hk, D, dtype;
     int32_t left, right, sinks;
     float scale;
+    // keys of a row split over `splits` workgroups (forward): their partial
+    // results, [splits][Hk][q rows * H / Hk] of D floats and of (maximum * c, sum)
+    int32_t splits;
+    float* part;
+    float2* part_ml;
+};
+
+// How a call is laid out on the device, from the shapes alone.
+struct AttnPlan {
+    bool few;        // at most 32 rows per sequence and key head: waves split the keys
+    int32_t splits;  // workgroups a row's keys are split over
 };
 
 struct RopeArgs {
@@ -46,7 +57,8 @@ struct RopeArgs {
     int32_t first_pair[kMaxAxes + 1];  // pairs of axis a: first_pair[a] .. first_pair[a+1]-1
 };
 
-hipError_t launch_attention(const AttnArgs& a, hipStream_t s);
+AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len);
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
 

@@ -47,34 +47,42 @@ __device__ __forceinline__ bool row_tile(const AttnArgs& a, const SeqArgs& s, in
 }
 
 // Keys that some row with a place in [pa, pb] sees, in tiles of BN: `sink`
-// tiles from key 0 on, then tiles first .. first + count - sink - 1.
+// tiles from key 0 on, then tiles first .. first + count - sink - 1.  (Rows
+// stay below 2^30 and windows below the rows, so places fit in 32 bits.)
 template <int BN>
 struct KeyTiles {
-    int sink, first, count;
-    __device__ __forceinline__ KeyTiles(const AttnArgs& a, int64_t pa, int64_t pb, int tk) {
-        int64_t hi = tk - 1, lo = 0;
+    int sink, first, count, from = 0;
+    __device__ __forceinline__ KeyTiles(const AttnArgs& a, int pa, int pb, int tk) {
+        int hi = tk - 1, lo = 0;
         if (a.right >= 0 && pb + a.right < hi) hi = pb + a.right;
         if (a.left >= 0 && pa - a.left > 0) lo = pa - a.left;
-        first = (int)(lo / BN);
+        first = lo / BN;
         sink = 0;
         count = 0;
         if (hi >= 0) {
-            const int last = (int)(hi / BN);
-            const int64_t n = a.sinks < hi + 1 ? a.sinks : hi + 1;
-            sink = (int)((n + BN - 1) / BN);
+            const int last = hi / BN;
+            const int n = a.sinks < hi + 1 ? a.sinks : hi + 1;
+            sink = (n + BN - 1) / BN;
             if (sink > first) sink = first;
             count = sink + (last >= first ? last - first + 1 : 0);
         }
     }
-    __device__ __forceinline__ int tile(int i) const { return i < sink ? i : first + i - sink; }
+    __device__ __forceinline__ int tile(int i) const {
+        i += from;
+        return i < sink ? i : first + i - sink;
+    }
+    // Keeps the tiles of part `split` of `splits` and returns their number.
+    __device__ __forceinline__ int part(int split, int splits) {
+        from = (int)((int64_t)count * split / splits);
+        return (int)((int64_t)count * (split + 1) / splits) - from;
+    }
 };
 
 // How the keys j0 .. j0 + BN - 1 look to rows with places in [pa, pb]: 0 no
 // row sees any, 1 some rows hide some, 2 every row sees all.
 template <int BN>
-__device__ __forceinline__ int tile_view(const AttnArgs& a, int64_t pa, int64_t pb, int tk,
-                                         int j0) {
-    const int64_t j1 = (int64_t)j0 + BN - 1;
+__device__ __forceinline__ int tile_view(const AttnArgs& a, int pa, int pb, int tk, int j0) {
+    const int j1 = j0 + BN - 1;
     const bool left_all = a.left < 0 || j0 >= pb - a.left || j1 < a.sinks;
     const bool left_none = a.left >= 0 && j1 < pa - a.left && j0 >= a.sinks;
     const bool right_all = j1 < tk && (a.right < 0 || j1 <= pa + a.right);
@@ -124,6 +132,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     const int G = a.H / a.Hk;
     RowTile t;
     if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
+    const int split = blockIdx.y;
 
     // this lane's row
     const int r = wave * 32 + (lane & 31);
@@ -142,18 +151,18 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
         }
     }
     // places of the workgroup's, the wave's and the lane's rows
-    const int64_t off = (int64_t)t.tk - t.tq;
+    const int off = t.tk - t.tq;
     const int last = t.rows > 0 ? t.rows - 1 : 0;
-    const int64_t pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
+    const int pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
     const int wl = wave * 32 + 31 < last ? wave * 32 + 31 : last;
-    const int64_t wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
+    const int wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
     const bool wave_live = wave * 32 < t.rows;
-    const int64_t p = qi + off;
-    const int hi = (int)(a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1);
-    const int lo = (int)(a.left >= 0 && p - a.left > 0 ? p - a.left : 0);
+    const int p = qi + off;
+    const int hi = a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1;
+    const int lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
 
     KeyTiles<BN> kt(a, pa, pb, t.tk);
-    const int n = t.rows > 0 ? kt.count : 0;
+    const int n = t.rows > 0 ? kt.part(split, a.splits) : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     Stage<T, DP, BN, 256> sk, sv;
@@ -166,12 +175,12 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     };
     auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        sk.store(buf, tid);
+        sk.store(buf, a.D, tid);
         // a value that some row must not see is multiplied by a weight of 0
         // there: an infinite one has to leave the product
-        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sv.clean())
+        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sv.clean(tid))
             bad_tag[i & 1] = i + 1;
-        sv.store(buf + BN * Tl::kPitch, tid);
+        sv.store(buf + BN * Tl::kPitch, a.D, tid);
     };
 
     f32x16 o[DB];
@@ -245,17 +254,272 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     }
     l = pair_sum(l);
     const bool some = m != -INFINITY || l != 0.0f;
-    const float inv = live && some ? 1.0f / l : 0.0f;
-    T* out = (T*)a.out.data + qrow * a.out.row + h * a.out.head;
     if (!some) {
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[db] = 0.0f;
     }
-    store_row<T, DB>(o, inv, r < t.rows || r < t.pad ? out : nullptr, a.D, lane);
+    if (a.splits > 1) {
+        const int64_t at = ((int64_t)split * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + r;
+        store_row<float, DB>(o, 1.0f, live ? a.part + at * a.D : nullptr, a.D, lane);
+        if (live && half == 0) a.part_ml[at] = make_float2(some ? mc : -INFINITY, l);
+        return;
+    }
+    const float inv = live && some ? 1.0f / l : 0.0f;
+    T* out = (T*)a.out.data + qrow * a.out.row + h * a.out.head;
+    store_row<T, DB>(o, inv, live || r < t.pad ? out : nullptr, a.D, lane);
     if (a.lse && half == 0 && (live || r < t.pad))
         a.lse[qrow * a.H + h] =
             !live ? 0.0f
                   : some ? (mc + __builtin_amdgcn_logf(l)) * 0.693147180559945f : -INFINITY;
+}
+
+// Forward for sequences of at most 32 rows per key head (one query, or a few,
+// against many keys): a workgroup takes 32 rows and its 4 waves take turns at
+// the key tiles, each with its own LDS, running maximum and sum; they are
+// joined at the end.  No wave waits for another inside the walk, so 4 tiles of
+// K and V per workgroup are on their way at a time.
+template <class T, int DP, int BN>
+__global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) > 3 ? 3 : 512 / (DP * (int)sizeof(T)))
+void attention_few_kernel(AttnArgs a) {
+    constexpr int BM = 32, DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
+    using Tl = Tile<T, DP>;
+    using Frag = typename Elem<T>::Frag;
+    constexpr int kWaveBytes = 2 * BN * Tl::kPitch;
+    // the join keeps 32 x DP floats of every wave in its tiles' place
+    static_assert(kWaveBytes >= BM * DP * 4, "join buffer");
+    __shared__ __attribute__((aligned(16))) char smem[4 * kWaveBytes];
+    __shared__ float2 ml[4][BM];
+    FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = a.H / a.Hk;
+    RowTile t;
+    if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
+    const int split = blockIdx.y;
+
+    const int r = lane & 31;
+    const int qi = (t.row0 + r) / G, h = t.hk * G + (t.row0 + r) - qi * G;
+    const bool live = r < t.rows;
+    const int64_t qrow = t.q0 + qi;
+    Frag qf[STEPS];
+    {
+        const T* q = (const T*)a.q.data + qrow * a.q.row + h * a.q.head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = s * 16 + half * 8;
+            Frag f = {};
+            if (live && d < a.D) f = *(const Frag*)(q + d);
+            qf[s] = f;
+        }
+    }
+    const int off = t.tk - t.tq;
+    const int last = t.rows > 0 ? t.rows - 1 : 0;
+    const int pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
+    const int p = qi + off;
+    const int hi = a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1;
+    const int lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
+
+    KeyTiles<BN> kt(a, pa, pb, t.tk);
+    const int n = t.rows > 0 ? kt.part(split, a.splits) : 0;
+    const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
+    const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
+    Stage<T, DP, BN, 64> sk, sv;
+    FPSTOK_LDS char* kbuf = lds + wave * kWaveBytes;
+    FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
+    auto load = [&](int i) {
+        const int64_t j0 = (int64_t)kt.tile(i) * BN;
+        sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, lane);
+        sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, lane);
+    };
+
+    f32x16 o[DB];
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[db] = 0.0f;
+    const float c = a.scale * 1.44269504088896f;  // log2 e
+    float m = -INFINITY, mc = 0.0f, l = 0.0f;
+
+    if (wave < n) load(wave);
+    for (int i = wave; i < n; i += 4) {
+        const int j0 = kt.tile(i) * BN;
+        const int view = tile_view<BN>(a, pa, pb, t.tk, j0);
+        const bool bad = view == 1 && __any(sv.clean(lane));
+        wave_sync();  // the wave's reads of the last tile are done
+        sk.store(kbuf, a.D, lane);
+        sv.store(vbuf, a.D, lane);
+        wave_sync();
+        if (i + 4 < n) load(i + 4);
+        float s[KB * 16];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            f32x16 x = 0.0f;
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st)
+                x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b * 16 + e] = x[e];
+        }
+        if (view == 1) {
+#pragma unroll
+            for (int e = 0; e < KB * 16; ++e) {
+                const int j = j0 + (e >> 4) * 32 + ((e >> 2) & 3) * 8 + half * 4 + (e & 3);
+                if (j > hi || (j < lo && j >= a.sinks)) s[e] = -INFINITY;
+            }
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int e = 1; e < KB * 16; ++e) mx = fmaxf(mx, s[e]);
+        mx = pair_max(mx);
+        if (__any(mx * c > mc + 8.0f || m == -INFINITY)) {
+            const float m2 = fmaxf(m, mx);
+            const float mc2 = m2 == -INFINITY ? 0.0f : m2 * c;
+            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mc - mc2);
+            m = m2;
+            mc = mc2;
+            l *= f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[db] *= f;
+        }
+#pragma unroll
+        for (int e = 0; e < KB * 16; ++e) {
+            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -mc));
+            l += s[e];
+        }
+#pragma unroll
+        for (int k = 0; k < KB * 2; ++k) {
+            const Frag pf = to_frag<T>(s + k * 8);
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+                o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, o[db]);
+        }
+        if (bad)
+            add_bad<T, DB>(o, vb, a.v.row, j0, j0 + BN < hi + 1 ? j0 + BN : hi + 1, a.D, half,
+                           [&](int j) { return j >= lo || j < a.sinks; });
+    }
+    l = pair_sum(l);
+    if (m == -INFINITY && l == 0.0f) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] = 0.0f;
+    }
+    wave_sync();
+    if (half == 0) ml[wave][r] = make_float2(m == -INFINITY && l == 0.0f ? -INFINITY : mc, l);
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            using f4 = float __attribute__((ext_vector_type(4)));
+            f4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = o[db][g * 4 + e];
+            *(FPSTOK_LDS f4*)(kbuf + (r * DP + db * 32 + g * 8 + half * 4) * 4) = x;
+        }
+    __syncthreads();
+    // 4 elements per thread and turn
+    const int rows = t.rows > t.pad ? t.rows : t.pad;
+    for (int x = tid; x < rows * (DP / 4); x += 256) {
+        using f4 = float __attribute__((ext_vector_type(4)));
+        const int row = x / (DP / 4), d = (x % (DP / 4)) * 4;
+        if (d >= a.D) continue;
+        const int q = (t.row0 + row) / G, hh = t.hk * G + (t.row0 + row) - q * G;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][row].x);
+        float sum = 0.0f;
+        f4 y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 z = ml[w][row];
+            if (z.x == -INFINITY && z.y == 0.0f) continue;
+            const float f = __builtin_amdgcn_exp2f(z.x - top);
+            sum += z.y * f;
+            y += f * *(FPSTOK_LDS f4*)(lds + w * kWaveBytes + (row * DP + d) * 4);
+        }
+        const bool here = row < t.rows, some = top != -INFINITY || sum != 0.0f;
+        if (a.splits > 1) {
+            if (!here) continue;
+            const int64_t at =
+                ((int64_t)split * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + row;
+            *(f4*)(a.part + at * a.D + d) = y;
+            if (d == 0) a.part_ml[at] = make_float2(some ? top : -INFINITY, sum);
+            continue;
+        }
+        y *= here && some ? 1.0f / sum : 0.0f;
+        if (!here || !some) y = 0.0f;
+        using T4 = T __attribute__((ext_vector_type(4)));
+        *(T4*)((T*)a.out.data + (t.q0 + q) * a.out.row + hh * a.out.head + d) =
+            __builtin_convertvector(y, T4);
+        if (a.lse && d == 0)
+            a.lse[(t.q0 + q) * a.H + hh] =
+                !here ? 0.0f
+                      : some ? (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f : -INFINITY;
+    }
+}
+
+// Joins the parts of a row whose keys were split: a workgroup per (query,
+// head).  Its threads take 4 elements each of every kGroups-th part, so a
+// thread's loads do not wait for one another; the groups' sums are added in
+// order.
+template <class T>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+    using f4 = float __attribute__((ext_vector_type(4)));
+    constexpr int kGroups = 8;
+    __shared__ float factor[256];  // at most 256 parts
+    __shared__ f4 sums[kGroups][32];
+    __shared__ float wave_top[4], wave_sum[4];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x / a.H;
+    const int h = (int)(blockIdx.x % a.H), G = a.H / a.Hk, hk = h / G;
+    bool here = true;
+    if (a.qs.cu) {
+        if (row < cu_at(a.qs, 0) || row >= cu_at(a.qs, a.qs.B)) return;
+    } else {
+        here = row % a.qs.cap < a.qs.count[row / a.qs.cap];
+    }
+    const int64_t step = (int64_t)a.Hk * a.qs.rows * G;
+    const int64_t at = ((int64_t)hk * a.qs.rows + row) * G + h - hk * G;
+    float2 z = make_float2(-INFINITY, 0.0f);
+    if (here && tid < a.splits) z = a.part_ml[tid * step + at];
+    const bool seen = !(z.x == -INFINITY && z.y == 0.0f);
+    float top = z.x;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) wave_top[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    const float f = seen ? __builtin_amdgcn_exp2f(z.x - top) : 0.0f;
+    factor[tid] = f;
+    float sum = z.y * f;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+    if (lane == 0) wave_sum[tid >> 6] = sum;
+    __syncthreads();
+    sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+    const int d = (tid & 31) * 4, group = tid >> 5;
+    if (here) {
+        f4 y = 0.0f;
+        const float* part = a.part + at * a.D + (d < a.D ? d : 0);
+        const int64_t stride = step * a.D;
+#pragma unroll 4
+        for (int s = group; s < a.splits; s += kGroups)
+            y += factor[s] * *(const f4*)(part + s * stride);
+        sums[group][tid & 31] = y;
+    }
+    __syncthreads();
+    const bool some = here && (top != -INFINITY || sum != 0.0f);
+    if (tid < 32 && d < a.D) {
+        f4 y = 0.0f;
+        if (some) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) y += sums[g][tid];
+            y *= 1.0f / sum;
+        }
+        using T4 = T __attribute__((ext_vector_type(4)));
+        *(T4*)((T*)a.out.data + row * a.out.row + h * a.out.head + d) =
+            __builtin_convertvector(y, T4);
+    }
+    if (a.lse && tid == 0)
+        a.lse[row * a.H + h] =
+            !here ? 0.0f
+                  : some ? (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f : -INFINITY;
 }
 
 // grad_q, and the rows' statistics for the kernel below.  Rows and key tiles as
@@ -312,15 +576,15 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
                     make_float2(lse2, delta);
         }
     }
-    const int64_t off = (int64_t)t.tk - t.tq;
+    const int off = t.tk - t.tq;
     const int last = t.rows > 0 ? t.rows - 1 : 0;
-    const int64_t pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
+    const int pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
     const int wl = wave * 32 + 31 < last ? wave * 32 + 31 : last;
-    const int64_t wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
+    const int wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
     const bool wave_live = wave * 32 < t.rows;
-    const int64_t p = qi + off;
-    const int hi = (int)(a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1);
-    const int lo = (int)(a.left >= 0 && p - a.left > 0 ? p - a.left : 0);
+    const int p = qi + off;
+    const int hi = a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1;
+    const int lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
 
     KeyTiles<BN> kt(a, pa, pb, t.tk);
     const int n = t.rows > 0 ? kt.count : 0;
@@ -336,10 +600,10 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
     };
     auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sk.clean())
+        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sk.clean(tid))
             bad_tag[i & 1] = i + 1;
-        sk.store(buf, tid);
-        sv.store(buf + BN * Tl::kPitch, tid);
+        sk.store(buf, a.D, tid);
+        sv.store(buf + BN * Tl::kPitch, a.D, tid);
     };
 
     f32x16 dq[DB];
@@ -446,60 +710,73 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
         }
     }
     // rows that see some key of the tile, and those that see this lane's key
-    const int64_t off = (int64_t)t.tk - t.tq;
+    const int off = t.tk - t.tq;
     const int j = t.row0 + r;
-    int64_t i0 = 0, i1 = t.tq - 1, e0 = 0, e1 = t.tq - 1;
+    int i0 = 0, i1 = t.tq - 1, e0 = 0, e1 = t.tq - 1;
     if (a.right >= 0) {
         if (t.row0 - a.right - off > 0) i0 = t.row0 - a.right - off;
         if (j - a.right - off > 0) e0 = j - a.right - off;
     }
     if (a.left >= 0) {
-        const int64_t jl = t.row0 + t.rows - 1;
+        const int jl = t.row0 + t.rows - 1;
         if (t.row0 >= a.sinks && jl + a.left - off < i1) i1 = jl + a.left - off;
         if (j >= a.sinks && j + a.left - off < e1) e1 = j + a.left - off;
     }
-    const int64_t n_rows = t.rows > 0 && i1 >= i0 ? (i1 - i0 + 1) * G : 0;
+    const int64_t n_rows = t.rows > 0 && i1 >= i0 ? (int64_t)(i1 - i0 + 1) * G : 0;
     const int n = (int)((n_rows + BQ - 1) / BQ);
-    const int64_t first = i0 * G;  // row (query * G + head) of the walk's start
-    // this lane's rows, counted from there
-    const int64_t see0 = e0 * G - first, see1 = (e1 + 1) * G - first;
+    // this lane's rows, counted from the walk's start (query i0, head 0)
+    const int64_t see0 = (int64_t)(e0 - i0) * G, see1 = (int64_t)(e1 + 1 - i0) * G;
 
-    const T* qb = (const T*)a.q.data + t.q0 * a.q.row + (int64_t)t.hk * G * a.q.head;
-    const T* gb = (const T*)a.grad_out.data + t.q0 * a.grad_out.row +
+    const T* qb = (const T*)a.q.data + (t.q0 + i0) * a.q.row + (int64_t)t.hk * G * a.q.head;
+    const T* gb = (const T*)a.grad_out.data + (t.q0 + i0) * a.grad_out.row +
                   (int64_t)t.hk * G * a.grad_out.head;
-    const float2* sb = a.stat + ((int64_t)t.hk * a.qs.rows + t.q0) * G + first;
+    const float2* sb = a.stat + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
+    const float over_g = 1.0f / (float)G;
     if (tid < 2) bad_tag[tid] = 0;
 
-    StageRows<T, DP, BQ, 256> sq, sg;
-    float2 sst = make_float2(0.0f, 0.0f);
-    auto load = [&](int i) {
-        const int64_t at = first + (int64_t)i * BQ;
-        const int64_t left = n_rows - (int64_t)i * BQ;
-        const int rows = left < BQ ? (int)left : BQ;
-        sq.load(qb, a.q.row, a.q.head, at, G, rows, a.D, tid);
-        sg.load(gb, a.grad_out.row, a.grad_out.head, at, G, rows, a.D, tid);
-        sst = make_float2(0.0f, 0.0f);
-        if (tid < rows) sst = sb[(int64_t)i * BQ + tid];
+    // tile i of the walk: its first row is head `g` of query i0 + `q`
+    struct Place {
+        int q, g, rows;
     };
-    auto view_of = [&](int i, int k0) {  // the tile's rows against 32 keys
-        const int64_t at = first + (int64_t)i * BQ;
-        const int64_t end = first + n_rows < at + BQ ? first + n_rows : at + BQ;
-        return tile_view<32>(a, at / G + off, (end - 1) / G + off, t.tk, t.row0 + k0);
+    const int step_q = BQ / G, step_g = BQ % G;
+    Place next{0, 0, 0}, cur;
+    auto rows_of = [&](int i) {
+        const int64_t left = n_rows - (int64_t)i * BQ;
+        return left < BQ ? (int)left : BQ;
+    };
+    auto view_of = [&](const Place& at, int k0) {  // the tile's rows against 32 keys
+        const int pa = i0 + at.q + off;
+        return tile_view<32>(a, pa, pa + group_div(at.g + at.rows - 1, over_g), t.tk, t.row0 + k0);
+    };
+    Stage<T, DP, BQ, 256> sq, sg;
+    float2 sst = make_float2(0.0f, 0.0f);
+    auto load = [&](int i) {  // tiles in turn
+        if (i > 0) {
+            next.q += step_q;
+            next.g += step_g;
+            if (next.g >= G) ++next.q, next.g -= G;
+        }
+        next.rows = rows_of(i);
+        sq.load_group(qb + next.q * a.q.row, a.q.row, a.q.head, next.g, G, over_g, next.rows, a.D,
+                      tid);
+        sg.load_group(gb + next.q * a.grad_out.row, a.grad_out.row, a.grad_out.head, next.g, G,
+                      over_g, next.rows, a.D, tid);
+        sst = sb[(int64_t)i * BQ + (tid < next.rows ? tid : next.rows - 1)];
     };
     auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
         bool part = false;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(i, w * 32) != 2;
+        for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(next, w * 32) != 2;
         if (part) {
-            const bool bq = sq.clean(), bg = sg.clean();
+            const bool bq = sq.clean(tid), bg = sg.clean(tid);
             if (bq || bg) bad_tag[i & 1] = i + 1;
         }
-        sq.store(buf, tid);
-        sg.store(buf + BQ * Tl::kPitch, tid);
+        sq.store(buf, a.D, tid);
+        sg.store(buf + BQ * Tl::kPitch, a.D, tid);
         if (tid < BQ) {
-            stat[i & 1][0][tid] = sst.x;
-            stat[i & 1][1][tid] = sst.y;
+            stat[i & 1][0][tid] = tid < next.rows ? sst.x : 0.0f;
+            stat[i & 1][1][tid] = tid < next.rows ? sst.y : 0.0f;
         }
     };
 
@@ -515,8 +792,9 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
     }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
+        cur = next;
         if (i + 1 < n) load(i + 1);
-        const int view = wave * 32 < t.rows ? view_of(i, wave * 32) : 0;
+        const int view = wave * 32 < t.rows ? view_of(cur, wave * 32) : 0;
         if (view != 0) {
             const FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
             const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
@@ -562,7 +840,7 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
                 int64_t b0 = (int64_t)i * BQ, b1 = b0 + BQ < n_rows ? b0 + BQ : n_rows;
                 if (b0 < see0) b0 = see0;
                 if (b1 > see1) b1 = see1;
-                for (int64_t x = first + b0; x < first + b1; ++x) {
+                for (int64_t x = b0; x < b1; ++x) {
                     const int64_t qi = x / G, g = x - qi * G;
                     const auto all = [](int) { return true; };
                     add_bad<T, DB>(dk, qb + qi * a.q.row + g * a.q.head, 0, 0, 1, a.D, half, all);
@@ -591,13 +869,47 @@ static int64_t row_slots(const SeqArgs& s, int G, int BM) {
     return (int64_t)s.B * (((int64_t)s.cap * G + BM - 1) / BM);
 }
 
+// Splits a row's keys until the grid has `want` workgroups, but not into
+// parts of fewer than `least` keys.
+static int key_splits(const AttnArgs& a, int64_t blocks, int64_t q_len, int64_t k_len,
+                      int64_t want, int64_t least) {
+    int64_t seen = k_len;
+    if (a.left >= 0 && a.right >= 0 && seen > q_len + a.left + a.right + a.sinks)
+        seen = q_len + a.left + a.right + a.sinks;
+    int64_t n = (want + blocks - 1) / (blocks > 0 ? blocks : 1);
+    if (n > seen / least) n = seen / least;
+    return n < 1 ? 1 : n > 256 ? 256 : (int)n;
+}
+
+AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
+    const int G = a.H / a.Hk;
+    AttnPlan p;
+    p.few = (int64_t)q_len * G <= 32;
+    const int BM = p.few ? 32 : 128;
+    const int64_t blocks = row_slots(a.qs, G, BM) * a.Hk;
+    p.splits = p.few ? key_splits(a, blocks, q_len, k_len, 2048, 512)
+                     : key_splits(a, blocks, 128 / G + 1, k_len, 512, 1024);
+    return p;
+}
+
 template <class T>
-static hipError_t forward(const AttnArgs& a, hipStream_t s) {
-    const int64_t blocks = row_slots(a.qs, a.H / a.Hk, 128) * a.Hk;
-    if (a.D <= 64)
-        attention_kernel<T, 64, 64><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
-    else
-        attention_kernel<T, 128, sizeof(T) == 2 ? 64 : 32><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
+static hipError_t forward(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+    constexpr bool k16 = sizeof(T) == 2;
+    const int64_t blocks = row_slots(a.qs, a.H / a.Hk, plan.few ? 32 : 128) * a.Hk;
+    const dim3 grid((unsigned)blocks, (unsigned)a.splits);
+    if (plan.few) {
+        if (a.D <= 64)
+            attention_few_kernel<T, 64, 32><<<grid, 256, 0, s>>>(a);
+        else
+            attention_few_kernel<T, 128, 32><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (a.D <= 64)
+            attention_kernel<T, 64, 64><<<grid, 256, 0, s>>>(a);
+        else
+            attention_kernel<T, 128, k16 ? 64 : 32><<<grid, 256, 0, s>>>(a);
+    }
+    if (a.splits > 1)
+        attention_join_kernel<T><<<dim3((unsigned)(a.qs.rows * a.H)), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -621,9 +933,10 @@ static hipError_t backward(const AttnArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_attention(const AttnArgs& a, hipStream_t s) {
-    return a.dtype == 0 ? forward<float>(a, s)
-                        : a.dtype == 1 ? forward<_Float16>(a, s) : forward<__bf16>(a, s);
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+    return a.dtype == 0   ? forward<float>(a, plan, s)
+           : a.dtype == 1 ? forward<_Float16>(a, plan, s)
+                          : forward<__bf16>(a, plan, s);
 }
 
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s) {

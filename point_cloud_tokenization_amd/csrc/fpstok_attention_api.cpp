@@ -62,10 +62,12 @@ static fpstok_status check_attn(const fpstok_seqs* qs, const fpstok_seqs* ks,
         return fail(FPSTOK_EINVAL, "num_sinks must be in [0, %d]", FPSTOK_MAX_SINKS);
     if (!std::isfinite(p->scale) || p->scale <= 0.0f)
         return fail(FPSTOK_EINVAL, "scale must be finite and > 0");
-    // one workgroup per wave of rows and head at the finest split
-    if (qs->num_rows * p->num_heads >= ((int64_t)1 << 33) ||
-        ks->num_rows * p->num_kv_heads >= ((int64_t)1 << 33))
-        return fail(FPSTOK_EUNSUPPORTED, "rows times heads >= 2^33");
+    // rows, places and windows are 32-bit numbers in the kernels
+    if (qs->num_rows >= ((int64_t)1 << 30) || ks->num_rows >= ((int64_t)1 << 30))
+        return fail(FPSTOK_EUNSUPPORTED, "num_rows >= 2^30");
+    if (qs->num_rows * p->num_heads >= ((int64_t)1 << 31) ||
+        ks->num_rows * p->num_kv_heads >= ((int64_t)1 << 31))
+        return fail(FPSTOK_EUNSUPPORTED, "rows times heads >= 2^31");
     return FPSTOK_OK;
 }
 
@@ -116,17 +118,41 @@ static AttnArgs attn_args(const fpstok_seqs* qs, const fpstok_seqs* ks,
     a.Hk = p->num_kv_heads;
     a.D = p->head_dim;
     a.dtype = p->dtype;
-    a.left = p->window_left;
-    a.right = p->window_right;
+    // a window that reaches over every row hides nothing
+    a.left = p->window_left < ks->num_rows ? p->window_left : -1;
+    a.right = p->window_right < qs->num_rows ? p->window_right : -1;
     a.sinks = p->num_sinks;
     a.scale = p->scale;
     return a;
 }
 
-static size_t attn_workspace(const fpstok_seqs* qs, const fpstok_seqs*,
-                             const fpstok_attn_params* p, bool backward) {
-    if (!backward) return 0;
-    return ((size_t)qs->num_rows * p->num_heads * sizeof(float2) + 255) & ~(size_t)255;
+// A length to plan with: the caller's bound, or else the slots of a padded
+// sequence or the mean length of packed ones.
+static int32_t likely_len(const fpstok_seqs* s) {
+    if (s->max_len > 0) return s->max_len;
+    if (s->token_count) return s->capacity;
+    return s->num_seqs > 0 ? (int32_t)((s->num_rows + s->num_seqs - 1) / s->num_seqs) : 0;
+}
+
+static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Plans a call and lays out its workspace (pointers are offsets from `ws`);
+// returns the bytes it needs.
+static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backward, void* ws,
+                      AttnArgs& a, AttnPlan& plan) {
+    const size_t rows = (size_t)qs->num_rows * a.H;
+    char* at = (char*)ws;
+    if (backward) {
+        a.stat = (float2*)at;
+        return align256(rows * sizeof(float2));
+    }
+    plan = plan_attention(a, likely_len(qs), likely_len(ks));
+    a.splits = plan.splits;
+    if (plan.splits == 1) return 0;
+    const size_t ml = align256(rows * plan.splits * sizeof(float2));
+    a.part_ml = (float2*)at;
+    a.part = (float*)(at + ml);
+    return ml + align256(rows * plan.splits * a.D * sizeof(float));
 }
 
 static fpstok_status check_attn_ws(size_t need, void* ws, size_t ws_bytes) {
@@ -147,7 +173,9 @@ FPSTOK_API size_t fpstok_attention_workspace_size(const fpstok_seqs* qs, const f
                                                   const fpstok_attn_params* p, int32_t backward) {
     if (!ks) ks = qs;
     if (check_attn(qs, ks, p) != FPSTOK_OK) return 0;
-    return attn_workspace(qs, ks, p, backward != 0);
+    AttnArgs a = attn_args(qs, ks, p);
+    AttnPlan plan;
+    return lay_out(qs, ks, backward != 0, nullptr, a, plan);
 }
 
 FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_seqs* ks,
@@ -166,16 +194,17 @@ FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_se
         (st = check_heads(out, "out", nq, H, D, dt, 16, true)) != FPSTOK_OK)
         return st;
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
-    if ((st = check_attn_ws(attn_workspace(qs, ks, p, false), ws, ws_bytes)) != FPSTOK_OK)
+    AttnArgs a = attn_args(qs, ks, p);
+    AttnPlan plan;
+    if ((st = check_attn_ws(lay_out(qs, ks, false, ws, a, plan), ws, ws_bytes)) != FPSTOK_OK)
         return st;
     if (qs->num_seqs == 0 || nq == 0) return ok();
-    AttnArgs a = attn_args(qs, ks, p);
     a.q = heads_arg(q);
     a.k = heads_arg(k);
     a.v = heads_arg(v);
     a.out = heads_arg(out);
     a.lse = lse;
-    const hipError_t e = launch_attention(a, (hipStream_t)stream);
+    const hipError_t e = launch_attention(a, plan, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "attention kernel launch");
     return ok();
 }
@@ -202,10 +231,11 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
         return st;
     if (nq > 0 && !lse) return fail(FPSTOK_EINVAL, "lse is NULL");
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
-    if ((st = check_attn_ws(attn_workspace(qs, ks, p, true), ws, ws_bytes)) != FPSTOK_OK)
+    AttnArgs a = attn_args(qs, ks, p);
+    AttnPlan plan;
+    if ((st = check_attn_ws(lay_out(qs, ks, true, ws, a, plan), ws, ws_bytes)) != FPSTOK_OK)
         return st;
     if (qs->num_seqs == 0 || nq + nk == 0) return ok();
-    AttnArgs a = attn_args(qs, ks, p);
     a.q = heads_arg(q);
     a.k = heads_arg(k);
     a.v = heads_arg(v);
@@ -215,7 +245,6 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
     a.grad_k = heads_arg(grad_k);
     a.grad_v = heads_arg(grad_v);
     a.lse = const_cast<float*>(lse);
-    a.stat = (float2*)ws;
     const hipError_t e = launch_attention_backward(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "attention gradient kernel launch");
     return ok();

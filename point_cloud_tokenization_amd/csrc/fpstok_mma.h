@@ -157,39 +157,84 @@ __device__ __forceinline__ u32x4 chunk_clean(u32x4 x) {
     return x;
 }
 
+// n / G for 0 <= n < 2^17, G <= 2^16, over_g = 1.0f / G: n + 1/2 lies at least
+// 1 / (2 G) from a multiple of G in units of G, and the product is off by less
+// than n / G * 2^-22 <= 2^-5 / G.
+__device__ __forceinline__ int group_div(int n, float over_g) {
+    return (int)(((float)n + 0.5f) * over_g);
+}
+
 // Rows of a tile on their way from memory to LDS, by THREADS threads: load()
 // issues the loads, store() writes them.  Rows at or past `rows` and elements
-// at or past D read as zero and nothing of them is touched in memory.
+// at or past D become zero: their lanes load a place that exists instead (a
+// load under a divergent branch would be waited for before the branch ends)
+// and drop the value in store().  `rows` must be at least 1.
 template <class T, int DP, int ROWS, int THREADS>
 struct Stage {
     using Tl = Tile<T, DP>;
     static constexpr int kPer = ROWS * Tl::kChunks / THREADS;
-    static_assert(ROWS * Tl::kChunks % THREADS == 0, "whole chunks per thread");
+    static constexpr int kStep = THREADS / Tl::kChunks;  // rows between a thread's chunks
+    static_assert(ROWS * Tl::kChunks % THREADS == 0 && THREADS % Tl::kChunks == 0,
+                  "whole chunks per thread");
     u32x4 x[kPer];
+    int have;  // valid rows of the tile
+
+    static __device__ __forceinline__ int row(int tid) { return tid / Tl::kChunks; }
+    static __device__ __forceinline__ int chunk(int tid) { return tid % Tl::kChunks; }
 
     __device__ __forceinline__ void load(const T* base, int64_t stride, int rows, int D, int tid) {
+        const int c = chunk(tid) * Tl::kElems < D ? chunk(tid) * Tl::kElems : 0;
+        have = rows;
+        if (rows >= ROWS) {
+            const T* p = base + row(tid) * stride + c;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = i * THREADS + tid, r = at / Tl::kChunks, c = at % Tl::kChunks;
-            u32x4 v = {0, 0, 0, 0};
-            if (r < rows && c * Tl::kElems < D)
-                v = *(const u32x4*)(base + r * stride + c * Tl::kElems);
-            x[i] = v;
+            for (int i = 0; i < kPer; ++i) x[i] = *(const u32x4*)(p + i * (kStep * stride));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = i * kStep + row(tid);
+                x[i] = *(const u32x4*)(base + (r < rows ? r : rows - 1) * stride + c);
+            }
         }
     }
-    __device__ __forceinline__ void store(FPSTOK_LDS char* t, int tid) const {
+    // Rows query * G + head of a group of heads: row i of the tile belongs to
+    // query (g0 + i) / G past `base`, whose head `(g0 + i) % G` starts `head`
+    // elements further each.  g0 < G; over_g = 1 / G.
+    __device__ __forceinline__ void load_group(const T* base, int64_t stride, int64_t head, int g0,
+                                               int G, float over_g, int rows, int D, int tid) {
+        const int c = chunk(tid) * Tl::kElems < D ? chunk(tid) * Tl::kElems : 0;
+        have = rows;
+        if (G == 1 && rows >= ROWS) {
+            const T* p = base + row(tid) * stride + c;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = i * THREADS + tid, r = at / Tl::kChunks, c = at % Tl::kChunks;
-            *(FPSTOK_LDS u32x4*)(t + Tl::place(r, c)) = x[i];
+            for (int i = 0; i < kPer; ++i) x[i] = *(const u32x4*)(p + i * (kStep * stride));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = i * kStep + row(tid);
+                const int n = g0 + (r < rows ? r : rows - 1);
+                const int q = group_div(n, over_g);
+                x[i] = *(const u32x4*)(base + q * stride + (n - q * G) * head + c);
+            }
         }
     }
-    // Infinite and not-a-number elements become zero; true if there were any.
-    __device__ __forceinline__ bool clean() {
+    __device__ __forceinline__ void store(FPSTOK_LDS char* t, int D, int tid) {
+        if (have < ROWS || D < DP) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (i * kStep + row(tid) >= have || chunk(tid) * Tl::kElems >= D) x[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            *(FPSTOK_LDS u32x4*)(t + Tl::place(i * kStep + row(tid), chunk(tid))) = x[i];
+    }
+    // Infinite and not-a-number elements of rows that exist become zero; true
+    // if there were any.
+    __device__ __forceinline__ bool clean(int tid) {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (chunk_bad<T>(x[i])) {
+            if (i * kStep + row(tid) < have && chunk_bad<T>(x[i])) {
                 x[i] = chunk_clean<T>(x[i]);
                 bad = true;
             }
@@ -197,26 +242,12 @@ struct Stage {
     }
 };
 
-// The same for rows numbered query * G + head of a group of heads: row `at` +
-// i of the tile starts at base + (row / G) * stride + (row % G) * head.
-template <class T, int DP, int ROWS, int THREADS>
-struct StageRows : Stage<T, DP, ROWS, THREADS> {
-    using Base = Stage<T, DP, ROWS, THREADS>;
-    __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t head, int64_t at,
-                                         int G, int rows, int D, int tid) {
-        using Tl = Tile<T, DP>;
-#pragma unroll
-        for (int i = 0; i < Base::kPer; ++i) {
-            const int n = i * THREADS + tid, r = n / Tl::kChunks, c = n % Tl::kChunks;
-            u32x4 v = {0, 0, 0, 0};
-            if (r < rows && c * Tl::kElems < D) {
-                const int64_t q = (at + r) / G, g = (at + r) - q * G;
-                v = *(const u32x4*)(base + q * stride + g * head + c * Tl::kElems);
-            }
-            this->x[i] = v;
-        }
-    }
-};
+// Orders a wave's own LDS writes and reads across its lanes (other waves are
+// not waited for).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 // max / sum of a value over the two lanes l and l ^ 32.
 __device__ __forceinline__ float pair_max(float x) {
