@@ -4,6 +4,8 @@
 
 namespace fpstok {
 
+constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
+
 // The rows of one workgroup's tile.  A row is a (query, head of the group) pair
 // of one key head, numbered query * G + head: every row of a tile reads the
 // same keys, so one query of 8 heads is 8 rows of a tile, and K and V are read
@@ -90,25 +92,150 @@ __device__ __forceinline__ int tile_view(const AttnArgs& a, int pa, int pb, int 
     return left_none || right_none ? 0 : left_all && right_all ? 2 : 1;
 }
 
-// Adds the infinite and not-a-number values of rows [j0, j1) that this lane
-// sees (`sees`) to its transposed result.  Rare: only for tiles that hold such
-// values and that some row's mask hides in part.
-template <class T, int DB, class Sees>
-__device__ __forceinline__ void add_bad(f32x16* acc, const T* base, int64_t stride, int j0, int j1,
-                                        int D, int half, Sees sees) {
-    for (int j = j0; j < j1; ++j) {
-        if (!sees(j)) continue;
+// The keys one row sees: [lo, lo + span] and those below `sink`.
+struct Window {
+    int lo, sink;
+    uint32_t span;
+    __device__ __forceinline__ Window(const AttnArgs& a, int p, int tk) {
+        const int hi = a.right >= 0 && p + a.right < tk - 1 ? p + a.right : tk - 1;
+        lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
+        sink = a.sinks < hi + 1 ? a.sinks : hi + 1;
+        span = hi - lo;
+        if (hi < lo) lo = 0x7fffffff, span = 0;  // none: no key has that number
+    }
+    __device__ __forceinline__ bool hides(int j) const {
+        return ((uint32_t)(j - lo) > span) & (j >= sink);
+    }
+    // Registers of a transposed block of 32 keys from key j0 on (half: lane >> 5)
+    // whose key the row does not see become `fill`.  No key at or past `sinks`
+    // is a sink, so most tiles need one comparison per key.
+    __device__ __forceinline__ void mask(float* x, int j0, int half, int sinks, float fill) const {
+        const int jb = j0 + half * 4;
+        if (j0 >= sinks) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int at = (e >> 2) * 8 + (e & 3);
+                x[e] = (uint32_t)(jb - lo + at) > span ? fill : x[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = hides(jb + (e >> 2) * 8 + (e & 3)) ? fill : x[e];
+        }
+    }
+};
+
+// Adds the infinite and not-a-number elements of `src` to `dst`: the result
+// of a row that sees them, where a tile that other rows do not see whole was
+// multiplied without them.  Rare, so it works on the stored result.
+template <class T, class TO>
+__device__ __forceinline__ void add_bad(TO* dst, const T* src, int D) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+        const float x = (float)src[d];
+        if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) dst[d] = (TO)((float)dst[d] + x);
+    }
+}
+
+// The rows of one workgroup, its waves and its lanes (32 rows per wave across
+// the lanes, both halves of a wave the same 32), and their places among the
+// keys.  `first_row`: the first row of this wave's 32 in the tile.
+struct QueryRows {
+    int r, qi, h, pa, pb, wa, wb;
+    int64_t row;
+    bool live;
+    __device__ __forceinline__ QueryRows(const RowTile& t, int G, int first_row, int lane) {
+        r = first_row + (lane & 31);
+        qi = (t.row0 + r) / G;
+        h = t.hk * G + (t.row0 + r) - qi * G;
+        live = r < t.rows;
+        row = t.q0 + qi;
+        const int off = t.tk - t.tq, last = t.rows > 0 ? t.rows - 1 : 0;
+        const int wl = first_row + 31 < last ? first_row + 31 : last;
+        pa = t.row0 / G + off;
+        pb = (t.row0 + last) / G + off;
+        wa = (t.row0 + first_row) / G + off;
+        wb = (t.row0 + wl) / G + off;
+    }
+    // This lane's row of a view, as operands of STEPS product steps.
+    template <class T, int STEPS>
+    __device__ __forceinline__ void load(typename Elem<T>::Frag* f, const HeadsArg& v, int D,
+                                         int half) const {
+        const T* p = (const T*)v.data + row * v.row + h * v.head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = s * 16 + half * 8;
+            typename Elem<T>::Frag x = {};
+            if (live && d < D) x = *(const typename Elem<T>::Frag*)(p + d);
+            f[s] = x;
+        }
+    }
+};
+
+// add_bad over the keys that one row sees of the tiles that the workgroup's
+// rows do not all see whole.
+template <int BN, class T, class TO>
+__device__ __forceinline__ void add_bad_keys(TO* dst, const AttnArgs& a, const KeyTiles<BN>& kt,
+                                             int n, const QueryRows& q, int tk, const Window& w,
+                                             const T* base, int64_t stride) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const int j0 = kt.tile(i) * BN;
+        if (tile_view<BN>(a, q.pa, q.pb, tk, j0) != 1) continue;
+#pragma unroll 1
+        for (int j = j0; j < j0 + BN && j < tk; ++j)
+            if (!w.hides(j)) add_bad(dst, base + j * stride, a.D);
+    }
+}
+
+// A row's running maximum (m, and mc = m * c as subtracted), sum and result.
+// The maximum a row subtracts is moved only when it grew by more than 2^8 (a
+// rescale costs as many multiplications as the result has registers); weights
+// stay below 2^8.
+template <class T, int DB, int KB>
+struct Softmax {
+    float m = -INFINITY, mc = 0.0f, l = 0.0f;
+    f32x16 o[DB];
+    __device__ __forceinline__ Softmax() {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] = 0.0f;
+    }
+    // Scores s of KB * 32 keys (transposed, -infinity where hidden) become
+    // weights; result and sum are rescaled to the new maximum.
+    __device__ __forceinline__ void weights(float* s, float c) {
+        float mx = s[0];
+#pragma unroll
+        for (int e = 1; e < KB * 16; ++e) mx = fmaxf(mx, s[e]);
+        mx = pair_max(mx);
+        if (__any((mx * c > mc + 8.0f) | (m == -INFINITY))) {
+            const float m2 = fmaxf(m, mx);
+            const float mc2 = m2 == -INFINITY ? 0.0f : m2 * c;
+            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mc - mc2);
+            m = m2;
+            mc = mc2;
+            l *= f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[db] *= f;
+        }
+#pragma unroll
+        for (int e = 0; e < KB * 16; ++e) {
+            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -mc));
+            l += s[e];
+        }
+    }
+    // The sum over both halves; false (and a zero result) if no key was seen.
+    __device__ __forceinline__ bool finish() {
+        l = pair_sum(l);
+        const bool some = (m != -INFINITY) | (l != 0.0f);
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = db * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                if (d < D) {
-                    const float x = (float)base[j * stride + d];
-                    if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) acc[db][e] += x;
-                }
-            }
+            for (int e = 0; e < 16; ++e) o[db][e] = some ? o[db][e] : 0.0f;
+        return some;
     }
+};
+
+__device__ __forceinline__ float log_sum(float mc, float l) {
+    return (mc + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Forward.  A workgroup of 4 waves takes 128 rows (32 per wave) of one key
@@ -116,58 +243,31 @@ __device__ __forceinline__ void add_bad(f32x16* acc, const T* base, int64_t stri
 // S^T = K Q^T (keys in registers, its 32 rows across the lanes), so a row's
 // maximum and sum are a lane's own registers plus one exchange with lane ^ 32,
 // its factor is one value per lane, and the weights, rounded to the type, are
-// already the operand of O^T += V^T P^T.  The maximum a row subtracts is moved
-// only when it grew by more than 2^8 (a rescale of O costs as many
-// multiplications as it has registers; weights stay below 2^8).
+// already the operand of O^T += V^T P^T.
 template <class T, int DP, int BN>
-__global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
-    constexpr int BM = 128, DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(AttnArgs a) {
+    constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
-    __shared__ int bad_tag[2];
+    __shared__ int bad;  // a tile was stored without its infinite values
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.H / a.Hk;
     RowTile t;
-    if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
-    const int split = blockIdx.y;
-
-    // this lane's row
-    const int r = wave * 32 + (lane & 31);
-    const int qi = (t.row0 + r) / G, h = t.hk * G + (t.row0 + r) - qi * G;
-    const bool live = r < t.rows;
-    const int64_t qrow = t.q0 + qi;
+    if (!row_tile<128>(a, a.qs, blockIdx.x, G, t)) return;
+    const QueryRows q(t, G, wave * 32, lane);
     Frag qf[STEPS];
-    {
-        const T* q = (const T*)a.q.data + qrow * a.q.row + h * a.q.head;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int d = s * 16 + half * 8;
-            Frag f = {};
-            if (live && d < a.D) f = *(const Frag*)(q + d);
-            qf[s] = f;
-        }
-    }
-    // places of the workgroup's, the wave's and the lane's rows
-    const int off = t.tk - t.tq;
-    const int last = t.rows > 0 ? t.rows - 1 : 0;
-    const int pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
-    const int wl = wave * 32 + 31 < last ? wave * 32 + 31 : last;
-    const int wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
+    q.load<T, STEPS>(qf, a.q, a.D, half);
+    const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
-    const int p = qi + off;
-    const int hi = a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1;
-    const int lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
 
-    KeyTiles<BN> kt(a, pa, pb, t.tk);
-    const int n = t.rows > 0 ? kt.part(split, a.splits) : 0;
+    KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
+    const int n = t.rows > 0 ? kt.part(blockIdx.y, a.splits) : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     Stage<T, DP, BN, 256> sk, sv;
-    if (tid < 2) bad_tag[tid] = 0;
-
     auto load = [&](int i) {
         const int64_t j0 = (int64_t)kt.tile(i) * BN;
         sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, tid);
@@ -176,29 +276,23 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
     auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
         sk.store(buf, a.D, tid);
-        // a value that some row must not see is multiplied by a weight of 0
-        // there: an infinite one has to leave the product
-        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sv.clean(tid))
-            bad_tag[i & 1] = i + 1;
+        // a value that some row must not see meets a weight of 0 there: an
+        // infinite one has to leave the product
+        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 && sv.clean(tid)) bad = 1;
         sv.store(buf + BN * Tl::kPitch, a.D, tid);
     };
 
-    f32x16 o[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db) o[db] = 0.0f;
-    const float c = a.scale * 1.44269504088896f;  // log2 e
-    float m = -INFINITY, mc = 0.0f, l = 0.0f;
-
-    if (n > 0) {
-        load(0);
-        __syncthreads();
-        store(0);
-    }
+    Softmax<T, DB, KB> sm;
+    const float c = a.scale * kLog2e;
+    if (tid == 0) bad = 0;
+    if (n > 0) load(0);
+    __syncthreads();
+    if (n > 0) store(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = kt.tile(i) * BN;
         if (i + 1 < n) load(i + 1);
-        const int view = wave_live ? tile_view<BN>(a, wa, wb, t.tk, j0) : 0;
+        const int view = wave_live ? tile_view<BN>(a, q.wa, q.wb, t.tk, j0) : 0;
         if (view != 0) {
             const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
             const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
@@ -214,63 +308,44 @@ __global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
             }
             if (view == 1) {
 #pragma unroll
-                for (int e = 0; e < KB * 16; ++e) {
-                    const int j = j0 + (e >> 4) * 32 + ((e >> 2) & 3) * 8 + half * 4 + (e & 3);
-                    if (j > hi || (j < lo && j >= a.sinks)) s[e] = -INFINITY;
-                }
+                for (int b = 0; b < KB; ++b)
+                    win.mask(s + b * 16, j0 + b * 32, half, a.sinks, -INFINITY);
             }
-            float mx = s[0];
-#pragma unroll
-            for (int e = 1; e < KB * 16; ++e) mx = fmaxf(mx, s[e]);
-            mx = pair_max(mx);
-            if (__any(mx * c > mc + 8.0f || m == -INFINITY)) {
-                const float m2 = fmaxf(m, mx);
-                const float mc2 = m2 == -INFINITY ? 0.0f : m2 * c;
-                const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mc - mc2);
-                m = m2;
-                mc = mc2;
-                l *= f;
-#pragma unroll
-                for (int db = 0; db < DB; ++db) o[db] *= f;
-            }
-#pragma unroll
-            for (int e = 0; e < KB * 16; ++e) {
-                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -mc));
-                l += s[e];
-            }
+            sm.weights(s, c);
 #pragma unroll
             for (int k = 0; k < KB * 2; ++k) {
                 const Frag pf = to_frag<T>(s + k * 8);
 #pragma unroll
                 for (int db = 0; db < DB; ++db)
-                    o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, o[db]);
+                    sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
             }
-            if (bad_tag[i & 1] == i + 1)
-                add_bad<T, DB>(o, vb, a.v.row, j0, j0 + BN < hi + 1 ? j0 + BN : hi + 1, a.D, half,
-                               [&](int j) { return j >= lo || j < a.sinks; });
         }
         if (i + 1 < n) store(i + 1);
         __syncthreads();
     }
-    l = pair_sum(l);
-    const bool some = m != -INFINITY || l != 0.0f;
-    if (!some) {
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] = 0.0f;
-    }
+    const bool some = sm.finish();
     if (a.splits > 1) {
-        const int64_t at = ((int64_t)split * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + r;
-        store_row<float, DB>(o, 1.0f, live ? a.part + at * a.D : nullptr, a.D, lane);
-        if (live && half == 0) a.part_ml[at] = make_float2(some ? mc : -INFINITY, l);
+        const int64_t at =
+            ((int64_t)blockIdx.y * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + q.r;
+        float* part = a.part + at * a.D;
+        store_row<float, DB>(sm.o, 1.0f, q.live ? part : nullptr, a.D, lane);
+        if (q.live && half == 0) a.part_ml[at] = make_float2(some ? sm.mc : -INFINITY, sm.l);
+        if (bad) {
+            __syncthreads();
+            if (q.live && half == 0)
+                add_bad_keys<BN>(part, a, kt, n, q, t.tk, win, vb, a.v.row);
+        }
         return;
     }
-    const float inv = live && some ? 1.0f / l : 0.0f;
-    T* out = (T*)a.out.data + qrow * a.out.row + h * a.out.head;
-    store_row<T, DB>(o, inv, live || r < t.pad ? out : nullptr, a.D, lane);
-    if (a.lse && half == 0 && (live || r < t.pad))
-        a.lse[qrow * a.H + h] =
-            !live ? 0.0f
-                  : some ? (mc + __builtin_amdgcn_logf(l)) * 0.693147180559945f : -INFINITY;
+    const bool write = q.live || q.r < t.pad;
+    T* out = (T*)a.out.data + q.row * a.out.row + q.h * a.out.head;
+    store_row<T, DB>(sm.o, q.live && some ? 1.0f / sm.l : 0.0f, write ? out : nullptr, a.D, lane);
+    if (a.lse && half == 0 && write)
+        a.lse[q.row * a.H + q.h] = !q.live ? 0.0f : some ? log_sum(sm.mc, sm.l) : -INFINITY;
+    if (bad) {
+        __syncthreads();
+        if (q.live && half == 0) add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, vb, a.v.row);
+    }
 }
 
 // Forward for sequences of at most 32 rows per key head (one query, or a few,
@@ -282,6 +357,7 @@ template <class T, int DP, int BN>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) > 3 ? 3 : 512 / (DP * (int)sizeof(T)))
 void attention_few_kernel(AttnArgs a) {
     constexpr int BM = 32, DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
+    using f4 = float __attribute__((ext_vector_type(4)));
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     constexpr int kWaveBytes = 2 * BN * Tl::kPitch;
@@ -289,38 +365,20 @@ void attention_few_kernel(AttnArgs a) {
     static_assert(kWaveBytes >= BM * DP * 4, "join buffer");
     __shared__ __attribute__((aligned(16))) char smem[4 * kWaveBytes];
     __shared__ float2 ml[4][BM];
+    __shared__ int bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.H / a.Hk;
     RowTile t;
     if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
-    const int split = blockIdx.y;
-
-    const int r = lane & 31;
-    const int qi = (t.row0 + r) / G, h = t.hk * G + (t.row0 + r) - qi * G;
-    const bool live = r < t.rows;
-    const int64_t qrow = t.q0 + qi;
+    const QueryRows q(t, G, 0, lane);
     Frag qf[STEPS];
-    {
-        const T* q = (const T*)a.q.data + qrow * a.q.row + h * a.q.head;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int d = s * 16 + half * 8;
-            Frag f = {};
-            if (live && d < a.D) f = *(const Frag*)(q + d);
-            qf[s] = f;
-        }
-    }
-    const int off = t.tk - t.tq;
-    const int last = t.rows > 0 ? t.rows - 1 : 0;
-    const int pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
-    const int p = qi + off;
-    const int hi = a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1;
-    const int lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
+    q.load<T, STEPS>(qf, a.q, a.D, half);
+    const Window win(a, q.qi + t.tk - t.tq, t.tk);
 
-    KeyTiles<BN> kt(a, pa, pb, t.tk);
-    const int n = t.rows > 0 ? kt.part(split, a.splits) : 0;
+    KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
+    const int n = t.rows > 0 ? kt.part(blockIdx.y, a.splits) : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     Stage<T, DP, BN, 64> sk, sv;
@@ -332,17 +390,15 @@ void attention_few_kernel(AttnArgs a) {
         sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, lane);
     };
 
-    f32x16 o[DB];
-#pragma unroll
-    for (int db = 0; db < DB; ++db) o[db] = 0.0f;
-    const float c = a.scale * 1.44269504088896f;  // log2 e
-    float m = -INFINITY, mc = 0.0f, l = 0.0f;
-
+    Softmax<T, DB, KB> sm;
+    const float c = a.scale * kLog2e;
     if (wave < n) load(wave);
+    if (tid == 0) bad = 0;
+    __syncthreads();
     for (int i = wave; i < n; i += 4) {
         const int j0 = kt.tile(i) * BN;
-        const int view = tile_view<BN>(a, pa, pb, t.tk, j0);
-        const bool bad = view == 1 && __any(sv.clean(lane));
+        const int view = tile_view<BN>(a, q.pa, q.pb, t.tk, j0);
+        if (view == 1 && sv.clean(lane)) bad = 1;
         wave_sync();  // the wave's reads of the last tile are done
         sk.store(kbuf, a.D, lane);
         sv.store(vbuf, a.D, lane);
@@ -360,66 +416,39 @@ void attention_few_kernel(AttnArgs a) {
         }
         if (view == 1) {
 #pragma unroll
-            for (int e = 0; e < KB * 16; ++e) {
-                const int j = j0 + (e >> 4) * 32 + ((e >> 2) & 3) * 8 + half * 4 + (e & 3);
-                if (j > hi || (j < lo && j >= a.sinks)) s[e] = -INFINITY;
-            }
+            for (int b = 0; b < KB; ++b)
+                win.mask(s + b * 16, j0 + b * 32, half, a.sinks, -INFINITY);
         }
-        float mx = s[0];
-#pragma unroll
-        for (int e = 1; e < KB * 16; ++e) mx = fmaxf(mx, s[e]);
-        mx = pair_max(mx);
-        if (__any(mx * c > mc + 8.0f || m == -INFINITY)) {
-            const float m2 = fmaxf(m, mx);
-            const float mc2 = m2 == -INFINITY ? 0.0f : m2 * c;
-            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mc - mc2);
-            m = m2;
-            mc = mc2;
-            l *= f;
-#pragma unroll
-            for (int db = 0; db < DB; ++db) o[db] *= f;
-        }
-#pragma unroll
-        for (int e = 0; e < KB * 16; ++e) {
-            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -mc));
-            l += s[e];
-        }
+        sm.weights(s, c);
 #pragma unroll
         for (int k = 0; k < KB * 2; ++k) {
             const Frag pf = to_frag<T>(s + k * 8);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
-                o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, o[db]);
+                sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
         }
-        if (bad)
-            add_bad<T, DB>(o, vb, a.v.row, j0, j0 + BN < hi + 1 ? j0 + BN : hi + 1, a.D, half,
-                           [&](int j) { return j >= lo || j < a.sinks; });
     }
-    l = pair_sum(l);
-    if (m == -INFINITY && l == 0.0f) {
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] = 0.0f;
-    }
+    const bool seen = sm.finish();
     wave_sync();
-    if (half == 0) ml[wave][r] = make_float2(m == -INFINITY && l == 0.0f ? -INFINITY : mc, l);
+    if (half == 0) ml[wave][q.r] = make_float2(seen ? sm.mc : -INFINITY, sm.l);
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            using f4 = float __attribute__((ext_vector_type(4)));
             f4 x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = o[db][g * 4 + e];
-            *(FPSTOK_LDS f4*)(kbuf + (r * DP + db * 32 + g * 8 + half * 4) * 4) = x;
+            for (int e = 0; e < 4; ++e) x[e] = sm.o[db][g * 4 + e];
+            *(FPSTOK_LDS f4*)(kbuf + (q.r * DP + db * 32 + g * 8 + half * 4) * 4) = x;
         }
     __syncthreads();
     // 4 elements per thread and turn
+    const int64_t part0 =
+        ((int64_t)blockIdx.y * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0;
     const int rows = t.rows > t.pad ? t.rows : t.pad;
     for (int x = tid; x < rows * (DP / 4); x += 256) {
-        using f4 = float __attribute__((ext_vector_type(4)));
         const int row = x / (DP / 4), d = (x % (DP / 4)) * 4;
         if (d >= a.D) continue;
-        const int q = (t.row0 + row) / G, hh = t.hk * G + (t.row0 + row) - q * G;
+        const int qi = (t.row0 + row) / G, h = t.hk * G + (t.row0 + row) - qi * G;
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][row].x);
@@ -428,29 +457,35 @@ void attention_few_kernel(AttnArgs a) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const float2 z = ml[w][row];
-            if (z.x == -INFINITY && z.y == 0.0f) continue;
-            const float f = __builtin_amdgcn_exp2f(z.x - top);
+            const float f = z.x == -INFINITY && z.y == 0.0f ? 0.0f
+                                                              : __builtin_amdgcn_exp2f(z.x - top);
             sum += z.y * f;
             y += f * *(FPSTOK_LDS f4*)(lds + w * kWaveBytes + (row * DP + d) * 4);
         }
         const bool here = row < t.rows, some = top != -INFINITY || sum != 0.0f;
         if (a.splits > 1) {
             if (!here) continue;
-            const int64_t at =
-                ((int64_t)split * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + row;
-            *(f4*)(a.part + at * a.D + d) = y;
-            if (d == 0) a.part_ml[at] = make_float2(some ? top : -INFINITY, sum);
+            *(f4*)(a.part + (part0 + row) * a.D + d) = y;
+            if (d == 0) a.part_ml[part0 + row] = make_float2(some ? top : -INFINITY, sum);
             continue;
         }
         y *= here && some ? 1.0f / sum : 0.0f;
         if (!here || !some) y = 0.0f;
         using T4 = T __attribute__((ext_vector_type(4)));
-        *(T4*)((T*)a.out.data + (t.q0 + q) * a.out.row + hh * a.out.head + d) =
+        *(T4*)((T*)a.out.data + (t.q0 + qi) * a.out.row + h * a.out.head + d) =
             __builtin_convertvector(y, T4);
         if (a.lse && d == 0)
-            a.lse[(t.q0 + q) * a.H + hh] =
-                !here ? 0.0f
-                      : some ? (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f : -INFINITY;
+            a.lse[(t.q0 + qi) * a.H + h] = !here ? 0.0f : some ? log_sum(top, sum) : -INFINITY;
+    }
+    if (bad) {
+        __syncthreads();
+        if (wave == 0 && half == 0 && q.live) {
+            if (a.splits > 1)
+                add_bad_keys<BN>(a.part + (part0 + q.r) * a.D, a, kt, n, q, t.tk, win, vb, a.v.row);
+            else
+                add_bad_keys<BN>((T*)a.out.data + q.row * a.out.row + q.h * a.out.head, a, kt, n, q,
+                                 t.tk, win, vb, a.v.row);
+        }
     }
 }
 
@@ -527,72 +562,50 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 // dP^T = V dO^T, and dS^T = P^T (dP^T - delta), rounded to the type, is the
 // operand of dQ^T += K^T dS^T.
 template <class T, int DP, int BN>
-__global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
-    constexpr int BM = 128, DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kernel(AttnArgs a) {
+    constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
-    __shared__ int bad_tag[2];
+    __shared__ int bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.H / a.Hk;
     RowTile t;
-    if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
-
-    const int r = wave * 32 + (lane & 31);
-    const int qi = (t.row0 + r) / G, h = t.hk * G + (t.row0 + r) - qi * G;
-    const bool live = r < t.rows;
-    const int64_t qrow = t.q0 + qi;
+    if (!row_tile<128>(a, a.qs, blockIdx.x, G, t)) return;
+    const QueryRows q(t, G, wave * 32, lane);
+    const Window win(a, q.qi + t.tk - t.tq, t.tk);
+    const bool wave_live = wave * 32 < t.rows;
     Frag qf[STEPS], gf[STEPS];
     float delta = 0.0f, lse2 = 0.0f;
     {
-        const T* q = (const T*)a.q.data + qrow * a.q.row + h * a.q.head;
-        const T* g = (const T*)a.grad_out.data + qrow * a.grad_out.row + h * a.grad_out.head;
-        const T* o = (const T*)a.out.data + qrow * a.out.row + h * a.out.head;
+        Frag of[STEPS];
+        q.load<T, STEPS>(qf, a.q, a.D, half);
+        q.load<T, STEPS>(gf, a.grad_out, a.D, half);
+        q.load<T, STEPS>(of, a.out, a.D, half);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int d = s * 16 + half * 8;
-            Frag fq = {}, fg = {}, fo = {};
-            if (live && d < a.D) {
-                fq = *(const Frag*)(q + d);
-                fg = *(const Frag*)(g + d);
-                fo = *(const Frag*)(o + d);
-            }
-            qf[s] = fq;
-            gf[s] = fg;
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                delta = __builtin_fmaf((float)fg[e], (float)fo[e], delta);
-        }
+                delta = __builtin_fmaf((float)gf[s][e], (float)of[s][e], delta);
         delta = pair_sum(delta);
-        if (live) {
+        if (q.live) {
             // a row that sees nothing: every weight is masked, the value
             // only has to be finite
-            const float v = a.lse[qrow * a.H + h];
-            lse2 = v == -INFINITY ? 0.0f : v * 1.44269504088896f;
+            const float v = a.lse[q.row * a.H + q.h];
+            lse2 = v == -INFINITY ? 0.0f : v * kLog2e;
             if (half == 0)
-                a.stat[((int64_t)t.hk * a.qs.rows + t.q0) * G + t.row0 + r] =
+                a.stat[((int64_t)t.hk * a.qs.rows + t.q0) * G + t.row0 + q.r] =
                     make_float2(lse2, delta);
         }
     }
-    const int off = t.tk - t.tq;
-    const int last = t.rows > 0 ? t.rows - 1 : 0;
-    const int pa = t.row0 / G + off, pb = (t.row0 + last) / G + off;
-    const int wl = wave * 32 + 31 < last ? wave * 32 + 31 : last;
-    const int wa = (t.row0 + wave * 32) / G + off, wb = (t.row0 + wl) / G + off;
-    const bool wave_live = wave * 32 < t.rows;
-    const int p = qi + off;
-    const int hi = a.right >= 0 && p + a.right < t.tk - 1 ? p + a.right : t.tk - 1;
-    const int lo = a.left >= 0 && p - a.left > 0 ? p - a.left : 0;
 
-    KeyTiles<BN> kt(a, pa, pb, t.tk);
+    KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
     const int n = t.rows > 0 ? kt.count : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     Stage<T, DP, BN, 256> sk, sv;
-    if (tid < 2) bad_tag[tid] = 0;
-
     auto load = [&](int i) {
         const int64_t j0 = (int64_t)kt.tile(i) * BN;
         sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, tid);
@@ -600,8 +613,7 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
     };
     auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        if (tile_view<BN>(a, pa, pb, t.tk, kt.tile(i) * BN) == 1 && sk.clean(tid))
-            bad_tag[i & 1] = i + 1;
+        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 && sk.clean(tid)) bad = 1;
         sk.store(buf, a.D, tid);
         sv.store(buf + BN * Tl::kPitch, a.D, tid);
     };
@@ -609,18 +621,16 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
     f32x16 dq[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
-    const float c = a.scale * 1.44269504088896f;
-
-    if (n > 0) {
-        load(0);
-        __syncthreads();
-        store(0);
-    }
+    const float c = a.scale * kLog2e;
+    if (tid == 0) bad = 0;
+    if (n > 0) load(0);
+    __syncthreads();
+    if (n > 0) store(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = kt.tile(i) * BN;
         if (i + 1 < n) load(i + 1);
-        const int view = wave_live ? tile_view<BN>(a, wa, wb, t.tk, j0) : 0;
+        const int view = wave_live ? tile_view<BN>(a, q.wa, q.wb, t.tk, j0) : 0;
         if (view != 0) {
             const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
             const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
@@ -634,17 +644,9 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
                 }
                 float ds[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2));
-                    ds[e] = w * (y[e] - delta);
-                }
-                if (view == 1) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int j = j0 + b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                        if (j > hi || (j < lo && j >= a.sinks)) ds[e] = 0.0f;
-                    }
-                }
+                for (int e = 0; e < 16; ++e)
+                    ds[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2)) * (y[e] - delta);
+                if (view == 1) win.mask(ds, j0 + b * 32, half, a.sinks, 0.0f);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const Frag f = to_frag<T>(ds + k * 8);
@@ -654,19 +656,20 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
                             Elem<T>::mma(Tl::col_frag(kbuf, b * 32 + k * 16, db, lane), f, dq[db]);
                 }
             }
-            if (bad_tag[i & 1] == i + 1)
-                add_bad<T, DB>(dq, kb, a.k.row, j0, j0 + BN < hi + 1 ? j0 + BN : hi + 1, a.D, half,
-                               [&](int j) { return j >= lo || j < a.sinks; });
         }
         if (i + 1 < n) store(i + 1);
         __syncthreads();
     }
-    T* out = (T*)a.grad_q.data + qrow * a.grad_q.row + h * a.grad_q.head;
-    if (!live) {
+    T* out = (T*)a.grad_q.data + q.row * a.grad_q.row + q.h * a.grad_q.head;
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dq[db][e] = q.live ? dq[db][e] : 0.0f;
+    store_row<T, DB>(dq, a.scale, q.live || q.r < t.pad ? out : nullptr, a.D, lane);
+    if (bad) {
+        __syncthreads();
+        if (q.live && half == 0) add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, kb, a.k.row);
     }
-    store_row<T, DB>(dq, a.scale, live || r < t.pad ? out : nullptr, a.D, lane);
 }
 
 // grad_k and grad_v.  A workgroup takes 128 keys of one key head (32 per wave,
@@ -676,19 +679,20 @@ __global__ __launch_bounds__(256) void attention_dq_kernel(AttnArgs a) {
 // dV^T += dO^T P and dK^T += Q^T dS.  The heads of the group are rows of the same
 // walk: their gradients add up in the accumulators, in a fixed order.
 template <class T, int DP, int BQ>
-__global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
-    constexpr int BM = 128, DB = DP / 32, QB = BQ / 32, STEPS = DP / 16;
+__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 128 ? 2 : 1)
+void attention_dkv_kernel(AttnArgs a) {
+    constexpr int DB = DP / 32, QB = BQ / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BQ * Tl::kPitch];
     __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];
-    __shared__ int bad_tag[2];
+    __shared__ int bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.H / a.Hk;
     RowTile t;
-    if (!row_tile<BM>(a, a.ks, blockIdx.x, 1, t)) return;
+    if (!row_tile<128>(a, a.ks, blockIdx.x, 1, t)) return;
 
     const int r = wave * 32 + (lane & 31);
     const bool live = r < t.rows;
@@ -709,7 +713,7 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
             vf[s] = fv;
         }
     }
-    // rows that see some key of the tile, and those that see this lane's key
+    // queries that see some key of the tile, and those that see this lane's key
     const int off = t.tk - t.tq;
     const int j = t.row0 + r;
     int i0 = 0, i1 = t.tq - 1, e0 = 0, e1 = t.tq - 1;
@@ -732,7 +736,6 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
                   (int64_t)t.hk * G * a.grad_out.head;
     const float2* sb = a.stat + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
     const float over_g = 1.0f / (float)G;
-    if (tid < 2) bad_tag[tid] = 0;
 
     // tile i of the walk: its first row is head `g` of query i0 + `q`
     struct Place {
@@ -747,6 +750,12 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
     auto view_of = [&](const Place& at, int k0) {  // the tile's rows against 32 keys
         const int pa = i0 + at.q + off;
         return tile_view<32>(a, pa, pa + group_div(at.g + at.rows - 1, over_g), t.tk, t.row0 + k0);
+    };
+    auto partly = [&](const Place& at) {  // some row of the tile does not see some key
+        bool part = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(at, w * 32) != 2;
+        return part;
     };
     Stage<T, DP, BQ, 256> sq, sg;
     float2 sst = make_float2(0.0f, 0.0f);
@@ -765,12 +774,9 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
     };
     auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
-        bool part = false;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(next, w * 32) != 2;
-        if (part) {
+        if (partly(next)) {
             const bool bq = sq.clean(tid), bg = sg.clean(tid);
-            if (bq || bg) bad_tag[i & 1] = i + 1;
+            if (bq || bg) bad = 1;
         }
         sq.store(buf, a.D, tid);
         sg.store(buf + BQ * Tl::kPitch, a.D, tid);
@@ -783,13 +789,11 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
     f32x16 dk[DB], dv[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
-    const float c = a.scale * 1.44269504088896f;
-
-    if (n > 0) {
-        load(0);
-        __syncthreads();
-        store(0);
-    }
+    const float c = a.scale * kLog2e;
+    if (tid == 0) bad = 0;
+    if (n > 0) load(0);
+    __syncthreads();
+    if (n > 0) store(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         cur = next;
@@ -809,19 +813,21 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
                 float w[16], ds[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int q = b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                    w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -stat[i & 1][0][q]));
-                    ds[e] = w[e] * (y[e] - stat[i & 1][1][q]);
+                    const int at = b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                    w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -stat[i & 1][0][at]));
+                    ds[e] = w[e] * (y[e] - stat[i & 1][1][at]);
                 }
                 if (view == 1) {
-                    // rows of the walk as 32-bit distances from the tile's start
+                    // this lane's rows, from the block's start, cut to it
                     const int64_t at = (int64_t)i * BQ + b * 32 + half * 4;
                     const int s0 = (int)(see0 - at < -64 ? -64 : see0 - at > 64 ? 64 : see0 - at);
                     const int s1 = (int)(see1 - at < -64 ? -64 : see1 - at > 64 ? 64 : see1 - at);
+                    const uint32_t span = s1 > s0 ? s1 - s0 : 0;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int q = (e >> 2) * 8 + (e & 3);
-                        if (q < s0 || q >= s1) w[e] = 0.0f, ds[e] = 0.0f;
+                        const bool hide = (uint32_t)((e >> 2) * 8 + (e & 3) - s0) >= span;
+                        w[e] = hide ? 0.0f : w[e];
+                        ds[e] = hide ? 0.0f : ds[e];
                     }
                 }
 #pragma unroll
@@ -836,31 +842,37 @@ __global__ __launch_bounds__(256) void attention_dkv_kernel(AttnArgs a) {
                     }
                 }
             }
-            if (bad_tag[i & 1] == i + 1) {
-                int64_t b0 = (int64_t)i * BQ, b1 = b0 + BQ < n_rows ? b0 + BQ : n_rows;
-                if (b0 < see0) b0 = see0;
-                if (b1 > see1) b1 = see1;
-                for (int64_t x = b0; x < b1; ++x) {
-                    const int64_t qi = x / G, g = x - qi * G;
-                    const auto all = [](int) { return true; };
-                    add_bad<T, DB>(dk, qb + qi * a.q.row + g * a.q.head, 0, 0, 1, a.D, half, all);
-                    add_bad<T, DB>(dv, gb + qi * a.grad_out.row + g * a.grad_out.head, 0, 0, 1,
-                                   a.D, half, all);
-                }
-            }
         }
         if (i + 1 < n) store(i + 1);
         __syncthreads();
     }
     T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
     T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
-    if (!live) {
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
-    }
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            dk[db][e] = live ? dk[db][e] : 0.0f;
+            dv[db][e] = live ? dv[db][e] : 0.0f;
+        }
     const bool write = live || r < t.pad;
     store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane);
     store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane);
+    if (bad) {
+        __syncthreads();
+        if (live && half == 0)
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const int64_t x0 = (int64_t)i * BQ;
+                if (!partly(Place{(int)(x0 / G), (int)(x0 % G), rows_of(i)})) continue;
+#pragma unroll 1
+                for (int64_t x = x0 > see0 ? x0 : see0; x < x0 + BQ && x < see1; ++x) {
+                    const int64_t qi = x / G, g = x - qi * G;
+                    add_bad(ok, qb + qi * a.q.row + g * a.q.head, a.D);
+                    add_bad(ov, gb + qi * a.grad_out.row + g * a.grad_out.head, a.D);
+                }
+            }
+    }
 }
 
 // Slots of a grid that covers every tile of BM rows of every sequence.
