@@ -39,6 +39,11 @@ struct AttnArgs {
     int32_t splits;
     float* part;
     float2* part_ml;
+    // rows that see a sequence's sinks from behind its first key tile's window
+    // (backward): walked in chunks of sink_chunk rows, whose parts of the
+    // sinks' gradients are [slots][Hk][2][sinks][D] (grad_k, grad_v)
+    int32_t sink_chunk;
+    float* sink_part;
 };
 
 // How a call is laid out on the device, from the shapes alone.
@@ -57,6 +62,8 @@ struct RopeArgs {
     int32_t first_pair[kMaxAxes + 1];  // pairs of axis a: first_pair[a] .. first_pair[a+1]-1
 };
 
+// Chunks of `chunk` rows that cover every sequence (their numbering: find_seq).
+int64_t row_slots(const SeqArgs& s, int G, int chunk);
 AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);

@@ -14,7 +14,7 @@ struct RowTile {
     int64_t q0, k0;  // first buffer rows of the sequence
     int tq, tk, row0, rows;  // rows: those of the tile that exist
     int pad;                 // rows of the tile inside a padded sequence's slots
-    int hk;
+    int hk, b;
 };
 
 // Decodes a workgroup's place in the grid: heads fastest, so that with 8 key
@@ -42,6 +42,7 @@ __device__ __forceinline__ bool row_tile(const AttnArgs& a, const SeqArgs& s, in
     const int64_t left = (int64_t)len * G - tile * BM;
     if (s.cu && left <= 0) return false;
     const int64_t pad = s.cu ? 0 : (int64_t)s.cap * G - tile * BM;
+    t.b = b;
     t.row0 = (int)(tile * BM);
     t.rows = left < 0 ? 0 : left < BM ? (int)left : BM;
     t.pad = pad < BM ? (int)pad : BM;
@@ -672,6 +673,163 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     }
 }
 
+// The last query that sees a sequence's first key tile (128 keys, the sinks
+// among them) through the window, -1 if none does; later ones see its sinks
+// only.
+__device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk) {
+    const int jl = (tk < 128 ? tk : 128) - 1, i1 = jl + a.left - (tk - tq);
+    return i1 < -1 ? -1 : i1 < tq - 1 ? i1 : tq - 1;
+}
+
+// First sink chunk of sequence b in the numbering of its parts.
+__device__ __forceinline__ int64_t sink_slot(const AttnArgs& a, int b, int G) {
+    if (a.qs.cu) return first_slot(a.qs, b, G, a.sink_chunk);
+    return (int64_t)b * (((int64_t)a.qs.cap * G + a.sink_chunk - 1) / a.sink_chunk);
+}
+
+// The sinks' gradients from the rows that see nothing else of the first key
+// tile: in a long sequence that is nearly every row, and one workgroup walking
+// them all would take longer than everything else.  A workgroup takes a chunk
+// of them, its waves 32 rows in turn; nothing is masked.  The chunks' parts
+// are added in order by the kernel below.
+template <class T, int DP>
+__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 128 ? 2 : 1)
+void attention_sink_kernel(AttnArgs a) {
+    constexpr int DB = DP / 32, STEPS = DP / 16;
+    using f4 = float __attribute__((ext_vector_type(4)));
+    using Tl = Tile<T, DP>;
+    using Frag = typename Elem<T>::Frag;
+    constexpr int kTile = 32 * Tl::kPitch;
+    // 32 x DP floats of a wave's result in its tiles' place
+    constexpr int kWaveBytes = 2 * kTile > 32 * DP * 4 ? 2 * kTile : 32 * DP * 4;
+    __shared__ __attribute__((aligned(16))) char smem[4 * kWaveBytes];
+    __shared__ __attribute__((aligned(16))) float stat[4][2][32];
+    FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = a.H / a.Hk, hk = (int)(blockIdx.x % a.Hk);
+    const int64_t slot = blockIdx.x / a.Hk;
+    const int64_t per = ((int64_t)a.qs.cap * G + a.sink_chunk - 1) / a.sink_chunk;
+    const int b = a.qs.cu ? find_seq(a.qs, slot, G, a.sink_chunk) : (int)(slot / per);
+    const int64_t c = slot - sink_slot(a, b, G);
+    int64_t q0, k0;
+    int tq, tk;
+    seq_rows(a.qs, b, q0, tq);
+    seq_rows(a.ks, b, k0, tk);
+    if (c < 0 || tq == 0 || tk == 0) return;
+    const int i0 = last_by_window(a, tq, tk) + 1;
+    const int64_t n_rows = (int64_t)(tq - i0) * G, from = c * a.sink_chunk;
+    if (from >= n_rows) return;
+    const int rows = n_rows - from < a.sink_chunk ? (int)(n_rows - from) : a.sink_chunk;
+    const int sinks = a.sinks < tk ? a.sinks : tk;
+    const float over_g = 1.0f / (float)G;
+    // the chunk starts at head g0 of query i0 + from / G
+    const int64_t qf = from / G;
+    const int g0 = (int)(from - qf * G);
+    const T* qb = (const T*)a.q.data + (q0 + i0 + qf) * a.q.row + (int64_t)hk * G * a.q.head;
+    const T* gb = (const T*)a.grad_out.data + (q0 + i0 + qf) * a.grad_out.row +
+                  (int64_t)hk * G * a.grad_out.head;
+    const float2* sb = a.stat + ((int64_t)hk * a.qs.rows + q0 + i0) * G + from;
+    FPSTOK_LDS char* qbuf = lds + wave * kWaveBytes;
+    FPSTOK_LDS char* gbuf = qbuf + kTile;
+    const float cs = a.scale * kLog2e;
+
+    for (int s0 = 0; s0 < sinks; s0 += 32) {
+        const int j = s0 + (lane & 31);
+        const bool live = j < sinks;
+        Frag kf[STEPS], vf[STEPS];
+        const T* k = (const T*)a.k.data + (k0 + j) * a.k.row + hk * a.k.head;
+        const T* v = (const T*)a.v.data + (k0 + j) * a.v.row + hk * a.v.head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = s * 16 + half * 8;
+            Frag fk = {}, fv = {};
+            if (live && d < a.D) {
+                fk = *(const Frag*)(k + d);
+                fv = *(const Frag*)(v + d);
+            }
+            kf[s] = fk;
+            vf[s] = fv;
+        }
+        f32x16 dk[DB], dv[DB];
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
+        Stage<T, DP, 32, 64> sq, sg;
+        float2 st = make_float2(0.0f, 0.0f);
+        auto load = [&](int x) {
+            // query and head of row x of the chunk (x + g0 may pass 2^17)
+            const int q = (x + g0) / G, g = x + g0 - q * G;
+            const int left = rows - x;
+            sq.load_group(qb + q * a.q.row, a.q.row, a.q.head, g, G, over_g, left, a.D, lane);
+            sg.load_group(gb + q * a.grad_out.row, a.grad_out.row, a.grad_out.head, g, G, over_g,
+                          left, a.D, lane);
+            const int r = lane & 31;
+            st = sb[x + (r < left ? r : left - 1)];
+            if (r >= left) st = make_float2(0.0f, 0.0f);
+        };
+        if (wave * 32 < rows) load(wave * 32);
+        for (int x = wave * 32; x < rows; x += 128) {
+            wave_sync();  // the wave's reads of the last tile are done
+            sq.store(qbuf, a.D, lane);
+            sg.store(gbuf, a.D, lane);
+            if (half == 0) stat[wave][0][lane] = st.x, stat[wave][1][lane] = st.y;
+            wave_sync();
+            if (x + 128 < rows) load(x + 128);
+            f32x16 s = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int e = 0; e < STEPS; ++e) {
+                s = Elem<T>::mma(Tl::row_frag(qbuf, lane & 31, e, half), kf[e], s);
+                y = Elem<T>::mma(Tl::row_frag(gbuf, lane & 31, e, half), vf[e], y);
+            }
+            float w[16], ds[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int at = (e >> 2) * 8 + half * 4 + (e & 3);
+                w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], cs, -stat[wave][0][at]));
+                ds[e] = w[e] * (y[e] - stat[wave][1][at]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const Frag fw = to_frag<T>(w + e * 8), fs = to_frag<T>(ds + e * 8);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    dv[db] = Elem<T>::mma(Tl::col_frag(gbuf, e * 16, db, lane), fw, dv[db]);
+                    dk[db] = Elem<T>::mma(Tl::col_frag(qbuf, e * 16, db, lane), fs, dk[db]);
+                }
+            }
+        }
+        // the waves' results, added in order: [key][DP] floats in LDS
+        float* part = a.sink_part + ((slot * a.Hk + hk) * 2 * a.sinks + s0) * a.D;
+        const int keys = sinks - s0 < 32 ? sinks - s0 : 32;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    f4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = which ? dv[db][g * 4 + e] : dk[db][g * 4 + e];
+                    *(FPSTOK_LDS f4*)(qbuf + ((lane & 31) * DP + db * 32 + g * 8 + half * 4) * 4) =
+                        x;
+                }
+            __syncthreads();
+            for (int x = tid; x < keys * (DP / 4); x += 256) {
+                const int key = x / (DP / 4), d = (x % (DP / 4)) * 4;
+                if (d >= a.D) continue;
+                f4 y = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    y += *(FPSTOK_LDS f4*)(lds + w * kWaveBytes + (key * DP + d) * 4);
+                *(f4*)(part + (int64_t)which * a.sinks * a.D + key * a.D + d) = y;
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // grad_k and grad_v.  A workgroup takes 128 keys of one key head (32 per wave,
 // across the lanes) and walks the rows (query, head of the group) that see
 // them, BQ at a time: S = Q K^T and dP = dO V^T have the rows in registers, so P
@@ -723,7 +881,9 @@ void attention_dkv_kernel(AttnArgs a) {
     }
     if (a.left >= 0) {
         const int jl = t.row0 + t.rows - 1;
-        if (t.row0 >= a.sinks && jl + a.left - off < i1) i1 = jl + a.left - off;
+        // (of the rows past its window, the tile with the sinks gets their
+        // gradients from the kernel above)
+        if (jl + a.left - off < i1) i1 = jl + a.left - off;
         if (j >= a.sinks && j + a.left - off < e1) e1 = j + a.left - off;
     }
     const int64_t n_rows = t.rows > 0 && i1 >= i0 ? (int64_t)(i1 - i0 + 1) * G : 0;
@@ -846,6 +1006,33 @@ void attention_dkv_kernel(AttnArgs a) {
         if (i + 1 < n) store(i + 1);
         __syncthreads();
     }
+    if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks) {
+        const int64_t past = (int64_t)(t.tq - 1 - last_by_window(a, t.tq, t.tk)) * G;
+        const int chunks = (int)((past + a.sink_chunk - 1) / a.sink_chunk);
+        if (chunks > 0) {
+            const bool mine = live && r < a.sinks;
+            const int64_t first = sink_slot(a, t.b, G);
+            const int64_t step = (int64_t)a.Hk * 2 * a.sinks * a.D;
+            const float* part = a.sink_part + (first * a.Hk + t.hk) * 2 * a.sinks * a.D +
+                                (mine ? r : 0) * a.D;
+            // dK is scaled when it is stored, and so is this
+            for (int x = 0; x < chunks; ++x, part += step)
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        using f4 = float __attribute__((ext_vector_type(4)));
+                        const int d = db * 32 + g * 8 + half * 4, at = d < a.D ? d : 0;
+                        const f4 pk = *(const f4*)(part + at);
+                        const f4 pv = *(const f4*)(part + (int64_t)a.sinks * a.D + at);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            dk[db][g * 4 + e] += mine ? pk[e] : 0.0f;
+                            dv[db][g * 4 + e] += mine ? pv[e] : 0.0f;
+                        }
+                    }
+        }
+    }
     T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
     T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
 #pragma unroll
@@ -875,10 +1062,9 @@ void attention_dkv_kernel(AttnArgs a) {
     }
 }
 
-// Slots of a grid that covers every tile of BM rows of every sequence.
-static int64_t row_slots(const SeqArgs& s, int G, int BM) {
-    if (s.cu) return s.rows * G / BM + s.B;
-    return (int64_t)s.B * (((int64_t)s.cap * G + BM - 1) / BM);
+int64_t row_slots(const SeqArgs& s, int G, int chunk) {
+    if (s.cu) return s.rows * G / chunk + s.B;
+    return (int64_t)s.B * (((int64_t)s.cap * G + chunk - 1) / chunk);
 }
 
 // Splits a row's keys until the grid has `want` workgroups, but not into
@@ -935,6 +1121,13 @@ static hipError_t backward(const AttnArgs& a, hipStream_t s) {
             attention_dq_kernel<T, 64, 64><<<q, 256, 0, s>>>(a);
         else
             attention_dq_kernel<T, 128, k16 ? 64 : 32><<<q, 256, 0, s>>>(a);
+    }
+    if (a.sink_part && a.qs.rows > 0) {
+        const dim3 c((unsigned)(row_slots(a.qs, a.H / a.Hk, a.sink_chunk) * a.Hk));
+        if (a.D <= 64)
+            attention_sink_kernel<T, 64><<<c, 256, 0, s>>>(a);
+        else
+            attention_sink_kernel<T, 128><<<c, 256, 0, s>>>(a);
     }
     if (a.ks.rows > 0) {
         if (a.D <= 64)
