@@ -30,7 +30,8 @@ struct AttnArgs {
     SeqArgs qs, ks;
     HeadsArg q, k, v, out, grad_out, grad_q, grad_k, grad_v;
     float* lse;    // [q rows][H], or null (forward)
-    float2* stat;  // [Hk][q rows * H / Hk] log2(e) lse, delta (backward)
+    float* lse2;   // [Hk][q rows * H / Hk] log2(e) lse (backward)
+    float* delta;  // the same shape: sum of grad_out * out
     int32_t H, Hk, D, dtype;
     int32_t left, right, sinks;
     float scale;

@@ -268,27 +268,31 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(
     const int n = t.rows > 0 ? kt.part(blockIdx.y, a.splits) : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
-    Stage<T, DP, BN, 256> sk, sv;
-    auto load = [&](int i) {
-        const int64_t j0 = (int64_t)kt.tile(i) * BN;
-        sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, tid);
-        sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, tid);
-    };
-    auto store = [&](int i) {
+    const Dma<T, DP, BN> dma(a.D, tid);
+    auto load = [&](int i) {  // tile i on its way to its buffer
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        sk.store(buf, a.D, tid);
+        const int64_t j0 = (int64_t)kt.tile(i) * BN;
+        dma.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, buf, wave);
+        dma.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, buf + BN * Tl::kPitch, wave);
+    };
+    auto arrive = [&](int i) {  // this wave's part of it is there
+        dma_wait();
         // a value that some row must not see meets a weight of 0 there: an
         // infinite one has to leave the product
-        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 && sv.clean(tid)) bad = 1;
-        sv.store(buf + BN * Tl::kPitch, a.D, tid);
+        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 &&
+            dma.clean(lds + ((i & 1) * 2 + 1) * BN * Tl::kPitch, tid))
+            bad = 1;
     };
 
     Softmax<T, DB, KB> sm;
     const float c = a.scale * kLog2e;
     if (tid == 0) bad = 0;
-    if (n > 0) load(0);
+    if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
-    if (n > 0) store(0);
+    if (n > 0) {
+        load(0);
+        arrive(0);
+    }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = kt.tile(i) * BN;
@@ -321,7 +325,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(
                     sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
             }
         }
-        if (i + 1 < n) store(i + 1);
+        if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
     const bool some = sm.finish();
@@ -596,9 +600,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
             // only has to be finite
             const float v = a.lse[q.row * a.H + q.h];
             lse2 = v == -INFINITY ? 0.0f : v * kLog2e;
-            if (half == 0)
-                a.stat[((int64_t)t.hk * a.qs.rows + t.q0) * G + t.row0 + q.r] =
-                    make_float2(lse2, delta);
+            const int64_t at = ((int64_t)t.hk * a.qs.rows + t.q0) * G + t.row0 + q.r;
+            if (half == 0) a.lse2[at] = lse2, a.delta[at] = delta;
         }
     }
 
@@ -606,17 +609,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     const int n = t.rows > 0 ? kt.count : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
-    Stage<T, DP, BN, 256> sk, sv;
-    auto load = [&](int i) {
-        const int64_t j0 = (int64_t)kt.tile(i) * BN;
-        sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, tid);
-        sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, tid);
-    };
-    auto store = [&](int i) {
+    const Dma<T, DP, BN> dma(a.D, tid);
+    auto load = [&](int i) {  // tile i on its way to its buffer
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 && sk.clean(tid)) bad = 1;
-        sk.store(buf, a.D, tid);
-        sv.store(buf + BN * Tl::kPitch, a.D, tid);
+        const int64_t j0 = (int64_t)kt.tile(i) * BN;
+        dma.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, buf, wave);
+        dma.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, buf + BN * Tl::kPitch, wave);
+    };
+    auto arrive = [&](int i) {
+        dma_wait();
+        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 &&
+            dma.clean(lds + (i & 1) * 2 * BN * Tl::kPitch, tid))
+            bad = 1;
     };
 
     f32x16 dq[DB];
@@ -624,9 +628,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
     const float c = a.scale * kLog2e;
     if (tid == 0) bad = 0;
-    if (n > 0) load(0);
+    if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
-    if (n > 0) store(0);
+    if (n > 0) {
+        load(0);
+        arrive(0);
+    }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = kt.tile(i) * BN;
@@ -658,7 +665,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
                 }
             }
         }
-        if (i + 1 < n) store(i + 1);
+        if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
     T* out = (T*)a.grad_q.data + q.row * a.grad_q.row + q.h * a.grad_q.head;
@@ -729,7 +736,7 @@ void attention_sink_kernel(AttnArgs a) {
     const T* qb = (const T*)a.q.data + (q0 + i0 + qf) * a.q.row + (int64_t)hk * G * a.q.head;
     const T* gb = (const T*)a.grad_out.data + (q0 + i0 + qf) * a.grad_out.row +
                   (int64_t)hk * G * a.grad_out.head;
-    const float2* sb = a.stat + ((int64_t)hk * a.qs.rows + q0 + i0) * G + from;
+    const int64_t stat0 = ((int64_t)hk * a.qs.rows + q0 + i0) * G + from;
     FPSTOK_LDS char* qbuf = lds + wave * kWaveBytes;
     FPSTOK_LDS char* gbuf = qbuf + kTile;
     const float cs = a.scale * kLog2e;
@@ -764,7 +771,8 @@ void attention_sink_kernel(AttnArgs a) {
             sg.load_group(gb + q * a.grad_out.row, a.grad_out.row, a.grad_out.head, g, G, over_g,
                           left, a.D, lane);
             const int r = lane & 31;
-            st = sb[x + (r < left ? r : left - 1)];
+            const int64_t at = stat0 + x + (r < left ? r : left - 1);
+            st = make_float2(a.lse2[at], a.delta[at]);
             if (r >= left) st = make_float2(0.0f, 0.0f);
         };
         if (wave * 32 < rows) load(wave * 32);
@@ -837,13 +845,13 @@ void attention_sink_kernel(AttnArgs a) {
 // dV^T += dO^T P and dK^T += Q^T dS.  The heads of the group are rows of the same
 // walk: their gradients add up in the accumulators, in a fixed order.
 template <class T, int DP, int BQ>
-__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 128 ? 2 : 1)
+__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1)
 void attention_dkv_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, QB = BQ / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BQ * Tl::kPitch];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];
+    __shared__ __attribute__((aligned(16))) float stat[2][2][64];
     __shared__ int bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -889,12 +897,14 @@ void attention_dkv_kernel(AttnArgs a) {
     const int64_t n_rows = t.rows > 0 && i1 >= i0 ? (int64_t)(i1 - i0 + 1) * G : 0;
     const int n = (int)((n_rows + BQ - 1) / BQ);
     // this lane's rows, counted from the walk's start (query i0, head 0)
-    const int64_t see0 = (int64_t)(e0 - i0) * G, see1 = (int64_t)(e1 + 1 - i0) * G;
+    const int64_t see0 = (int64_t)(e0 - i0) * G;
+    const int64_t see1 = (int64_t)((e1 < i1 ? e1 : i1) + 1 - i0) * G;
 
     const T* qb = (const T*)a.q.data + (t.q0 + i0) * a.q.row + (int64_t)t.hk * G * a.q.head;
     const T* gb = (const T*)a.grad_out.data + (t.q0 + i0) * a.grad_out.row +
                   (int64_t)t.hk * G * a.grad_out.head;
-    const float2* sb = a.stat + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
+    const float* lse_b = a.lse2 + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
+    const float* delta_b = a.delta + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
     const float over_g = 1.0f / (float)G;
 
     // tile i of the walk: its first row is head `g` of query i0 + `q`
@@ -909,7 +919,9 @@ void attention_dkv_kernel(AttnArgs a) {
     };
     auto view_of = [&](const Place& at, int k0) {  // the tile's rows against 32 keys
         const int pa = i0 + at.q + off;
-        return tile_view<32>(a, pa, pa + group_div(at.g + at.rows - 1, over_g), t.tk, t.row0 + k0);
+        const int v = tile_view<32>(a, pa, pa + group_div(at.g + at.rows - 1, over_g), t.tk,
+                                    t.row0 + k0);
+        return v == 2 && at.rows < BQ ? 1 : v;  // rows past the last are masked
     };
     auto partly = [&](const Place& at) {  // some row of the tile does not see some key
         bool part = false;
@@ -917,8 +929,7 @@ void attention_dkv_kernel(AttnArgs a) {
         for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(at, w * 32) != 2;
         return part;
     };
-    Stage<T, DP, BQ, 256> sq, sg;
-    float2 sst = make_float2(0.0f, 0.0f);
+    const Dma<T, DP, BQ> dma(a.D, tid);
     auto load = [&](int i) {  // tiles in turn
         if (i > 0) {
             next.q += step_q;
@@ -926,23 +937,23 @@ void attention_dkv_kernel(AttnArgs a) {
             if (next.g >= G) ++next.q, next.g -= G;
         }
         next.rows = rows_of(i);
-        sq.load_group(qb + next.q * a.q.row, a.q.row, a.q.head, next.g, G, over_g, next.rows, a.D,
-                      tid);
-        sg.load_group(gb + next.q * a.grad_out.row, a.grad_out.row, a.grad_out.head, next.g, G,
-                      over_g, next.rows, a.D, tid);
-        sst = sb[(int64_t)i * BQ + (tid < next.rows ? tid : next.rows - 1)];
-    };
-    auto store = [&](int i) {
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
-        if (partly(next)) {
-            const bool bq = sq.clean(tid), bg = sg.clean(tid);
-            if (bq || bg) bad = 1;
+        dma.load_group(qb + next.q * a.q.row, a.q.row, a.q.head, next.g, G, over_g, next.rows, buf,
+                       wave);
+        dma.load_group(gb + next.q * a.grad_out.row, a.grad_out.row, a.grad_out.head, next.g, G,
+                       over_g, next.rows, buf + BQ * Tl::kPitch, wave);
+        if (wave < 2) {
+            const float* src = (wave == 0 ? lse_b : delta_b) + (int64_t)i * BQ;
+            dma4(src, (uint32_t)(lane < next.rows ? lane : next.rows - 1) * 4u,
+                 (uint32_t)(uintptr_t)(FPSTOK_LDS float*)stat[i & 1][wave]);
         }
-        sq.store(buf, a.D, tid);
-        sg.store(buf + BQ * Tl::kPitch, a.D, tid);
-        if (tid < BQ) {
-            stat[i & 1][0][tid] = tid < next.rows ? sst.x : 0.0f;
-            stat[i & 1][1][tid] = tid < next.rows ? sst.y : 0.0f;
+    };
+    auto arrive = [&](int i) {
+        dma_wait();
+        if (partly(next)) {
+            FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
+            const bool bq = dma.clean(buf, tid), bg = dma.clean(buf + BQ * Tl::kPitch, tid);
+            if (bq || bg) bad = 1;
         }
     };
 
@@ -951,9 +962,12 @@ void attention_dkv_kernel(AttnArgs a) {
     for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
     const float c = a.scale * kLog2e;
     if (tid == 0) bad = 0;
-    if (n > 0) load(0);
+    if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
-    if (n > 0) store(0);
+    if (n > 0) {
+        load(0);
+        arrive(0);
+    }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         cur = next;
@@ -1003,7 +1017,7 @@ void attention_dkv_kernel(AttnArgs a) {
                 }
             }
         }
-        if (i + 1 < n) store(i + 1);
+        if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
     if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks) {

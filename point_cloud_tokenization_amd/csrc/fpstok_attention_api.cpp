@@ -81,8 +81,10 @@ static fpstok_status check_heads(const fpstok_heads* v, const char* what, int64_
     const int w = elem_bytes(dtype);
     if (v->row_stride < 0 || v->head_stride < 0)
         return fail(FPSTOK_EINVAL, "%s: negative stride", what);
-    if (v->row_stride > ((int64_t)1 << 40) || v->head_stride > ((int64_t)1 << 40))
-        return fail(FPSTOK_EUNSUPPORTED, "%s: stride > 2^40", what);
+    if (v->row_stride > ((int64_t)1 << 23))  // a tile's rows within 32-bit byte offsets
+        return fail(FPSTOK_EUNSUPPORTED, "%s: row_stride > 2^23", what);
+    if (v->head_stride > ((int64_t)1 << 40))
+        return fail(FPSTOK_EUNSUPPORTED, "%s: head_stride > 2^40", what);
     if (((uintptr_t)v->data % align) != 0 || ((uintptr_t)(v->row_stride * w) % align) != 0 ||
         ((uintptr_t)(v->head_stride * w) % align) != 0)
         return fail(FPSTOK_EINVAL, "%s: data and strides must be aligned to %d bytes", what,
@@ -143,8 +145,9 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
     const size_t rows = (size_t)qs->num_rows * a.H;
     char* at = (char*)ws;
     if (backward) {
-        a.stat = (float2*)at;
-        const size_t stat = align256(rows * sizeof(float2));
+        a.lse2 = (float*)at;
+        a.delta = (float*)(at + align256(rows * sizeof(float)));
+        const size_t stat = 2 * align256(rows * sizeof(float));
         if (a.left < 0 || a.sinks == 0) return stat;
         // about 512 workgroups of sink rows, of 1024 rows or more
         const int G = a.H / a.Hk;

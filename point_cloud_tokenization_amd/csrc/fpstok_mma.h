@@ -242,6 +242,106 @@ struct Stage {
     }
 };
 
+// 16 bytes per lane from base + off (bytes) straight to LDS at lds + 16 lane,
+// without a register in between; done once the wave's vmcnt is back at 0
+// (dma_wait).  The instruction takes its LDS address from M0.  The compiler
+// would wait for such a load before the next LDS read of any kind; here the
+// reads of one buffer go on while the other one fills.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void dma16(const void* addr, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(lds), "v"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Rows of a tile straight from memory to LDS by the 4 waves of a workgroup.
+// Lane l of a load fills the l-th 16 bytes of its part of the tile, so the
+// swizzle is in the address it reads from.  Rows at or past `rows` (at least
+// 1) hold a copy of the last one: whoever reads the tile masks them.  Chunks
+// at or past D are not loaded: they keep the zeros of zero().
+template <class T, int DP, int ROWS>
+struct Dma {
+    using Tl = Tile<T, DP>;
+    static constexpr int kPer = ROWS * Tl::kChunks / 256;
+    static constexpr int kStep = 256 / Tl::kChunks;  // rows between a thread's chunks
+    static constexpr int kBytes = ROWS * Tl::kPitch;
+    static_assert(ROWS * Tl::kChunks % 256 == 0 && kStep % 8 == 0, "whole chunks, one swizzle");
+    int row, col;   // this thread's first row and its element in it
+    bool loads;
+    __device__ __forceinline__ Dma(int D, int tid) {
+        row = tid / Tl::kChunks;
+        col = ((tid % Tl::kChunks) ^ Tl::swz(row)) * Tl::kElems;
+        loads = col < D;
+    }
+    static __device__ __forceinline__ void zero(FPSTOK_LDS char* buf, int bytes, int tid) {
+        for (int i = tid * 16; i < bytes; i += 256 * 16) *(FPSTOK_LDS u32x4*)(buf + i) = 0;
+    }
+    __device__ __forceinline__ void load(const T* base, int64_t stride, int rows,
+                                         FPSTOK_LDS char* buf, int wave) const {
+        const uint32_t lds = (uint32_t)(uintptr_t)buf + wave * 1024;
+        if (!loads) return;
+        if (rows >= ROWS) {
+            const uint32_t off = (uint32_t)(row * (int)stride + col) * (uint32_t)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) dma16(base + i * (kStep * stride), off, lds + i * 4096);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = i * kStep + row < rows ? i * kStep + row : rows - 1;
+                const uint32_t off = (uint32_t)(r * (int)stride + col) * (uint32_t)sizeof(T);
+                dma16(base, off, lds + i * 4096);
+            }
+        }
+    }
+    // Rows query * G + head of a group of heads: row i of the tile is head
+    // (g0 + i) % G of query (g0 + i) / G past `base`.  g0 < G; over_g = 1 / G.
+    __device__ __forceinline__ void load_group(const T* base, int64_t stride, int64_t head, int g0,
+                                               int G, float over_g, int rows, FPSTOK_LDS char* buf,
+                                               int wave) const {
+        if (G == 1) {
+            load(base, stride, rows, buf, wave);
+            return;
+        }
+        const uint32_t lds = (uint32_t)(uintptr_t)buf + wave * 1024;
+        if (!loads) return;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = i * kStep + row;
+            const int n = g0 + (r < rows ? r : rows - 1);
+            const int q = group_div(n, over_g);
+            dma16(base + q * stride + (n - q * G) * head + col, lds + i * 4096);
+        }
+    }
+    // After dma_wait: infinite and not-a-number elements of the chunks this
+    // thread loaded become zero; true if there were any.
+    __device__ __forceinline__ bool clean(FPSTOK_LDS char* buf, int tid) const {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            FPSTOK_LDS u32x4* p = (FPSTOK_LDS u32x4*)(buf + i * 4096 + tid * 16);
+            const u32x4 x = *p;
+            if (chunk_bad<T>(x)) {
+                *p = chunk_clean<T>(x);
+                bad = true;
+            }
+        }
+        return bad;
+    }
+};
+
 // Orders a wave's own LDS writes and reads across its lanes (other waves are
 // not waited for).
 __device__ __forceinline__ void wave_sync() {

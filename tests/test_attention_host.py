@@ -189,7 +189,8 @@ def test_attention_refuses_counts_and_workspace(L):
     assert _forward(L, qs=_seqs(rows=1 << 31)) == F.EUNSUPPORTED
     assert _forward(L, qs=_seqs(B=(1 << 24) + 1)) == F.EUNSUPPORTED
     assert _forward(L, qs=_seqs(rows=(1 << 31) - 1), pr=_params(num_heads=64)) == F.EUNSUPPORTED
-    assert _forward(L, q=_heads(row=1 << 41)) == F.EUNSUPPORTED
+    assert _forward(L, q=_heads(row=1 << 24)) == F.EUNSUPPORTED
+    assert _forward(L, q=_heads(head=1 << 41)) == F.EUNSUPPORTED
 
 
 def test_attention_nothing_to_do(L):
