@@ -24,12 +24,12 @@ HIPCC_FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off", "-fno-fast-math", "-fvisibility=hidden",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # the register-resident FPS reads its pulse arrays with a uniform dynamic
-    # index; this limit lets every instantiation keep them in VGPRs (no
-    # scratch memory)
-    "-mllvm", "-amdgpu-promote-alloca-to-vector-limit=1024",
     "-Wall", "-Wno-unused-command-line-argument",
 ]
+# The register-resident FPS reads its pulse arrays with a uniform dynamic
+# index; this limit lets every instantiation keep them in VGPRs (no scratch
+# memory).  The attention kernels index theirs with constants only.
+SOURCE_FLAGS = {SOURCES[0]: ["-mllvm", "-amdgpu-promote-alloca-to-vector-limit=1024"]}
 
 
 def hipcc() -> str:
@@ -45,8 +45,9 @@ def build(verbose: bool = False, extra=()) -> str:
         jobs, linked = [], []
         for src in SOURCES:
             obj = os.path.join(objs, os.path.basename(src) + ".o")
-            cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f != "-shared"], *extra, "-c",
-                   "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", obj, src]
+            cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f != "-shared"],
+                   *SOURCE_FLAGS.get(src, []), *extra, "-c", "-I", os.path.join(ROOT, "include"),
+                   "-I", CSRC, "-o", obj, src]
             if verbose:
                 print(" ".join(cmd), flush=True)
             jobs.append((cmd, subprocess.Popen(cmd)))
@@ -66,7 +67,7 @@ def build(verbose: bool = False, extra=()) -> str:
 def device_asm(out_path: str) -> str:
     """Compile the kernels to gfx950 assembly (for the build checks)."""
     cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")],
-           "--cuda-device-only", "-S", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+           *SOURCE_FLAGS[SOURCES[0]], "--cuda-device-only", "-S", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
            "-o", out_path, SOURCES[0]]
     subprocess.run(cmd, check=True, capture_output=True)
     return out_path

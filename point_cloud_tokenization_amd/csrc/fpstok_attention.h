@@ -30,7 +30,7 @@ struct AttnArgs {
     SeqArgs qs, ks;
     HeadsArg q, k, v, out, grad_out, grad_q, grad_k, grad_v;
     float* lse;    // [q rows][H], or null (forward)
-    float* lse2;   // [Hk][q rows * H / Hk] log2(e) lse (backward)
+    float* lse2;   // [H][q rows] log2(e) lse (backward)
     float* delta;  // the same shape: sum of grad_out * out
     int32_t H, Hk, D, dtype;
     int32_t left, right, sinks;
@@ -41,7 +41,7 @@ struct AttnArgs {
     float* part;
     float2* part_ml;
     // rows that see a sequence's sinks from behind its first key tile's window
-    // (backward): walked in chunks of sink_chunk rows, whose parts of the
+    // (backward): walked in chunks of sink_chunk queries, whose parts of the
     // sinks' gradients are [slots][Hk][2][sinks][D] (grad_k, grad_v)
     int32_t sink_chunk;
     float* sink_part;

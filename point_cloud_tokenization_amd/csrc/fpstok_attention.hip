@@ -93,6 +93,30 @@ __device__ __forceinline__ int tile_view(const AttnArgs& a, int pa, int pb, int 
     return left_none || right_none ? 0 : left_all && right_all ? 2 : 1;
 }
 
+// tile_view for many tiles of the same rows: ranges of j0.
+template <int BN>
+struct View {
+    int pa, pb, tk, all_lo, any_lo;
+    uint32_t all_span, any_span;
+    __device__ __forceinline__ View(const AttnArgs& a, int pa, int pb, int tk)
+        : pa(pa), pb(pb), tk(tk) {
+        int hi = tk - BN;
+        if (a.right >= 0 && pa + a.right - (BN - 1) < hi) hi = pa + a.right - (BN - 1);
+        all_lo = a.left >= 0 && pb - a.left > 0 ? pb - a.left : 0;
+        all_span = (uint32_t)(hi - all_lo);
+        if (hi < all_lo) all_lo = 0x7fffffff, all_span = 0;
+        hi = tk - 1;
+        if (a.right >= 0 && pb + a.right < hi) hi = pb + a.right;
+        any_lo = a.left >= 0 && pa - a.left - (BN - 1) > 0 ? pa - a.left - (BN - 1) : 0;
+        any_span = (uint32_t)(hi - any_lo);
+        if (hi < any_lo) any_lo = 0x7fffffff, any_span = 0;
+    }
+    __device__ __forceinline__ int of(const AttnArgs& a, int j0) const {
+        if (j0 < a.sinks) return tile_view<BN>(a, pa, pb, tk, j0);
+        return (uint32_t)(j0 - all_lo) <= all_span ? 2 : (uint32_t)(j0 - any_lo) <= any_span;
+    }
+};
+
 // The keys one row sees: [lo, lo + span] and those below `sink`.
 struct Window {
     int lo, sink;
@@ -110,7 +134,7 @@ struct Window {
     // Registers of a transposed block of 32 keys from key j0 on (half: lane >> 5)
     // whose key the row does not see become `fill`.  No key at or past `sinks`
     // is a sink, so most tiles need one comparison per key.
-    __device__ __forceinline__ void mask(float* x, int j0, int half, int sinks, float fill) const {
+    __device__ __forceinline__ void mask(f32x16& x, int j0, int half, int sinks, float fill) const {
         const int jb = j0 + half * 4;
         if (j0 >= sinks) {
 #pragma unroll
@@ -200,12 +224,12 @@ struct Softmax {
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[db] = 0.0f;
     }
-    // Scores s of KB * 32 keys (transposed, -infinity where hidden) become
-    // weights; result and sum are rescaled to the new maximum.
-    __device__ __forceinline__ void weights(float* s, float c) {
-        float mx = s[0];
+    // Takes the maximum of the scores s of KB * 32 keys (transposed, -infinity
+    // where hidden); result and sum are rescaled if it has grown.
+    __device__ __forceinline__ void grow(const f32x16 (&s)[KB], float c) {
+        float mx = s[0][0];
 #pragma unroll
-        for (int e = 1; e < KB * 16; ++e) mx = fmaxf(mx, s[e]);
+        for (int e = 1; e < KB * 16; ++e) mx = fmaxf(mx, s[e >> 4][e & 15]);
         mx = pair_max(mx);
         if (__any((mx * c > mc + 8.0f) | (m == -INFINITY))) {
             const float m2 = fmaxf(m, mx);
@@ -217,10 +241,14 @@ struct Softmax {
 #pragma unroll
             for (int db = 0; db < DB; ++db) o[db] *= f;
         }
+    }
+    // The scores become weights.
+    __device__ __forceinline__ void weights(f32x16 (&s)[KB], float c) {
 #pragma unroll
         for (int e = 0; e < KB * 16; ++e) {
-            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -mc));
-            l += s[e];
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 4][e & 15], c, -mc));
+            s[e >> 4][e & 15] = w;
+            l += w;
         }
     }
     // The sum over both halves; false (and a zero result) if no key was seen.
@@ -269,18 +297,28 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     const Dma<T, DP, BN> dma(a.D, tid);
-    auto load = [&](int i) {  // tile i on its way to its buffer
+    const uint32_t off_k = dma.offset(a.k.row), off_v = dma.offset(a.v.row);
+    // the tile loaded last and its keys
+    int jn = n > 0 ? kt.tile(0) * BN : 0;
+    const T* kp = kb + jn * a.k.row;
+    const T* vp = vb + jn * a.v.row;
+    auto load = [&](int i) {  // tile i on its way to its buffer; tiles in turn
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        const int64_t j0 = (int64_t)kt.tile(i) * BN;
-        dma.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, buf, wave);
-        dma.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, buf + BN * Tl::kPitch, wave);
+        if (i > 0) {
+            const int skip = kt.from + i == kt.sink ? kt.first * BN - jn : BN;
+            jn += skip;
+            kp += skip * a.k.row;
+            vp += skip * a.v.row;
+        }
+        dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
+        dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
     };
+    const View<BN> all(a, q.pa, q.pb, t.tk), mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {  // this wave's part of it is there
         dma_wait();
         // a value that some row must not see meets a weight of 0 there: an
         // infinite one has to leave the product
-        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 &&
-            dma.clean(lds + ((i & 1) * 2 + 1) * BN * Tl::kPitch, tid))
+        if (all.of(a, jn) == 1 && dma.clean(lds + ((i & 1) * 2 + 1) * BN * Tl::kPitch, tid))
             bad = 1;
     };
 
@@ -295,31 +333,31 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(
     }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
-        const int j0 = kt.tile(i) * BN;
+        const int j0 = jn;
         if (i + 1 < n) load(i + 1);
-        const int view = wave_live ? tile_view<BN>(a, q.wa, q.wb, t.tk, j0) : 0;
+        const int view = wave_live ? mine.of(a, j0) : 0;
         if (view != 0) {
             const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
             const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
-            float s[KB * 16];
+            f32x16 s[KB];
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 f32x16 x = 0.0f;
 #pragma unroll
                 for (int st = 0; st < STEPS; ++st)
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) s[b * 16 + e] = x[e];
+                s[b] = x;
             }
             if (view == 1) {
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
-                    win.mask(s + b * 16, j0 + b * 32, half, a.sinks, -INFINITY);
+                    win.mask(s[b], j0 + b * 32, half, a.sinks, -INFINITY);
             }
+            sm.grow(s, c);
             sm.weights(s, c);
 #pragma unroll
             for (int k = 0; k < KB * 2; ++k) {
-                const Frag pf = to_frag<T>(s + k * 8);
+                const Frag pf = to_frag<T>(s[k >> 1], k & 1);
 #pragma unroll
                 for (int db = 0; db < DB; ++db)
                     sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
@@ -395,6 +433,7 @@ void attention_few_kernel(AttnArgs a) {
         sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, lane);
     };
 
+    const View<BN> all(a, q.pa, q.pb, t.tk);
     Softmax<T, DB, KB> sm;
     const float c = a.scale * kLog2e;
     if (wave < n) load(wave);
@@ -402,32 +441,32 @@ void attention_few_kernel(AttnArgs a) {
     __syncthreads();
     for (int i = wave; i < n; i += 4) {
         const int j0 = kt.tile(i) * BN;
-        const int view = tile_view<BN>(a, q.pa, q.pb, t.tk, j0);
+        const int view = all.of(a, j0);
         if (view == 1 && sv.clean(lane)) bad = 1;
         wave_sync();  // the wave's reads of the last tile are done
         sk.store(kbuf, a.D, lane);
         sv.store(vbuf, a.D, lane);
         wave_sync();
         if (i + 4 < n) load(i + 4);
-        float s[KB * 16];
+        f32x16 s[KB];
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
             f32x16 x = 0.0f;
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
                 x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[b * 16 + e] = x[e];
+            s[b] = x;
         }
         if (view == 1) {
 #pragma unroll
             for (int b = 0; b < KB; ++b)
-                win.mask(s + b * 16, j0 + b * 32, half, a.sinks, -INFINITY);
+                win.mask(s[b], j0 + b * 32, half, a.sinks, -INFINITY);
         }
-        sm.weights(s, c);
+        sm.grow(s, c);
+            sm.weights(s, c);
 #pragma unroll
         for (int k = 0; k < KB * 2; ++k) {
-            const Frag pf = to_frag<T>(s + k * 8);
+            const Frag pf = to_frag<T>(s[k >> 1], k & 1);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
                 sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
@@ -600,7 +639,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
             // only has to be finite
             const float v = a.lse[q.row * a.H + q.h];
             lse2 = v == -INFINITY ? 0.0f : v * kLog2e;
-            const int64_t at = ((int64_t)t.hk * a.qs.rows + t.q0) * G + t.row0 + q.r;
+            const int64_t at = (int64_t)q.h * a.qs.rows + q.row;
             if (half == 0) a.lse2[at] = lse2, a.delta[at] = delta;
         }
     }
@@ -610,17 +649,26 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     const Dma<T, DP, BN> dma(a.D, tid);
-    auto load = [&](int i) {  // tile i on its way to its buffer
+    const uint32_t off_k = dma.offset(a.k.row), off_v = dma.offset(a.v.row);
+    // the tile loaded last and its keys
+    int jn = n > 0 ? kt.tile(0) * BN : 0;
+    const T* kp = kb + jn * a.k.row;
+    const T* vp = vb + jn * a.v.row;
+    auto load = [&](int i) {  // tile i on its way to its buffer; tiles in turn
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        const int64_t j0 = (int64_t)kt.tile(i) * BN;
-        dma.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, buf, wave);
-        dma.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, buf + BN * Tl::kPitch, wave);
+        if (i > 0) {
+            const int skip = kt.from + i == kt.sink ? kt.first * BN - jn : BN;
+            jn += skip;
+            kp += skip * a.k.row;
+            vp += skip * a.v.row;
+        }
+        dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
+        dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
     };
+    const View<BN> all(a, q.pa, q.pb, t.tk), mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {
         dma_wait();
-        if (tile_view<BN>(a, q.pa, q.pb, t.tk, kt.tile(i) * BN) == 1 &&
-            dma.clean(lds + (i & 1) * 2 * BN * Tl::kPitch, tid))
-            bad = 1;
+        if (all.of(a, jn) == 1 && dma.clean(lds + (i & 1) * 2 * BN * Tl::kPitch, tid)) bad = 1;
     };
 
     f32x16 dq[DB];
@@ -636,9 +684,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
-        const int j0 = kt.tile(i) * BN;
+        const int j0 = jn;
         if (i + 1 < n) load(i + 1);
-        const int view = wave_live ? tile_view<BN>(a, q.wa, q.wb, t.tk, j0) : 0;
+        const int view = wave_live ? mine.of(a, j0) : 0;
         if (view != 0) {
             const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
             const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
@@ -650,14 +698,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
                     y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
                 }
-                float ds[16];
+                f32x16 ds;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     ds[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2)) * (y[e] - delta);
                 if (view == 1) win.mask(ds, j0 + b * 32, half, a.sinks, 0.0f);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const Frag f = to_frag<T>(ds + k * 8);
+                    const Frag f = to_frag<T>(ds, k);
 #pragma unroll
                     for (int db = 0; db < DB; ++db)
                         dq[db] =
@@ -689,9 +737,9 @@ __device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk)
 }
 
 // First sink chunk of sequence b in the numbering of its parts.
-__device__ __forceinline__ int64_t sink_slot(const AttnArgs& a, int b, int G) {
-    if (a.qs.cu) return first_slot(a.qs, b, G, a.sink_chunk);
-    return (int64_t)b * (((int64_t)a.qs.cap * G + a.sink_chunk - 1) / a.sink_chunk);
+__device__ __forceinline__ int64_t sink_slot(const AttnArgs& a, int b) {
+    if (a.qs.cu) return first_slot(a.qs, b, 1, a.sink_chunk);
+    return (int64_t)b * ((a.qs.cap + a.sink_chunk - 1) / a.sink_chunk);
 }
 
 // The sinks' gradients from the rows that see nothing else of the first key
@@ -716,27 +764,24 @@ void attention_sink_kernel(AttnArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.H / a.Hk, hk = (int)(blockIdx.x % a.Hk);
     const int64_t slot = blockIdx.x / a.Hk;
-    const int64_t per = ((int64_t)a.qs.cap * G + a.sink_chunk - 1) / a.sink_chunk;
-    const int b = a.qs.cu ? find_seq(a.qs, slot, G, a.sink_chunk) : (int)(slot / per);
-    const int64_t c = slot - sink_slot(a, b, G);
+    const int per = (a.qs.cap + a.sink_chunk - 1) / a.sink_chunk;
+    const int b = a.qs.cu ? find_seq(a.qs, slot, 1, a.sink_chunk) : (int)(slot / per);
+    const int64_t c = slot - sink_slot(a, b);
     int64_t q0, k0;
     int tq, tk;
     seq_rows(a.qs, b, q0, tq);
     seq_rows(a.ks, b, k0, tk);
     if (c < 0 || tq == 0 || tk == 0) return;
     const int i0 = last_by_window(a, tq, tk) + 1;
-    const int64_t n_rows = (int64_t)(tq - i0) * G, from = c * a.sink_chunk;
-    if (from >= n_rows) return;
-    const int rows = n_rows - from < a.sink_chunk ? (int)(n_rows - from) : a.sink_chunk;
+    const int64_t from = c * a.sink_chunk;
+    if (from >= tq - i0) return;
+    const int left = tq - i0 - (int)from, rows = left < a.sink_chunk ? left : a.sink_chunk;
     const int sinks = a.sinks < tk ? a.sinks : tk;
-    const float over_g = 1.0f / (float)G;
-    // the chunk starts at head g0 of query i0 + from / G
-    const int64_t qf = from / G;
-    const int g0 = (int)(from - qf * G);
-    const T* qb = (const T*)a.q.data + (q0 + i0 + qf) * a.q.row + (int64_t)hk * G * a.q.head;
-    const T* gb = (const T*)a.grad_out.data + (q0 + i0 + qf) * a.grad_out.row +
+    // the chunk's first query, in head 0 of the group
+    const int64_t row0 = q0 + i0 + from;
+    const T* qb = (const T*)a.q.data + row0 * a.q.row + (int64_t)hk * G * a.q.head;
+    const T* gb = (const T*)a.grad_out.data + row0 * a.grad_out.row +
                   (int64_t)hk * G * a.grad_out.head;
-    const int64_t stat0 = ((int64_t)hk * a.qs.rows + q0 + i0) * G + from;
     FPSTOK_LDS char* qbuf = lds + wave * kWaveBytes;
     FPSTOK_LDS char* gbuf = qbuf + kTile;
     const float cs = a.scale * kLog2e;
@@ -763,33 +808,32 @@ void attention_sink_kernel(AttnArgs a) {
         for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
         Stage<T, DP, 32, 64> sq, sg;
         float2 st = make_float2(0.0f, 0.0f);
-        auto load = [&](int x) {
-            // query and head of row x of the chunk (x + g0 may pass 2^17)
-            const int q = (x + g0) / G, g = x + g0 - q * G;
-            const int left = rows - x;
-            sq.load_group(qb + q * a.q.row, a.q.row, a.q.head, g, G, over_g, left, a.D, lane);
-            sg.load_group(gb + q * a.grad_out.row, a.grad_out.row, a.grad_out.head, g, G, over_g,
-                          left, a.D, lane);
-            const int r = lane & 31;
-            const int64_t at = stat0 + x + (r < left ? r : left - 1);
+        auto load = [&](int g, int x) {  // 32 queries from x on, head g of the group
+            sq.load(qb + x * a.q.row + g * a.q.head, a.q.row, rows - x, a.D, lane);
+            sg.load(gb + x * a.grad_out.row + g * a.grad_out.head, a.grad_out.row, rows - x, a.D,
+                    lane);
+            const int r = lane & 31, last = rows - x - 1;
+            const int64_t at = (int64_t)(hk * G + g) * a.qs.rows + row0 + x + (r < last ? r : last);
             st = make_float2(a.lse2[at], a.delta[at]);
-            if (r >= left) st = make_float2(0.0f, 0.0f);
+            if (r > last) st = make_float2(0.0f, 0.0f);
         };
-        if (wave * 32 < rows) load(wave * 32);
-        for (int x = wave * 32; x < rows; x += 128) {
+        if (wave * 32 < rows) load(0, wave * 32);
+        for (int g = 0, x = wave * 32; g < G && x < rows;) {
             wave_sync();  // the wave's reads of the last tile are done
             sq.store(qbuf, a.D, lane);
             sg.store(gbuf, a.D, lane);
             if (half == 0) stat[wave][0][lane] = st.x, stat[wave][1][lane] = st.y;
             wave_sync();
-            if (x + 128 < rows) load(x + 128);
+            x += 128;
+            if (x >= rows) x = wave * 32, ++g;
+            if (g < G) load(g, x);
             f32x16 s = 0.0f, y = 0.0f;
 #pragma unroll
             for (int e = 0; e < STEPS; ++e) {
                 s = Elem<T>::mma(Tl::row_frag(qbuf, lane & 31, e, half), kf[e], s);
                 y = Elem<T>::mma(Tl::row_frag(gbuf, lane & 31, e, half), vf[e], y);
             }
-            float w[16], ds[16];
+            f32x16 w, ds;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int at = (e >> 2) * 8 + half * 4 + (e & 3);
@@ -798,7 +842,7 @@ void attention_sink_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const Frag fw = to_frag<T>(w + e * 8), fs = to_frag<T>(ds + e * 8);
+                const Frag fw = to_frag<T>(w, e), fs = to_frag<T>(ds, e);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
                     dv[db] = Elem<T>::mma(Tl::col_frag(gbuf, e * 16, db, lane), fw, dv[db]);
@@ -839,18 +883,22 @@ void attention_sink_kernel(AttnArgs a) {
 }
 
 // grad_k and grad_v.  A workgroup takes 128 keys of one key head (32 per wave,
-// across the lanes) and walks the rows (query, head of the group) that see
-// them, BQ at a time: S = Q K^T and dP = dO V^T have the rows in registers, so P
+// across the lanes) and walks the queries that see them, BQ at a time, head
+// after head of the group: S = Q K^T and dP = dO V^T have the rows in registers, so P
 // and dS = P (dP - delta), rounded to the type, are the operands of
-// dV^T += dO^T P and dK^T += Q^T dS.  The heads of the group are rows of the same
-// walk: their gradients add up in the accumulators, in a fixed order.
+// dV^T += dO^T P and dK^T += Q^T dS.  The gradients of the group's heads add up
+// in the accumulators, in a fixed order.
 template <class T, int DP, int BQ>
-__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1)
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1)
 void attention_dkv_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, QB = BQ / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
-    __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BQ * Tl::kPitch];
+    // at DP = 128 of a 16-bit type the accumulators leave no registers for V:
+    // it is read from LDS
+    constexpr bool kVLds = DP > 64 && sizeof(T) == 2;
+    constexpr int kV = 2 * 2 * BQ * Tl::kPitch;
+    __shared__ __attribute__((aligned(16))) char smem[kV + (kVLds ? 128 * Tl::kPitch : 0)];
     __shared__ __attribute__((aligned(16))) float stat[2][2][64];
     __shared__ int bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
@@ -879,78 +927,84 @@ void attention_dkv_kernel(AttnArgs a) {
             vf[s] = fv;
         }
     }
-    // queries that see some key of the tile, and those that see this lane's key
-    const int off = t.tk - t.tq;
-    const int j = t.row0 + r;
-    int i0 = 0, i1 = t.tq - 1, e0 = 0, e1 = t.tq - 1;
-    if (a.right >= 0) {
-        if (t.row0 - a.right - off > 0) i0 = t.row0 - a.right - off;
-        if (j - a.right - off > 0) e0 = j - a.right - off;
-    }
-    if (a.left >= 0) {
-        const int jl = t.row0 + t.rows - 1;
-        // (of the rows past its window, the tile with the sinks gets their
-        // gradients from the kernel above)
-        if (jl + a.left - off < i1) i1 = jl + a.left - off;
-        if (j >= a.sinks && j + a.left - off < e1) e1 = j + a.left - off;
-    }
-    const int64_t n_rows = t.rows > 0 && i1 >= i0 ? (int64_t)(i1 - i0 + 1) * G : 0;
-    const int n = (int)((n_rows + BQ - 1) / BQ);
-    // this lane's rows, counted from the walk's start (query i0, head 0)
-    const int64_t see0 = (int64_t)(e0 - i0) * G;
-    const int64_t see1 = (int64_t)((e1 < i1 ? e1 : i1) + 1 - i0) * G;
+    // queries i0 .. i1 see some key of the tile (of the rows past its window,
+    // the tile with the sinks gets their gradients from the kernel above), e0 ..
+    // e1 of them this lane's key
+    const int off = t.tk - t.tq, j = t.row0 + r;
+    const int j_last = t.row0 + t.rows - 1;
+    int i0 = 0, i1 = t.tq - 1, e0 = 0, e1;
+    if (a.right >= 0 && t.row0 - a.right - off > 0) i0 = t.row0 - a.right - off;
+    if (a.left >= 0 && j_last + a.left - off < i1) i1 = j_last + a.left - off;
+    if (a.right >= 0 && j - a.right - off > 0) e0 = j - a.right - off;
+    e1 = a.left >= 0 && j >= a.sinks && j + a.left - off < i1 ? j + a.left - off : i1;
+    uint32_t e_span = (uint32_t)(e1 - e0);
+    if (e1 < e0) e0 = 0x7fffffff, e_span = 0;  // none: no query has that number
+    const int nq = t.rows > 0 && i1 >= i0 ? i1 - i0 + 1 : 0;
+    const int per = (nq + BQ - 1) / BQ, n = per * G;
+    // tiles of BQ queries from x on whose every row sees each of the keys j0 ..
+    // j1, and those where some row sees some: x - lo <= span
+    struct Range {
+        int lo;
+        uint32_t span;
+        __device__ __forceinline__ Range(int a, int b) : lo(a), span((uint32_t)(b - a)) {
+            if (b < a) lo = 0x7fffffff, span = 0;
+        }
+        __device__ __forceinline__ bool has(int x) const { return (uint32_t)(x - lo) <= span; }
+    };
+    auto all_range = [&](int j0, int j1) {
+        const int lo = a.right >= 0 && j1 - a.right - off > 0 ? j1 - a.right - off : 0;
+        int hi = i1;
+        if (a.left >= 0 && j1 >= a.sinks && j0 + a.left - off < hi) hi = j0 + a.left - off;
+        return Range(lo, hi - (BQ - 1));
+    };
+    auto any_range = [&](int j0, int j1) {
+        const int lo = a.right >= 0 ? j0 - a.right - off - (BQ - 1) : 0;
+        int hi = i1;
+        if (a.left >= 0 && j0 >= a.sinks && j1 + a.left - off < hi) hi = j1 + a.left - off;
+        return Range(lo < 0 ? 0 : lo, hi);
+    };
+    const int wj0 = t.row0 + wave * 32, wj1 = wj0 + 31 < j_last ? wj0 + 31 : j_last;
+    const Range wave_all = all_range(wj0, wj1), wave_any = any_range(wj0, wj1);
+    const Range tile_all = all_range(t.row0, j_last);
+    const bool wave_live = wave * 32 < t.rows;
 
-    const T* qb = (const T*)a.q.data + (t.q0 + i0) * a.q.row + (int64_t)t.hk * G * a.q.head;
-    const T* gb = (const T*)a.grad_out.data + (t.q0 + i0) * a.grad_out.row +
-                  (int64_t)t.hk * G * a.grad_out.head;
-    const float* lse_b = a.lse2 + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
-    const float* delta_b = a.delta + ((int64_t)t.hk * a.qs.rows + t.q0 + i0) * G;
-    const float over_g = 1.0f / (float)G;
-
-    // tile i of the walk: its first row is head `g` of query i0 + `q`
-    struct Place {
-        int q, g, rows;
-    };
-    const int step_q = BQ / G, step_g = BQ % G;
-    Place next{0, 0, 0}, cur;
-    auto rows_of = [&](int i) {
-        const int64_t left = n_rows - (int64_t)i * BQ;
-        return left < BQ ? (int)left : BQ;
-    };
-    auto view_of = [&](const Place& at, int k0) {  // the tile's rows against 32 keys
-        const int pa = i0 + at.q + off;
-        const int v = tile_view<32>(a, pa, pa + group_div(at.g + at.rows - 1, over_g), t.tk,
-                                    t.row0 + k0);
-        return v == 2 && at.rows < BQ ? 1 : v;  // rows past the last are masked
-    };
-    auto partly = [&](const Place& at) {  // some row of the tile does not see some key
-        bool part = false;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) part |= w * 32 < t.rows && view_of(at, w * 32) != 2;
-        return part;
-    };
     const Dma<T, DP, BQ> dma(a.D, tid);
+    const uint32_t off_q = dma.offset(a.q.row), off_g = dma.offset(a.grad_out.row);
+    // the first query of the tile loaded last
+    int xn = i0;
+    const int64_t row_i0 = t.q0 + i0;
+    const T* qp = (const T*)a.q.data + row_i0 * a.q.row + (int64_t)t.hk * G * a.q.head;
+    const T* gp =
+        (const T*)a.grad_out.data + row_i0 * a.grad_out.row + (int64_t)t.hk * G * a.grad_out.head;
+    int64_t stat_at = (int64_t)t.hk * G * a.qs.rows + row_i0;
     auto load = [&](int i) {  // tiles in turn
         if (i > 0) {
-            next.q += step_q;
-            next.g += step_g;
-            if (next.g >= G) ++next.q, next.g -= G;
+            if (xn + BQ <= i1) {
+                xn += BQ;
+                qp += BQ * a.q.row;
+                gp += BQ * a.grad_out.row;
+                stat_at += BQ;
+            } else {
+                const int back = xn - i0;
+                xn = i0;
+                qp += a.q.head - back * a.q.row;
+                gp += a.grad_out.head - back * a.grad_out.row;
+                stat_at += a.qs.rows - back;
+            }
         }
-        next.rows = rows_of(i);
+        const int rows = i1 - xn + 1;
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
-        dma.load_group(qb + next.q * a.q.row, a.q.row, a.q.head, next.g, G, over_g, next.rows, buf,
-                       wave);
-        dma.load_group(gb + next.q * a.grad_out.row, a.grad_out.row, a.grad_out.head, next.g, G,
-                       over_g, next.rows, buf + BQ * Tl::kPitch, wave);
+        dma.load(qp, off_q, a.q.row, rows, buf, wave);
+        dma.load(gp, off_g, a.grad_out.row, rows, buf + BQ * Tl::kPitch, wave);
         if (wave < 2) {
-            const float* src = (wave == 0 ? lse_b : delta_b) + (int64_t)i * BQ;
-            dma4(src, (uint32_t)(lane < next.rows ? lane : next.rows - 1) * 4u,
+            const float* src = (wave == 0 ? a.lse2 : a.delta) + stat_at;
+            dma4(src, (uint32_t)(lane < rows ? lane : rows - 1) * 4u,
                  (uint32_t)(uintptr_t)(FPSTOK_LDS float*)stat[i & 1][wave]);
         }
     };
     auto arrive = [&](int i) {
         dma_wait();
-        if (partly(next)) {
+        if (!tile_all.has(xn)) {
             FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
             const bool bq = dma.clean(buf, tid), bg = dma.clean(buf + BQ * Tl::kPitch, tid);
             if (bq || bg) bad = 1;
@@ -965,14 +1019,20 @@ void attention_dkv_kernel(AttnArgs a) {
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
     if (n > 0) {
+        if constexpr (kVLds)
+        {
+            const Dma<T, DP, 128> dma_v(a.D, tid);
+            dma_v.load((const T*)a.v.data + (t.k0 + t.row0) * a.v.row + t.hk * a.v.head,
+                       dma_v.offset(a.v.row), a.v.row, t.rows, lds + kV, wave);
+        }
         load(0);
         arrive(0);
     }
     __syncthreads();
     for (int i = 0; i < n; ++i) {
-        cur = next;
+        const int x0 = xn;
         if (i + 1 < n) load(i + 1);
-        const int view = wave * 32 < t.rows ? view_of(cur, wave * 32) : 0;
+        const int view = !wave_live ? 0 : wave_all.has(x0) ? 2 : wave_any.has(x0);
         if (view != 0) {
             const FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
             const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
@@ -982,9 +1042,12 @@ void attention_dkv_kernel(AttnArgs a) {
 #pragma unroll
                 for (int st = 0; st < STEPS; ++st) {
                     x = Elem<T>::mma(Tl::row_frag(qbuf, b * 32 + (lane & 31), st, half), kf[st], x);
-                    y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), vf[st], y);
+                    Frag v = vf[st];
+                    if constexpr (kVLds)
+                        v = Tl::row_frag(lds + kV, wave * 32 + (lane & 31), st, half);
+                    y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), v, y);
                 }
-                float w[16], ds[16];
+                f32x16 w, ds;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int at = b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
@@ -992,21 +1055,17 @@ void attention_dkv_kernel(AttnArgs a) {
                     ds[e] = w[e] * (y[e] - stat[i & 1][1][at]);
                 }
                 if (view == 1) {
-                    // this lane's rows, from the block's start, cut to it
-                    const int64_t at = (int64_t)i * BQ + b * 32 + half * 4;
-                    const int s0 = (int)(see0 - at < -64 ? -64 : see0 - at > 64 ? 64 : see0 - at);
-                    const int s1 = (int)(see1 - at < -64 ? -64 : see1 - at > 64 ? 64 : see1 - at);
-                    const uint32_t span = s1 > s0 ? s1 - s0 : 0;
+                    const int at = x0 + b * 32 + half * 4 - e0;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const bool hide = (uint32_t)((e >> 2) * 8 + (e & 3) - s0) >= span;
+                        const bool hide = (uint32_t)(at + (e >> 2) * 8 + (e & 3)) > e_span;
                         w[e] = hide ? 0.0f : w[e];
                         ds[e] = hide ? 0.0f : ds[e];
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const Frag fw = to_frag<T>(w + k * 8), fs = to_frag<T>(ds + k * 8);
+                    const Frag fw = to_frag<T>(w, k), fs = to_frag<T>(ds, k);
 #pragma unroll
                     for (int db = 0; db < DB; ++db) {
                         dv[db] =
@@ -1021,11 +1080,11 @@ void attention_dkv_kernel(AttnArgs a) {
         __syncthreads();
     }
     if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks) {
-        const int64_t past = (int64_t)(t.tq - 1 - last_by_window(a, t.tq, t.tk)) * G;
-        const int chunks = (int)((past + a.sink_chunk - 1) / a.sink_chunk);
+        const int past = t.tq - 1 - last_by_window(a, t.tq, t.tk);
+        const int chunks = (past + a.sink_chunk - 1) / a.sink_chunk;
         if (chunks > 0) {
             const bool mine = live && r < a.sinks;
-            const int64_t first = sink_slot(a, t.b, G);
+            const int64_t first = sink_slot(a, t.b);
             const int64_t step = (int64_t)a.Hk * 2 * a.sinks * a.D;
             const float* part = a.sink_part + (first * a.Hk + t.hk) * 2 * a.sinks * a.D +
                                 (mine ? r : 0) * a.D;
@@ -1061,18 +1120,22 @@ void attention_dkv_kernel(AttnArgs a) {
     store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane);
     if (bad) {
         __syncthreads();
-        if (live && half == 0)
+        if (live && half == 0 && e1 >= e0)
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                const int64_t x0 = (int64_t)i * BQ;
-                if (!partly(Place{(int)(x0 / G), (int)(x0 % G), rows_of(i)})) continue;
+            for (int g = 0; g < G; ++g)
 #pragma unroll 1
-                for (int64_t x = x0 > see0 ? x0 : see0; x < x0 + BQ && x < see1; ++x) {
-                    const int64_t qi = x / G, g = x - qi * G;
-                    add_bad(ok, qb + qi * a.q.row + g * a.q.head, a.D);
-                    add_bad(ov, gb + qi * a.grad_out.row + g * a.grad_out.head, a.D);
+                for (int x = i0; x <= i1; x += BQ) {
+                    if (tile_all.has(x)) continue;
+#pragma unroll 1
+                    for (int i = x > e0 ? x : e0; i < x + BQ && i <= e1; ++i) {
+                        const int64_t row = t.q0 + i, h = t.hk * G + g;
+                        add_bad(ok, (const T*)a.q.data + row * a.q.row + h * a.q.head, a.D);
+                        add_bad(ov,
+                                (const T*)a.grad_out.data + row * a.grad_out.row +
+                                    h * a.grad_out.head,
+                                a.D);
+                    }
                 }
-            }
     }
 }
 
@@ -1137,7 +1200,7 @@ static hipError_t backward(const AttnArgs& a, hipStream_t s) {
             attention_dq_kernel<T, 128, k16 ? 64 : 32><<<q, 256, 0, s>>>(a);
     }
     if (a.sink_part && a.qs.rows > 0) {
-        const dim3 c((unsigned)(row_slots(a.qs, a.H / a.Hk, a.sink_chunk) * a.Hk));
+        const dim3 c((unsigned)(row_slots(a.qs, 1, a.sink_chunk) * a.Hk));
         if (a.D <= 64)
             attention_sink_kernel<T, 64><<<c, 256, 0, s>>>(a);
         else

@@ -149,13 +149,12 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
         a.delta = (float*)(at + align256(rows * sizeof(float)));
         const size_t stat = 2 * align256(rows * sizeof(float));
         if (a.left < 0 || a.sinks == 0) return stat;
-        // about 512 workgroups of sink rows, of 1024 rows or more
-        const int G = a.H / a.Hk;
-        int64_t chunk = (int64_t)rows / 512;
-        chunk = chunk < 1024 ? 1024 : (chunk + 127) / 128 * 128;
+        // about 512 workgroups of queries past the sinks, of 256 queries or more
+        int64_t chunk = qs->num_rows * a.Hk / 512;
+        chunk = chunk < 256 ? 256 : (chunk + 127) / 128 * 128;
         a.sink_chunk = (int32_t)chunk;
         a.sink_part = (float*)(at + stat);
-        return stat + align256((size_t)row_slots(a.qs, G, a.sink_chunk) * a.Hk * 2 * a.sinks *
+        return stat + align256((size_t)row_slots(a.qs, 1, a.sink_chunk) * a.Hk * 2 * a.sinks *
                                a.D * sizeof(float));
     }
     plan = plan_attention(a, likely_len(qs), likely_len(ks));

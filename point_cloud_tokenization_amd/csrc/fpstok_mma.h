@@ -59,21 +59,25 @@ struct Elem<float> {
     }
 };
 
-// Eight float32 registers of a result, rounded to the type, as the operand of
+// Registers 8 k .. 8 k + 7 of a result, rounded to the type, as the operand of
 // the next product (folded order).
 template <class T>
-__device__ __forceinline__ typename Elem<T>::Frag to_frag(const float* x) {
+__device__ __forceinline__ typename Elem<T>::Frag to_frag(const f32x16& x, int k) {
     using f32x8 = float __attribute__((ext_vector_type(8)));
-    f32x8 v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = x[j];
+    const f32x8 v = k ? __builtin_shufflevector(x, x, 8, 9, 10, 11, 12, 13, 14, 15)
+                      : __builtin_shufflevector(x, x, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_convertvector(v, typename Elem<T>::Frag);
 }
 
-// A tile of rows of DP elements in LDS, in 16-byte chunks.  Chunk c of a row
-// is stored at place c ^ swz(row): reading one chunk of 8 adjacent rows, and
-// the 32 bytes of 4 adjacent rows that one transposing read of 16 lanes
-// takes, then falls on different banks.
+// A tile of rows of DP elements in LDS, in 16-byte chunks; chunk c of a row is
+// stored at place c ^ swz(row).  LDS has 64 banks of 4 bytes, 16 chunks wide;
+// the swizzle spreads over them
+//   the same chunk of the 16 rows that a 16-byte read takes at a time (lanes
+//   0-3, 12-15 and 20-27, or 4-11, 16-19 and 28-31 of a half wave: measured);
+//   the 64 bytes of 4 adjacent rows that a transposing read takes at a time,
+//   or, of float32, the 128 bytes of the rows r and r + 4.
+// It is linear: swz(x ^ y) = swz(x) ^ swz(y).  (A swizzle over 8 rows only
+// measured a conflict on every read, half of all LDS cycles.)
 template <class T, int DP>
 struct Tile {
     static constexpr int kElems = 16 / (int)sizeof(T);  // per chunk
@@ -81,8 +85,12 @@ struct Tile {
     static constexpr int kPitch = DP * (int)sizeof(T);  // bytes
     using Frag = typename Elem<T>::Frag;
 
-    static __device__ __forceinline__ int swz(int row) {
-        return ((row & 3) << 1) | ((row >> 2) & 1);
+    static __device__ __forceinline__ constexpr int swz(int row) {
+        const int x = (row >> 3) & 1;
+        if constexpr (sizeof(T) == 4) return ((row & 4) << 1) | ((row & 3) << 1) | x;
+        // two rows of 128 bytes fill the banks: their parity is in the address
+        if constexpr (kPitch == 128) return ((row & 2) << 1) | ((row & 4) >> 1) | x;
+        return ((row & 3) << 2) | ((row & 4) >> 1) | x;
     }
     static __device__ __forceinline__ int place(int row, int chunk) {
         return row * kPitch + ((chunk ^ swz(row)) << 4);
@@ -112,10 +120,11 @@ struct Tile {
             using s4 = short __attribute__((ext_vector_type(4)));
             const int i = lane & 15, r = ((lane >> 5) << 2) + (i >> 2);
             const int c = db * 4 + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
-            const FPSTOK_LDS char* p = t + row0 * kPitch + place(r, c) + (i & 1) * 8;
-            const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FPSTOK_LDS s4*)p);
+            const int low = (i & 1) * 8;
+            const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (FPSTOK_LDS s4*)(t + (row0 * kPitch + place(r, c ^ swz(row0)) + low)));
             const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (FPSTOK_LDS s4*)(p + 8 * kPitch));
+                (FPSTOK_LDS s4*)(t + ((row0 + 8) * kPitch + place(r, c ^ swz(row0 + 8)) + low)));
             return __builtin_bit_cast(Frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             const int d = db * 32 + (lane & 31), h4 = (lane >> 5) << 2;
@@ -123,8 +132,7 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int r = (j >> 2) * 8 + h4 + (j & 3);
-                f[j] = *(const FPSTOK_LDS float*)(t + row0 * kPitch + place(r, d >> 2) +
-                                                 (d & 3) * 4);
+                f[j] = *(const FPSTOK_LDS float*)(t + place(row0 + r, d >> 2) + (d & 3) * 4);
             }
             return f;
         }
@@ -157,13 +165,6 @@ __device__ __forceinline__ u32x4 chunk_clean(u32x4 x) {
     return x;
 }
 
-// n / G for 0 <= n < 2^17, G <= 2^16, over_g = 1.0f / G: n + 1/2 lies at least
-// 1 / (2 G) from a multiple of G in units of G, and the product is off by less
-// than n / G * 2^-22 <= 2^-5 / G.
-__device__ __forceinline__ int group_div(int n, float over_g) {
-    return (int)(((float)n + 0.5f) * over_g);
-}
-
 // Rows of a tile on their way from memory to LDS, by THREADS threads: load()
 // issues the loads, store() writes them.  Rows at or past `rows` and elements
 // at or past D become zero: their lanes load a place that exists instead (a
@@ -194,27 +195,6 @@ struct Stage {
             for (int i = 0; i < kPer; ++i) {
                 const int r = i * kStep + row(tid);
                 x[i] = *(const u32x4*)(base + (r < rows ? r : rows - 1) * stride + c);
-            }
-        }
-    }
-    // Rows query * G + head of a group of heads: row i of the tile belongs to
-    // query (g0 + i) / G past `base`, whose head `(g0 + i) % G` starts `head`
-    // elements further each.  g0 < G; over_g = 1 / G.
-    __device__ __forceinline__ void load_group(const T* base, int64_t stride, int64_t head, int g0,
-                                               int G, float over_g, int rows, int D, int tid) {
-        const int c = chunk(tid) * Tl::kElems < D ? chunk(tid) * Tl::kElems : 0;
-        have = rows;
-        if (G == 1 && rows >= ROWS) {
-            const T* p = base + row(tid) * stride + c;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = *(const u32x4*)(p + i * (kStep * stride));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int r = i * kStep + row(tid);
-                const int n = g0 + (r < rows ? r : rows - 1);
-                const int q = group_div(n, over_g);
-                x[i] = *(const u32x4*)(base + q * stride + (n - q * G) * head + c);
             }
         }
     }
@@ -253,12 +233,6 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
                  : "s"(lds), "v"(off), "s"(base)
                  : "memory");
 }
-__device__ __forceinline__ void dma16(const void* addr, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :
-                 : "s"(lds), "v"(addr)
-                 : "memory");
-}
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  :
@@ -278,51 +252,42 @@ struct Dma {
     static constexpr int kPer = ROWS * Tl::kChunks / 256;
     static constexpr int kStep = 256 / Tl::kChunks;  // rows between a thread's chunks
     static constexpr int kBytes = ROWS * Tl::kPitch;
-    static_assert(ROWS * Tl::kChunks % 256 == 0 && kStep % 8 == 0, "whole chunks, one swizzle");
-    int row, col;   // this thread's first row and its element in it
-    bool loads;
-    __device__ __forceinline__ Dma(int D, int tid) {
+    static_assert(ROWS * Tl::kChunks % 256 == 0, "whole chunks per thread");
+    int row, chunk;  // this thread's first row and the chunk it loads of it
+    int D;
+    __device__ __forceinline__ Dma(int D, int tid) : D(D) {
         row = tid / Tl::kChunks;
-        col = ((tid % Tl::kChunks) ^ Tl::swz(row)) * Tl::kElems;
-        loads = col < D;
+        chunk = (tid % Tl::kChunks) ^ Tl::swz(row);
+    }
+    // First element of the chunk this thread loads of row i * kStep + row.
+    __device__ __forceinline__ int col(int i) const {
+        return (chunk ^ Tl::swz(i * kStep)) * Tl::kElems;
     }
     static __device__ __forceinline__ void zero(FPSTOK_LDS char* buf, int bytes, int tid) {
         for (int i = tid * 16; i < bytes; i += 256 * 16) *(FPSTOK_LDS u32x4*)(buf + i) = 0;
     }
-    __device__ __forceinline__ void load(const T* base, int64_t stride, int rows,
+    // This thread's byte offset from a tile's first row, for load().
+    __device__ __forceinline__ uint32_t offset(int64_t stride) const {
+        return (uint32_t)(row * (int)stride + col(0)) * (uint32_t)sizeof(T);
+    }
+    __device__ __forceinline__ void load(const T* base, uint32_t offset, int64_t stride, int rows,
                                          FPSTOK_LDS char* buf, int wave) const {
         const uint32_t lds = (uint32_t)(uintptr_t)buf + wave * 1024;
-        if (!loads) return;
-        if (rows >= ROWS) {
-            const uint32_t off = (uint32_t)(row * (int)stride + col) * (uint32_t)sizeof(T);
+        if (rows >= ROWS && Tl::swz(kStep) == 0) {
+            if (col(0) < D) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) dma16(base + i * (kStep * stride), off, lds + i * 4096);
+                for (int i = 0; i < kPer; ++i)
+                    dma16(base, offset + (uint32_t)(i * kStep * (int)stride) * (uint32_t)sizeof(T),
+                          lds + i * 4096);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int r = i * kStep + row < rows ? i * kStep + row : rows - 1;
-                const uint32_t off = (uint32_t)(r * (int)stride + col) * (uint32_t)sizeof(T);
-                dma16(base, off, lds + i * 4096);
+                if (col(i) < D)
+                    dma16(base, (uint32_t)(r * (int)stride + col(i)) * (uint32_t)sizeof(T),
+                          lds + i * 4096);
             }
-        }
-    }
-    // Rows query * G + head of a group of heads: row i of the tile is head
-    // (g0 + i) % G of query (g0 + i) / G past `base`.  g0 < G; over_g = 1 / G.
-    __device__ __forceinline__ void load_group(const T* base, int64_t stride, int64_t head, int g0,
-                                               int G, float over_g, int rows, FPSTOK_LDS char* buf,
-                                               int wave) const {
-        if (G == 1) {
-            load(base, stride, rows, buf, wave);
-            return;
-        }
-        const uint32_t lds = (uint32_t)(uintptr_t)buf + wave * 1024;
-        if (!loads) return;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int r = i * kStep + row;
-            const int n = g0 + (r < rows ? r : rows - 1);
-            const int q = group_div(n, over_g);
-            dma16(base + q * stride + (n - q * G) * head + col, lds + i * 4096);
         }
     }
     // After dma_wait: infinite and not-a-number elements of the chunks this
