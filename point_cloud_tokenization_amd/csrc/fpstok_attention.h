@@ -33,6 +33,8 @@ struct AttnArgs {
     float* lse2;   // [H][q rows] log2(e) lse (backward)
     float* delta;  // the same shape: sum of grad_out * out
     int32_t H, Hk, D, dtype;
+    int32_t G, g_shift;  // H / Hk; its logarithm if it is a power of two, else -1
+    int32_t same_seqs;   // ks is qs
     int32_t left, right, sinks;
     float scale;
     // keys of a row split over `splits` workgroups (forward): their partial
@@ -41,9 +43,9 @@ struct AttnArgs {
     float* part;
     float2* part_ml;
     // rows that see a sequence's sinks from behind its first key tile's window
-    // (backward): walked in chunks of sink_chunk queries, whose parts of the
+    // (backward): walked in chunks of 2^sink_shift queries, whose parts of the
     // sinks' gradients are [slots][Hk][2][sinks][D] (grad_k, grad_v)
-    int32_t sink_chunk;
+    int32_t sink_shift;
     float* sink_part;
 };
 
@@ -63,8 +65,8 @@ struct RopeArgs {
     int32_t first_pair[kMaxAxes + 1];  // pairs of axis a: first_pair[a] .. first_pair[a+1]-1
 };
 
-// Chunks of `chunk` rows that cover every sequence (their numbering: find_seq).
-int64_t row_slots(const SeqArgs& s, int G, int chunk);
+// Slots of 2^shift rows that cover every sequence (their numbering: slot_of).
+int64_t row_slots(const SeqArgs& s, int G, int shift);
 AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);

@@ -19,33 +19,38 @@ struct RowTile {
 
 // Decodes a workgroup's place in the grid: heads fastest, so that with 8 key
 // heads (or a multiple) a head's tiles stay on one of the 8 XCDs and share its
-// L2.  Later tiles first where the mask is causal: they see more keys.
-template <int BM>
-__device__ __forceinline__ bool row_tile(const AttnArgs& a, const SeqArgs& s, int64_t block, int G,
-                                         RowTile& t) {
-    t.hk = (int)(block % a.Hk);
-    const int64_t slot = block / a.Hk;
-    int b;
-    int64_t tile;
+// L2.
+// KEYS: the tile is of keys (G = 1), not of rows of queries.
+template <int SHIFT, bool KEYS>
+__device__ __forceinline__ bool row_tile(const AttnArgs& a, uint32_t block, RowTile& t) {
+    const SeqArgs& s = KEYS ? a.ks : a.qs;
+    const int G = KEYS ? 1 : a.G;
+    t.hk = (int)(block % (uint32_t)a.Hk);
+    const uint32_t slot = block / (uint32_t)a.Hk;
+    int64_t start, tile;
+    int len;
     if (s.cu) {
-        b = find_seq(s, slot, G, BM);
-        tile = slot - first_slot(s, b, G, BM);
+        t.b = find_seq(s, slot, G, SHIFT, start, len, tile);
         if (tile < 0) return false;
     } else {
-        const int per = (int)(((int64_t)s.cap * G + BM - 1) / BM);
-        b = (int)(slot / per);
+        const uint32_t per = (uint32_t)(((int64_t)s.cap * G + (1 << SHIFT) - 1) >> SHIFT);
+        t.b = (int)(slot / per);
         tile = slot % per;
+        seq_rows(s, t.b, start, len);
     }
-    seq_rows(a.qs, b, t.q0, t.tq);
-    seq_rows(a.ks, b, t.k0, t.tk);
-    const int len = &s == &a.qs ? t.tq : t.tk;
-    const int64_t left = (int64_t)len * G - tile * BM;
+    const int64_t left = (int64_t)len * G - (tile << SHIFT);
     if (s.cu && left <= 0) return false;
-    const int64_t pad = s.cu ? 0 : (int64_t)s.cap * G - tile * BM;
-    t.b = b;
-    t.row0 = (int)(tile * BM);
-    t.rows = left < 0 ? 0 : left < BM ? (int)left : BM;
-    t.pad = pad < BM ? (int)pad : BM;
+    const int64_t pad = s.cu ? 0 : (int64_t)s.cap * G - (tile << SHIFT);
+    int64_t start2 = start;
+    int len2 = len;
+    if (!a.same_seqs) seq_rows(KEYS ? a.qs : a.ks, t.b, start2, len2);
+    t.q0 = KEYS ? start2 : start;
+    t.tq = KEYS ? len2 : len;
+    t.k0 = KEYS ? start : start2;
+    t.tk = KEYS ? len : len2;
+    t.row0 = (int)(tile << SHIFT);
+    t.rows = left < 0 ? 0 : left < (1 << SHIFT) ? (int)left : 1 << SHIFT;
+    t.pad = pad < (1 << SHIFT) ? (int)pad : 1 << SHIFT;
     return true;
 }
 
@@ -161,6 +166,28 @@ __device__ __forceinline__ void add_bad(TO* dst, const T* src, int D) {
     }
 }
 
+// Row `p` of D elements as operands of STEPS product steps, zero where it is
+// not `live` (its lanes load `any`, a row that exists: loads under a divergent
+// branch would be waited for one by one).
+template <class T, int STEPS>
+__device__ __forceinline__ void load_row(typename Elem<T>::Frag* f, const T* p, bool live,
+                                         const T* any, int D, int half) {
+    using Frag = typename Elem<T>::Frag;
+    p = live ? p : any;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int d = s * 16 + half * 8;
+        f[s] = *(const Frag*)(p + (d < D ? d : 0));
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const bool has = live && s * 16 + half * 8 < D;
+        u32x4* x = (u32x4*)&f[s];
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(Frag) / 16; ++e) x[e] = has ? x[e] : 0;
+    }
+}
+
 // The rows of one workgroup, its waves and its lanes (32 rows per wave across
 // the lanes, both halves of a wave the same 32), and their places among the
 // keys.  `first_row`: the first row of this wave's 32 in the tile.
@@ -168,31 +195,31 @@ struct QueryRows {
     int r, qi, h, pa, pb, wa, wb;
     int64_t row;
     bool live;
-    __device__ __forceinline__ QueryRows(const RowTile& t, int G, int first_row, int lane) {
+    __device__ __forceinline__ QueryRows(const AttnArgs& a, const RowTile& t, int first_row,
+                                         int lane) {
+        const int G = a.G;
+        // row / G: a shift where the group is a power of two
+        auto query = [&](int row) {
+            return a.g_shift >= 0 ? row >> a.g_shift : (int)((uint32_t)row / (uint32_t)G);
+        };
         r = first_row + (lane & 31);
-        qi = (t.row0 + r) / G;
+        qi = query(t.row0 + r);
         h = t.hk * G + (t.row0 + r) - qi * G;
         live = r < t.rows;
         row = t.q0 + qi;
         const int off = t.tk - t.tq, last = t.rows > 0 ? t.rows - 1 : 0;
         const int wl = first_row + 31 < last ? first_row + 31 : last;
-        pa = t.row0 / G + off;
-        pb = (t.row0 + last) / G + off;
-        wa = (t.row0 + first_row) / G + off;
-        wb = (t.row0 + wl) / G + off;
+        pa = query(t.row0) + off;
+        pb = query(t.row0 + last) + off;
+        wa = query(t.row0 + first_row) + off;
+        wb = query(t.row0 + wl) + off;
     }
     // This lane's row of a view, as operands of STEPS product steps.
     template <class T, int STEPS>
     __device__ __forceinline__ void load(typename Elem<T>::Frag* f, const HeadsArg& v, int D,
                                          int half) const {
-        const T* p = (const T*)v.data + row * v.row + h * v.head;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int d = s * 16 + half * 8;
-            typename Elem<T>::Frag x = {};
-            if (live && d < D) x = *(const typename Elem<T>::Frag*)(p + d);
-            f[s] = x;
-        }
+        load_row<T, STEPS>(f, (const T*)v.data + row * v.row + h * v.head, live, (const T*)v.data,
+                           D, half);
     }
 };
 
@@ -283,10 +310,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int G = a.H / a.Hk;
+    const int G = a.G;
     RowTile t;
-    if (!row_tile<128>(a, a.qs, blockIdx.x, G, t)) return;
-    const QueryRows q(t, G, wave * 32, lane);
+    if (!row_tile<7, false>(a, blockIdx.x, t)) return;
+    const QueryRows q(a, t, wave * 32, lane);
     Frag qf[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
@@ -412,10 +439,10 @@ void attention_few_kernel(AttnArgs a) {
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int G = a.H / a.Hk;
+    const int G = a.G;
     RowTile t;
-    if (!row_tile<BM>(a, a.qs, blockIdx.x, G, t)) return;
-    const QueryRows q(t, G, 0, lane);
+    if (!row_tile<5, false>(a, blockIdx.x, t)) return;
+    const QueryRows q(a, t, 0, lane);
     Frag qf[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
@@ -546,7 +573,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     __shared__ float wave_top[4], wave_sum[4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x / a.H;
-    const int h = (int)(blockIdx.x % a.H), G = a.H / a.Hk, hk = h / G;
+    const int h = (int)(blockIdx.x % a.H), G = a.G, hk = h / G;
     bool here = true;
     if (a.qs.cu) {
         if (row < cu_at(a.qs, 0) || row >= cu_at(a.qs, a.qs.B)) return;
@@ -615,34 +642,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int G = a.H / a.Hk;
     RowTile t;
-    if (!row_tile<128>(a, a.qs, blockIdx.x, G, t)) return;
-    const QueryRows q(t, G, wave * 32, lane);
+    if (!row_tile<7, false>(a, blockIdx.x, t)) return;
+    const QueryRows q(a, t, wave * 32, lane);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
-    Frag qf[STEPS], gf[STEPS];
-    float delta = 0.0f, lse2 = 0.0f;
-    {
-        Frag of[STEPS];
-        q.load<T, STEPS>(qf, a.q, a.D, half);
-        q.load<T, STEPS>(gf, a.grad_out, a.D, half);
-        q.load<T, STEPS>(of, a.out, a.D, half);
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                delta = __builtin_fmaf((float)gf[s][e], (float)of[s][e], delta);
-        delta = pair_sum(delta);
-        if (q.live) {
-            // a row that sees nothing: every weight is masked, the value
-            // only has to be finite
-            const float v = a.lse[q.row * a.H + q.h];
-            lse2 = v == -INFINITY ? 0.0f : v * kLog2e;
-            const int64_t at = (int64_t)q.h * a.qs.rows + q.row;
-            if (half == 0) a.lse2[at] = lse2, a.delta[at] = delta;
-        }
-    }
+    Frag qf[STEPS], gf[STEPS], of[STEPS];
+    q.load<T, STEPS>(qf, a.q, a.D, half);
+    q.load<T, STEPS>(gf, a.grad_out, a.D, half);
+    q.load<T, STEPS>(of, a.out, a.D, half);
+    const float lse = q.live ? a.lse[q.row * a.H + q.h] : 0.0f;
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
     const int n = t.rows > 0 ? kt.count : 0;
@@ -678,10 +687,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     if (tid == 0) bad = 0;
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
-    if (n > 0) {
-        load(0);
-        arrive(0);
+    if (n > 0) load(0);
+    float delta = 0.0f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)gf[s][e], (float)of[s][e], delta);
+    delta = pair_sum(delta);
+    // a row that sees nothing: every weight is masked, the value only has to
+    // be finite
+    const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+    if (q.live && half == 0) {
+        const int64_t at = (int64_t)q.h * a.qs.rows + q.row;
+        a.lse2[at] = lse2;
+        a.delta[at] = delta;
     }
+    if (n > 0) arrive(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
@@ -736,12 +757,6 @@ __device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk)
     return i1 < -1 ? -1 : i1 < tq - 1 ? i1 : tq - 1;
 }
 
-// First sink chunk of sequence b in the numbering of its parts.
-__device__ __forceinline__ int64_t sink_slot(const AttnArgs& a, int b) {
-    if (a.qs.cu) return first_slot(a.qs, b, 1, a.sink_chunk);
-    return (int64_t)b * ((a.qs.cap + a.sink_chunk - 1) / a.sink_chunk);
-}
-
 // The sinks' gradients from the rows that see nothing else of the first key
 // tile: in a long sequence that is nearly every row, and one workgroup walking
 // them all would take longer than everything else.  A workgroup takes a chunk
@@ -762,20 +777,25 @@ void attention_sink_kernel(AttnArgs a) {
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int G = a.H / a.Hk, hk = (int)(blockIdx.x % a.Hk);
-    const int64_t slot = blockIdx.x / a.Hk;
-    const int per = (a.qs.cap + a.sink_chunk - 1) / a.sink_chunk;
-    const int b = a.qs.cu ? find_seq(a.qs, slot, 1, a.sink_chunk) : (int)(slot / per);
-    const int64_t c = slot - sink_slot(a, b);
-    int64_t q0, k0;
-    int tq, tk;
-    seq_rows(a.qs, b, q0, tq);
+    const int G = a.G, hk = (int)(blockIdx.x % (uint32_t)a.Hk);
+    const uint32_t slot = blockIdx.x / (uint32_t)a.Hk;
+    const int chunk = 1 << a.sink_shift;
+    int64_t q0, k0, c;
+    int tq, tk, b;
+    if (a.qs.cu) {
+        b = find_seq(a.qs, slot, 1, a.sink_shift, q0, tq, c);
+    } else {
+        const uint32_t per = (uint32_t)((a.qs.cap + chunk - 1) >> a.sink_shift);
+        b = (int)(slot / per);
+        c = slot % per;
+        seq_rows(a.qs, b, q0, tq);
+    }
     seq_rows(a.ks, b, k0, tk);
     if (c < 0 || tq == 0 || tk == 0) return;
     const int i0 = last_by_window(a, tq, tk) + 1;
-    const int64_t from = c * a.sink_chunk;
+    const int64_t from = c << a.sink_shift;
     if (from >= tq - i0) return;
-    const int left = tq - i0 - (int)from, rows = left < a.sink_chunk ? left : a.sink_chunk;
+    const int left = tq - i0 - (int)from, rows = left < chunk ? left : chunk;
     const int sinks = a.sinks < tk ? a.sinks : tk;
     // the chunk's first query, in head 0 of the group
     const int64_t row0 = q0 + i0 + from;
@@ -790,19 +810,10 @@ void attention_sink_kernel(AttnArgs a) {
         const int j = s0 + (lane & 31);
         const bool live = j < sinks;
         Frag kf[STEPS], vf[STEPS];
-        const T* k = (const T*)a.k.data + (k0 + j) * a.k.row + hk * a.k.head;
-        const T* v = (const T*)a.v.data + (k0 + j) * a.v.row + hk * a.v.head;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int d = s * 16 + half * 8;
-            Frag fk = {}, fv = {};
-            if (live && d < a.D) {
-                fk = *(const Frag*)(k + d);
-                fv = *(const Frag*)(v + d);
-            }
-            kf[s] = fk;
-            vf[s] = fv;
-        }
+        load_row<T, STEPS>(kf, (const T*)a.k.data + (k0 + j) * a.k.row + hk * a.k.head, live,
+                           (const T*)a.k.data, a.D, half);
+        load_row<T, STEPS>(vf, (const T*)a.v.data + (k0 + j) * a.v.row + hk * a.v.head, live,
+                           (const T*)a.v.data, a.D, half);
         f32x16 dk[DB], dv[DB];
 #pragma unroll
         for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
@@ -851,7 +862,7 @@ void attention_sink_kernel(AttnArgs a) {
             }
         }
         // the waves' results, added in order: [key][DP] floats in LDS
-        float* part = a.sink_part + ((slot * a.Hk + hk) * 2 * a.sinks + s0) * a.D;
+        float* part = a.sink_part + (((int64_t)slot * a.Hk + hk) * 2 * a.sinks + s0) * a.D;
         const int keys = sinks - s0 < 32 ? sinks - s0 : 32;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
@@ -904,29 +915,19 @@ void attention_dkv_kernel(AttnArgs a) {
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int G = a.H / a.Hk;
+    const int G = a.G;
     RowTile t;
-    if (!row_tile<128>(a, a.ks, blockIdx.x, 1, t)) return;
+    if (!row_tile<7, true>(a, blockIdx.x, t)) return;
 
     const int r = wave * 32 + (lane & 31);
     const bool live = r < t.rows;
     const int64_t krow = t.k0 + t.row0 + r;
     Frag kf[STEPS], vf[STEPS];
-    {
-        const T* k = (const T*)a.k.data + krow * a.k.row + t.hk * a.k.head;
-        const T* v = (const T*)a.v.data + krow * a.v.row + t.hk * a.v.head;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int d = s * 16 + half * 8;
-            Frag fk = {}, fv = {};
-            if (live && d < a.D) {
-                fk = *(const Frag*)(k + d);
-                fv = *(const Frag*)(v + d);
-            }
-            kf[s] = fk;
-            vf[s] = fv;
-        }
-    }
+    load_row<T, STEPS>(kf, (const T*)a.k.data + krow * a.k.row + t.hk * a.k.head, live,
+                       (const T*)a.k.data, a.D, half);
+    if constexpr (!kVLds)
+        load_row<T, STEPS>(vf, (const T*)a.v.data + krow * a.v.row + t.hk * a.v.head, live,
+                           (const T*)a.v.data, a.D, half);
     // queries i0 .. i1 see some key of the tile (of the rows past its window,
     // the tile with the sinks gets their gradients from the kernel above), e0 ..
     // e1 of them this lane's key
@@ -1042,9 +1043,11 @@ void attention_dkv_kernel(AttnArgs a) {
 #pragma unroll
                 for (int st = 0; st < STEPS; ++st) {
                     x = Elem<T>::mma(Tl::row_frag(qbuf, b * 32 + (lane & 31), st, half), kf[st], x);
-                    Frag v = vf[st];
+                    Frag v;
                     if constexpr (kVLds)
                         v = Tl::row_frag(lds + kV, wave * 32 + (lane & 31), st, half);
+                    else
+                        v = vf[st];
                     y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), v, y);
                 }
                 f32x16 w, ds;
@@ -1081,10 +1084,12 @@ void attention_dkv_kernel(AttnArgs a) {
     }
     if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks) {
         const int past = t.tq - 1 - last_by_window(a, t.tq, t.tk);
-        const int chunks = (past + a.sink_chunk - 1) / a.sink_chunk;
+        const int chunks = (past + (1 << a.sink_shift) - 1) >> a.sink_shift;
         if (chunks > 0) {
             const bool mine = live && r < a.sinks;
-            const int64_t first = sink_slot(a, t.b);
+            const int64_t first =
+                a.qs.cu ? slot_of(t.q0, t.b, 1, a.sink_shift)
+                        : (int64_t)t.b * ((a.qs.cap + (1 << a.sink_shift) - 1) >> a.sink_shift);
             const int64_t step = (int64_t)a.Hk * 2 * a.sinks * a.D;
             const float* part = a.sink_part + (first * a.Hk + t.hk) * 2 * a.sinks * a.D +
                                 (mine ? r : 0) * a.D;
@@ -1139,9 +1144,9 @@ void attention_dkv_kernel(AttnArgs a) {
     }
 }
 
-int64_t row_slots(const SeqArgs& s, int G, int chunk) {
-    if (s.cu) return s.rows * G / chunk + s.B;
-    return (int64_t)s.B * (((int64_t)s.cap * G + chunk - 1) / chunk);
+int64_t row_slots(const SeqArgs& s, int G, int shift) {
+    if (s.cu) return (s.rows * G >> shift) + s.B;
+    return (int64_t)s.B * (((int64_t)s.cap * G + (1 << shift) - 1) >> shift);
 }
 
 // Splits a row's keys until the grid has `want` workgroups, but not into
@@ -1157,11 +1162,10 @@ static int key_splits(const AttnArgs& a, int64_t blocks, int64_t q_len, int64_t 
 }
 
 AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
-    const int G = a.H / a.Hk;
+    const int G = a.G;
     AttnPlan p;
     p.few = (int64_t)q_len * G <= 32;
-    const int BM = p.few ? 32 : 128;
-    const int64_t blocks = row_slots(a.qs, G, BM) * a.Hk;
+    const int64_t blocks = row_slots(a.qs, G, p.few ? 5 : 7) * a.Hk;
     p.splits = p.few ? key_splits(a, blocks, q_len, k_len, 2048, 512)
                      : key_splits(a, blocks, 128 / G + 1, k_len, 512, 1024);
     return p;
@@ -1170,7 +1174,7 @@ AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
 template <class T>
 static hipError_t forward(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
-    const int64_t blocks = row_slots(a.qs, a.H / a.Hk, plan.few ? 32 : 128) * a.Hk;
+    const int64_t blocks = row_slots(a.qs, a.G, plan.few ? 5 : 7) * a.Hk;
     const dim3 grid((unsigned)blocks, (unsigned)a.splits);
     if (plan.few) {
         if (a.D <= 64)
@@ -1191,8 +1195,8 @@ static hipError_t forward(const AttnArgs& a, const AttnPlan& plan, hipStream_t s
 template <class T>
 static hipError_t backward(const AttnArgs& a, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
-    const dim3 q((unsigned)(row_slots(a.qs, a.H / a.Hk, 128) * a.Hk));
-    const dim3 k((unsigned)(row_slots(a.ks, 1, 128) * a.Hk));
+    const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
+    const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk));
     if (a.qs.rows > 0) {
         if (a.D <= 64)
             attention_dq_kernel<T, 64, 64><<<q, 256, 0, s>>>(a);
@@ -1200,7 +1204,7 @@ static hipError_t backward(const AttnArgs& a, hipStream_t s) {
             attention_dq_kernel<T, 128, k16 ? 64 : 32><<<q, 256, 0, s>>>(a);
     }
     if (a.sink_part && a.qs.rows > 0) {
-        const dim3 c((unsigned)(row_slots(a.qs, 1, a.sink_chunk) * a.Hk));
+        const dim3 c((unsigned)(row_slots(a.qs, 1, a.sink_shift) * a.Hk));
         if (a.D <= 64)
             attention_sink_kernel<T, 64><<<c, 256, 0, s>>>(a);
         else

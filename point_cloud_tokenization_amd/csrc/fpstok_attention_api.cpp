@@ -118,6 +118,9 @@ static AttnArgs attn_args(const fpstok_seqs* qs, const fpstok_seqs* ks,
     a.ks = seq_args(ks);
     a.H = p->num_heads;
     a.Hk = p->num_kv_heads;
+    a.G = a.H / a.Hk;
+    a.g_shift = (a.G & (a.G - 1)) == 0 ? __builtin_ctz((unsigned)a.G) : -1;
+    a.same_seqs = qs == ks;
     a.D = p->head_dim;
     a.dtype = p->dtype;
     // a window that reaches over every row hides nothing
@@ -150,11 +153,10 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
         const size_t stat = 2 * align256(rows * sizeof(float));
         if (a.left < 0 || a.sinks == 0) return stat;
         // about 512 workgroups of queries past the sinks, of 256 queries or more
-        int64_t chunk = qs->num_rows * a.Hk / 512;
-        chunk = chunk < 256 ? 256 : (chunk + 127) / 128 * 128;
-        a.sink_chunk = (int32_t)chunk;
+        a.sink_shift = 8;
+        while (qs->num_rows * a.Hk >> a.sink_shift > 512) ++a.sink_shift;
         a.sink_part = (float*)(at + stat);
-        return stat + align256((size_t)row_slots(a.qs, 1, a.sink_chunk) * a.Hk * 2 * a.sinks *
+        return stat + align256((size_t)row_slots(a.qs, 1, a.sink_shift) * a.Hk * 2 * a.sinks *
                                a.D * sizeof(float));
     }
     plan = plan_attention(a, likely_len(qs), likely_len(ks));

@@ -28,29 +28,44 @@ __device__ __forceinline__ void seq_rows(const SeqArgs& s, int b, int64_t& start
     }
 }
 
-// Largest b in [0, B) with floor(cu[b] * G / tile) + b <= t, by the whole wave:
-// each round tests 64 evenly spaced candidates at once.  In this numbering
-// sequence b owns the slots from floor(cu[b] * G / tile) + b on, and it needs
-// ceil(len * G / tile) of them, which end at or before the next sequence's
-// first, so a grid of floor(rows * G / tile) + B slots covers every batch
-// without knowing its lengths.  Every index stays in [0, B) for any cu.
-__device__ __forceinline__ int find_seq(const SeqArgs& s, int64_t t, int G, int tile) {
+// Packed sequences in slots of 2^shift rows, `G` rows per buffer row: sequence
+// b owns the slots from floor(cu[b] * G / 2^shift) + b on.  It needs
+// ceil(len * G / 2^shift) of them, which end at or before the next sequence's
+// first, so a grid of floor(rows * G / 2^shift) + B slots covers every batch
+// without knowing its lengths.
+__device__ __forceinline__ int64_t slot_of(int64_t cu, int b, int G, int shift) {
+    return (int64_t)((uint64_t)(cu * G) >> shift) + b;
+}
+
+// The sequence that owns `slot` (the largest b whose first slot is not past
+// it), its rows, and the slot's number within it (negative if it is none's),
+// by the whole wave: a round tests 64 evenly spaced candidates at once, and
+// the last has both ends of the sequence at hand.  Every index stays in
+// [0, B) whatever cu holds.
+__device__ __forceinline__ int find_seq(const SeqArgs& s, int64_t slot, int G, int shift,
+                                        int64_t& start, int& len, int64_t& at) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = s.B;
-    while (n > 1) {
+    while (n > 64) {
         const int step = (n + 63) >> 6;
         const int i = lane * step;
-        const bool in = i < n && (cu_at(s, lo + i) * G) / tile + lo + i <= t;
+        const bool in = i < n && slot_of(cu_at(s, lo + i), lo + i, G, shift) <= slot;
         const int hits = __popcll(__ballot(in));
         const int k = hits > 0 ? hits - 1 : 0;
         lo += k * step;
         n = n - k * step < step ? n - k * step : step;
     }
-    return __builtin_amdgcn_readfirstlane(lo);
-}
-
-__device__ __forceinline__ int64_t first_slot(const SeqArgs& s, int b, int G, int tile) {
-    return (cu_at(s, b) * G) / tile + b;
+    const int i = lo + (lane < n ? lane : n - 1);
+    const int64_t c0 = cu_at(s, i), c1 = cu_at(s, i + 1);
+    const int hits = __popcll(__ballot(lane < n && slot_of(c0, i, G, shift) <= slot));
+    const int k = hits > 0 ? hits - 1 : 0;
+    // rows fit in 31 bits
+    start = __builtin_amdgcn_readlane((int)c0, k);
+    const int64_t left = (int64_t)__builtin_amdgcn_readlane((int)c1, k) - start;
+    len = left > 0 ? (int)left : 0;
+    lo = __builtin_amdgcn_readfirstlane(lo + k);
+    at = slot - slot_of(start, lo, G, shift);
+    return lo;
 }
 
 }  // namespace fpstok
