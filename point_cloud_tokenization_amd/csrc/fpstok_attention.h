@@ -62,6 +62,7 @@ struct RopeArgs {
     const void* positions;
     const float* freqs;
     int32_t D, dtype, int_positions, axes, R, interleaved, inverse;
+    int32_t block_rows;  // rows per workgroup (set by the launch)
     int32_t first_pair[kMaxAxes + 1];  // pairs of axis a: first_pair[a] .. first_pair[a+1]-1
 };
 

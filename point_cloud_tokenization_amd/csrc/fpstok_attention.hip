@@ -301,7 +301,7 @@ __device__ __forceinline__ float log_sum(float mc, float l) {
 // its factor is one value per lane, and the weights, rounded to the type, are
 // already the operand of O^T += V^T P^T.
 template <class T, int DP, int BN>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void attention_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;

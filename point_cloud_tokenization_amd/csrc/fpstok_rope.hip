@@ -31,30 +31,37 @@ __device__ __forceinline__ void sincos_angle(double angle, float& sn, float& cs)
     cs = ((quad + 1) & 2) ? -b : b;
 }
 
+// Angle of pair p on a row, as the kernel's sine and cosine.
+__device__ __forceinline__ void row_sincos(const RopeArgs& a, int64_t row, int p, float& sn,
+                                           float& cs) {
+    int ax = 0;
+    while (p >= a.first_pair[ax + 1]) ++ax;
+    const int64_t at = row * a.axes + ax;
+    const double pos = a.int_positions ? (double)((const int32_t*)a.positions)[at]
+                                       : (double)((const float*)a.positions)[at];
+    sincos_angle(pos * (double)a.freqs[p], sn, cs);
+    if (a.inverse) sn = -sn;
+}
+
+// True if `row` is one of a sequence's; `skip`: it is not to be written.
+__device__ __forceinline__ bool row_here(const SeqArgs& s, int64_t row, int64_t end, bool& skip) {
+    skip = row >= end;
+    return !skip && (s.cu || row % s.cap < s.count[row / s.cap]);
+}
+
+// Any alignment: a thread per (row, element pair), head after head.
 template <class T>
-__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
+__global__ __launch_bounds__(256) void rope_pair_kernel(RopeArgs a) {
     const int half = a.D / 2;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row = t / half;
     const int p = (int)(t % half);
-    if (row >= a.seqs.rows) return;
-    bool pad = false;
-    if (a.seqs.cu) {
-        if (row >= cu_at(a.seqs, a.seqs.B)) return;
-    } else {
-        pad = row % a.seqs.cap >= a.seqs.count[row / a.seqs.cap];
-    }
+    bool skip;
+    const bool here = row_here(a.seqs, row, a.seqs.cu ? cu_at(a.seqs, a.seqs.B) : a.seqs.rows, skip);
+    if (skip) return;
     float sn = 0.0f, cs = 1.0f;
     const bool turn = p < a.R;
-    if (turn && !pad) {
-        int ax = 0;
-        while (p >= a.first_pair[ax + 1]) ++ax;
-        const int64_t at = row * a.axes + ax;
-        const double pos = a.int_positions ? (double)((const int32_t*)a.positions)[at]
-                                           : (double)((const float*)a.positions)[at];
-        sincos_angle(pos * (double)a.freqs[p], sn, cs);
-        if (a.inverse) sn = -sn;
-    }
+    if (turn && here) row_sincos(a, row, p, sn, cs);
     const int e1 = turn && !a.interleaved ? p : 2 * p;
     const int e2 = turn && !a.interleaved ? p + a.R : 2 * p + 1;
     for (int which = 0; which < 2; ++which) {
@@ -62,7 +69,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
         T* out = (T*)a.out[which].data + row * a.out[which].row;
         for (int h = 0; h < a.heads[which]; ++h) {
             float y1 = 0.0f, y2 = 0.0f;
-            if (!pad) {
+            if (here) {
                 const float x1 = (float)in[e1], x2 = (float)in[e2];
                 y1 = turn ? x1 * cs - x2 * sn : x1;
                 y2 = turn ? x1 * sn + x2 * cs : x2;
@@ -75,16 +82,135 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     }
 }
 
-hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
-    const int64_t threads = a.seqs.rows * (a.D / 2);
-    const dim3 grid((unsigned)((threads + 255) / 256));
-    if (a.dtype == 0)
-        rope_kernel<float><<<grid, 256, 0, s>>>(a);
-    else if (a.dtype == 1)
-        rope_kernel<_Float16><<<grid, 256, 0, s>>>(a);
+// Rows of heads aligned to 16 bytes.  A workgroup takes a.block_rows rows: their
+// sines and cosines are formed once, in LDS, for all heads of q and k; then a
+// thread turns 16 bytes (interleaved) or 16 bytes and their partners R
+// elements further (half), kItems of them on their way at a time, adjacent
+// threads adjacent in memory.
+template <class T, bool INTER>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
+    constexpr int V = 16 / (int)sizeof(T), kItems = 4;
+    using Vec = T __attribute__((ext_vector_type(V)));
+    extern __shared__ float2 table[];  // [row][pair] cosine, sine
+    const int R = a.R, tid = threadIdx.x;
+    const int64_t end = a.seqs.cu ? cu_at(a.seqs, a.seqs.B) : a.seqs.rows;
+    const int64_t row0 = (int64_t)blockIdx.x * a.block_rows;
+    const int rows = end - row0 < a.block_rows ? (int)(end - row0) : a.block_rows;
+    if (rows <= 0) return;
+    const int turned = INTER ? 2 * R / V : R / V;  // turned items of a head
+    const int per_head = turned + (a.D - 2 * R) / V, heads = a.heads[0] + a.heads[1];
+    const int per_row = per_head * heads, total = per_row * rows;
+    Vec x[kItems], y[kItems];
+    T* to[kItems];
+    int row[kItems], item[kItems];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (base - tid + i * 256 >= total) break;  // none of the workgroup's
+            const uint32_t n = base + i * 256 < total ? base + i * 256 : total - 1;
+            const uint32_t r = n / (uint32_t)per_row, m = n - r * per_row;
+            const uint32_t h = m / (uint32_t)per_head, u = m - h * per_head;
+            const bool k = (int)h >= a.heads[0];
+            const HeadsArg& in = a.in[k];
+            const HeadsArg& out = a.out[k];
+            const int64_t hh = (int)h - (k ? a.heads[0] : 0);
+            // first element: of the turned part, or of the rest of the head
+            const int e = (int)u < turned ? (int)u * V : 2 * R + ((int)u - turned) * V;
+            const T* from = (const T*)in.data + (row0 + r) * in.row + hh * in.head + e;
+            to[i] = (T*)out.data + (row0 + r) * out.row + hh * out.head + e;
+            row[i] = (int)r;
+            item[i] = (int)u;
+            x[i] = *(const Vec*)from;
+            // (the rest of a head has no partner: its own element again)
+            if constexpr (!INTER) y[i] = *(const Vec*)((int)u < turned ? from + R : from);
+        }
+    };
+    fetch(tid);
+    for (int n = tid; n < rows * R; n += 256) {
+        const int r = n / R;
+        float sn, cs;
+        row_sincos(a, row0 + r, n - r * R, sn, cs);
+        table[n] = make_float2(cs, sn);
+    }
+    __syncthreads();
+    for (int base = tid; base - tid < total; base += 256 * kItems) {
+        if (base != tid) fetch(base);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (base + i * 256 >= total) break;
+            bool skip;
+            const bool here = row_here(a.seqs, row0 + row[i], end, skip);
+            const bool turn = item[i] < turned;
+            if constexpr (INTER) {
+                if (turn) {
+                    const float2* cs = table + row[i] * R + item[i] * (V / 2);
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 c = cs[e / 2];
+                        const float x1 = (float)x[i][e], x2 = (float)x[i][e + 1];
+                        x[i][e] = (T)(x1 * c.x - x2 * c.y);
+                        x[i][e + 1] = (T)(x1 * c.y + x2 * c.x);
+                    }
+                }
+            } else {
+                if (turn) {
+                    const float2* cs = table + row[i] * R + item[i] * V;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float2 c = cs[e];
+                        const float x1 = (float)x[i][e], x2 = (float)y[i][e];
+                        x[i][e] = (T)(x1 * c.x - x2 * c.y);
+                        y[i][e] = (T)(x1 * c.y + x2 * c.x);
+                    }
+                    *(Vec*)(to[i] + R) = here ? y[i] : Vec{};
+                }
+            }
+            *(Vec*)to[i] = here ? x[i] : Vec{};
+        }
+    }
+}
+
+// 16-byte items need every head of every view, and the turned part of a head,
+// to start and end on 16 bytes.
+static bool by_16_bytes(const RopeArgs& a) {
+    const int w = a.dtype == 0 ? 4 : 2, V = 16 / w;
+    if ((a.interleaved ? 2 * a.R : a.R) % V != 0 || a.D % V != 0) return false;
+    for (int i = 0; i < 2; ++i) {
+        if (a.heads[i] == 0) continue;
+        for (const HeadsArg* v : {&a.in[i], &a.out[i]})
+            if ((uintptr_t)v->data % 16 != 0 || v->row * w % 16 != 0 || v->head * w % 16 != 0)
+                return false;
+    }
+    return true;
+}
+
+template <class T>
+static hipError_t rope(RopeArgs a, hipStream_t s) {
+    if (!by_16_bytes(a)) {
+        const int64_t threads = a.seqs.rows * (a.D / 2);
+        rope_pair_kernel<T><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    // as many rows per workgroup as leave 1024 workgroups (on 5,541 rows: 256
+    // workgroups 11.9 us, 512 10.7, 1024 9.8, 2048 9.8 to 10.7), at most 16,
+    // and a table of at most 32 KB
+    int64_t rows = a.seqs.rows / 1024;
+    if (rows > 16) rows = 16;
+    if (rows > 4096 / a.R) rows = 4096 / a.R;
+    a.block_rows = rows < 1 ? 1 : (int32_t)rows;
+    const dim3 grid((unsigned)((a.seqs.rows + a.block_rows - 1) / a.block_rows));
+    const size_t lds = (size_t)a.block_rows * a.R * sizeof(float2);
+    if (a.interleaved)
+        rope_kernel<T, true><<<grid, 256, lds, s>>>(a);
     else
-        rope_kernel<__bf16><<<grid, 256, 0, s>>>(a);
+        rope_kernel<T, false><<<grid, 256, lds, s>>>(a);
     return hipGetLastError();
+}
+
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
+    return a.dtype == 0   ? rope<float>(a, s)
+           : a.dtype == 1 ? rope<_Float16>(a, s)
+                          : rope<__bf16>(a, s);
 }
 
 }  // namespace fpstok
