@@ -1,4 +1,6 @@
 // Attention over the rows of variable-length sequences and its gradients.
+#include <type_traits>
+
 #include "fpstok_mma.h"
 #include "fpstok_seqs.h"
 
@@ -239,11 +241,22 @@ __device__ __forceinline__ void add_bad_keys(TO* dst, const AttnArgs& a, const K
     }
 }
 
+// A result's registers become zero in lanes where `keep` is false (what they
+// hold may not be finite); one test if there are none.
+template <int DB>
+__device__ __forceinline__ void zero_unless(f32x16* x, bool keep) {
+    if (__all(keep)) return;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[db][e] = keep ? x[db][e] : 0.0f;
+}
+
 // A row's running maximum (m, and mc = m * c as subtracted), sum and result.
 // The maximum a row subtracts is moved only when it grew by more than 2^8 (a
 // rescale costs as many multiplications as the result has registers); weights
 // stay below 2^8.
-template <class T, int DB, int KB>
+template <class T, int DB>
 struct Softmax {
     float m = -INFINITY, mc = 0.0f, l = 0.0f;
     f32x16 o[DB];
@@ -251,8 +264,9 @@ struct Softmax {
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[db] = 0.0f;
     }
-    // Takes the maximum of the scores s of KB * 32 keys (transposed, -infinity
+    // Takes the maximum of the scores s of 32 KB keys (transposed, -infinity
     // where hidden); result and sum are rescaled if it has grown.
+    template <int KB>
     __device__ __forceinline__ void grow(const f32x16 (&s)[KB], float c) {
         float mx = s[0][0];
 #pragma unroll
@@ -270,6 +284,7 @@ struct Softmax {
         }
     }
     // The scores become weights.
+    template <int KB>
     __device__ __forceinline__ void weights(f32x16 (&s)[KB], float c) {
 #pragma unroll
         for (int e = 0; e < KB * 16; ++e) {
@@ -278,16 +293,13 @@ struct Softmax {
             l += w;
         }
     }
-    // The sum over both halves; false (and a zero result) if no key was seen.
+    // The sum over both halves; false if no key was seen.
     __device__ __forceinline__ bool finish() {
         l = pair_sum(l);
-        const bool some = (m != -INFINITY) | (l != 0.0f);
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[db][e] = some ? o[db][e] : 0.0f;
-        return some;
+        return (m != -INFINITY) | (l != 0.0f);
     }
+    // The result becomes zero where `keep` is false; one test if none is.
+    __device__ __forceinline__ void only(bool keep) { zero_unless<DB>(o, keep); }
 };
 
 __device__ __forceinline__ float log_sum(float mc, float l) {
@@ -340,7 +352,8 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
         dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
         dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
     };
-    const View<BN> all(a, q.pa, q.pb, t.tk), mine(a, q.wa, q.wb, t.tk);
+    const View<BN> all(a, q.pa, q.pb, t.tk);
+    const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {  // this wave's part of it is there
         dma_wait();
         // a value that some row must not see meets a weight of 0 there: an
@@ -349,8 +362,36 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
             bad = 1;
     };
 
-    Softmax<T, DB, KB> sm;
+    Softmax<T, DB> sm;
     const float c = a.scale * kLog2e;
+    // 32 NB keys from row `from` of the tile at kbuf on (key j0 + from)
+    auto attend = [&](auto NB, const FPSTOK_LDS char* kbuf, int from, int j0, int v0, int v1) {
+        constexpr int kNB = decltype(NB)::value;
+        const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
+        kbuf += from * Tl::kPitch;
+        vbuf += from * Tl::kPitch;
+        f32x16 s[kNB];
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+            f32x16 x = 0.0f;
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st)
+                x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
+            s[b] = x;
+        }
+        // (v0: what the first block looks like, v1: the second)
+        if (v0 != 2) win.mask(s[0], j0 + from, half, a.sinks, -INFINITY);
+        if (kNB == 2 && v1 != 2) win.mask(s[kNB - 1], j0 + 32, half, a.sinks, -INFINITY);
+        sm.grow(s, c);
+        sm.weights(s, c);
+#pragma unroll
+        for (int k = 0; k < kNB * 2; ++k) {
+            const Frag pf = to_frag<T>(s[k >> 1], k & 1);
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+                sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
+        }
+    };
     if (tid == 0) bad = 0;
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
@@ -362,34 +403,16 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
         if (i + 1 < n) load(i + 1);
-        const int view = wave_live ? mine.of(a, j0) : 0;
-        if (view != 0) {
-            const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-            const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
-            f32x16 s[KB];
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                f32x16 x = 0.0f;
-#pragma unroll
-                for (int st = 0; st < STEPS; ++st)
-                    x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-                s[b] = x;
-            }
-            if (view == 1) {
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-                    win.mask(s[b], j0 + b * 32, half, a.sinks, -INFINITY);
-            }
-            sm.grow(s, c);
-            sm.weights(s, c);
-#pragma unroll
-            for (int k = 0; k < KB * 2; ++k) {
-                const Frag pf = to_frag<T>(s[k >> 1], k & 1);
-#pragma unroll
-                for (int db = 0; db < DB; ++db)
-                    sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
-            }
-        }
+        const int v0 = wave_live ? mine.of(a, j0) : 0;
+        const int v1 = KB == 2 && wave_live ? mine.of(a, j0 + 32) : 0;
+        const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
+        // a tile with one block of 32 keys in sight costs half; at DP = 128 the
+        // second copy of the code cost more than that (causal 16k 1.41 ms
+        // against 1.25)
+        if (KB == 2 && (DP == 128 ? (v0 | v1) != 0 : v0 != 0 && v1 != 0))
+            attend(std::integral_constant<int, KB>(), kbuf, 0, j0, v0, v1);
+        else if ((v0 | v1) != 0 && (KB == 1 || DP == 64))
+            attend(std::integral_constant<int, 1>(), kbuf, v0 != 0 ? 0 : 32, j0, v0 | v1, 0);
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
@@ -398,6 +421,7 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
         const int64_t at =
             ((int64_t)blockIdx.y * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + q.r;
         float* part = a.part + at * a.D;
+        sm.only(some);
         store_row<float, DB>(sm.o, 1.0f, q.live ? part : nullptr, a.D, lane);
         if (q.live && half == 0) a.part_ml[at] = make_float2(some ? sm.mc : -INFINITY, sm.l);
         if (bad) {
@@ -409,6 +433,7 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
     }
     const bool write = q.live || q.r < t.pad;
     T* out = (T*)a.out.data + q.row * a.out.row + q.h * a.out.head;
+    sm.only(q.live && some);
     store_row<T, DB>(sm.o, q.live && some ? 1.0f / sm.l : 0.0f, write ? out : nullptr, a.D, lane);
     if (a.lse && half == 0 && write)
         a.lse[q.row * a.H + q.h] = !q.live ? 0.0f : some ? log_sum(sm.mc, sm.l) : -INFINITY;
@@ -461,7 +486,7 @@ void attention_few_kernel(AttnArgs a) {
     };
 
     const View<BN> all(a, q.pa, q.pb, t.tk);
-    Softmax<T, DB, KB> sm;
+    Softmax<T, DB> sm;
     const float c = a.scale * kLog2e;
     if (wave < n) load(wave);
     if (tid == 0) bad = 0;
@@ -500,6 +525,7 @@ void attention_few_kernel(AttnArgs a) {
         }
     }
     const bool seen = sm.finish();
+    sm.only(seen);
     wave_sync();
     if (half == 0) ml[wave][q.r] = make_float2(seen ? sm.mc : -INFINITY, sm.l);
 #pragma unroll
@@ -674,7 +700,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
         dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
         dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
     };
-    const View<BN> all(a, q.pa, q.pb, t.tk), mine(a, q.wa, q.wb, t.tk);
+    const View<BN> all(a, q.pa, q.pb, t.tk);
+    const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {
         dma_wait();
         if (all.of(a, jn) == 1 && dma.clean(lds + (i & 1) * 2 * BN * Tl::kPitch, tid)) bad = 1;
@@ -684,11 +711,32 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
 #pragma unroll
     for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
     const float c = a.scale * kLog2e;
+    float delta = 0.0f, lse2 = 0.0f;
+    auto block = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask) {
+        const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
+        f32x16 x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
+            y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
+        }
+        f32x16 ds;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            ds[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2)) * (y[e] - delta);
+        if (mask) win.mask(ds, j0 + b * 32, half, a.sinks, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Frag f = to_frag<T>(ds, k);
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+                dq[db] = Elem<T>::mma(Tl::col_frag(kbuf, b * 32 + k * 16, db, lane), f, dq[db]);
+        }
+    };
     if (tid == 0) bad = 0;
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
     if (n > 0) load(0);
-    float delta = 0.0f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -696,7 +744,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     delta = pair_sum(delta);
     // a row that sees nothing: every weight is masked, the value only has to
     // be finite
-    const float lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+    lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
     if (q.live && half == 0) {
         const int64_t at = (int64_t)q.h * a.qs.rows + q.row;
         a.lse2[at] = lse2;
@@ -707,41 +755,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
         if (i + 1 < n) load(i + 1);
-        const int view = wave_live ? mine.of(a, j0) : 0;
-        if (view != 0) {
-            const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-            const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
+        const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                f32x16 x = 0.0f, y = 0.0f;
-#pragma unroll
-                for (int st = 0; st < STEPS; ++st) {
-                    x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-                    y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
-                }
-                f32x16 ds;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    ds[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2)) * (y[e] - delta);
-                if (view == 1) win.mask(ds, j0 + b * 32, half, a.sinks, 0.0f);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const Frag f = to_frag<T>(ds, k);
-#pragma unroll
-                    for (int db = 0; db < DB; ++db)
-                        dq[db] =
-                            Elem<T>::mma(Tl::col_frag(kbuf, b * 32 + k * 16, db, lane), f, dq[db]);
-                }
-            }
+        for (int b = 0; b < KB; ++b) {
+            const int view = wave_live ? mine.of(a, j0 + b * 32) : 0;
+            if (view != 0) block(kbuf, b, j0, view == 1);
         }
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
     T* out = (T*)a.grad_q.data + q.row * a.grad_q.row + q.h * a.grad_q.head;
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) dq[db][e] = q.live ? dq[db][e] : 0.0f;
+    zero_unless<DB>(dq, q.live);
     store_row<T, DB>(dq, a.scale, q.live || q.r < t.pad ? out : nullptr, a.D, lane);
     if (bad) {
         __syncthreads();
@@ -942,8 +966,9 @@ void attention_dkv_kernel(AttnArgs a) {
     if (e1 < e0) e0 = 0x7fffffff, e_span = 0;  // none: no query has that number
     const int nq = t.rows > 0 && i1 >= i0 ? i1 - i0 + 1 : 0;
     const int per = (nq + BQ - 1) / BQ, n = per * G;
-    // tiles of BQ queries from x on whose every row sees each of the keys j0 ..
-    // j1, and those where some row sees some: x - lo <= span
+    // `rows` (all_range) or 32 (any_range) queries from x on: x - lo <= span if
+    // each of them exists and sees each of the keys j0 .. j1, or if some may see
+    // some
     struct Range {
         int lo;
         uint32_t span;
@@ -952,21 +977,21 @@ void attention_dkv_kernel(AttnArgs a) {
         }
         __device__ __forceinline__ bool has(int x) const { return (uint32_t)(x - lo) <= span; }
     };
-    auto all_range = [&](int j0, int j1) {
+    auto all_range = [&](int j0, int j1, int rows) {
         const int lo = a.right >= 0 && j1 - a.right - off > 0 ? j1 - a.right - off : 0;
         int hi = i1;
         if (a.left >= 0 && j1 >= a.sinks && j0 + a.left - off < hi) hi = j0 + a.left - off;
-        return Range(lo, hi - (BQ - 1));
+        return Range(lo, hi - (rows - 1));
     };
     auto any_range = [&](int j0, int j1) {
-        const int lo = a.right >= 0 ? j0 - a.right - off - (BQ - 1) : 0;
+        const int lo = a.right >= 0 ? j0 - a.right - off - 31 : 0;
         int hi = i1;
         if (a.left >= 0 && j0 >= a.sinks && j1 + a.left - off < hi) hi = j1 + a.left - off;
         return Range(lo < 0 ? 0 : lo, hi);
     };
     const int wj0 = t.row0 + wave * 32, wj1 = wj0 + 31 < j_last ? wj0 + 31 : j_last;
-    const Range wave_all = all_range(wj0, wj1), wave_any = any_range(wj0, wj1);
-    const Range tile_all = all_range(t.row0, j_last);
+    const Range wave_all = all_range(wj0, wj1, 32), wave_any = any_range(wj0, wj1);
+    const Range tile_all = all_range(t.row0, j_last, BQ);
     const bool wave_live = wave * 32 < t.rows;
 
     const Dma<T, DP, BQ> dma(a.D, tid);
@@ -1016,6 +1041,46 @@ void attention_dkv_kernel(AttnArgs a) {
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
     const float c = a.scale * kLog2e;
+    auto block = [&](const FPSTOK_LDS char* qbuf, const float (*stat)[64], int b, int x0,
+                     bool mask) {
+        const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
+        f32x16 x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            Frag v;
+            if constexpr (kVLds)
+                v = Tl::row_frag(lds + kV, wave * 32 + (lane & 31), st, half);
+            else
+                v = vf[st];
+            x = Elem<T>::mma(Tl::row_frag(qbuf, b * 32 + (lane & 31), st, half), kf[st], x);
+            y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), v, y);
+        }
+        f32x16 w, ds;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int at = b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+            w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -stat[0][at]));
+            ds[e] = w[e] * (y[e] - stat[1][at]);
+        }
+        if (mask) {
+            const int at = x0 + b * 32 + half * 4 - e0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const bool hide = (uint32_t)(at + (e >> 2) * 8 + (e & 3)) > e_span;
+                w[e] = hide ? 0.0f : w[e];
+                ds[e] = hide ? 0.0f : ds[e];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Frag fw = to_frag<T>(w, k), fs = to_frag<T>(ds, k);
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                dv[db] = Elem<T>::mma(Tl::col_frag(gbuf, b * 32 + k * 16, db, lane), fw, dv[db]);
+                dk[db] = Elem<T>::mma(Tl::col_frag(qbuf, b * 32 + k * 16, db, lane), fs, dk[db]);
+            }
+        }
+    };
     if (tid == 0) bad = 0;
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
@@ -1033,52 +1098,12 @@ void attention_dkv_kernel(AttnArgs a) {
     for (int i = 0; i < n; ++i) {
         const int x0 = xn;
         if (i + 1 < n) load(i + 1);
-        const int view = !wave_live ? 0 : wave_all.has(x0) ? 2 : wave_any.has(x0);
-        if (view != 0) {
-            const FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
-            const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
+        const FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
+        const float(*st)[64] = stat[i & 1];
 #pragma unroll
-            for (int b = 0; b < QB; ++b) {
-                f32x16 x = 0.0f, y = 0.0f;
-#pragma unroll
-                for (int st = 0; st < STEPS; ++st) {
-                    x = Elem<T>::mma(Tl::row_frag(qbuf, b * 32 + (lane & 31), st, half), kf[st], x);
-                    Frag v;
-                    if constexpr (kVLds)
-                        v = Tl::row_frag(lds + kV, wave * 32 + (lane & 31), st, half);
-                    else
-                        v = vf[st];
-                    y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), v, y);
-                }
-                f32x16 w, ds;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
-                    w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -stat[i & 1][0][at]));
-                    ds[e] = w[e] * (y[e] - stat[i & 1][1][at]);
-                }
-                if (view == 1) {
-                    const int at = x0 + b * 32 + half * 4 - e0;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const bool hide = (uint32_t)(at + (e >> 2) * 8 + (e & 3)) > e_span;
-                        w[e] = hide ? 0.0f : w[e];
-                        ds[e] = hide ? 0.0f : ds[e];
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const Frag fw = to_frag<T>(w, k), fs = to_frag<T>(ds, k);
-#pragma unroll
-                    for (int db = 0; db < DB; ++db) {
-                        dv[db] =
-                            Elem<T>::mma(Tl::col_frag(gbuf, b * 32 + k * 16, db, lane), fw, dv[db]);
-                        dk[db] =
-                            Elem<T>::mma(Tl::col_frag(qbuf, b * 32 + k * 16, db, lane), fs, dk[db]);
-                    }
-                }
-            }
-        }
+        for (int b = 0; b < QB; ++b)
+            if (wave_live && wave_any.has(x0 + b * 32))
+                block(qbuf, st, b, x0, !wave_all.has(x0 + b * 32));
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
@@ -1113,13 +1138,8 @@ void attention_dkv_kernel(AttnArgs a) {
     }
     T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
     T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            dk[db][e] = live ? dk[db][e] : 0.0f;
-            dv[db][e] = live ? dv[db][e] : 0.0f;
-        }
+    zero_unless<DB>(dk, live);
+    zero_unless<DB>(dv, live);
     const bool write = live || r < t.pad;
     store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane);
     store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane);
