@@ -28,7 +28,9 @@ __device__ __forceinline__ bool row_tile(const AttnArgs& a, uint32_t block, RowT
     const SeqArgs& s = KEYS ? a.ks : a.qs;
     const int G = KEYS ? 1 : a.G;
     t.hk = (int)(block % (uint32_t)a.Hk);
-    const uint32_t slot = block / (uint32_t)a.Hk;
+    uint32_t slot = block / (uint32_t)a.Hk;
+    // later rows see more keys where only the right is bounded: those first
+    if (!KEYS && a.right >= 0 && a.left < 0) slot = gridDim.x / (uint32_t)a.Hk - 1 - slot;
     int64_t start, tile;
     int len;
     if (s.cu) {
