@@ -1,6 +1,4 @@
 // Attention over the rows of variable-length sequences and its gradients.
-#include <type_traits>
-
 #include "fpstok_mma.h"
 #include "fpstok_seqs.h"
 
@@ -85,8 +83,10 @@ struct KeyTiles {
     }
     // Keeps the tiles of part `split` of `splits` and returns their number.
     __device__ __forceinline__ int part(int split, int splits) {
-        from = (int)((int64_t)count * split / splits);
-        return (int)((int64_t)count * (split + 1) / splits) - from;
+        if (splits == 1) return count;
+        const int per = (int)(((uint32_t)count + (uint32_t)splits - 1) / (uint32_t)splits);
+        from = split * per < count ? split * per : count;
+        return count - from < per ? count - from : per;
     }
 };
 
@@ -315,8 +315,8 @@ __device__ __forceinline__ float log_sum(float mc, float l) {
 // its factor is one value per lane, and the weights, rounded to the type, are
 // already the operand of O^T += V^T P^T.
 template <class T, int DP, int BN>
-__global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void attention_kernel(AttnArgs a) {
-    constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
+__global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_kernel(AttnArgs a) {
+    constexpr int DB = DP / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
@@ -366,28 +366,27 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
 
     Softmax<T, DB> sm;
     const float c = a.scale * kLog2e;
-    // 32 NB keys from row `from` of the tile at kbuf on (key j0 + from)
-    auto attend = [&](auto NB, const FPSTOK_LDS char* kbuf, int from, int j0, int v0, int v1) {
-        constexpr int kNB = decltype(NB)::value;
-        const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
+    constexpr int NB = DP == 64 || BN == 32 ? 1 : 2;
+    // 32 NB keys (j0 on) from row `from` of the tile at kbuf on; v0, v1: what
+    // the first and the second block of 32 look like (tile_view)
+    auto attend = [&](const FPSTOK_LDS char* kbuf, int from, int j0, int v0, int v1) {
+        const FPSTOK_LDS char* vbuf = kbuf + (BN + from) * Tl::kPitch;
         kbuf += from * Tl::kPitch;
-        vbuf += from * Tl::kPitch;
-        f32x16 s[kNB];
+        f32x16 s[NB];
 #pragma unroll
-        for (int b = 0; b < kNB; ++b) {
+        for (int b = 0; b < NB; ++b) {
             f32x16 x = 0.0f;
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
                 x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             s[b] = x;
         }
-        // (v0: what the first block looks like, v1: the second)
-        if (v0 != 2) win.mask(s[0], j0 + from, half, a.sinks, -INFINITY);
-        if (kNB == 2 && v1 != 2) win.mask(s[kNB - 1], j0 + 32, half, a.sinks, -INFINITY);
+        if (v0 != 2) win.mask(s[0], j0, half, a.sinks, -INFINITY);
+        if (NB == 2 && v1 != 2) win.mask(s[NB - 1], j0 + 32, half, a.sinks, -INFINITY);
         sm.grow(s, c);
         sm.weights(s, c);
 #pragma unroll
-        for (int k = 0; k < kNB * 2; ++k) {
+        for (int k = 0; k < NB * 2; ++k) {
             const Frag pf = to_frag<T>(s[k >> 1], k & 1);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
@@ -405,16 +404,18 @@ __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 256 ? 2 : 1) void atten
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
         if (i + 1 < n) load(i + 1);
-        const int v0 = wave_live ? mine.of(a, j0) : 0;
-        const int v1 = KB == 2 && wave_live ? mine.of(a, j0 + 32) : 0;
         const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
-        // a tile with one block of 32 keys in sight costs half; at DP = 128 the
-        // second copy of the code cost more than that (causal 16k 1.41 ms
-        // against 1.25)
-        if (KB == 2 && (DP == 128 ? (v0 | v1) != 0 : v0 != 0 && v1 != 0))
-            attend(std::integral_constant<int, KB>(), kbuf, 0, j0, v0, v1);
-        else if ((v0 | v1) != 0 && (KB == 1 || DP == 64))
-            attend(std::integral_constant<int, 1>(), kbuf, v0 != 0 ? 0 : 32, j0, v0 | v1, 0);
+        // NB blocks of 32 keys at a time.  At D = 64 the walk is bound by the
+        // vector unit: one block at a time skips blocks out of sight and leaves
+        // registers for four workgroups per compute unit (two at a time: 84k-pulse
+        // windows 184 us against 168).  At D = 128 two at a time keep the
+        // matrix cores fed (one at a time: causal 16k 1.41 ms against 1.25).
+#pragma unroll 1
+        for (int b = 0; b < BN; b += NB * 32) {
+            const int v0 = wave_live ? mine.of(a, j0 + b) : 0;
+            const int v1 = NB == 2 && wave_live ? mine.of(a, j0 + b + 32) : 0;
+            if ((v0 | v1) != 0) attend(kbuf, b, j0 + b, v0, v1);
+        }
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }

@@ -222,21 +222,28 @@ struct Stage {
     }
 };
 
-// 16 bytes per lane from base + off (bytes) straight to LDS at lds + 16 lane,
-// without a register in between; done once the wave's vmcnt is back at 0
+__device__ __forceinline__ const void* wave_uniform(const void* p) {
+    const uint64_t x = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (const void*)((uint64_t)hi << 32 | lo);
+}
+
+// 16 bytes per lane from base + off (bytes) straight to LDS at lds + 16 lane
+// (base and lds the same in every lane), without a register in between; done once the wave's vmcnt is back at 0
 // (dma_wait).  The instruction takes its LDS address from M0.  The compiler
 // would wait for such a load before the next LDS read of any kind; here the
 // reads of one buffer go on while the other one fills.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(lds), "v"(off), "s"(base)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(wave_uniform(base))
                  : "memory");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  :
-                 : "s"(lds), "v"(off), "s"(base)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(wave_uniform(base))
                  : "memory");
 }
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
