@@ -46,6 +46,10 @@ struct AttnArgs {
     // (backward): walked in chunks of 2^sink_shift queries, whose parts of the
     // sinks' gradients are [slots][Hk][2][sinks][D] (grad_k, grad_v)
     int32_t sink_shift;
+    // a key's walk split over `k_splits` workgroups (backward): their parts,
+    // [k_splits][grad_k, grad_v][Hk][k rows][D]
+    int32_t k_splits;
+    float* k_part;
     float* sink_part;
 };
 
@@ -68,6 +72,8 @@ struct RopeArgs {
 
 // Slots of 2^shift rows that cover every sequence (their numbering: slot_of).
 int64_t row_slots(const SeqArgs& s, int G, int shift);
+// Workgroups that the walk of 128 keys' gradients is split over.
+int plan_key_parts(const AttnArgs& a, int32_t q_len);
 AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);

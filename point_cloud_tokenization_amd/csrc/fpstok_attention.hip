@@ -410,12 +410,16 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
         // registers for four workgroups per compute unit (two at a time: 84k-pulse
         // windows 184 us against 168).  At D = 128 two at a time keep the
         // matrix cores fed (one at a time: causal 16k 1.41 ms against 1.25).
-#pragma unroll 1
-        for (int b = 0; b < BN; b += NB * 32) {
+        auto blocks = [&](int b) {
             const int v0 = wave_live ? mine.of(a, j0 + b) : 0;
             const int v1 = NB == 2 && wave_live ? mine.of(a, j0 + b + 32) : 0;
             if ((v0 | v1) != 0) attend(kbuf, b, j0 + b, v0, v1);
-        }
+        };
+        if constexpr (NB * 32 == BN)
+            blocks(0);
+        else
+#pragma unroll 1
+            for (int b = 0; b < BN; b += NB * 32) blocks(b);
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
@@ -920,12 +924,19 @@ void attention_sink_kernel(AttnArgs a) {
     }
 }
 
+// Where part `split` of a key's gradients lies: [split][grad_k, grad_v][Hk][row].
+__device__ __forceinline__ int64_t k_part_at(const AttnArgs& a, int split, int hk, int64_t row) {
+    return (((int64_t)split * 2 * a.Hk + hk) * a.ks.rows + row) * a.D;
+}
+
 // grad_k and grad_v.  A workgroup takes 128 keys of one key head (32 per wave,
 // across the lanes) and walks the queries that see them, BQ at a time, head
 // after head of the group: S = Q K^T and dP = dO V^T have the rows in registers, so P
 // and dS = P (dP - delta), rounded to the type, are the operands of
 // dV^T += dO^T P and dK^T += Q^T dS.  The gradients of the group's heads add up
-// in the accumulators, in a fixed order.
+// in the accumulators, in a fixed order.  Where that leaves few workgroups (few
+// keys, many queries or heads) the walk is split over several, whose parts are
+// added by the kernel below.
 template <class T, int DP, int BQ>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1)
 void attention_dkv_kernel(AttnArgs a) {
@@ -968,7 +979,14 @@ void attention_dkv_kernel(AttnArgs a) {
     uint32_t e_span = (uint32_t)(e1 - e0);
     if (e1 < e0) e0 = 0x7fffffff, e_span = 0;  // none: no query has that number
     const int nq = t.rows > 0 && i1 >= i0 ? i1 - i0 + 1 : 0;
-    const int per = (nq + BQ - 1) / BQ, n = per * G;
+    // this workgroup's tiles of the walk: [from, from + n) of per tiles a head
+    const int per = (nq + BQ - 1) / BQ, walk = per * G;
+    int from = 0, n = walk;
+    if (a.k_splits > 1) {
+        const int each = (int)(((uint32_t)walk + (uint32_t)a.k_splits - 1) / (uint32_t)a.k_splits);
+        from = (int)blockIdx.y * each < walk ? (int)blockIdx.y * each : walk;
+        n = walk - from < each ? walk - from : each;
+    }
     // `rows` (all_range) or 32 (any_range) queries from x on: x - lo <= span if
     // each of them exists and sees each of the keys j0 .. j1, or if some may see
     // some
@@ -999,13 +1017,13 @@ void attention_dkv_kernel(AttnArgs a) {
 
     const Dma<T, DP, BQ> dma(a.D, tid);
     const uint32_t off_q = dma.offset(a.q.row), off_g = dma.offset(a.grad_out.row);
-    // the first query of the tile loaded last
-    int xn = i0;
-    const int64_t row_i0 = t.q0 + i0;
-    const T* qp = (const T*)a.q.data + row_i0 * a.q.row + (int64_t)t.hk * G * a.q.head;
-    const T* gp =
-        (const T*)a.grad_out.data + row_i0 * a.grad_out.row + (int64_t)t.hk * G * a.grad_out.head;
-    int64_t stat_at = (int64_t)t.hk * G * a.qs.rows + row_i0;
+    // the first query of the tile loaded last, and where it lies
+    const int head0 = n > 0 ? from / per : 0;
+    int xn = i0 + (n > 0 ? from - head0 * per : 0) * BQ;
+    const int64_t row_n = t.q0 + xn, head_n = (int64_t)t.hk * G + head0;
+    const T* qp = (const T*)a.q.data + row_n * a.q.row + head_n * a.q.head;
+    const T* gp = (const T*)a.grad_out.data + row_n * a.grad_out.row + head_n * a.grad_out.head;
+    int64_t stat_at = head_n * a.qs.rows + row_n;
     auto load = [&](int i) {  // tiles in turn
         if (i > 0) {
             if (xn + BQ <= i1) {
@@ -1110,7 +1128,7 @@ void attention_dkv_kernel(AttnArgs a) {
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
-    if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks) {
+    if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks && blockIdx.y == 0) {
         const int past = t.tq - 1 - last_by_window(a, t.tq, t.tk);
         const int chunks = (past + (1 << a.sink_shift) - 1) >> a.sink_shift;
         if (chunks > 0) {
@@ -1139,32 +1157,76 @@ void attention_dkv_kernel(AttnArgs a) {
                     }
         }
     }
-    T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
-    T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
     zero_unless<DB>(dk, live);
     zero_unless<DB>(dv, live);
+    // add_bad over the queries of this workgroup's part that see this key in
+    // tiles that the workgroup's keys do not all see whole
+    auto add_hidden = [&](auto* to_k, auto* to_v) {
+        __syncthreads();
+        if (!live || half != 0 || e1 < e0) return;
+#pragma unroll 1
+        for (int i = from; i < from + n; ++i) {
+            const int g = i / per, x = i0 + (i - g * per) * BQ;
+            if (tile_all.has(x)) continue;
+#pragma unroll 1
+            for (int y = x > e0 ? x : e0; y < x + BQ && y <= e1; ++y) {
+                const int64_t row = t.q0 + y, h = (int64_t)t.hk * G + g;
+                add_bad(to_k, (const T*)a.q.data + row * a.q.row + h * a.q.head, a.D);
+                add_bad(to_v,
+                        (const T*)a.grad_out.data + row * a.grad_out.row + h * a.grad_out.head,
+                        a.D);
+            }
+        }
+    };
+    if (a.k_splits > 1) {
+        float* part = a.k_part + k_part_at(a, blockIdx.y, t.hk, krow);
+        float* part_v = part + k_part_at(a, 0, a.Hk, 0);
+        store_row<float, DB>(dk, 1.0f, live ? part : nullptr, a.D, lane);
+        store_row<float, DB>(dv, 1.0f, live ? part_v : nullptr, a.D, lane);
+        if (bad) add_hidden(part, part_v);
+        return;
+    }
+    T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
+    T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
     const bool write = live || r < t.pad;
     store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane);
     store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane);
-    if (bad) {
-        __syncthreads();
-        if (live && half == 0 && e1 >= e0)
-#pragma unroll 1
-            for (int g = 0; g < G; ++g)
-#pragma unroll 1
-                for (int x = i0; x <= i1; x += BQ) {
-                    if (tile_all.has(x)) continue;
-#pragma unroll 1
-                    for (int i = x > e0 ? x : e0; i < x + BQ && i <= e1; ++i) {
-                        const int64_t row = t.q0 + i, h = t.hk * G + g;
-                        add_bad(ok, (const T*)a.q.data + row * a.q.row + h * a.q.head, a.D);
-                        add_bad(ov,
-                                (const T*)a.grad_out.data + row * a.grad_out.row +
-                                    h * a.grad_out.head,
-                                a.D);
-                    }
-                }
+    if (bad) add_hidden(ok, ov);
+}
+
+// Adds the parts of keys whose walk was split, in order: 4 elements of one key
+// and head per thread.
+template <class T>
+__global__ __launch_bounds__(256) void attention_join_dkv_kernel(AttnArgs a) {
+    using f4 = float __attribute__((ext_vector_type(4)));
+    using T4 = T __attribute__((ext_vector_type(4)));
+    const uint32_t per = (uint32_t)a.D / 4;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t at = x / per;
+    const int d = (int)(x - at * per) * 4;
+    const int64_t row = at / a.Hk;
+    const int hk = (int)(at - row * a.Hk);
+    if (row >= a.ks.rows) return;
+    bool here = true;
+    if (a.ks.cu) {
+        if (row < cu_at(a.ks, 0) || row >= cu_at(a.ks, a.ks.B)) return;
+    } else {
+        here = row % a.ks.cap < a.ks.count[row / a.ks.cap];
     }
+    f4 k = 0.0f, v = 0.0f;
+    if (here) {
+        const int64_t v_at = k_part_at(a, 0, a.Hk, 0);
+#pragma unroll 4
+        for (int s = 0; s < a.k_splits; ++s) {
+            const float* part = a.k_part + k_part_at(a, s, hk, row) + d;
+            k += *(const f4*)part;
+            v += *(const f4*)(part + v_at);
+        }
+    }
+    *(T4*)((T*)a.grad_k.data + row * a.grad_k.row + hk * a.grad_k.head + d) =
+        __builtin_convertvector(k * a.scale, T4);
+    *(T4*)((T*)a.grad_v.data + row * a.grad_v.row + hk * a.grad_v.head + d) =
+        __builtin_convertvector(v, T4);
 }
 
 int64_t row_slots(const SeqArgs& s, int G, int shift) {
@@ -1194,6 +1256,18 @@ AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
     return p;
 }
 
+int plan_key_parts(const AttnArgs& a, int32_t q_len) {
+    // workgroups of 128 keys, each with a walk of about this many queries
+    const int64_t blocks = row_slots(a.ks, 1, 7) * a.Hk;
+    int64_t walk = q_len;
+    if (a.left >= 0 && a.right >= 0 && walk > 128 + a.left + a.right)
+        walk = 128 + (int64_t)a.left + a.right;
+    walk *= a.G;
+    int64_t n = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
+    if (n > walk / 512) n = walk / 512;
+    return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+}
+
 template <class T>
 static hipError_t forward(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
@@ -1219,7 +1293,7 @@ template <class T>
 static hipError_t backward(const AttnArgs& a, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
-    const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk));
+    const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk), (unsigned)a.k_splits);
     if (a.qs.rows > 0) {
         if (a.D <= 64)
             attention_dq_kernel<T, 64, 64><<<q, 256, 0, s>>>(a);
@@ -1238,6 +1312,11 @@ static hipError_t backward(const AttnArgs& a, hipStream_t s) {
             attention_dkv_kernel<T, 64, k16 ? 64 : 32><<<k, 256, 0, s>>>(a);
         else
             attention_dkv_kernel<T, 128, 32><<<k, 256, 0, s>>>(a);
+        if (a.k_splits > 1) {
+            const int64_t threads = a.ks.rows * a.Hk * (a.D / 4);
+            attention_join_dkv_kernel<T>
+                <<<dim3((unsigned)((threads + 255) / 256)), 256, 0, s>>>(a);
+        }
     }
     return hipGetLastError();
 }

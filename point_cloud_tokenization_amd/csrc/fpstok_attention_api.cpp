@@ -150,13 +150,18 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
     if (backward) {
         a.lse2 = (float*)at;
         a.delta = (float*)(at + align256(rows * sizeof(float)));
-        const size_t stat = 2 * align256(rows * sizeof(float));
-        if (a.left < 0 || a.sinks == 0) return stat;
+        size_t need = 2 * align256(rows * sizeof(float));
+        a.k_splits = plan_key_parts(a, likely_len(qs));
+        if (a.k_splits > 1) {
+            a.k_part = (float*)(at + need);
+            need += align256((size_t)a.k_splits * 2 * a.Hk * ks->num_rows * a.D * sizeof(float));
+        }
+        if (a.left < 0 || a.sinks == 0) return need;
         // about 512 workgroups of queries past the sinks, of 256 queries or more
         a.sink_shift = 8;
         while (qs->num_rows * a.Hk >> a.sink_shift > 512) ++a.sink_shift;
-        a.sink_part = (float*)(at + stat);
-        return stat + align256((size_t)row_slots(a.qs, 1, a.sink_shift) * a.Hk * 2 * a.sinks *
+        a.sink_part = (float*)(at + need);
+        return need + align256((size_t)row_slots(a.qs, 1, a.sink_shift) * a.Hk * 2 * a.sinks *
                                a.D * sizeof(float));
     }
     plan = plan_attention(a, likely_len(qs), likely_len(ks));

@@ -554,3 +554,14 @@ def test_tokens_through_a_layer(F):
         m = c[i + 1] - c[i]
         assert torch.equal(full[i, :m], out.view(B * P, H * D)[c[i]:c[i + 1]])
         assert float(full[i, m:].abs().sum()) == 0.0
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("lens,k_lens,H,Hk,left,right,sinks", [
+    ([700], None, 8, 1, -1, -1, 0), ([900, 3], None, 4, 1, 300, 0, 40),
+    ([1500, 0, 40], [60, 5, 7], 4, 2, -1, -1, 0), ([1200], [130], 3, 1, -1, 0, 0)])
+@pytest.mark.parametrize("form", ["packed", "padded"])
+def test_few_keys_many_queries(F, dtype, lens, k_lens, H, Hk, left, right, sinks, form):
+    """Walks of grad_k and grad_v that are split over workgroups."""
+    run(F, "split walk", lens, k_lens, H=H, Hk=Hk, D=40, dtype=dtype, left=left, right=right,
+        sinks=sinks, form=form, hint=True, extra=3 if form == "packed" else 0)
