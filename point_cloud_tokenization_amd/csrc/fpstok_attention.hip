@@ -665,7 +665,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 // in the forward kernel; per 32 keys a wave forms S^T = K Q^T and
 // dP^T = V dO^T, and dS^T = P^T (dP^T - delta), rounded to the type, is the
 // operand of dQ^T += K^T dS^T.
-template <class T, int DP, int BN>
+//
+// delta = grad_out times the rounded out is off by that rounding, and in rows
+// of few keys this is a large part of grad_q's and grad_k's error (8 keys of
+// bfloat16: 1.57 times the error of rounding the exact gradient, 1.42 without;
+// 64 keys: 1.45 and 1.43).  dS summed over the keys, which should be 0, gives the
+// difference to the exact delta: where one tile is all a row tile sees it is
+// formed from that tile first, and with a window of fewer than 32 keys (TWICE)
+// the whole walk is made twice.
+template <class T, int DP, int BN, bool TWICE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
@@ -719,6 +727,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
     const float c = a.scale * kLog2e;
     float delta = 0.0f, lse2 = 0.0f;
+    // sum of dS over the keys of 32 rows from row b of the tile at kbuf on
+    auto add_delta = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask, float& sum) {
+        f32x16 x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            const int row = b + (lane & 31);
+            x = Elem<T>::mma(Tl::row_frag(kbuf, row, st, half), qf[st], x);
+            y = Elem<T>::mma(Tl::row_frag(kbuf + BN * Tl::kPitch, row, st, half), gf[st], y);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2)) * (y[e] - delta);
+        if (mask) win.mask(x, j0 + b, half, a.sinks, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += x[e];
+    };
     auto block = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
@@ -752,13 +776,45 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     // a row that sees nothing: every weight is masked, the value only has to
     // be finite
     lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+    if (n > 0) arrive(0);
+    __syncthreads();
+    float off_by = 0.0f;
+    if (!TWICE && sizeof(T) == 2 && n == 1 && wave_live) {
+#pragma unroll 1
+        for (int b = 0; b < BN; b += 32) {
+            const int view = mine.of(a, jn + b);
+            if (view != 0) add_delta(lds, b, jn, view == 1, off_by);
+        }
+        delta += pair_sum(off_by);
+    }
+    if constexpr (TWICE) {
+        for (int i = 0; i < n; ++i) {
+            const int j0 = jn;
+            if (i + 1 < n) load(i + 1);
+#pragma unroll 1
+            for (int b = 0; b < BN; b += 32) {
+                const int view = wave_live ? mine.of(a, j0 + b) : 0;
+                if (view != 0)
+                    add_delta(lds + (i & 1) * 2 * BN * Tl::kPitch, b, j0, view == 1, off_by);
+            }
+            if (i + 1 < n) arrive(i + 1);
+            __syncthreads();
+        }
+        delta += pair_sum(off_by);
+        jn = n > 0 ? kt.tile(0) * BN : 0;
+        kp = kb + jn * a.k.row;
+        vp = vb + jn * a.v.row;
+        if (n > 0) {
+            load(0);
+            arrive(0);
+        }
+        __syncthreads();
+    }
     if (q.live && half == 0) {
         const int64_t at = (int64_t)q.h * a.qs.rows + q.row;
         a.lse2[at] = lse2;
         a.delta[at] = delta;
     }
-    if (n > 0) arrive(0);
-    __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
         if (i + 1 < n) load(i + 1);
@@ -1295,10 +1351,18 @@ static hipError_t backward(const AttnArgs& a, hipStream_t s) {
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
     const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk), (unsigned)a.k_splits);
     if (a.qs.rows > 0) {
-        if (a.D <= 64)
-            attention_dq_kernel<T, 64, 64><<<q, 256, 0, s>>>(a);
-        else
-            attention_dq_kernel<T, 128, k16 ? 64 : 32><<<q, 256, 0, s>>>(a);
+        const bool narrow = k16 && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
+        if (a.D <= 64) {
+            if (narrow)
+                attention_dq_kernel<T, 64, 64, k16><<<q, 256, 0, s>>>(a);
+            else
+                attention_dq_kernel<T, 64, 64, false><<<q, 256, 0, s>>>(a);
+        } else {
+            if (narrow)
+                attention_dq_kernel<T, 128, k16 ? 64 : 32, k16><<<q, 256, 0, s>>>(a);
+            else
+                attention_dq_kernel<T, 128, k16 ? 64 : 32, false><<<q, 256, 0, s>>>(a);
+        }
     }
     if (a.sink_part && a.qs.rows > 0) {
         const dim3 c((unsigned)(row_slots(a.qs, 1, a.sink_shift) * a.Hk));
