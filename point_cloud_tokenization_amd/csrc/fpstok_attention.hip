@@ -378,7 +378,8 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
             f32x16 x = 0.0f;
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
-                x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
+                if (sizeof(T) == 2 || st * 16 < a.D)  // (float32: a step is 8 instructions)
+                    x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             s[b] = x;
         }
         if (v0 != 2) win.mask(s[0], j0, half, a.sinks, -INFINITY);
@@ -390,7 +391,8 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
             const Frag pf = to_frag<T>(s[k >> 1], k & 1);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
-                sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
+                if (sizeof(T) == 2 || db * 32 < a.D)
+                    sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
         }
     };
     if (tid == 0) bad = 0;
@@ -513,7 +515,8 @@ void attention_few_kernel(AttnArgs a) {
             f32x16 x = 0.0f;
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
-                x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
+                if (sizeof(T) == 2 || st * 16 < a.D)  // (float32: a step is 8 instructions)
+                    x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             s[b] = x;
         }
         if (view == 1) {
@@ -528,7 +531,8 @@ void attention_few_kernel(AttnArgs a) {
             const Frag pf = to_frag<T>(s[k >> 1], k & 1);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
-                sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
+                if (sizeof(T) == 2 || db * 32 < a.D)
+                    sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
         }
     }
     const bool seen = sm.finish();
