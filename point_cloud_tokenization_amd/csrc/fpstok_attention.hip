@@ -14,21 +14,30 @@ struct RowTile {
     int64_t q0, k0;  // first buffer rows of the sequence
     int tq, tk, row0, rows;  // rows: those of the tile that exist
     int pad;                 // rows of the tile inside a padded sequence's slots
-    int hk, b;
+    int hk, b, part;  // part: of a split walk
 };
 
 // Decodes a workgroup's place in the grid: heads fastest, so that with 8 key
 // heads (or a multiple) a head's tiles stay on one of the 8 XCDs and share its
 // L2.
 // KEYS: the tile is of keys (G = 1), not of rows of queries.
+// Of a walk split into `parts`, the parts of one tile are neighbours (a stride
+// between them would give a compute unit the same tile's again and again).
 template <int SHIFT, bool KEYS>
-__device__ __forceinline__ bool row_tile(const AttnArgs& a, uint32_t block, RowTile& t) {
+__device__ __forceinline__ bool row_tile(const AttnArgs& a, int parts, RowTile& t) {
     const SeqArgs& s = KEYS ? a.ks : a.qs;
     const int G = KEYS ? 1 : a.G;
-    t.hk = (int)(block % (uint32_t)a.Hk);
-    uint32_t slot = block / (uint32_t)a.Hk;
+    const uint32_t place = blockIdx.x / (uint32_t)a.Hk;
+    t.hk = (int)(blockIdx.x - place * (uint32_t)a.Hk);
+    uint32_t slot = place, slots = gridDim.x / (uint32_t)a.Hk;
+    t.part = 0;
+    if (parts > 1) {
+        slot = place / (uint32_t)parts;
+        slots /= (uint32_t)parts;
+        t.part = (int)(place - slot * (uint32_t)parts);
+    }
     // later rows see more keys where only the right is bounded: those first
-    if (!KEYS && a.right >= 0 && a.left < 0) slot = gridDim.x / (uint32_t)a.Hk - 1 - slot;
+    if (!KEYS && a.right >= 0 && a.left < 0) slot = slots - 1 - slot;
     int64_t start, tile;
     int len;
     if (s.cu) {
@@ -326,7 +335,7 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.G;
     RowTile t;
-    if (!row_tile<7, false>(a, blockIdx.x, t)) return;
+    if (!row_tile<7, false>(a, a.splits, t)) return;
     const QueryRows q(a, t, wave * 32, lane);
     Frag qf[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
@@ -334,7 +343,7 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
     const bool wave_live = wave * 32 < t.rows;
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
-    const int n = t.rows > 0 ? kt.part(blockIdx.y, a.splits) : 0;
+    const int n = t.rows > 0 ? kt.part(t.part, a.splits) : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     const Dma<T, DP, BN> dma(a.D, tid);
@@ -428,7 +437,7 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
     const bool some = sm.finish();
     if (a.splits > 1) {
         const int64_t at =
-            ((int64_t)blockIdx.y * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + q.r;
+            ((int64_t)t.part * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0 + q.r;
         float* part = a.part + at * a.D;
         sm.only(some);
         store_row<float, DB>(sm.o, 1.0f, q.live ? part : nullptr, a.D, lane);
@@ -475,14 +484,14 @@ void attention_few_kernel(AttnArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.G;
     RowTile t;
-    if (!row_tile<5, false>(a, blockIdx.x, t)) return;
+    if (!row_tile<5, false>(a, a.splits, t)) return;
     const QueryRows q(a, t, 0, lane);
     Frag qf[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
-    const int n = t.rows > 0 ? kt.part(blockIdx.y, a.splits) : 0;
+    const int n = t.rows > 0 ? kt.part(t.part, a.splits) : 0;
     const T* kb = (const T*)a.k.data + t.k0 * a.k.row + t.hk * a.k.head;
     const T* vb = (const T*)a.v.data + t.k0 * a.v.row + t.hk * a.v.head;
     Stage<T, DP, BN, 64> sk, sv;
@@ -551,7 +560,7 @@ void attention_few_kernel(AttnArgs a) {
     __syncthreads();
     // 4 elements per thread and turn
     const int64_t part0 =
-        ((int64_t)blockIdx.y * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0;
+        ((int64_t)t.part * a.Hk + t.hk) * a.qs.rows * G + t.q0 * G + t.row0;
     const int rows = t.rows > t.pad ? t.rows : t.pad;
     for (int x = tid; x < rows * (DP / 4); x += 256) {
         const int row = x / (DP / 4), d = (x % (DP / 4)) * 4;
@@ -688,7 +697,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     RowTile t;
-    if (!row_tile<7, false>(a, blockIdx.x, t)) return;
+    if (!row_tile<7, false>(a, 1, t)) return;
     const QueryRows q(a, t, wave * 32, lane);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
@@ -1015,7 +1024,7 @@ void attention_dkv_kernel(AttnArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.G;
     RowTile t;
-    if (!row_tile<7, true>(a, blockIdx.x, t)) return;
+    if (!row_tile<7, true>(a, a.k_splits, t)) return;
 
     const int r = wave * 32 + (lane & 31);
     const bool live = r < t.rows;
@@ -1044,7 +1053,7 @@ void attention_dkv_kernel(AttnArgs a) {
     int from = 0, n = walk;
     if (a.k_splits > 1) {
         const int each = (int)(((uint32_t)walk + (uint32_t)a.k_splits - 1) / (uint32_t)a.k_splits);
-        from = (int)blockIdx.y * each < walk ? (int)blockIdx.y * each : walk;
+        from = t.part * each < walk ? t.part * each : walk;
         n = walk - from < each ? walk - from : each;
     }
     // `rows` (all_range) or 32 (any_range) queries from x on: x - lo <= span if
@@ -1188,7 +1197,7 @@ void attention_dkv_kernel(AttnArgs a) {
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
-    if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks && blockIdx.y == 0) {
+    if (a.left >= 0 && t.row0 == 0 && t.rows > 0 && wave * 32 < a.sinks && t.part == 0) {
         const int past = t.tq - 1 - last_by_window(a, t.tq, t.tk);
         const int chunks = (past + (1 << a.sink_shift) - 1) >> a.sink_shift;
         if (chunks > 0) {
@@ -1239,7 +1248,7 @@ void attention_dkv_kernel(AttnArgs a) {
         }
     };
     if (a.k_splits > 1) {
-        float* part = a.k_part + k_part_at(a, blockIdx.y, t.hk, krow);
+        float* part = a.k_part + k_part_at(a, t.part, t.hk, krow);
         float* part_v = part + k_part_at(a, 0, a.Hk, 0);
         store_row<float, DB>(dk, 1.0f, live ? part : nullptr, a.D, lane);
         store_row<float, DB>(dv, 1.0f, live ? part_v : nullptr, a.D, lane);
@@ -1311,7 +1320,7 @@ AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
     AttnPlan p;
     p.few = (int64_t)q_len * G <= 32;
     const int64_t blocks = row_slots(a.qs, G, p.few ? 5 : 7) * a.Hk;
-    p.splits = p.few ? key_splits(a, blocks, q_len, k_len, 2048, 512)
+    p.splits = p.few ? key_splits(a, blocks, q_len, k_len, 1024, 512)
                      : key_splits(a, blocks, 128 / G + 1, k_len, 512, 1024);
     return p;
 }
@@ -1332,7 +1341,7 @@ template <class T>
 static hipError_t forward(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const int64_t blocks = row_slots(a.qs, a.G, plan.few ? 5 : 7) * a.Hk;
-    const dim3 grid((unsigned)blocks, (unsigned)a.splits);
+    const dim3 grid((unsigned)(blocks * a.splits));
     if (plan.few) {
         if (a.D <= 64)
             attention_few_kernel<T, 64, 32><<<grid, 256, 0, s>>>(a);
@@ -1353,7 +1362,7 @@ template <class T>
 static hipError_t backward(const AttnArgs& a, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
-    const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk), (unsigned)a.k_splits);
+    const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk * a.k_splits));
     if (a.qs.rows > 0) {
         const bool narrow = k16 && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
         if (a.D <= 64) {
