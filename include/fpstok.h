@@ -330,8 +330,8 @@ fpstok_status fpstok_random_start(const int64_t* offsets, int64_t num_events, ui
  * num_rows rows, in one of two forms; exactly one of cu_seqlens and
  * token_count is given:
  *   packed (cu_seqlens, as fpstok_pack writes it): sequence b is rows
- *     cu_seqlens[b] .. cu_seqlens[b+1]-1.  Rows behind the last sequence are
- *     neither read nor written.
+ *     cu_seqlens[b] .. cu_seqlens[b+1]-1.  Rows ahead of the first sequence and
+ *     behind the last are neither read nor written.
  *   padded (token_count, as fpstok_tokenize writes it): sequence b is the
  *     first token_count[b] of the rows b*capacity .. (b+1)*capacity-1, and
  *     num_rows = B*capacity.  The other slots are not read; outputs get 0
@@ -353,7 +353,8 @@ typedef struct {
 /* A [num_rows][heads][head_dim] view: head h of row r starts at
  * data + r*row_stride + h*head_stride, its elements are adjacent.  Strides in
  * elements; inputs may use any stride >= 0 (0: the same row or head again),
- * outputs' rows and heads must not overlap. */
+ * outputs' rows and heads must not overlap.  A row_stride above 2^23 or a
+ * head_stride above 2^40 is refused (EUNSUPPORTED). */
 typedef struct {
     void* data;
     int64_t row_stride;
@@ -388,11 +389,12 @@ typedef struct {
  *   s_ij = scale * sum_d q_i[d] k_j[d],  lse_i = log sum_j exp(s_ij),
  *   out_i = sum_j exp(s_ij - lse_i) v_j.
  * A query that sees no key gets out = 0 and lse = -inf.  What a query does not
- * see never reaches its result, not-a-number and infinite values included.
+ * see never reaches its result, not-a-number and infinite values included; a
+ * query whose every visible score is -infinity counts as one that sees none.
  *   q_seqs, k_seqs  the queries' and the keys' sequences (k_seqs NULL: the
  *                   queries'); as many of one as of the other
  *   q   [q rows][H][D] in;  k, v [k rows][num_kv_heads][D] in
- *   out [q rows][H][D] out
+ *   out [q rows][H][D] out, no overlap with an input
  *   lse [q rows][H] f32 out, contiguous, or NULL
  * Scores, softmax and sums are held in float32; with a 16-bit dtype the
  * weights exp(s - max) are rounded to it for the product with v.  Results are
@@ -401,8 +403,10 @@ typedef struct {
  *       256-byte aligned (NULL if that is 0)
  * data pointers are 16-byte aligned, and so are the strides in bytes.
  * Errors: EINVAL (NULL or misaligned pointers, strides, sizes or parameters
- * out of range), EWORKSPACE, EUNSUPPORTED (2^30 rows or more, or 2^31 rows
- * times heads or more), EHIP. */
+ * out of range), EWORKSPACE, EUNSUPPORTED (2^30 rows or more, 2^31 rows times
+ * heads or more, or more work than one launch holds: about rows * H / 128 +
+ * num_seqs * num_kv_heads, rows * H / 32 for sequences of a few queries, has to
+ * stay below 2^24), EHIP. */
 fpstok_status fpstok_attention(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
                                const fpstok_attn_params* params, const fpstok_heads* q,
                                const fpstok_heads* k, const fpstok_heads* v,
@@ -460,7 +464,8 @@ typedef struct {
  * of axis a turns by angle = positions[r][a] * freqs[p],
  *   y1 = x1 cos - x2 sin,  y2 = x1 sin + x2 cos,
  * elements in no pair are copied.  Angles are formed and reduced in float64
- * (exact for |angle| < 2^40), the turn is float32, rounded once.  The gradient
+ * (the product is exact for float32 positions and for int32 ones below 2^29, the
+ * reduction below 2^40), the turn is float32, rounded once.  The gradient
  * with respect to the input is the same call with inverse = 1.
  *   seqs       the rows (one form for q and k); padded slots get 0
  *   positions  [num_rows][A] in, contiguous
@@ -470,7 +475,7 @@ typedef struct {
  *   pointer and strides), k_out may be k_in; no other overlap.
  * Pointers and strides need the alignment of one element; heads aligned to 16
  * bytes are moved 16 bytes at a time.  No workspace.  Errors: EINVAL,
- * EUNSUPPORTED, EHIP. */
+ * EUNSUPPORTED (num_rows * max(D, 64) >= 2^33), EHIP. */
 fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_params* params,
                           const void* positions, const float* freqs, const fpstok_heads* q_in,
                           const fpstok_heads* q_out, const fpstok_heads* k_in,

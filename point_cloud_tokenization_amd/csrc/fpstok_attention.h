@@ -57,6 +57,7 @@ struct AttnArgs {
 struct AttnPlan {
     bool few;        // at most 32 rows per sequence and key head: waves split the keys
     int32_t splits;  // workgroups a row's keys are split over
+    int64_t blocks;  // workgroups of the largest launch
 };
 
 struct RopeArgs {

@@ -156,21 +156,34 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
             a.k_part = (float*)(at + need);
             need += align256((size_t)a.k_splits * 2 * a.Hk * ks->num_rows * a.D * sizeof(float));
         }
+        const int64_t q_blocks = row_slots(a.qs, a.G, 7) * a.Hk;
+        const int64_t k_blocks = row_slots(a.ks, 1, 7) * a.Hk * a.k_splits;
+        plan.blocks = q_blocks > k_blocks ? q_blocks : k_blocks;
         if (a.left < 0 || a.sinks == 0) return need;
         // about 512 workgroups of queries past the sinks, of 256 queries or more
         a.sink_shift = 8;
         while (qs->num_rows * a.Hk >> a.sink_shift > 512) ++a.sink_shift;
         a.sink_part = (float*)(at + need);
-        return need + align256((size_t)row_slots(a.qs, 1, a.sink_shift) * a.Hk * 2 * a.sinks *
-                               a.D * sizeof(float));
+        const int64_t chunks = row_slots(a.qs, 1, a.sink_shift) * a.Hk;
+        if (chunks > plan.blocks) plan.blocks = chunks;
+        return need + align256((size_t)chunks * 2 * a.sinks * a.D * sizeof(float));
     }
     plan = plan_attention(a, likely_len(qs), likely_len(ks));
     a.splits = plan.splits;
+    plan.blocks = row_slots(a.qs, a.G, plan.few ? 5 : 7) * a.Hk * a.splits;
     if (plan.splits == 1) return 0;
     const size_t ml = align256(rows * plan.splits * sizeof(float2));
     a.part_ml = (float2*)at;
     a.part = (float*)(at + ml);
     return ml + align256(rows * plan.splits * a.D * sizeof(float));
+}
+
+// A launch holds less than 2^32 threads, 256 a workgroup.
+static fpstok_status check_grid(const AttnPlan& plan) {
+    if (plan.blocks >= ((int64_t)1 << 24))
+        return fail(FPSTOK_EUNSUPPORTED, "%lld workgroups, at most 2^24 - 1 in a launch",
+                    (long long)plan.blocks);
+    return FPSTOK_OK;
 }
 
 static fpstok_status check_attn_ws(size_t need, void* ws, size_t ws_bytes) {
@@ -193,7 +206,8 @@ FPSTOK_API size_t fpstok_attention_workspace_size(const fpstok_seqs* qs, const f
     if (check_attn(qs, ks, p) != FPSTOK_OK) return 0;
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    return lay_out(qs, ks, backward != 0, nullptr, a, plan);
+    const size_t need = lay_out(qs, ks, backward != 0, nullptr, a, plan);
+    return check_grid(plan) == FPSTOK_OK ? need : 0;
 }
 
 FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_seqs* ks,
@@ -214,7 +228,9 @@ FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_se
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    if ((st = check_attn_ws(lay_out(qs, ks, false, ws, a, plan), ws, ws_bytes)) != FPSTOK_OK)
+    const size_t need = lay_out(qs, ks, false, ws, a, plan);
+    if ((st = check_grid(plan)) != FPSTOK_OK ||
+        (st = check_attn_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;
     if (qs->num_seqs == 0 || nq == 0) return ok();
     a.q = heads_arg(q);
@@ -251,7 +267,9 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    if ((st = check_attn_ws(lay_out(qs, ks, true, ws, a, plan), ws, ws_bytes)) != FPSTOK_OK)
+    const size_t need = lay_out(qs, ks, true, ws, a, plan);
+    if ((st = check_grid(plan)) != FPSTOK_OK ||
+        (st = check_attn_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;
     if (qs->num_seqs == 0 || nq + nk == 0) return ok();
     a.q = heads_arg(q);
@@ -304,6 +322,10 @@ FPSTOK_API fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_
     if (k_in && (p->num_kv_heads < 1 || p->num_kv_heads > 65536))
         return fail(FPSTOK_EINVAL, "num_kv_heads must be in [1, 65536]");
     const int64_t n = seqs->num_rows;
+    // a launch holds less than 2^32 threads: one per element pair of a row, or
+    // 256 per 8 rows or more
+    if (n * (p->head_dim > 64 ? p->head_dim : 64) >= ((int64_t)1 << 33))
+        return fail(FPSTOK_EUNSUPPORTED, "num_rows * max(head_dim, 64) >= 2^33");
     const uintptr_t w = (uintptr_t)elem_bytes(p->dtype);
     const fpstok_heads* in[2] = {q_in, k_in};
     const fpstok_heads* out[2] = {q_out, k_out};

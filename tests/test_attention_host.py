@@ -193,6 +193,28 @@ def test_attention_refuses_counts_and_workspace(L):
     assert _forward(L, q=_heads(head=1 << 41)) == F.EUNSUPPORTED
 
 
+def test_attention_refuses_more_workgroups_than_a_launch_holds(L):
+    """A launch holds 2^24 - 1 workgroups of 256 threads: one per 128 rows (32
+    where sequences are short) and one per sequence, for every key head."""
+    wide = _params(num_heads=64, num_kv_heads=64)
+    fwd = {n: _heads(row=4096) for n in ("q", "k", "v", "out")}
+    bwd = dict(fwd, **{n: _heads(row=4096) for n in ("grad_out", "grad_q", "grad_k", "grad_v")})
+    for kw in (dict(qs=_seqs(B=1 << 20, rows=1 << 20), pr=wide),
+               dict(qs=_seqs(B=1 << 18, rows=1 << 18), ks=_seqs(B=1 << 18, rows=1 << 18), pr=wide),
+               dict(qs=_seqs(B=1 << 23, rows=100)),
+               dict(qs=_seqs(B=1 << 20, rows=1 << 20, cu=None, tc=0x20000, cap=1), pr=wide)):
+        assert _forward(L, **kw, **fwd) == F.EUNSUPPORTED
+        assert b"workgroups" in L.fpstok_last_error()
+        assert _backward(L, **kw, **bwd) == F.EUNSUPPORTED
+        for backward in (0, 1):
+            pr = kw.get("pr", _params())
+            assert L.fpstok_attention_workspace_size(ctypes.byref(kw["qs"]), None,
+                                                     ctypes.byref(pr), backward) == 0
+    # the keys' gradients alone
+    kw = dict(qs=_seqs(B=1 << 18, rows=1 << 18), ks=_seqs(B=1 << 18, rows=1 << 24), pr=wide)
+    assert _backward(L, **kw, **bwd) == F.EUNSUPPORTED
+
+
 def test_attention_nothing_to_do(L):
     assert _forward(L, qs=_seqs(B=0, rows=0, cu=None)) == F.OK
     assert _backward(L, qs=_seqs(B=0, rows=0, cu=None)) == F.OK
@@ -227,6 +249,13 @@ def _rope(L, seqs=None, pos=0x10000, freqs=0x20000, k=True, views=(), **kw):
 def test_rope_refuses(L, bad):
     assert _rope(L, **bad) == F.EINVAL
     assert L.fpstok_last_error()
+
+
+def test_rope_refuses_more_rows_than_a_launch_holds(L):
+    assert _rope(L, seqs=_seqs(rows=1 << 27)) == F.EUNSUPPORTED
+    assert _rope(L, seqs=_seqs(rows=1 << 27), head_dim=8, pairs=(1, 1, 1, 1)) == F.EUNSUPPORTED
+    assert _rope(L, seqs=_seqs(rows=1 << 23), head_dim=1024, views=dict(
+        q_out=_heads(0x200000, 4096, 1024), k_out=_heads(0x400000, 4096, 1024))) == F.EUNSUPPORTED
 
 
 def test_rope_nothing_to_do(L):
