@@ -43,9 +43,17 @@ __device__ __forceinline__ void row_sincos(const RopeArgs& a, int64_t row, int p
     if (a.inverse) sn = -sn;
 }
 
+// The rows ahead of the first packed sequence, and those up to the last one's
+// end.
+__device__ __forceinline__ int64_t rows_begin(const SeqArgs& s) { return s.cu ? cu_at(s, 0) : 0; }
+__device__ __forceinline__ int64_t rows_end(const SeqArgs& s) {
+    return s.cu ? cu_at(s, s.B) : s.rows;
+}
+
 // True if `row` is one of a sequence's; `skip`: it is not to be written.
-__device__ __forceinline__ bool row_here(const SeqArgs& s, int64_t row, int64_t end, bool& skip) {
-    skip = row >= end;
+__device__ __forceinline__ bool row_here(const SeqArgs& s, int64_t row, int64_t begin, int64_t end,
+                                         bool& skip) {
+    skip = row < begin || row >= end;
     return !skip && (s.cu || row % s.cap < s.count[row / s.cap]);
 }
 
@@ -57,7 +65,7 @@ __global__ __launch_bounds__(256) void rope_pair_kernel(RopeArgs a) {
     const int64_t row = t / half;
     const int p = (int)(t % half);
     bool skip;
-    const bool here = row_here(a.seqs, row, a.seqs.cu ? cu_at(a.seqs, a.seqs.B) : a.seqs.rows, skip);
+    const bool here = row_here(a.seqs, row, rows_begin(a.seqs), rows_end(a.seqs), skip);
     if (skip) return;
     float sn = 0.0f, cs = 1.0f;
     const bool turn = p < a.R;
@@ -93,7 +101,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     using Vec = T __attribute__((ext_vector_type(V)));
     extern __shared__ float2 table[];  // [row][pair] cosine, sine
     const int R = a.R, tid = threadIdx.x;
-    const int64_t end = a.seqs.cu ? cu_at(a.seqs, a.seqs.B) : a.seqs.rows;
+    const int64_t begin = rows_begin(a.seqs), end = rows_end(a.seqs);
     const int64_t row0 = (int64_t)blockIdx.x * a.block_rows;
     const int rows = end - row0 < a.block_rows ? (int)(end - row0) : a.block_rows;
     if (rows <= 0) return;
@@ -139,7 +147,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
         for (int i = 0; i < kItems; ++i) {
             if (base + i * 256 >= total) break;
             bool skip;
-            const bool here = row_here(a.seqs, row0 + row[i], end, skip);
+            const bool here = row_here(a.seqs, row0 + row[i], begin, end, skip);
+            if (skip) continue;
             const bool turn = item[i] < turned;
             if constexpr (INTER) {
                 if (turn) {

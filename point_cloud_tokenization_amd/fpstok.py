@@ -508,7 +508,9 @@ def make_heads(t, name, heads=None, rows=None, like=None):
             raise ValueError("%s is on %s, expected %s" % (name, t.device, like.device))
         if t.shape[2] != like.shape[2]:
             raise ValueError("%s must have heads of %d elements" % (name, like.shape[2]))
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    # (the stride of a single row or head is not used, and may be anything)
+    return Heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0,
+                 t.stride(1) if t.shape[1] > 1 else 0)
 
 
 class _DeviceCall:

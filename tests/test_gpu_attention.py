@@ -495,6 +495,65 @@ def test_rope_sizes_strides_and_in_place(F, n):
         assert torch.equal(odd, out[0])
 
 
+# ------------------------------------------------ parts of larger batches
+
+@pytest.mark.parametrize("H,Hk", [(4, 2), (8, 1)])
+def test_rows_ahead_of_the_first_sequence(F, H, Hk):
+    """cu_seqlens that starts past 0 (some events of a larger batch): nothing
+    is read or written ahead of its rows."""
+    gen = torch.Generator().manual_seed(64)
+    cu = torch.tensor([37, 37, 140, 300], dtype=torch.int32)
+    n, D, pairs = 320, 64, (8, 8, 8, 8)
+    seq = [(37, 0), (37, 103), (140, 160)]
+    inside = torch.zeros(n, dtype=torch.bool)
+    inside[37:300] = True
+    q, k, v, go = (rand(gen, (n, h, D), torch.bfloat16) for h in (H, Hk, Hk, H))
+    for t in (q, k, v, go):
+        t[~inside] = float("nan")
+    pos = torch.randn((n, 4), generator=gen)
+    qs = F.make_seqs(n, cu_seqlens=cu.cuda())
+    fr = F.rope_frequencies(pairs)
+    log("rows ahead: rotary positions")
+    for width in (D, D - 1):  # 16 bytes at a time, and element by element
+        x = torch.full((n, H, D + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+        x[..., :D] = q.cuda()
+        src = q.cuda() if width == D else x[..., :D]
+        r = F.Rope(src, None, pos.cuda(), fr.cuda(), pairs, qs)
+        r.q_out.fill_(7.0)
+        got = r()[0]
+        torch.cuda.synchronize()
+        val, tol = ref.rope(torch.where(inside[:, None, None], q, torch.zeros_like(q)), pos, fr,
+                            pairs, False)
+        val[~inside.numpy()], tol[~inside.numpy()] = 7.0, 0.0
+        ref.check(got, (val, tol), "rope")
+    log("rows ahead: attention")
+    att = F.Attention(q.cuda(), k.cuda(), v.cuda(), qs, training=True)
+    for t in (att.out, att.lse) + att.grads:
+        t.fill_(7.0)
+    out, lse = att()
+    grads = att.backward(go.cuda())
+    torch.cuda.synchronize()
+    want = ref.attention(q, k, v, seq, seq, grad=go)
+    for name, t in zip(("out", "lse", "grad_q", "grad_k", "grad_v"), (out, lse) + grads):
+        assert bool((t[~inside] == 7.0).all()), name
+        val, tol = want[name]
+        ref.check(t[inside], (val[inside.numpy()], tol[inside.numpy()]), name)
+
+
+def test_strides_of_single_rows_and_heads(F):
+    """The stride of a dimension of one element is never used."""
+    gen = torch.Generator().manual_seed(65)
+    qs, seq, _ = layout(F, [1], "packed")
+    for H in (1, 4):
+        flat = rand(gen, (4 * 64,), torch.bfloat16)
+        q = flat.as_strided((1, H, 64), (1 << 30, 64 if H > 1 else 3, 1))
+        want = ref.attention(q, q, q, seq, seq)
+        dev = flat.cuda().as_strided(q.shape, q.stride())
+        out, _ = F.Attention(dev, dev, dev, qs)()
+        torch.cuda.synchronize()
+        ref.check(out, want["out"], "one row of %d heads" % H)
+
+
 # ----------------------------------------------------------- used together
 
 def test_tokens_through_a_layer(F):
