@@ -534,7 +534,7 @@ void attention_few_kernel(AttnArgs a) {
                 win.mask(s[b], j0 + b * 32, half, a.sinks, -INFINITY);
         }
         sm.grow(s, c);
-            sm.weights(s, c);
+        sm.weights(s, c);
 #pragma unroll
         for (int k = 0; k < KB * 2; ++k) {
             const Frag pf = to_frag<T>(s[k >> 1], k & 1);
