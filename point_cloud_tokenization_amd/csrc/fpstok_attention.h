@@ -31,7 +31,7 @@ struct AttnArgs {
     HeadsArg q, k, v, out, grad_out, grad_q, grad_k, grad_v;
     float* lse;    // [q rows][H], or null (forward)
     float* lse2;   // [H][q rows] log2(e) lse (backward)
-    float* delta;  // the same shape: sum of grad_out * out
+    float* delta;  // the same shape: sum of grad_out * out (or its exact value)
     int32_t H, Hk, D, dtype;
     int32_t G, g_shift;  // H / Hk; its logarithm if it is a power of two, else -1
     int32_t same_seqs;   // ks is qs

@@ -321,8 +321,20 @@ __device__ __forceinline__ float log_sum(float mc, float l) {
 // head and walks the tiles of BN keys they see.  Per tile a wave forms
 // S^T = K Q^T (keys in registers, its 32 rows across the lanes), so a row's
 // maximum and sum are a lane's own registers plus one exchange with lane ^ 32,
-// its factor is one value per lane, and the weights, rounded to the type, are
-// already the operand of O^T += V^T P^T.
+// its factor is one value per lane, and the weights, rounded to the type (a
+// product of 32-bit weights would run at an eighth of the rate; half a step of
+// the type on weights of one sign), are already the operand of O^T += V^T P^T.
+//
+// Two tiles' buffers: the next tile is on its way (global memory to LDS, no
+// registers) while this one is used.  At D = 128 the matrix cores bound it:
+// 16k causal, 16 heads on 4, bfloat16: 1.17 ms, 1.03 PFLOP/s, 84 % of a large
+// library product.  At D = 64 the vector unit does: a wave's 32 x 64 scores cost
+// it about 1000 cycles (exponential, product, maximum, sum and rounding of
+// each), the matrix cores half of that; a workgroup's sequence, its rows and
+// first tile take another 6000 to 7000 cycles, more than the walk of a short
+// event.  84k pulses, window 257, 8 heads on 2: 0.14 ms; 64 events of at most
+// 128 tokens, 12 heads: 14 us (7 us of bytes).  A third buffer cost 5 %, scores
+// formed one tile ahead 5 to 15 % (and spills at D = 128).
 template <class T, int DP, int BN>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, STEPS = DP / 16;
@@ -465,7 +477,13 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
 // against many keys): a workgroup takes 32 rows and its 4 waves take turns at
 // the key tiles, each with its own LDS, running maximum and sum; they are
 // joined at the end.  No wave waits for another inside the walk, so 4 tiles of
-// K and V per workgroup are on their way at a time.
+// K and V per workgroup are on their way at a time.  Bound by reading K and V
+// once: 256 padded events of up to 1024 tokens, 12 heads, 84 us; 4 sequences of
+// up to 131072 keys of 8 heads (32 query heads, D = 128), split, 170 us and 5 us
+// for the join: 5.2 TB/s, a large copy's rate.  Tiles of 64 keys leave one
+// workgroup per compute unit: 435 us there.  Sequences of more than 32 rows are
+// slower here (64 events of up to 128 tokens: 30 us against 14), for every 32
+// rows read all keys again.
 template <class T, int DP, int BN>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) > 3 ? 3 : 512 / (DP * (int)sizeof(T)))
 void attention_few_kernel(AttnArgs a) {
@@ -685,7 +703,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 // 64 keys: 1.45 and 1.43).  dS summed over the keys, which should be 0, gives the
 // difference to the exact delta: where one tile is all a row tile sees it is
 // formed from that tile first, and with a window of fewer than 32 keys (TWICE)
-// the whole walk is made twice.
+// the whole walk is made twice (at 256 events of up to 256 tokens this is 3 % of
+// the backward pass).
+//
+// 3 products where 2 are the gradient's own: forming S and dP here and again
+// for grad_k and grad_v costs 2 of 7, and adding one kernel's grad_q up over the
+// workgroups of a sequence's keys would cost a float32 result per workgroup, or
+// atomics whose order changes it.  6000 + 2111 + 64 rows, 16 heads on 8, D =
+// 128, bfloat16: 0.48 ms, 1.04 PFLOP/s; 256 events of up to 256 tokens, 12
+// heads, D = 64: 114 us.
 template <class T, int DP, int BN, bool TWICE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
@@ -861,7 +887,9 @@ __device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk)
 // tile: in a long sequence that is nearly every row, and one workgroup walking
 // them all would take longer than everything else.  A workgroup takes a chunk
 // of them, its waves 32 rows in turn; nothing is masked.  The chunks' parts
-// are added in order by the kernel below.
+// are added in order by the kernel below.  (40k + 12k + 2.5k pulses, 4 sinks, 8
+// heads on 4: the walk in one workgroup 4 ms, in chunks 27 us.  At float32 and
+// D > 64 its two results and two operands pass the registers and spill.)
 template <class T, int DP>
 __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 128 ? 2 : 1)
 void attention_sink_kernel(AttnArgs a) {
@@ -1005,7 +1033,9 @@ __device__ __forceinline__ int64_t k_part_at(const AttnArgs& a, int split, int h
 // dV^T += dO^T P and dK^T += Q^T dS.  The gradients of the group's heads add up
 // in the accumulators, in a fixed order.  Where that leaves few workgroups (few
 // keys, many queries or heads) the walk is split over several, whose parts are
-// added by the kernel below.
+// added by the kernel below.  4 products: 6000 + 2111 + 64 rows, D = 128: 0.73 ms,
+// 0.91 PFLOP/s (V's operands from LDS, for its registers hold accumulators); at
+// D = 64 the vector unit bounds it: 256 events of up to 256 tokens, 143 us.
 template <class T, int DP, int BQ>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1)
 void attention_dkv_kernel(AttnArgs a) {

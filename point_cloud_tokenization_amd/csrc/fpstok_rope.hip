@@ -94,7 +94,11 @@ __global__ __launch_bounds__(256) void rope_pair_kernel(RopeArgs a) {
 // sines and cosines are formed once, in LDS, for all heads of q and k; then a
 // thread turns 16 bytes (interleaved) or 16 bytes and their partners R
 // elements further (half), kItems of them on their way at a time, adjacent
-// threads adjacent in memory.
+// threads adjacent in memory.  Bound by the bytes: 150,000 rows of 16 + 4 heads of
+// 128 bfloat16 in 0.29 to 0.31 ms, 5.0 to 5.3 TB/s (a large copy's rate); 5,541
+// rows of 12 + 4 heads of 64 in 8 us, of which a launch is half; one event's 128
+// rows in 4.7 us, a launch.  One element pair per thread, above, took 362, 11 and
+// 8.5 us.
 template <class T, bool INTER>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     constexpr int V = 16 / (int)sizeof(T), kItems = 4;
