@@ -692,6 +692,50 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
                   : some ? (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f : -INFINITY;
 }
 
+// The same for many rows: 4 elements of one (query, head) per thread, its parts
+// one after the other.
+template <class T>
+__global__ __launch_bounds__(256) void attention_join_rows_kernel(AttnArgs a) {
+    using f4 = float __attribute__((ext_vector_type(4)));
+    using T4 = T __attribute__((ext_vector_type(4)));
+    const uint32_t per = (uint32_t)a.D / 4;
+    const uint32_t x = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t rh = x / per;
+    const int d = (int)(x - rh * per) * 4;
+    const uint32_t row = rh / (uint32_t)a.H;
+    if (row >= a.qs.rows) return;
+    const int h = (int)(rh - row * (uint32_t)a.H), hk = h / a.G;
+    bool here = true;
+    if (a.qs.cu) {
+        if (row < cu_at(a.qs, 0) || row >= cu_at(a.qs, a.qs.B)) return;
+    } else {
+        const uint32_t b = row / (uint32_t)a.qs.cap;
+        here = (int)(row - b * (uint32_t)a.qs.cap) < a.qs.count[b];
+    }
+    const int64_t step = (int64_t)a.Hk * a.qs.rows * a.G;
+    const int64_t at = ((int64_t)hk * a.qs.rows + row) * a.G + h - hk * a.G;
+    float top = -INFINITY, sum = 0.0f;
+    f4 y = 0.0f;
+    if (here) {
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_ml[s * step + at].x);
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 z = a.part_ml[s * step + at];
+            const float f =
+                z.x == -INFINITY && z.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(z.x - top);
+            sum += z.y * f;
+            y += f * *(const f4*)(a.part + (s * step + at) * a.D + d);
+        }
+    }
+    const bool some = here && (top != -INFINITY || sum != 0.0f);
+    y *= some ? 1.0f / sum : 0.0f;
+    if (!some) y = 0.0f;
+    *(T4*)((T*)a.out.data + row * a.out.row + h * a.out.head + d) = __builtin_convertvector(y, T4);
+    if (a.lse && d == 0)
+        a.lse[(int64_t)row * a.H + h] = !here ? 0.0f : some ? log_sum(top, sum) : -INFINITY;
+}
+
 // grad_q, and the rows' statistics for the kernel below.  Rows and key tiles as
 // in the forward kernel; per 32 keys a wave forms S^T = K Q^T and
 // dP^T = V dO^T, and dS^T = P^T (dP^T - delta), rounded to the type, is the
@@ -1333,16 +1377,16 @@ int64_t row_slots(const SeqArgs& s, int G, int shift) {
     return (int64_t)s.B * (((int64_t)s.cap * G + (1 << shift) - 1) >> shift);
 }
 
-// Splits a row's keys until the grid has `want` workgroups, but not into
-// parts of fewer than `least` keys.
-static int key_splits(const AttnArgs& a, int64_t blocks, int64_t q_len, int64_t k_len,
-                      int64_t want, int64_t least) {
+// Splits a row's keys until about `want` workgroups are there, into at least
+// `least` keys each.
+static int64_t key_splits(const AttnArgs& a, int64_t blocks, int64_t q_len, int64_t k_len,
+                          int64_t want, int64_t least) {
     int64_t seen = k_len;
     if (a.left >= 0 && a.right >= 0 && seen > q_len + a.left + a.right + a.sinks)
         seen = q_len + a.left + a.right + a.sinks;
-    int64_t n = (want + blocks - 1) / (blocks > 0 ? blocks : 1);
+    int64_t n = blocks > 0 ? want / blocks : 1;
     if (n > seen / least) n = seen / least;
-    return n < 1 ? 1 : n > 256 ? 256 : (int)n;
+    return n < 1 ? 1 : n > 256 ? 256 : n;
 }
 
 AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
@@ -1350,20 +1394,36 @@ AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
     AttnPlan p;
     p.few = (int64_t)q_len * G <= 32;
     const int64_t blocks = row_slots(a.qs, G, p.few ? 5 : 7) * a.Hk;
-    p.splits = p.few ? key_splits(a, blocks, q_len, k_len, 1024, 512)
-                     : key_splits(a, blocks, 128 / G + 1, k_len, 512, 1024);
+    if (p.few) {
+        p.splits = (int32_t)key_splits(a, blocks, q_len, k_len, 1024, 512);
+    } else {
+        // two workgroups per compute unit, unless nearly every one has a
+        // workgroup already (5000 rows, 5 heads of 64: 200 workgroups, 2 parts
+        // 74 us, unsplit 95; 2000 rows, 16 heads on 4, D = 128: 252 workgroups, 2
+        // parts 59 us, unsplit 52); 2500 rows of one head, parts of 256 keys or
+        // more 19 us, of 512 21
+        p.splits =
+            blocks > 224 ? 1 : (int32_t)key_splits(a, blocks, 128 / G + 1, k_len, 512, 256);
+    }
     return p;
 }
 
 int plan_key_parts(const AttnArgs& a, int32_t q_len) {
-    // workgroups of 128 keys, each with a walk of about this many queries
+    // workgroups of 128 keys, each with a walk of about this many queries, in at
+    // most as many parts as all run at once (5000 rows, 8 heads on 1: 10 parts of
+    // 40 workgroups 382 us a training step, 13 parts 430; 8 heads on 8, 320
+    // workgroups: unsplit 397, 2 parts 412) and in
+    // parts of 192 or more (a walk alone on its compute unit takes 1.6 us per 64
+    // queries, the join 5 us.  One event of 110 tokens, 8 heads on 1, all of a
+    // training step: parts of 512 or more 43 us, of 192 34; 21 padded events of
+    // up to 256 tokens, 12 heads: of 192 43 us, of 128 54)
     const int64_t blocks = row_slots(a.ks, 1, 7) * a.Hk;
     int64_t walk = q_len;
     if (a.left >= 0 && a.right >= 0 && walk > 128 + a.left + a.right)
         walk = 128 + (int64_t)a.left + a.right;
     walk *= a.G;
-    int64_t n = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
-    if (n > walk / 512) n = walk / 512;
+    int64_t n = blocks > 0 ? 512 / blocks : 1;
+    if (n > walk / 192) n = walk / 192;
     return n < 1 ? 1 : n > 64 ? 64 : (int)n;
 }
 
@@ -1383,8 +1443,16 @@ static hipError_t forward(const AttnArgs& a, const AttnPlan& plan, hipStream_t s
         else
             attention_kernel<T, 128, k16 ? 64 : 32><<<grid, 256, 0, s>>>(a);
     }
-    if (a.splits > 1)
-        attention_join_kernel<T><<<dim3((unsigned)(a.qs.rows * a.H)), 256, 0, s>>>(a);
+    if (a.splits > 1) {
+        // a workgroup per (query, head) for few of them (one query on 131k keys
+        // in 32 parts: 175 us against 180), a thread per 4 elements for many
+        // (5000 rows, 3 heads: 48 us against 64)
+        const int64_t joins = (a.qs.rows * a.H * (a.D / 4) + 255) / 256;
+        if (joins >= 128)
+            attention_join_rows_kernel<T><<<dim3((unsigned)joins), 256, 0, s>>>(a);
+        else
+            attention_join_kernel<T><<<dim3((unsigned)(a.qs.rows * a.H)), 256, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 

@@ -495,6 +495,18 @@ def test_rope_sizes_strides_and_in_place(F, n):
         assert torch.equal(odd, out[0])
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("form", ["packed", "padded"])
+@pytest.mark.parametrize("q_lens,k_lens,H,Hk,D,right", [
+    ([700], None, 4, 2, 64, -1), ([601, 0, 77], None, 6, 2, 40, 0),
+    ([40, 3], [2000, 0], 4, 2, 64, -1), ([1100], [900], 2, 1, 128, 0)])
+def test_rows_whose_keys_are_split(F, dtype, form, q_lens, k_lens, H, Hk, D, right):
+    """Few workgroups: several take parts of a row's keys, joined for few rows
+    and for many."""
+    run(F, "split", q_lens, k_lens, H=H, Hk=Hk, D=D, dtype=dtype, right=right, form=form,
+        extra=5 if form == "packed" else 0)
+
+
 # ------------------------------------------------ parts of larger batches
 
 @pytest.mark.parametrize("H,Hk", [(4, 2), (8, 1)])
