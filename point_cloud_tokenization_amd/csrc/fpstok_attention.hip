@@ -1401,9 +1401,11 @@ AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
         // workgroup already (5000 rows, 5 heads of 64: 200 workgroups, 2 parts
         // 74 us, unsplit 95; 2000 rows, 16 heads on 4, D = 128: 252 workgroups, 2
         // parts 59 us, unsplit 52); 2500 rows of one head, parts of 256 keys or
-        // more 19 us, of 512 21
-        p.splits =
-            blocks > 224 ? 1 : (int32_t)key_splits(a, blocks, 128 / G + 1, k_len, 512, 256);
+        // more 19 us, of 512 21.  float32 tiles take 8 times as long, and four
+        // workgroups even the compute units out (3000 rows, 12 heads of 64: 320
+        // us, unsplit 450; 1500 rows: 114, with two 96).
+        const int64_t want = a.dtype == 0 ? 1024 : blocks > 224 ? 0 : 512;
+        p.splits = (int32_t)key_splits(a, blocks, 128 / G + 1, k_len, want, 256);
     }
     return p;
 }
