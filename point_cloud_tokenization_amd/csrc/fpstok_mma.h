@@ -238,13 +238,13 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(wave_uniform(base))
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(wave_uniform(base))
-                 : "memory");
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
