@@ -469,7 +469,9 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
         a.lse[q.row * a.H + q.h] = !q.live ? 0.0f : some ? log_sum(sm.mc, sm.l) : -INFINITY;
     if (bad) {
         __syncthreads();
-        if (q.live && half == 0) add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, vb, a.v.row);
+        // (a row whose every score is -infinity stays 0)
+        if (q.live && some && half == 0)
+            add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, vb, a.v.row);
     }
 }
 
@@ -615,9 +617,13 @@ void attention_few_kernel(AttnArgs a) {
     if (bad) {
         __syncthreads();
         if (wave == 0 && half == 0 && q.live) {
+            bool some = false;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                some |= !(ml[w][q.r].x == -INFINITY && ml[w][q.r].y == 0.0f);
             if (a.splits > 1)
                 add_bad_keys<BN>(a.part + (part0 + q.r) * a.D, a, kt, n, q, t.tk, win, vb, a.v.row);
-            else
+            else if (some)  // (a row whose every score is -infinity stays 0)
                 add_bad_keys<BN>((T*)a.out.data + q.row * a.out.row + q.h * a.out.head, a, kt, n, q,
                                  t.tk, win, vb, a.v.row);
         }
