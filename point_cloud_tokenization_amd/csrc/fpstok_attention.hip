@@ -861,10 +861,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)gf[s][e], (float)of[s][e], delta);
-    delta = pair_sum(delta);
-    // a row that sees nothing: every weight is masked, the value only has to
-    // be finite
-    lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
+    // a row that sees nothing, or nothing but scores of -infinity: its weights
+    // are exp2(score - infinity) = 0, here and for grad_k and grad_v
+    const bool some = lse != -INFINITY;
+    delta = some ? pair_sum(delta) : 0.0f;
+    lse2 = some ? lse * kLog2e : INFINITY;
     if (n > 0) arrive(0);
     __syncthreads();
     float off_by = 0.0f;
@@ -902,7 +903,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     if (q.live && half == 0) {
         const int64_t at = (int64_t)q.h * a.qs.rows + q.row;
         a.lse2[at] = lse2;
-        a.delta[at] = delta;
+        a.delta[at] = some ? delta : 0.0f;
     }
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
@@ -917,11 +918,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
         __syncthreads();
     }
     T* out = (T*)a.grad_q.data + q.row * a.grad_q.row + q.h * a.grad_q.head;
-    zero_unless<DB>(dq, q.live);
+    zero_unless<DB>(dq, q.live && some);
     store_row<T, DB>(dq, a.scale, q.live || q.r < t.pad ? out : nullptr, a.D, lane);
     if (bad) {
         __syncthreads();
-        if (q.live && half == 0) add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, kb, a.k.row);
+        if (q.live && some && half == 0) add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, kb, a.k.row);
     }
 }
 
@@ -936,7 +937,8 @@ __device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk)
 // The sinks' gradients from the rows that see nothing else of the first key
 // tile: in a long sequence that is nearly every row, and one workgroup walking
 // them all would take longer than everything else.  A workgroup takes a chunk
-// of them, its waves 32 rows in turn; nothing is masked.  The chunks' parts
+// of them, its waves 32 rows in turn; nothing is masked.  Rows without weights,
+// and rows past the last one, have lse2 = infinity (see below).  The chunks' parts
 // are added in order by the kernel below.  (40k + 12k + 2.5k pulses, 4 sinks, 8
 // heads on 4: the walk in one workgroup 4 ms, in chunks 27 us.  At float32 and
 // D > 64 its two results and two operands pass the registers and spill.)
@@ -1004,11 +1006,19 @@ void attention_sink_kernel(AttnArgs a) {
             const int r = lane & 31, last = rows - x - 1;
             const int64_t at = (int64_t)(hk * G + g) * a.qs.rows + row0 + x + (r < last ? r : last);
             st = make_float2(a.lse2[at], a.delta[at]);
-            if (r > last) st = make_float2(0.0f, 0.0f);
+            if (r > last) st = make_float2(INFINITY, 0.0f);
         };
         if (wave * 32 < rows) load(0, wave * 32);
         for (int g = 0, x = wave * 32; g < G && x < rows;) {
             wave_sync();  // the wave's reads of the last tile are done
+            const uint32_t gone = (uint32_t)__ballot(st.x == INFINITY);
+            if (gone != 0) {
+                sq.have = 32;  // (rows past the last one are copies of it)
+                sq.finite(gone, lane);
+                sg.drop(gone, lane);
+#pragma unroll
+                for (int e = 0; e < STEPS; ++e) vf[e] = frag_clean<T>(vf[e]);
+            }
             sq.store(qbuf, a.D, lane);
             sg.store(gbuf, a.D, lane);
             if (half == 0) stat[wave][0][lane] = st.x, stat[wave][1][lane] = st.y;
@@ -1086,6 +1096,14 @@ __device__ __forceinline__ int64_t k_part_at(const AttnArgs& a, int split, int h
 // added by the kernel below.  4 products: 6000 + 2111 + 64 rows, D = 128: 0.73 ms,
 // 0.91 PFLOP/s (V's operands from LDS, for its registers hold accumulators); at
 // D = 64 the vector unit bounds it: 256 events of up to 256 tokens, 143 us.
+//
+// A query whose every visible score is -infinity adds nothing: its lse2 is
+// infinity, so its weights exp2(score - infinity) are 0 as long as its scores
+// stay below infinity and nothing they multiply is infinite.  A tile with such
+// queries keeps the signs of their infinite elements only (1 in their place: a
+// term of a score that was -infinity stays so, or is finite) and takes 0 for
+// their gradient and for infinite values (any other query that sees one of those has
+// a delta that is not finite).
 template <class T, int DP, int BQ>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1)
 void attention_dkv_kernel(AttnArgs a) {
@@ -1202,8 +1220,10 @@ void attention_dkv_kernel(AttnArgs a) {
         dma_wait();
         if (!tile_all.has(xn)) {
             FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
-            const bool bq = dma.clean(buf, tid), bg = dma.clean(buf + BQ * Tl::kPitch, tid);
-            if (bq || bg) bad = 1;
+            // (a query with infinite elements has no finite score: its weights are
+            // 0, or its lse and with it all it adds is not a number)
+            Dma<T, DP, BQ>::finite(buf, ~0ull, tid);
+            if (dma.clean(buf + BQ * Tl::kPitch, tid)) bad = 1;
         }
     };
 
@@ -1267,9 +1287,22 @@ void attention_dkv_kernel(AttnArgs a) {
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int x0 = xn;
-        if (i + 1 < n) load(i + 1);
-        const FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
+        FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
         const float(*st)[64] = stat[i & 1];
+        // (the bits past BQ rows are the next tile's)
+        const uint64_t gone = __ballot(st[0][lane] == INFINITY);
+        if (gone != 0) {
+            Dma<T, DP, BQ>::finite(qbuf, gone, tid);
+            Dma<T, DP, BQ>::drop(qbuf + BQ * Tl::kPitch, gone, tid);
+            if constexpr (kVLds) {
+                Dma<T, DP, 128>::clean(lds + kV, tid);
+            } else {
+#pragma unroll
+                for (int e = 0; e < STEPS; ++e) vf[e] = frag_clean<T>(vf[e]);
+            }
+            __syncthreads();
+        }
+        if (i + 1 < n) load(i + 1);
 #pragma unroll
         for (int b = 0; b < QB; ++b)
             if (wave_live && wave_any.has(x0 + b * 32))
@@ -1308,9 +1341,13 @@ void attention_dkv_kernel(AttnArgs a) {
     }
     zero_unless<DB>(dk, live);
     zero_unless<DB>(dv, live);
-    // add_bad over the queries of this workgroup's part that see this key in
-    // tiles that the workgroup's keys do not all see whole
-    auto add_hidden = [&](auto* to_k, auto* to_v) {
+    // formed anew: at D = 128 no register is left to keep what follows from it
+    int lane_end = lane;
+    asm volatile("" : "+v"(lane_end));
+    // add_bad to grad_v over the queries of this workgroup's part that see this
+    // key, and have weights, in tiles that the workgroup's keys do not all see
+    // whole (grad_k has their delta, which is not finite either)
+    auto add_hidden = [&](auto* to_v) {
         __syncthreads();
         if (!live || half != 0 || e1 < e0) return;
 #pragma unroll 1
@@ -1320,7 +1357,7 @@ void attention_dkv_kernel(AttnArgs a) {
 #pragma unroll 1
             for (int y = x > e0 ? x : e0; y < x + BQ && y <= e1; ++y) {
                 const int64_t row = t.q0 + y, h = (int64_t)t.hk * G + g;
-                add_bad(to_k, (const T*)a.q.data + row * a.q.row + h * a.q.head, a.D);
+                if (a.lse2[h * a.qs.rows + row] == INFINITY) continue;
                 add_bad(to_v,
                         (const T*)a.grad_out.data + row * a.grad_out.row + h * a.grad_out.head,
                         a.D);
@@ -1330,17 +1367,17 @@ void attention_dkv_kernel(AttnArgs a) {
     if (a.k_splits > 1) {
         float* part = a.k_part + k_part_at(a, t.part, t.hk, krow);
         float* part_v = part + k_part_at(a, 0, a.Hk, 0);
-        store_row<float, DB>(dk, 1.0f, live ? part : nullptr, a.D, lane);
-        store_row<float, DB>(dv, 1.0f, live ? part_v : nullptr, a.D, lane);
-        if (bad) add_hidden(part, part_v);
+        store_row<float, DB>(dk, 1.0f, live ? part : nullptr, a.D, lane_end);
+        store_row<float, DB>(dv, 1.0f, live ? part_v : nullptr, a.D, lane_end);
+        if (bad) add_hidden(part_v);
         return;
     }
     T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
     T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
     const bool write = live || r < t.pad;
-    store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane);
-    store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane);
-    if (bad) add_hidden(ok, ov);
+    store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane_end);
+    store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane_end);
+    if (bad) add_hidden(ov);
 }
 
 // Adds the parts of keys whose walk was split, in order: 4 elements of one key

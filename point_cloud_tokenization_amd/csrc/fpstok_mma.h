@@ -31,6 +31,7 @@ struct Elem<__bf16> {
     using Frag = __bf16 __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7f807f80u;  // exponent bits of two elements
     static constexpr uint32_t kOne = 0x00800080u;
+    static constexpr uint32_t kUnit = 0x3f80u;  // 1.0
     static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
@@ -41,6 +42,7 @@ struct Elem<_Float16> {
     using Frag = _Float16 __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7c007c00u;
     static constexpr uint32_t kOne = 0x04000400u;
+    static constexpr uint32_t kUnit = 0x3c00u;  // 1.0
     static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
@@ -51,6 +53,7 @@ struct Elem<float> {
     using Frag = float __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7f800000u;
     static constexpr uint32_t kOne = 0x00800000u;
+    static constexpr uint32_t kUnit = 0x3f800000u;  // 1.0
     static __device__ __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -149,20 +152,32 @@ __device__ __forceinline__ bool chunk_bad(u32x4 x) {
     return (acc & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u)) != 0;
 }
 
-// The chunk with its infinite and not-a-number elements replaced by zero.
-template <class T>
+// The chunk with its infinite and not-a-number elements replaced by zero, or,
+// SIGN, by 1 of their sign.
+template <class T, bool SIGN = false>
 __device__ __forceinline__ u32x4 chunk_clean(u32x4 x) {
+    constexpr uint32_t one = SIGN ? Elem<T>::kUnit : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t c = (x[i] & Elem<T>::kExp) + Elem<T>::kOne;
         if constexpr (sizeof(T) == 2) {
-            if (c & 0x80000000u) x[i] &= 0x0000ffffu;
-            if (c & 0x00008000u) x[i] &= 0xffff0000u;
+            constexpr uint32_t sign = SIGN ? 0x8000u : 0;
+            if (c & 0x80000000u) x[i] = (x[i] & (sign << 16 | 0xffffu)) | one << 16;
+            if (c & 0x00008000u) x[i] = (x[i] & (sign | 0xffff0000u)) | one;
         } else {
-            if (c & 0x80000000u) x[i] = 0;
+            if (c & 0x80000000u) x[i] = (x[i] & (SIGN ? 0x80000000u : 0)) | one;
         }
     }
     return x;
+}
+
+// A lane's operand with its infinite and not-a-number elements replaced by zero.
+template <class T>
+__device__ __forceinline__ typename Elem<T>::Frag frag_clean(typename Elem<T>::Frag f) {
+    u32x4* x = (u32x4*)&f;
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(f) / 16; ++e) x[e] = chunk_clean<T>(x[e]);
+    return f;
 }
 
 // Rows of a tile on their way from memory to LDS, by THREADS threads: load()
@@ -207,6 +222,20 @@ struct Stage {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             *(FPSTOK_LDS u32x4*)(t + Tl::place(i * kStep + row(tid), chunk(tid))) = x[i];
+    }
+    // Rows whose bit is set become zero.
+    __device__ __forceinline__ void drop(uint32_t rows, int tid) {
+        static_assert(ROWS <= 32, "a bit per row");
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (rows >> (i * kStep + row(tid)) & 1) x[i] = 0;
+    }
+    // Infinite elements of rows whose bit is set become 1 of their sign.
+    __device__ __forceinline__ void finite(uint32_t rows, int tid) {
+        static_assert(ROWS <= 32, "a bit per row");
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (rows >> (i * kStep + row(tid)) & 1) x[i] = chunk_clean<T, true>(x[i]);
     }
     // Infinite and not-a-number elements of rows that exist become zero; true
     // if there were any.
@@ -297,9 +326,27 @@ struct Dma {
             }
         }
     }
-    // After dma_wait: infinite and not-a-number elements of the chunks this
-    // thread loaded become zero; true if there were any.
-    __device__ __forceinline__ bool clean(FPSTOK_LDS char* buf, int tid) const {
+    // After dma_wait, of the chunks this thread loaded: rows whose bit is set
+    // become zero; their infinite elements become 1 of their sign; all infinite
+    // and not-a-number elements become zero (true if there were any).
+    static __device__ __forceinline__ void drop(FPSTOK_LDS char* buf, uint64_t rows, int tid) {
+        static_assert(ROWS <= 64, "a bit per row");
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i)
+            if (rows >> (i * kStep + tid / Tl::kChunks) & 1)
+                *(FPSTOK_LDS u32x4*)(buf + i * 4096 + tid * 16) = 0;
+    }
+    static __device__ __forceinline__ void finite(FPSTOK_LDS char* buf, uint64_t rows, int tid) {
+        static_assert(ROWS <= 64, "a bit per row");
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+            FPSTOK_LDS u32x4* p = (FPSTOK_LDS u32x4*)(buf + i * 4096 + tid * 16);
+            const u32x4 x = *p;
+            if (chunk_bad<T>(x) && (rows >> (i * kStep + tid / Tl::kChunks) & 1))
+                *p = chunk_clean<T, true>(x);
+        }
+    }
+    static __device__ __forceinline__ bool clean(FPSTOK_LDS char* buf, int tid) {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {

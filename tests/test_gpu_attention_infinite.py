@@ -5,15 +5,28 @@ elements of one sign) has weight 0: the key adds nothing to its queries, and a
 query whose every visible score is -infinity counts as one that sees no key.
 What is left is compared with the reference of the same inputs with those
 pairs hidden, whether the kernels see a tile whole or in part."""
+import numpy as np
 import pytest
 import torch
 
+from tests import attention_ref as ref
 from tests.gpu_util import log
 from tests.test_gpu_attention import DT, F, layout, rand  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
+
+
+def reference(hide, *args, **kw):
+    """ref.attention with the pairs hide(tq, tk) (True: hidden) added to the
+    mask."""
+    keep = ref.visible
+    try:
+        ref.visible = lambda tq, tk, *w: keep(tq, tk, *w) & ~hide(tq, tk)
+        return ref.attention(*args, **kw)
+    finally:
+        ref.visible = keep
 
 
 # lengths, keys' lengths, H, Hk, window, sinks: one tile seen in part; whole
@@ -43,6 +56,69 @@ def inputs(F, shape, D, dtype, seed):  # noqa: F811
     q[..., 3] = q[..., 3].abs() + 0.5
     k[..., 3] = k[..., 3].abs() + 0.5
     return qs, ks, q_seq, k_seq, q, k, v, go
+
+
+def compute(F, shape, qs, ks, q, k, v, go):  # noqa: F811
+    att = F.Attention(q.cuda(), k.cuda(), v.cuda(), qs, ks, shape[4], shape[5], None, True)
+    out, lse = att()
+    grads = att.backward(go.cuda())
+    torch.cuda.synchronize()
+    return dict(zip(("out", "lse", "grad_q", "grad_k", "grad_v"), (out, lse) + grads))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("bad_grad", [False, True])
+def test_query_whose_scores_are_minus_infinity(F, shape, D, dtype, bad_grad):  # noqa: F811
+    """It gets 0 and -infinity, and adds nothing to any gradient, whatever its
+    own gradient is."""
+    log("infinite query %s D=%d %s %s" % (shape, D, dtype, bad_grad))
+    qs, ks, q_seq, k_seq, q, k, v, go = inputs(F, shape, D, dtype, 82)
+    n = q.shape[0]
+    rows = sorted({n // 3, n // 2, n - 1})
+    fixed, fixed_go = q.clone(), go.clone()
+    q[rows, :, 3] = -INF
+    fixed[rows, :, 3] = 0.0
+    if bad_grad:
+        go[rows[:1]], go[rows[1:], :, 5] = INF, float("nan")
+        fixed_go[rows] = 0.0
+
+    def hide(tq, tk):
+        h = np.zeros((tq, tk), dtype=bool)
+        h[rows] = True
+        return h
+
+    got = compute(F, shape, qs, ks, q, k, v, go)
+    want = reference(hide, fixed, k, v, q_seq, k_seq, *shape[4], shape[5], grad=fixed_go)
+    for name, t in got.items():
+        ref.check(t, want[name], name)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_key_seen_by_such_queries_only(F, D, dtype, sinks):  # noqa: F811
+    """Its gradients are 0, whatever it and its value hold."""
+    log("infinite pairs D=%d %s sinks %d" % (D, dtype, sinks))
+    shape = ([300], None, 4, 2, (0, 0), sinks)
+    qs, ks, q_seq, k_seq, q, k, v, go = inputs(F, shape, D, dtype, 85)
+    rows = [5, 100, 131, 299]
+    fixed = [t.clone() for t in (q, k, v, go)]
+    q[rows, :, 3], k[rows[1:], :, 3] = -INF, INF
+    v[rows, :, 4], go[rows, :, 5] = INF, -INF
+    for t in fixed:
+        t[rows] = 0.0
+
+    def hide(tq, tk):
+        h = np.zeros((tq, tk), dtype=bool)
+        h[rows] = True
+        return h
+
+    got = compute(F, shape, qs, ks, q, k, v, go)
+    want = reference(hide, *fixed[:3], q_seq, k_seq, *shape[4], shape[5], grad=fixed[3])
+    for name, t in got.items():
+        ref.check(t, want[name], name)
 
 
 @pytest.mark.parametrize("dtype", list(DT))
