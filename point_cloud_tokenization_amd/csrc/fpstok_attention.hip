@@ -167,15 +167,17 @@ struct Window {
     }
 };
 
-// Adds the infinite and not-a-number elements of `src` to `dst`: the result
-// of a row that sees them, where a tile that other rows do not see whole was
-// multiplied without them.  Rare, so it works on the stored result.
-template <class T, class TO>
+// Adds the infinite and not-a-number elements of `src`, or, ZERO, 0 times
+// them, to `dst`: the result of a row that sees them, where a tile that other
+// rows do not see whole was multiplied without them.  Rare, so it works on
+// the stored result.
+template <bool ZERO = false, class T, class TO>
 __device__ __forceinline__ void add_bad(TO* dst, const T* src, int D) {
 #pragma unroll 1
     for (int d = 0; d < D; ++d) {
         const float x = (float)src[d];
-        if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) dst[d] = (TO)((float)dst[d] + x);
+        if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) 
+            dst[d] = (TO)((float)dst[d] + (ZERO ? NAN : x));
     }
 }
 
@@ -238,7 +240,7 @@ struct QueryRows {
 
 // add_bad over the keys that one row sees of the tiles that the workgroup's
 // rows do not all see whole.
-template <int BN, class T, class TO>
+template <int BN, bool ZERO = false, class T, class TO>
 __device__ __forceinline__ void add_bad_keys(TO* dst, const AttnArgs& a, const KeyTiles<BN>& kt,
                                              int n, const QueryRows& q, int tk, const Window& w,
                                              const T* base, int64_t stride) {
@@ -248,7 +250,7 @@ __device__ __forceinline__ void add_bad_keys(TO* dst, const AttnArgs& a, const K
         if (tile_view<BN>(a, q.pa, q.pb, tk, j0) != 1) continue;
 #pragma unroll 1
         for (int j = j0; j < j0 + BN && j < tk; ++j)
-            if (!w.hides(j)) add_bad(dst, base + j * stride, a.D);
+            if (!w.hides(j)) add_bad<ZERO>(dst, base + j * stride, a.D);
     }
 }
 
@@ -762,6 +764,12 @@ __global__ __launch_bounds__(256) void attention_join_rows_kernel(AttnArgs a) {
 // atomics whose order changes it.  6000 + 2111 + 64 rows, 16 heads on 8, D =
 // 128, bfloat16: 0.48 ms, 1.04 PFLOP/s; 256 events of up to 256 tokens, 12
 // heads, D = 64: 114 us.
+//
+// A tile that some row does not see whole loses its infinite elements of K.  A
+// key that lost some has no finite score: in a row that sees it the score is
+// -infinity and the weight 0, or the row's lse is not a number and with it
+// its whole gradient.  So the scores of such keys are set to -infinity, and 0
+// times the lost element, which is not a number, is added after the walk.
 template <class T, int DP, int BN, bool TWICE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kernel(AttnArgs a) {
     constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
@@ -769,6 +777,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
     __shared__ int bad;
+    __shared__ int lost[2][BN];  // of a buffer's keys: 1 + the tile in which one lost elements
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -808,7 +817,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {
         dma_wait();
-        if (all.of(a, jn) == 1 && dma.clean(lds + (i & 1) * 2 * BN * Tl::kPitch, tid)) bad = 1;
+        if (all.of(a, jn) != 1) return;
+        FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
+        const uint32_t chunks = dma.clean(buf, tid);
+        if (chunks == 0) return;
+#pragma unroll 1
+        for (int k = 0; k < dma.kPer; ++k)
+            if (chunks >> k & 1) lost[i & 1][k * dma.kStep + dma.row] = i + 1;
+        bad = i + 1;
     };
 
     f32x16 dq[DB];
@@ -816,8 +832,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
     const float c = a.scale * kLog2e;
     float delta = 0.0f, lse2 = 0.0f;
+    // tile i may hold keys that lost elements
+    auto lost_in = [&](int i) { return __builtin_amdgcn_readfirstlane(bad) > i; };
+    // the scores of such keys, of 32 from row b of tile i on
+    auto hide_lost = [&](f32x16& x, int b, int i) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            x[e] = lost[i & 1][b + (e >> 2) * 8 + half * 4 + (e & 3)] == i + 1 ? -INFINITY : x[e];
+    };
     // sum of dS over the keys of 32 rows from row b of the tile at kbuf on
-    auto add_delta = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask, float& sum) {
+    auto add_delta = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask, bool holes, int i,
+                         float& sum) {
         f32x16 x = 0.0f, y = 0.0f;
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
@@ -825,6 +850,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
             x = Elem<T>::mma(Tl::row_frag(kbuf, row, st, half), qf[st], x);
             y = Elem<T>::mma(Tl::row_frag(kbuf + BN * Tl::kPitch, row, st, half), gf[st], y);
         }
+        if (holes) hide_lost(x, b, i);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -lse2)) * (y[e] - delta);
@@ -832,7 +858,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
 #pragma unroll
         for (int e = 0; e < 16; ++e) sum += x[e];
     };
-    auto block = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask) {
+    auto block = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask, bool holes, int i) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
 #pragma unroll
@@ -840,6 +866,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
             x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
         }
+        if (holes) hide_lost(x, b * 32, i);
         f32x16 ds;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -854,6 +881,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
         }
     };
     if (tid == 0) bad = 0;
+    if (tid < 2 * BN) lost[tid / BN][tid % BN] = 0;
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
     if (n > 0) load(0);
@@ -873,7 +901,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
 #pragma unroll 1
         for (int b = 0; b < BN; b += 32) {
             const int view = mine.of(a, jn + b);
-            if (view != 0) add_delta(lds, b, jn, view == 1, off_by);
+            if (view != 0) add_delta(lds, b, jn, view == 1, lost_in(0), 0, off_by);
         }
         delta += pair_sum(off_by);
     }
@@ -881,11 +909,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
         for (int i = 0; i < n; ++i) {
             const int j0 = jn;
             if (i + 1 < n) load(i + 1);
+            const bool holes = lost_in(i);
 #pragma unroll 1
             for (int b = 0; b < BN; b += 32) {
                 const int view = wave_live ? mine.of(a, j0 + b) : 0;
                 if (view != 0)
-                    add_delta(lds + (i & 1) * 2 * BN * Tl::kPitch, b, j0, view == 1, off_by);
+                    add_delta(lds + (i & 1) * 2 * BN * Tl::kPitch, b, j0, view == 1, holes, i,
+                              off_by);
             }
             if (i + 1 < n) arrive(i + 1);
             __syncthreads();
@@ -909,10 +939,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
         const int j0 = jn;
         if (i + 1 < n) load(i + 1);
         const FPSTOK_LDS char* kbuf = lds + (i & 1) * 2 * BN * Tl::kPitch;
+        const bool holes = lost_in(i);
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
             const int view = wave_live ? mine.of(a, j0 + b * 32) : 0;
-            if (view != 0) block(kbuf, b, j0, view == 1);
+            if (view != 0) block(kbuf, b, j0, view == 1, holes, i);
         }
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
@@ -922,7 +953,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     store_row<T, DB>(dq, a.scale, q.live || q.r < t.pad ? out : nullptr, a.D, lane);
     if (bad) {
         __syncthreads();
-        if (q.live && some && half == 0) add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, kb, a.k.row);
+        if (q.live && some && half == 0) 
+            add_bad_keys<BN, true>(out, a, kt, n, q, t.tk, win, kb, a.k.row);
     }
 }
 

@@ -328,7 +328,8 @@ struct Dma {
     }
     // After dma_wait, of the chunks this thread loaded: rows whose bit is set
     // become zero; their infinite elements become 1 of their sign; all infinite
-    // and not-a-number elements become zero (true if there were any).
+    // and not-a-number elements become zero (a bit for each chunk that had any:
+    // bit i of row i * kStep + row).
     static __device__ __forceinline__ void drop(FPSTOK_LDS char* buf, uint64_t rows, int tid) {
         static_assert(ROWS <= 64, "a bit per row");
 #pragma unroll 1
@@ -346,15 +347,16 @@ struct Dma {
                 *p = chunk_clean<T, true>(x);
         }
     }
-    static __device__ __forceinline__ bool clean(FPSTOK_LDS char* buf, int tid) {
-        bool bad = false;
+    static __device__ __forceinline__ uint32_t clean(FPSTOK_LDS char* buf, int tid) {
+        static_assert(kPer <= 32, "a bit per chunk");
+        uint32_t bad = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             FPSTOK_LDS u32x4* p = (FPSTOK_LDS u32x4*)(buf + i * 4096 + tid * 16);
             const u32x4 x = *p;
             if (chunk_bad<T>(x)) {
                 *p = chunk_clean<T>(x);
-                bad = true;
+                bad |= 1u << i;
             }
         }
         return bad;

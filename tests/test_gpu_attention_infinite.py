@@ -69,6 +69,39 @@ def compute(F, shape, qs, ks, q, k, v, go):  # noqa: F811
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("D", [40, 64, 128])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_seen_key_of_score_minus_infinity(F, shape, D, dtype):  # noqa: F811
+    log("infinite key %s D=%d %s" % (shape, D, dtype))
+    qs, ks, q_seq, k_seq, q, k, v, go = inputs(F, shape, D, dtype, 81)
+    m = k.shape[0]
+    keys = sorted({m // 3, m // 2, m - 1})
+    fixed = k.clone()
+    fixed[keys, :, 3] = 0.0
+    k[keys, :, 3] = -INF
+
+    def hide(tq, tk):
+        h = np.zeros((tq, tk), dtype=bool)
+        h[:, keys] = True
+        return h
+
+    got = compute(F, shape, qs, ks, q, k, v, go)
+    want = reference(hide, q, fixed, v, q_seq, k_seq, *shape[4], shape[5], grad=go)
+    # grad_q's own element 3 is 0 times -infinity in rows that see such a key
+    # beside others, and no other element is touched
+    sees = ref.visible(q.shape[0], m, *shape[4], shape[5])
+    rows = sees[:, keys].any(1) & np.delete(sees, keys, 1).any(1)
+    gq = got["grad_q"].float().cpu()
+    assert bool(torch.isnan(gq[torch.from_numpy(rows)][..., 3]).all())
+    val, tol = want["grad_q"]
+    clean = gq.to(DT[dtype])
+    clean[torch.from_numpy(rows), :, 3] = torch.from_numpy(val)[rows, :, 3].to(DT[dtype])
+    got["grad_q"] = clean
+    for name, t in got.items():
+        ref.check(t, want[name], name)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
 @pytest.mark.parametrize("bad_grad", [False, True])
 def test_query_whose_scores_are_minus_infinity(F, shape, D, dtype, bad_grad):  # noqa: F811
     """It gets 0 and -infinity, and adds nothing to any gradient, whatever its
