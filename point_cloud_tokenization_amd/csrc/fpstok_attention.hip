@@ -1321,8 +1321,10 @@ void attention_dkv_kernel(AttnArgs a) {
         const int x0 = xn;
         FPSTOK_LDS char* qbuf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
         const float(*st)[64] = stat[i & 1];
+        const float lse_here = st[0][lane];  // (on its way while the next tile is called for)
+        if (i + 1 < n) load(i + 1);
         // (the bits past BQ rows are the next tile's)
-        const uint64_t gone = __ballot(st[0][lane] == INFINITY);
+        const uint64_t gone = __ballot(lse_here == INFINITY);
         if (gone != 0) {
             Dma<T, DP, BQ>::finite(qbuf, gone, tid);
             Dma<T, DP, BQ>::drop(qbuf + BQ * Tl::kPitch, gone, tid);
@@ -1334,7 +1336,6 @@ void attention_dkv_kernel(AttnArgs a) {
             }
             __syncthreads();
         }
-        if (i + 1 < n) load(i + 1);
 #pragma unroll
         for (int b = 0; b < QB; ++b)
             if (wave_live && wave_any.has(x0 + b * 32))

@@ -339,7 +339,7 @@ struct Dma {
     }
     static __device__ __forceinline__ void finite(FPSTOK_LDS char* buf, uint64_t rows, int tid) {
         static_assert(ROWS <= 64, "a bit per row");
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < kPer; ++i) {
             FPSTOK_LDS u32x4* p = (FPSTOK_LDS u32x4*)(buf + i * 4096 + tid * 16);
             const u32x4 x = *p;
