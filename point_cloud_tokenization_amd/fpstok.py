@@ -549,10 +549,12 @@ class Attention(_DeviceCall):
     window = (left, right), -1 for unbounded; right = 0 is causal.  A call
     takes what the tensors hold by then; it returns (out, lse), the same
     buffers each time, and rows behind the last packed sequence keep what they
-    held (0 after construction)."""
+    held (0 after construction).  out and, in training, grads = (grad_q, grad_k,
+    grad_v) may be given; other buffers assigned to .grads take the place of
+    those before."""
 
     def __init__(self, q, k, v, q_seqs, k_seqs=None, window=(-1, -1), num_sinks=0, scale=None,
-                 training=False, out=None):
+                 training=False, out=None, grads=None):
         import torch
 
         super().__init__(q.device)
@@ -580,12 +582,29 @@ class Attention(_DeviceCall):
         self.ws = torch.empty(max(need), dtype=torch.uint8, device=q.device) if max(need) else None
         self._ws = (_ptr(self.ws), 0 if self.ws is None else self.ws.numel())
         self._fwd, self._bwd = lib().fpstok_attention, lib().fpstok_attention_backward
-        self.grads = None
-        if training:
+        self._training, self._grads = bool(training), None
+        if grads is not None:
+            self.grads = grads
+        elif training:
             self.grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
                                for t in (q, k, v))
-            gh = [make_heads(g, "gradient") for g in self.grads]
-            self._tail = tuple(ctypes.byref(h) for h in gh) + self._ws
+
+    @property
+    def grads(self):
+        """(grad_q, grad_k, grad_v), where backward writes; None if not training."""
+        return self._grads
+
+    @grads.setter
+    def grads(self, grads):
+        if not self._training:
+            raise ValueError("construct with training=True")
+        grads = tuple(grads)
+        if len(grads) != 3:
+            raise ValueError("grads must be (grad_q, grad_k, grad_v)")
+        views = [make_heads(g, name, rows=t.shape[0], heads=t.shape[1], like=t)
+                 for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads,
+                                       (self.q, self.k, self.v))]
+        self._grads, self._tail = grads, tuple(ctypes.byref(h) for h in views) + self._ws
 
     def __call__(self, stream=None):
         """fpstok_attention: (out, lse)."""
@@ -595,13 +614,13 @@ class Attention(_DeviceCall):
     def backward(self, grad_out, stream=None):
         """fpstok_attention_backward after a call on the same inputs:
         (grad_q, grad_k, grad_v)."""
-        if self.grads is None:
+        if self._grads is None:
             raise ValueError("construct with training=True")
         gh = make_heads(grad_out, "grad_out", rows=self.q.shape[0], heads=self.q.shape[1],
                         like=self.q)
         self._call(self._bwd, "fpstok_attention_backward",
                    self._head + (ctypes.byref(gh),) + self._tail, stream)
-        return self.grads
+        return self._grads
 
 
 def rope_frequencies(pairs, base=10000.0, top=1.0, device=None):
