@@ -514,7 +514,9 @@ def make_heads(t, name, heads=None, rows=None, like=None):
 
 
 class _DeviceCall:
-    """Calls a library function on the stream of one device."""
+    """Calls a library function on the stream of one device.  Buffers that the
+    constructor fills are ready for calls on any stream: a stream other than
+    the one they were filled on waits for that before its first call."""
 
     def __init__(self, device):
         import torch
@@ -522,6 +524,27 @@ class _DeviceCall:
         self.device = device
         self._index = device.index if device.index is not None else torch.cuda.current_device()
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._filled, self._ready = None, set()
+
+    def _fills_end(self):
+        """Marks the place of the constructor's fills on its current stream."""
+        import torch
+
+        with torch.cuda.device(self._index):
+            stream = torch.cuda.current_stream()
+            self._ready.add(stream.cuda_stream)
+            if not torch.cuda.is_current_stream_capturing():
+                self._filled = torch.cuda.Event()
+                self._filled.record(stream)
+
+    def _wait_for_fills(self, stream):
+        import torch
+
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+            # (work before a capture is no part of it: who captures has waited)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().wait_event(self._filled)
+                self._ready.add(torch.cuda.current_stream().cuda_stream)
 
     def _call(self, fn, where, args, stream):
         import torch
@@ -535,6 +558,8 @@ class _DeviceCall:
             s = self._raw_stream(self._index)
         else:
             s = torch.cuda.current_stream(self.device).cuda_stream
+        if self._filled is not None and s not in self._ready:
+            self._wait_for_fills(stream)
         rc = fn(*args, ctypes.c_void_p(s))
         if rc != OK:
             _check(rc, where)
@@ -588,6 +613,7 @@ class Attention(_DeviceCall):
         elif training:
             self.grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
                                for t in (q, k, v))
+        self._fills_end()
 
     @property
     def grads(self):
@@ -679,6 +705,8 @@ class Rope(_DeviceCall):
             self._args.append((ctypes.byref(seqs), ctypes.byref(pr), _ptr(positions), _ptr(freqs))
                               + views)
         self._fn = lib().fpstok_rope
+        if q_out is None or (k is not None and k_out is None):
+            self._fills_end()
 
     def __call__(self, inverse=False, stream=None):
         """fpstok_rope; inverse=True turns back (the gradient)."""
