@@ -515,8 +515,10 @@ def make_heads(t, name, heads=None, rows=None, like=None):
 
 class _DeviceCall:
     """Calls a library function on the stream of one device.  Buffers that the
-    constructor fills are ready for calls on any stream: a stream other than
-    the one they were filled on waits for that before its first call."""
+    constructor allocates are for calls on any stream: a stream other than the
+    one they were filled on waits for that before its first call, and the
+    allocator does not give them to others before that stream is done with
+    them."""
 
     def __init__(self, device):
         import torch
@@ -524,11 +526,13 @@ class _DeviceCall:
         self.device = device
         self._index = device.index if device.index is not None else torch.cuda.current_device()
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self._filled, self._ready = None, set()
+        self._filled, self._ready, self._own = None, set(), ()
 
-    def _fills_end(self):
-        """Marks the place of the constructor's fills on its current stream."""
+    def _allocated(self, *own):
+        """The constructor's own buffers, filled on its current stream."""
         import torch
+
+        self._own = own
 
         with torch.cuda.device(self._index):
             stream = torch.cuda.current_stream()
@@ -543,8 +547,11 @@ class _DeviceCall:
         with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
             # (work before a capture is no part of it: who captures has waited)
             if not torch.cuda.is_current_stream_capturing():
-                torch.cuda.current_stream().wait_event(self._filled)
-                self._ready.add(torch.cuda.current_stream().cuda_stream)
+                here = torch.cuda.current_stream()
+                here.wait_event(self._filled)
+                for t in self._own:
+                    t.record_stream(here)
+                self._ready.add(here.cuda_stream)
 
     def _call(self, fn, where, args, stream):
         import torch
@@ -608,12 +615,14 @@ class Attention(_DeviceCall):
         self._ws = (_ptr(self.ws), 0 if self.ws is None else self.ws.numel())
         self._fwd, self._bwd = lib().fpstok_attention, lib().fpstok_attention_backward
         self._training, self._grads = bool(training), None
+        own = [t for t in (self.lse, self.ws, self.out if out is None else None) if t is not None]
         if grads is not None:
             self.grads = grads
         elif training:
             self.grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
                                for t in (q, k, v))
-        self._fills_end()
+            own += self.grads
+        self._allocated(*own)
 
     @property
     def grads(self):
@@ -705,8 +714,11 @@ class Rope(_DeviceCall):
             self._args.append((ctypes.byref(seqs), ctypes.byref(pr), _ptr(positions), _ptr(freqs))
                               + views)
         self._fn = lib().fpstok_rope
-        if q_out is None or (k is not None and k_out is None):
-            self._fills_end()
+        own = [self.q_out] if q_out is None else []
+        if k is not None and k_out is None:
+            own.append(self.k_out)
+        if own:
+            self._allocated(*own)
 
     def __call__(self, inverse=False, stream=None):
         """fpstok_rope; inverse=True turns back (the gradient)."""

@@ -81,3 +81,27 @@ def test_captured_on_another_stream_than_constructed(F):  # noqa: F811
         torch.cuda.synchronize()
         for name, t in zip(("out", "lse", "grad_q", "grad_k", "grad_v"), got):
             ref.check(t, want[name], "eager %d %s" % (turn, name))
+
+
+def test_buffers_outlive_the_object_on_another_stream(F):  # noqa: F811
+    """The memory of a plan that is dropped while its call waits on another
+    stream is not given to a new tensor."""
+    qs, _, n = layout(F, [700], "packed")
+    q = torch.ones((n, 2, 64), dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    F.Attention(q, q, q, qs, training=True)()  # (loads the kernels)
+    torch.cuda.synchronize()
+    att = F.Attention(q, q, q, qs, training=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        occupy()
+    att(side)
+    att.backward(q, side)
+    held = {t.data_ptr(): t.numel() * t.element_size()
+            for t in (att.ws, att.lse, att.out) + att.grads}
+    del att
+    new = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in held.values()]
+    busy = not side.query()
+    torch.cuda.synchronize()
+    assert busy, "the other stream was done too early to tell"
+    assert not any(t.data_ptr() in held for t in new)
