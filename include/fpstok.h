@@ -331,11 +331,12 @@ fpstok_status fpstok_random_start(const int64_t* offsets, int64_t num_events, ui
  * token_count is given:
  *   packed (cu_seqlens, as fpstok_pack writes it): sequence b is rows
  *     cu_seqlens[b] .. cu_seqlens[b+1]-1.  Rows ahead of the first sequence and
- *     behind the last are neither read nor written.
+ *     behind the last are not written.
  *   padded (token_count, as fpstok_tokenize writes it): sequence b is the
  *     first token_count[b] of the rows b*capacity .. (b+1)*capacity-1, and
- *     num_rows = B*capacity.  The other slots are not read; outputs get 0
- *     there.
+ *     num_rows = B*capacity.  Outputs get 0 in the other slots.
+ * Nothing that a row of no sequence holds reaches a result (the attention may
+ * load such a row and drop it: all num_rows rows have to be there).
  * Lengths are device data: a call never waits for them.  Values out of range
  * are clamped into the buffer (a sequence whose end lies before its start is
  * empty), so they give wrong results but no access outside it. */

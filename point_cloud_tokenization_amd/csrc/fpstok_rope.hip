@@ -94,11 +94,14 @@ __global__ __launch_bounds__(256) void rope_pair_kernel(RopeArgs a) {
 // sines and cosines are formed once, in LDS, for all heads of q and k; then a
 // thread turns 16 bytes (interleaved) or 16 bytes and their partners R
 // elements further (half), kItems of them on their way at a time, adjacent
-// threads adjacent in memory.  Bound by the bytes: 150,000 rows of 16 + 4 heads of
-// 128 bfloat16 in 0.29 to 0.31 ms, 5.0 to 5.3 TB/s (a large copy's rate); 5,541
-// rows of 12 + 4 heads of 64 in 8 us, of which a launch is half; one event's 128
-// rows in 4.7 us, a launch.  One element pair per thread, above, took 362, 11 and
-// 8.5 us.
+// threads adjacent in memory.  Rows of no sequence are not read: their items
+// load a row of the workgroup that is one's (a load under a divergent branch
+// would be waited for before the branch ends) and drop it, and their sines are not
+// formed (1024 events of 4 rows in 128 slots: 74 us, 117 with them).  Bound by
+// the bytes: 150,000 rows of 16 + 4 heads of 128 bfloat16 in 0.31 ms, 5.0 TB/s
+// (a large copy's rate); 5,541 rows of 12 + 4 heads of 64 in 8 us, of which a
+// launch is half; one event's 128 rows in 4.7 us, a launch.  One element pair per
+// thread, above, took 362, 11 and 8.5 us.
 template <class T, bool INTER>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     constexpr int V = 16 / (int)sizeof(T), kItems = 4;
@@ -109,6 +112,18 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     const int64_t row0 = (int64_t)blockIdx.x * a.block_rows;
     const int rows = end - row0 < a.block_rows ? (int)(end - row0) : a.block_rows;
     if (rows <= 0) return;
+    // a bit for each of the rows (at most 16) that is a sequence's
+    uint32_t here = (1u << rows) - 1;
+    if (a.seqs.cu) {
+        if (begin - row0 >= rows) return;
+        if (begin > row0) here &= ~0u << (begin - row0);
+    } else {
+        bool skip;
+        const int r = tid & 63;
+        here = (uint32_t)__ballot(r < rows && row_here(a.seqs, row0 + (r < rows ? r : 0), begin, end,
+                                                       skip));
+    }
+    const int some = __builtin_ctz(here | 1u << 31);
     const int turned = INTER ? 2 * R / V : R / V;  // turned items of a head
     const int per_head = turned + (a.D - 2 * R) / V, heads = a.heads[0] + a.heads[1];
     const int per_row = per_head * heads, total = per_row * rows;
@@ -128,10 +143,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
             const int64_t hh = (int)h - (k ? a.heads[0] : 0);
             // first element: of the turned part, or of the rest of the head
             const int e = (int)u < turned ? (int)u * V : 2 * R + ((int)u - turned) * V;
-            const T* from = (const T*)in.data + (row0 + r) * in.row + hh * in.head + e;
+            const int64_t read = row0 + (here >> r & 1 ? (int)r : some);
+            const T* from = (const T*)in.data + read * in.row + hh * in.head + e;
             to[i] = (T*)out.data + (row0 + r) * out.row + hh * out.head + e;
             row[i] = (int)r;
             item[i] = (int)u;
+            x[i] = y[i] = Vec{};
+            if (here == 0) continue;
             x[i] = *(const Vec*)from;
             // (the rest of a head has no partner: its own element again)
             if constexpr (!INTER) y[i] = *(const Vec*)((int)u < turned ? from + R : from);
@@ -141,6 +159,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     for (int n = tid; n < rows * R; n += 256) {
         const int r = n / R;
         float sn, cs;
+        if (!(here >> r & 1)) continue;
         row_sincos(a, row0 + r, n - r * R, sn, cs);
         table[n] = make_float2(cs, sn);
     }
@@ -150,9 +169,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             if (base + i * 256 >= total) break;
-            bool skip;
-            const bool here = row_here(a.seqs, row0 + row[i], begin, end, skip);
-            if (skip) continue;
+            const bool live = here >> row[i] & 1;
+            if (!live && a.seqs.cu) continue;
             const bool turn = item[i] < turned;
             if constexpr (INTER) {
                 if (turn) {
@@ -175,10 +193,10 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
                         x[i][e] = (T)(x1 * c.x - x2 * c.y);
                         y[i][e] = (T)(x1 * c.y + x2 * c.x);
                     }
-                    *(Vec*)(to[i] + R) = here ? y[i] : Vec{};
+                    *(Vec*)(to[i] + R) = live ? y[i] : Vec{};
                 }
             }
-            *(Vec*)to[i] = here ? x[i] : Vec{};
+            *(Vec*)to[i] = live ? x[i] : Vec{};
         }
     }
 }
