@@ -64,11 +64,11 @@ def build(verbose: bool = False, extra=()) -> str:
     return LIB
 
 
-def device_asm(out_path: str) -> str:
-    """Compile the kernels to gfx950 assembly (for the build checks)."""
+def device_asm(out_path: str, source: str = SOURCES[0]) -> str:
+    """Compile the kernels of one source to gfx950 assembly (for the build checks)."""
     cmd = [hipcc(), *[f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")],
-           *SOURCE_FLAGS[SOURCES[0]], "--cuda-device-only", "-S", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-o", out_path, SOURCES[0]]
+           *SOURCE_FLAGS.get(source, []), "--cuda-device-only", "-S",
+           "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", out_path, source]
     subprocess.run(cmd, check=True, capture_output=True)
     return out_path
 

@@ -259,21 +259,26 @@ __device__ __forceinline__ const void* wave_uniform(const void* p) {
 }
 
 // 16 bytes per lane from base + off (bytes) straight to LDS at lds + 16 lane
-// (base and lds the same in every lane), without a register in between; done once the wave's vmcnt is back at 0
-// (dma_wait).  The instruction takes its LDS address from M0.  The compiler
-// would wait for such a load before the next LDS read of any kind; here the
-// reads of one buffer go on while the other one fills.
+// (base and lds the same in every lane), without a register in between; done
+// once the wave's vmcnt is back at 0 (dma_wait).  The compiler would wait for such
+// a load before the next LDS read of any kind; here the reads of one buffer go
+// on while the other one fills.  The instruction takes its LDS address from M0,
+// which the compiler itself does not use in these kernels (a check of the build
+// looks for that; a clobber of a reserved register would not be kept).  It may
+// follow the vector instruction that forms `base`, whose scalar registers a
+// memory instruction can read 5 wait states later at the earliest: s_mov counts
+// 1, s_nop 4 counts 5, and no pass of the compiler looks in here.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(wave_uniform(base))
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(wave_uniform(base))
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
