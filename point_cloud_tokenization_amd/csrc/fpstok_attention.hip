@@ -167,19 +167,80 @@ struct Window {
     }
 };
 
-// Adds the infinite and not-a-number elements of `src`, or, ZERO, 0 times
-// them, to `dst`: the result of a row that sees them, where a tile that other
-// rows do not see whole was multiplied without them.  Rare, so it works on
-// the stored result.
-template <bool ZERO = false, class T, class TO>
-__device__ __forceinline__ void add_bad(TO* dst, const T* src, int D) {
-#pragma unroll 1
-    for (int d = 0; d < D; ++d) {
-        const float x = (float)src[d];
-        if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) 
-            dst[d] = (TO)((float)dst[d] + (ZERO ? NAN : x));
+// The rows (keys or queries) that lost infinite or not-a-number elements in
+// the tiles of a workgroup's walk: a bit for each tile, modulo 32, and for
+// each row of it.  A tile whose number modulo 32 is another's may show rows of
+// that one too: whoever looks tests the elements themselves.
+struct BadRows {
+    uint32_t tiles;
+    uint32_t rows[32][2];
+    __device__ __forceinline__ void clear(int tid) {
+        if (tid < 64) rows[tid >> 1][tid & 1] = 0;
+        if (tid == 64) tiles = 0;
     }
-}
+    __device__ __forceinline__ void note(int tile, int row) {
+        atomicOr(&rows[tile & 31][row >> 5], 1u << (row & 31));
+        atomicOr(&tiles, 1u << (tile & 31));
+    }
+    // Rows of a tile, the same in every lane.
+    __device__ __forceinline__ uint64_t of(int tile) const {
+        const uint32_t lo = __builtin_amdgcn_readfirstlane(rows[tile & 31][0]);
+        const uint32_t hi = __builtin_amdgcn_readfirstlane(rows[tile & 31][1]);
+        return (uint64_t)hi << 32 | lo;
+    }
+};
+
+// The sum of the infinite and not-a-number elements of rows, or, ZERO, of 0
+// times them, for the result of a row that sees them, where a tile that other
+// rows do not see whole was multiplied without them.  The two halves of a wave
+// take every other 16 bytes of the 64 elements from d0 on.  Rare, so it works
+// on the stored result.  (Window of 256, 55k pulses, 8 heads on 4, an infinite
+// element in 1 of 100 rows of grad_out: 286 us a backward pass, 240 without any; in
+// every row 1.27 ms.  Element by element over all rows of such tiles: 17 and 18 ms.)
+template <class T, bool ZERO = false>
+struct BadSum {
+    static constexpr int V = 16 / (int)sizeof(T), C = 64 / (2 * V);
+    float sum[C * V];
+    int d0;
+    __device__ __forceinline__ BadSum(int d0) : d0(d0) {
+#pragma unroll
+        for (int e = 0; e < C * V; ++e) sum[e] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const T* src, int D, int half) {
+        u32x4 x[C];
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int d = d0 + (2 * c + half) * V;
+            x[c] = *(const u32x4*)(src + (d < D ? d : 0));
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) bad |= chunk_bad<T>(x[c]);
+        if (!bad) return;
+        using Vec = T __attribute__((ext_vector_type(V)));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const Vec v = __builtin_bit_cast(Vec, x[c]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float y = (float)v[e];
+                const bool hit = (__float_as_uint(y) & 0x7f800000u) == 0x7f800000u;
+                sum[c * V + e] += !hit ? 0.0f : ZERO ? NAN : y;
+            }
+        }
+    }
+    template <class TO>
+    __device__ __forceinline__ void store(TO* dst, int D, int half) const {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int d = d0 + (2 * c + half) * V;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (d < D && sum[c * V + e] != 0.0f)
+                    dst[d + e] = (TO)((float)dst[d + e] + sum[c * V + e]);
+        }
+    }
+};
 
 // Row `p` of D elements as operands of STEPS product steps, zero where it is
 // not `live` (its lanes load `any`, a row that exists: loads under a divergent
@@ -238,19 +299,27 @@ struct QueryRows {
     }
 };
 
-// add_bad over the keys that one row sees of the tiles that the workgroup's
-// rows do not all see whole.
+// BadSum over the keys that a lane's row sees of the tiles that the workgroup's
+// rows do not all see whole, added to `dst`.
 template <int BN, bool ZERO = false, class T, class TO>
 __device__ __forceinline__ void add_bad_keys(TO* dst, const AttnArgs& a, const KeyTiles<BN>& kt,
-                                             int n, const QueryRows& q, int tk, const Window& w,
-                                             const T* base, int64_t stride) {
+                                             int n, const BadRows& bad, const QueryRows& q, int tk,
+                                             const Window& w, bool live, int half, const T* base,
+                                             int64_t stride) {
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        const int j0 = kt.tile(i) * BN;
-        if (tile_view<BN>(a, q.pa, q.pb, tk, j0) != 1) continue;
+    for (int d0 = 0; d0 < a.D; d0 += 64) {
+        BadSum<T, ZERO> sum(d0);
 #pragma unroll 1
-        for (int j = j0; j < j0 + BN && j < tk; ++j)
-            if (!w.hides(j)) add_bad<ZERO>(dst, base + j * stride, a.D);
+        for (int i = 0; i < n; ++i) {
+            const int j0 = kt.tile(i) * BN;
+            if (tile_view<BN>(a, q.pa, q.pb, tk, j0) != 1) continue;
+#pragma unroll 1
+            for (uint64_t rows = bad.of(i); rows != 0; rows &= rows - 1) {
+                const int j = j0 + __builtin_ctzll(rows);
+                if (live && j < tk && !w.hides(j)) sum.add(base + j * stride, a.D, half);
+            }
+        }
+        if (live) sum.store(dst, a.D, half);
     }
 }
 
@@ -343,7 +412,7 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
-    __shared__ int bad;  // a tile was stored without its infinite values
+    __shared__ BadRows bad;  // values taken out of tiles
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -383,8 +452,12 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
         dma_wait();
         // a value that some row must not see meets a weight of 0 there: an
         // infinite one has to leave the product
-        if (all.of(a, jn) == 1 && dma.clean(lds + ((i & 1) * 2 + 1) * BN * Tl::kPitch, tid))
-            bad = 1;
+        if (all.of(a, jn) == 1) {
+            const uint32_t chunks = dma.clean(lds + ((i & 1) * 2 + 1) * BN * Tl::kPitch, tid);
+#pragma unroll 1
+            for (uint32_t c = chunks; c != 0; c &= c - 1)
+                bad.note(i, __builtin_ctz(c) * dma.kStep + dma.row);
+        }
     };
 
     Softmax<T, DB> sm;
@@ -418,7 +491,7 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
                     sm.o[db] = Elem<T>::mma(Tl::col_frag(vbuf, k * 16, db, lane), pf, sm.o[db]);
         }
     };
-    if (tid == 0) bad = 0;
+    bad.clear(tid);
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
     if (n > 0) {
@@ -456,10 +529,9 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
         sm.only(some);
         store_row<float, DB>(sm.o, 1.0f, q.live ? part : nullptr, a.D, lane);
         if (q.live && half == 0) a.part_ml[at] = make_float2(some ? sm.mc : -INFINITY, sm.l);
-        if (bad) {
+        if (bad.tiles != 0) {
             __syncthreads();
-            if (q.live && half == 0)
-                add_bad_keys<BN>(part, a, kt, n, q, t.tk, win, vb, a.v.row);
+            add_bad_keys<BN>(part, a, kt, n, bad, q, t.tk, win, q.live, half, vb, a.v.row);
         }
         return;
     }
@@ -469,11 +541,10 @@ __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T))) void attention_ke
     store_row<T, DB>(sm.o, q.live && some ? 1.0f / sm.l : 0.0f, write ? out : nullptr, a.D, lane);
     if (a.lse && half == 0 && write)
         a.lse[q.row * a.H + q.h] = !q.live ? 0.0f : some ? log_sum(sm.mc, sm.l) : -INFINITY;
-    if (bad) {
+    if (bad.tiles != 0) {
         __syncthreads();
         // (a row whose every score is -infinity stays 0)
-        if (q.live && some && half == 0)
-            add_bad_keys<BN>(out, a, kt, n, q, t.tk, win, vb, a.v.row);
+        add_bad_keys<BN>(out, a, kt, n, bad, q, t.tk, win, q.live && some, half, vb, a.v.row);
     }
 }
 
@@ -500,7 +571,7 @@ void attention_few_kernel(AttnArgs a) {
     static_assert(kWaveBytes >= BM * DP * 4, "join buffer");
     __shared__ __attribute__((aligned(16))) char smem[4 * kWaveBytes];
     __shared__ float2 ml[4][BM];
-    __shared__ int bad;
+    __shared__ BadRows bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -529,12 +600,17 @@ void attention_few_kernel(AttnArgs a) {
     Softmax<T, DB> sm;
     const float c = a.scale * kLog2e;
     if (wave < n) load(wave);
-    if (tid == 0) bad = 0;
+    bad.clear(tid);
     __syncthreads();
     for (int i = wave; i < n; i += 4) {
         const int j0 = kt.tile(i) * BN;
         const int view = all.of(a, j0);
-        if (view == 1 && sv.clean(lane)) bad = 1;
+        if (view == 1) {
+            const uint32_t chunks = sv.clean(lane);
+#pragma unroll 1
+            for (uint32_t c = chunks; c != 0; c &= c - 1)
+                bad.note(i, __builtin_ctz(c) * sv.kStep + sv.row(lane));
+        }
         wave_sync();  // the wave's reads of the last tile are done
         sk.store(kbuf, a.D, lane);
         sv.store(vbuf, a.D, lane);
@@ -616,18 +692,19 @@ void attention_few_kernel(AttnArgs a) {
         if (a.lse && d == 0)
             a.lse[(t.q0 + qi) * a.H + h] = !here ? 0.0f : some ? log_sum(top, sum) : -INFINITY;
     }
-    if (bad) {
+    if (bad.tiles != 0) {
         __syncthreads();
-        if (wave == 0 && half == 0 && q.live) {
+        if (wave == 0) {
             bool some = false;
 #pragma unroll
             for (int w = 0; w < 4; ++w)
                 some |= !(ml[w][q.r].x == -INFINITY && ml[w][q.r].y == 0.0f);
             if (a.splits > 1)
-                add_bad_keys<BN>(a.part + (part0 + q.r) * a.D, a, kt, n, q, t.tk, win, vb, a.v.row);
-            else if (some)  // (a row whose every score is -infinity stays 0)
-                add_bad_keys<BN>((T*)a.out.data + q.row * a.out.row + q.h * a.out.head, a, kt, n, q,
-                                 t.tk, win, vb, a.v.row);
+                add_bad_keys<BN>(a.part + (part0 + q.r) * a.D, a, kt, n, bad, q, t.tk, win,
+                                     q.live, half, vb, a.v.row);
+            else  // (a row whose every score is -infinity stays 0)
+                add_bad_keys<BN>((T*)a.out.data + q.row * a.out.row + q.h * a.out.head, a, kt,
+                                     n, bad, q, t.tk, win, q.live && some, half, vb, a.v.row);
         }
     }
 }
@@ -776,7 +853,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     using Tl = Tile<T, DP>;
     using Frag = typename Elem<T>::Frag;
     __shared__ __attribute__((aligned(16))) char smem[2 * 2 * BN * Tl::kPitch];
-    __shared__ int bad;
+    __shared__ BadRows bad;
     __shared__ int lost[2][BN];  // of a buffer's keys: 1 + the tile in which one lost elements
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -820,11 +897,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
         if (all.of(a, jn) != 1) return;
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
         const uint32_t chunks = dma.clean(buf, tid);
-        if (chunks == 0) return;
 #pragma unroll 1
-        for (int k = 0; k < dma.kPer; ++k)
-            if (chunks >> k & 1) lost[i & 1][k * dma.kStep + dma.row] = i + 1;
-        bad = i + 1;
+        for (uint32_t c = chunks; c != 0; c &= c - 1) {
+            const int row = __builtin_ctz(c) * dma.kStep + dma.row;
+            bad.note(i, row);
+            lost[i & 1][row] = i + 1;
+        }
     };
 
     f32x16 dq[DB];
@@ -833,7 +911,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     const float c = a.scale * kLog2e;
     float delta = 0.0f, lse2 = 0.0f;
     // tile i may hold keys that lost elements
-    auto lost_in = [&](int i) { return __builtin_amdgcn_readfirstlane(bad) > i; };
+    auto lost_in = [&](int i) { return __builtin_amdgcn_readfirstlane(bad.tiles) >> (i & 31) & 1; };
     // the scores of such keys, of 32 from row b of tile i on
     auto hide_lost = [&](f32x16& x, int b, int i) {
 #pragma unroll
@@ -880,7 +958,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
                 dq[db] = Elem<T>::mma(Tl::col_frag(kbuf, b * 32 + k * 16, db, lane), f, dq[db]);
         }
     };
-    if (tid == 0) bad = 0;
+    bad.clear(tid);
     if (tid < 2 * BN) lost[tid / BN][tid % BN] = 0;
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
@@ -951,10 +1029,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_dq_kern
     T* out = (T*)a.grad_q.data + q.row * a.grad_q.row + q.h * a.grad_q.head;
     zero_unless<DB>(dq, q.live && some);
     store_row<T, DB>(dq, a.scale, q.live || q.r < t.pad ? out : nullptr, a.D, lane);
-    if (bad) {
+    if (bad.tiles != 0) {
         __syncthreads();
-        if (q.live && some && half == 0) 
-            add_bad_keys<BN, true>(out, a, kt, n, q, t.tk, win, kb, a.k.row);
+        add_bad_keys<BN, true>(out, a, kt, n, bad, q, t.tk, win, q.live && some, half, kb,
+                                   a.k.row);
     }
 }
 
@@ -1148,7 +1226,7 @@ void attention_dkv_kernel(AttnArgs a) {
     constexpr int kV = 2 * 2 * BQ * Tl::kPitch;
     __shared__ __attribute__((aligned(16))) char smem[kV + (kVLds ? 128 * Tl::kPitch : 0)];
     __shared__ __attribute__((aligned(16))) float stat[2][2][64];
-    __shared__ int bad;
+    __shared__ BadRows bad;
     FPSTOK_LDS char* lds = (FPSTOK_LDS char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1255,7 +1333,10 @@ void attention_dkv_kernel(AttnArgs a) {
             // (a query with infinite elements has no finite score: its weights are
             // 0, or its lse and with it all it adds is not a number)
             Dma<T, DP, BQ>::finite(buf, ~0ull, tid);
-            if (dma.clean(buf + BQ * Tl::kPitch, tid)) bad = 1;
+            const uint32_t chunks = dma.clean(buf + BQ * Tl::kPitch, tid);
+#pragma unroll 1
+            for (uint32_t c = chunks; c != 0; c &= c - 1)
+                bad.note(i, __builtin_ctz(c) * dma.kStep + dma.row);
         }
     };
 
@@ -1303,7 +1384,7 @@ void attention_dkv_kernel(AttnArgs a) {
             }
         }
     };
-    if (tid == 0) bad = 0;
+    bad.clear(tid);
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
     if (n > 0) {
@@ -1377,40 +1458,48 @@ void attention_dkv_kernel(AttnArgs a) {
     // formed anew: at D = 128 no register is left to keep what follows from it
     int lane_end = lane;
     asm volatile("" : "+v"(lane_end));
-    // add_bad to grad_v over the queries of this workgroup's part that see this
+    const int64_t row_end = t.k0 + t.row0 + wave * 32 + (lane_end & 31);
+    // BadSum to grad_v over the queries of this workgroup's part that see this
     // key, and have weights, in tiles that the workgroup's keys do not all see
     // whole (grad_k has their delta, which is not finite either)
     auto add_hidden = [&](auto* to_v) {
         __syncthreads();
-        if (!live || half != 0 || e1 < e0) return;
+        const bool sees = live && e1 >= e0;
 #pragma unroll 1
-        for (int i = from; i < from + n; ++i) {
-            const int g = i / per, x = i0 + (i - g * per) * BQ;
-            if (tile_all.has(x)) continue;
+        for (int d0 = 0; d0 < a.D; d0 += 64) {
+            BadSum<T> sum(d0);
 #pragma unroll 1
-            for (int y = x > e0 ? x : e0; y < x + BQ && y <= e1; ++y) {
-                const int64_t row = t.q0 + y, h = (int64_t)t.hk * G + g;
-                if (a.lse2[h * a.qs.rows + row] == INFINITY) continue;
-                add_bad(to_v,
-                        (const T*)a.grad_out.data + row * a.grad_out.row + h * a.grad_out.head,
-                        a.D);
+            for (int i = 0; i < n; ++i) {
+                const int g = (from + i) / per, x = i0 + (from + i - g * per) * BQ;
+                if (tile_all.has(x)) continue;
+                const int64_t h = (int64_t)t.hk * G + g;
+#pragma unroll 1
+                for (uint64_t rows = bad.of(i); rows != 0; rows &= rows - 1) {
+                    const int y = x + __builtin_ctzll(rows);
+                    const int64_t row = t.q0 + y;
+                    if (sees && y >= e0 && y <= e1 && a.lse2[h * a.qs.rows + row] != INFINITY)
+                        sum.add((const T*)a.grad_out.data + row * a.grad_out.row +
+                                    h * a.grad_out.head,
+                                a.D, half);
+                }
             }
+            if (sees) sum.store(to_v, a.D, half);
         }
     };
     if (a.k_splits > 1) {
-        float* part = a.k_part + k_part_at(a, t.part, t.hk, krow);
+        float* part = a.k_part + k_part_at(a, t.part, t.hk, row_end);
         float* part_v = part + k_part_at(a, 0, a.Hk, 0);
         store_row<float, DB>(dk, 1.0f, live ? part : nullptr, a.D, lane_end);
         store_row<float, DB>(dv, 1.0f, live ? part_v : nullptr, a.D, lane_end);
-        if (bad) add_hidden(part_v);
+        if (bad.tiles != 0) add_hidden(part_v);
         return;
     }
-    T* ok = (T*)a.grad_k.data + krow * a.grad_k.row + t.hk * a.grad_k.head;
-    T* ov = (T*)a.grad_v.data + krow * a.grad_v.row + t.hk * a.grad_v.head;
+    T* ok = (T*)a.grad_k.data + row_end * a.grad_k.row + t.hk * a.grad_k.head;
+    T* ov = (T*)a.grad_v.data + row_end * a.grad_v.row + t.hk * a.grad_v.head;
     const bool write = live || r < t.pad;
     store_row<T, DB>(dk, a.scale, write ? ok : nullptr, a.D, lane_end);
     store_row<T, DB>(dv, 1.0f, write ? ov : nullptr, a.D, lane_end);
-    if (bad) add_hidden(ov);
+    if (bad.tiles != 0) add_hidden(ov);
 }
 
 // Adds the parts of keys whose walk was split, in order: 4 elements of one key

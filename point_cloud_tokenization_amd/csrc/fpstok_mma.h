@@ -237,15 +237,16 @@ struct Stage {
         for (int i = 0; i < kPer; ++i)
             if (rows >> (i * kStep + row(tid)) & 1) x[i] = chunk_clean<T, true>(x[i]);
     }
-    // Infinite and not-a-number elements of rows that exist become zero; true
-    // if there were any.
-    __device__ __forceinline__ bool clean(int tid) {
-        bool bad = false;
+    // Infinite and not-a-number elements of rows that exist become zero; a bit
+    // for each chunk that had any (bit i of row i * kStep + row).
+    __device__ __forceinline__ uint32_t clean(int tid) {
+        static_assert(kPer <= 32, "a bit per chunk");
+        uint32_t bad = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             if (i * kStep + row(tid) < have && chunk_bad<T>(x[i])) {
                 x[i] = chunk_clean<T>(x[i]);
-                bad = true;
+                bad |= 1u << i;
             }
         return bad;
     }

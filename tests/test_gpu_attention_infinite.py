@@ -174,3 +174,40 @@ def test_such_a_query_sees_infinite_values(F, shape, D, dtype):  # noqa: F811
     if others:
         assert not bool(torch.isfinite(out[others][..., 1:3].float()).any())
         assert bool(torch.isfinite(out[others][..., 3:].float()).all())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_seen_infinite_element_of_grad_out(F, shape, D, dtype):  # noqa: F811
+    """grad_v is infinite where the element meets a weight, grad_k wherever
+    the row is seen, and nothing else is touched."""
+    log("infinite gradient %s D=%d %s" % (shape, D, dtype))
+    qs, ks, q_seq, k_seq, q, k, v, go = inputs(F, shape, D, dtype, 84)
+    n, m, Hk = q.shape[0], k.shape[0], k.shape[1]
+    row = n - 1 - n // 4
+    go[row, 0, 7] = INF
+    fixed = go.clone()
+    fixed[row, 0, 7] = 0.0
+    got = compute(F, shape, qs, ks, q, k, v, go)
+    want = ref.attention(q, k, v, q_seq, k_seq, *shape[4], shape[5], grad=fixed)
+    seen = torch.from_numpy(ref.visible(n, m, *shape[4], shape[5])[row])
+    touched = torch.zeros((m, Hk), dtype=torch.bool)
+    touched[:, 0] = seen
+    gv, gk, gq = (got[x].float().cpu() for x in ("grad_v", "grad_k", "grad_q"))
+    assert not bool(torch.isfinite(gv[touched][:, 7]).any())
+    assert not bool(torch.isfinite(gk[touched]).any())
+    assert not bool(torch.isfinite(gq[row, 0]).any())
+    for name, t, hit in (("grad_v", gv, (touched, slice(7, 8))),
+                         ("grad_k", gk, (touched, slice(None))),
+                         ("grad_q", gq, None)):
+        val, tol = (torch.from_numpy(x) for x in want[name])
+        if hit is None:
+            t[row, 0] = val[row, 0].float()
+            tol[row, 0] = INF
+        else:
+            tol[hit[0]] = torch.where(torch.arange(D)[None].ge(hit[1].start or 0) &
+                                      torch.arange(D)[None].lt(hit[1].stop or D),
+                                      torch.full((1, D), INF, dtype=torch.float64), tol[hit[0]])
+            t = torch.where(torch.isinf(tol), torch.zeros_like(t), t)
+        ref.check(t, (val.numpy(), tol.numpy()), name)
