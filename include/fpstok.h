@@ -376,7 +376,8 @@ typedef struct {
     int32_t window_right;    /* keys visible behind it, -1: all; 0: causal          */
     int32_t num_sinks;       /* first keys of each sequence that window_left does   */
                              /* not hide: 0 .. FPSTOK_MAX_SINKS                     */
-    float scale;             /* of the scores; finite and > 0                       */
+    float scale;             /* of the scores; > 0, and scale * log2(e) finite in   */
+                             /* float32 (up to 2.35e38)                             */
 } fpstok_attn_params;
 
 /* Attention inside every sequence (graphnet PR #923, "What is added":

@@ -60,8 +60,9 @@ static fpstok_status check_attn(const fpstok_seqs* qs, const fpstok_seqs* ks,
         return fail(FPSTOK_EINVAL, "window_left and window_right must be >= -1");
     if (p->num_sinks < 0 || p->num_sinks > FPSTOK_MAX_SINKS)
         return fail(FPSTOK_EINVAL, "num_sinks must be in [0, %d]", FPSTOK_MAX_SINKS);
-    if (!std::isfinite(p->scale) || p->scale <= 0.0f)
-        return fail(FPSTOK_EINVAL, "scale must be finite and > 0");
+    // (the factor that the kernels multiply scores by)
+    if (!(p->scale > 0.0f) || !std::isfinite(p->scale * 1.44269504088896f))
+        return fail(FPSTOK_EINVAL, "scale must be > 0, and scale * log2(e) finite in float32");
     // rows, places and windows are 32-bit numbers in the kernels
     if (qs->num_rows >= ((int64_t)1 << 30) || ks->num_rows >= ((int64_t)1 << 30))
         return fail(FPSTOK_EUNSUPPORTED, "num_rows >= 2^30");

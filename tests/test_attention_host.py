@@ -282,3 +282,14 @@ def test_rope_frequencies():
     f = F.rope_frequencies((2, 0, 4), base=100.0, top=8.0)
     np.testing.assert_allclose(f.numpy(), [8, 0.8, 8, 8 / 100 ** 0.25, 0.8, 8 / 100 ** 0.75],
                                rtol=1e-6)
+
+
+@pytest.mark.parametrize("scale", [2.36e38, 3.4e38])
+def test_attention_refuses_scales_whose_kernel_factor_overflows(L, scale):
+    """The kernels multiply scores by scale * log2(e) in float32."""
+    assert _forward(L, pr=_params(scale=scale)) == F.EINVAL
+    assert _backward(L, pr=_params(scale=scale)) == F.EINVAL
+    # 2.35e38 log2(e) is 3.39e38, float32 ends at 3.403e38: past the parameters to the
+    # next check
+    assert _backward(L, pr=_params(scale=2.35e38), lse=None) == F.EINVAL
+    assert b"lse" in L.fpstok_last_error()
