@@ -75,7 +75,11 @@
 extern "C" {
 #endif
 
+/* Grows when a struct or call that was there before changes.  Calls that came
+ * since within a version: a macro here says that they are declared, their symbol
+ * that a library has them. */
 #define FPSTOK_ABI_VERSION 3
+#define FPSTOK_HAS_ATTENTION 1  /* fpstok_attention, its gradients, fpstok_rope */
 #define FPSTOK_MAX_PATCHES 1024 /* largest num_patches accepted             */
 #define FPSTOK_MAX_K 64         /* largest kNN list length accepted           */
 #define FPSTOK_MAX_LLOYD 1000   /* largest lloyd_iters accepted               */
@@ -424,8 +428,10 @@ fpstok_status fpstok_attention(const fpstok_seqs* q_seqs, const fpstok_seqs* k_s
  *   grad_q_i = scale * sum_j ds_ij k_j,   grad_k_j = scale * sum_i ds_ij q_i.
  * Rows no query sees, and queries that see no key, get 0.  Sums are held in
  * float32 in a fixed order (no floating-point atomics); with a 16-bit dtype w
- * and ds are rounded to it for the products.  In float16 a ds below 2^-24
- * vanishes: scale the loss as for any float16 gradient.
+ * and ds are rounded to it for the products.  In float16 a ds below 2^-25
+ * vanishes and one of 65520 or more becomes infinite (before scale and the sum
+ * over the pairs): the factor of the loss has to keep ds between the two, as it
+ * has to for any float16 gradient.  bfloat16 and float32 have no such bounds.
  *   out, lse  as fpstok_attention wrote them
  *   grad_q [q rows][H][D], grad_k, grad_v [k rows][num_kv_heads][D] out; they
  *   may not overlap one another or any input

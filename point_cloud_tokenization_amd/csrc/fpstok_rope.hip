@@ -120,8 +120,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     } else {
         bool skip;
         const int r = tid & 63;
-        here = (uint32_t)__ballot(r < rows && row_here(a.seqs, row0 + (r < rows ? r : 0), begin, end,
-                                                       skip));
+        here = (uint32_t)__ballot(
+            r < rows && row_here(a.seqs, row0 + (r < rows ? r : 0), begin, end, skip));
     }
     const int some = __builtin_ctz(here | 1u << 31);
     const int turned = INTER ? 2 * R / V : R / V;  // turned items of a head

@@ -692,9 +692,11 @@ class Rope(_DeviceCall):
         if freqs.numel() != sum(pairs):
             raise ValueError("freqs must hold %d values" % sum(pairs))
         if seqs.tensor.device != q.device:
-            raise ValueError("the sequences are on %s, expected %s" % (seqs.tensor.device, q.device))
+            raise ValueError("the sequences are on %s, expected %s" % (seqs.tensor.device,
+                                                                    q.device))
         qh = make_heads(q, "q", rows=seqs.num_rows)
-        self.q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        self.q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None \
+            else q_out
         qo = make_heads(self.q_out, "q_out", rows=q.shape[0], heads=q.shape[1], like=q)
         kh = ko = self.k_out = None
         if k is not None:

@@ -4,6 +4,8 @@ their definition), and what the C ABI refuses on the host before touching the
 device."""
 import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -293,3 +295,12 @@ def test_attention_refuses_scales_whose_kernel_factor_overflows(L, scale):
     # next check
     assert _backward(L, pr=_params(scale=2.35e38), lse=None) == F.EINVAL
     assert b"lse" in L.fpstok_last_error()
+
+
+def test_header_names_the_attention_for_a_c_caller(tmp_path):
+    """A C program can ask whether the calls are declared."""
+    src = tmp_path / "t.c"
+    src.write_text('#include "fpstok.h"\n#if FPSTOK_ABI_VERSION != 3 || !FPSTOK_HAS_ATTENTION\n'
+                   '#error old header\n#endif\nvoid *p = (void *)fpstok_attention;\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-fsyntax-only", "-I",
+                    os.path.dirname(F.HEADER), str(src)], check=True)
