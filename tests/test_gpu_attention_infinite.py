@@ -211,3 +211,37 @@ def test_seen_infinite_element_of_grad_out(F, shape, D, dtype):  # noqa: F811
                                       torch.full((1, D), INF, dtype=torch.float64), tol[hit[0]])
             t = torch.where(torch.isinf(tol), torch.zeros_like(t), t)
         ref.check(t, (val.numpy(), tol.numpy()), name)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D", [40, 64, 128])
+def test_seen_sink_of_score_minus_infinity(F, D, dtype):  # noqa: F811
+    """Among the sinks, whose gradients the rows past the window give in
+    chunks, beside queries that add nothing."""
+    log("infinite sink D=%d %s" % (D, dtype))
+    shape = ([777], None, 4, 2, (60, 0), 5)
+    qs, ks, q_seq, k_seq, q, k, v, go = inputs(F, shape, D, dtype, 86)
+    keys, rows = [1, 3], [250, 640, 776]
+    # (an element of their own for the queries: beside the keys' it would be +infinity)
+    k[..., 5] = k[..., 5].abs() + 0.5
+    fk, fq = k.clone(), q.clone()
+    fk[keys, :, 3], fq[rows, :, 5] = 0.0, 0.0
+    k[keys, :, 3], q[rows, :, 5] = -INF, -INF
+
+    def hide(tq, tk):
+        h = np.zeros((tq, tk), dtype=bool)
+        h[:, keys], h[rows] = True, True
+        return h
+
+    got = compute(F, shape, qs, ks, q, k, v, go)
+    want = reference(hide, fq, fk, v, q_seq, k_seq, *shape[4], shape[5], grad=go)
+    sees = ref.visible(777, 777, 60, 0, 5)[:, keys].any(1)
+    sees &= np.delete(ref.visible(777, 777, 60, 0, 5), keys, 1).any(1)
+    sees[rows] = False
+    sees = torch.from_numpy(sees)
+    gq = got["grad_q"].cpu()
+    assert bool(torch.isnan(gq[sees][..., 3].float()).all())
+    gq[sees, :, 3] = torch.from_numpy(want["grad_q"][0])[sees, :, 3].to(DT[dtype])
+    got["grad_q"] = gq
+    for name, t in got.items():
+        ref.check(t, want[name], name)

@@ -66,3 +66,36 @@ def test_packed_rows_in_the_middle(F, dtype, inter, first, last):  # noqa: F811
     cu = torch.tensor([first, (first + last) // 2, last], dtype=torch.int32)
     s = F.make_seqs(n, cu_seqlens=cu.cuda())
     ref.check(turn(F, x, pos, fr, s, inter, False), (val, tol), "packed")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n", [3, 2500])
+@pytest.mark.parametrize("D,pairs", [(1024, (512,)), (1024, (100, 0, 21)), (1022, (511,)), (2, (1,)),
+                                     (256, (1, 1, 1, 1))])
+def test_largest_and_smallest_heads(F, dtype, inter, n, D, pairs):  # noqa: F811
+    log("rope %d rows of %d, pairs %s, %s" % (n, D, pairs, dtype))
+    gen = torch.Generator().manual_seed(99)
+    q, k = rand(gen, (n, 3, D), DT[dtype]), rand(gen, (n, 1, D), DT[dtype])
+    pos = torch.randn((n, len(pairs)), generator=gen)
+    fr = F.rope_frequencies(pairs, top=20.0)
+    s = F.make_seqs(n, cu_seqlens=torch.tensor([0, n], dtype=torch.int32).cuda())
+    r = F.Rope(q.cuda(), k.cuda(), pos.cuda(), fr.cuda(), pairs, s, inter)
+    for t, x in zip(r(), (q, k)):
+        ref.check(t, ref.rope(x, pos, fr, pairs, inter), "heads of %d" % D)
+
+
+def test_rows_past_32_bit_offsets(F):  # noqa: F811
+    n, live = 2_900_000, 40
+    log("rope %d rows" % n)
+    gen = torch.Generator().manual_seed(100)
+    x, pos = rand(gen, (live, 8, 128), torch.bfloat16), torch.randn((live, 4), generator=gen)
+    far, where = torch.zeros((n, 8, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros(
+        (n, 4), device="cuda")
+    far[n - live:], where[n - live:] = x.cuda(), pos.cuda()
+    fr = F.rope_frequencies(PAIRS, top=20.0)
+    s = F.make_seqs(n, cu_seqlens=torch.tensor([0, n], dtype=torch.int32).cuda())
+    out = F.Rope(far, None, where, fr.cuda(), PAIRS, s)()[0]
+    torch.cuda.synchronize()
+    ref.check(out[n - live:], ref.rope(x, pos, fr, PAIRS), "far rows")
+    assert not bool(out[:n - live].any())
