@@ -833,14 +833,16 @@ __global__ __launch_bounds__(256) void attention_join_rows_kernel(AttnArgs a) {
 // difference to the exact delta: where one tile is all a row tile sees it is
 // formed from that tile first, and with a window of fewer than 32 keys (TWICE)
 // the whole walk is made twice (at 256 events of up to 256 tokens this is 3 % of
-// the backward pass).
+// the backward pass).  It goes by tiles, so the first rows of a long causal
+// sequence, which see few keys in a row tile that sees two key tiles, keep the
+// larger error.
 //
 // 3 products where 2 are the gradient's own: forming S and dP here and again
 // for grad_k and grad_v costs 2 of 7, and adding one kernel's grad_q up over the
 // workgroups of a sequence's keys would cost a float32 result per workgroup, or
 // atomics whose order changes it.  6000 + 2111 + 64 rows, 16 heads on 8, D =
 // 128, bfloat16: 0.48 ms, 1.04 PFLOP/s; 256 events of up to 256 tokens, 12
-// heads, D = 64: 114 us.
+// heads, D = 64: 117 us.
 //
 // A tile that some row does not see whole loses its infinite elements of K.  A
 // key that lost some has no finite score: in a row that sees it the score is
@@ -1203,9 +1205,9 @@ __device__ __forceinline__ int64_t k_part_at(const AttnArgs& a, int split, int h
 // dV^T += dO^T P and dK^T += Q^T dS.  The gradients of the group's heads add up
 // in the accumulators, in a fixed order.  Where that leaves few workgroups (few
 // keys, many queries or heads) the walk is split over several, whose parts are
-// added by the kernel below.  4 products: 6000 + 2111 + 64 rows, D = 128: 0.73 ms,
-// 0.91 PFLOP/s (V's operands from LDS, for its registers hold accumulators); at
-// D = 64 the vector unit bounds it: 256 events of up to 256 tokens, 143 us.
+// added by the kernel below.  4 products: 6000 + 2111 + 64 rows, D = 128: 0.74 ms,
+// 0.90 PFLOP/s (V's operands from LDS, for its registers hold accumulators); at
+// D = 64 the vector unit bounds it: 256 events of up to 256 tokens, 149 us.
 //
 // A query whose every visible score is -infinity adds nothing: its lse2 is
 // infinity, so its weights exp2(score - infinity) are 0 as long as its scores
@@ -1565,8 +1567,13 @@ AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len) {
         // two workgroups per compute unit, unless nearly every one has a
         // workgroup already (5000 rows, 5 heads of 64: 200 workgroups, 2 parts
         // 74 us, unsplit 95; 2000 rows, 16 heads on 4, D = 128: 252 workgroups, 2
-        // parts 59 us, unsplit 52); 2500 rows of one head, parts of 256 keys or
-        // more 19 us, of 512 21.  float32 tiles take 8 times as long, and four
+        // parts 59 us, unsplit 52).  How much 2 parts of 225 to 256 workgroups
+        // would take goes by the keys: 1.16 times one part at 16 heads on 4 of
+        // 128 and 1800 to 2050 rows, 0.97 with a causal mask; 0.95 and 0.76 at 8
+        // heads of 128 and 3600 to 4100 rows; 0.77 and 0.64 at 5 heads of 64 and 5800
+        // to 6500 rows, and from 257 workgroups on both are the same.  The step at
+        // 224 keeps the first of these.  2500 rows of one head, parts of 256 keys
+        // or more 19 us, of 512 21.  float32 tiles take 8 times as long, and four
         // workgroups even the compute units out (3000 rows, 12 heads of 64: 320
         // us, unsplit 450; 1500 rows: 114, with two 96).
         const int64_t want = a.dtype == 0 ? 1024 : blocks > 224 ? 0 : 512;
