@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("form", ["packed", "padded"])
 @pytest.mark.parametrize("q_max,k_max", [(1, 1), (1, 5000), (5000, 1)])
 @pytest.mark.parametrize("window,sinks", [((-1, -1), 0), ((60, 0), 3)])
-def test_bounds_on_the_length_that_do_not_hold(F, dtype, form, q_max, k_max, window, sinks):  # noqa: F811,E501
+def test_bounds_on_the_length_that_do_not_hold(  # noqa: F811
+        F, dtype, form, q_max, k_max, window, sinks):  # noqa: F811
     log("wrong bounds %d %d %s %s %s" % (q_max, k_max, form, dtype, window))
     gen = torch.Generator().manual_seed(101)
     H, Hk, D = 4, 2, 64

@@ -49,8 +49,8 @@ def test_padded_slots(F, dtype, inter, in_place, cap, seqs, empty):  # noqa: F81
 
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("first,last", [(0, 5000), (1, 4999), (2047, 2049), (4998, 5000), (333, 334),
-                                        (17, 17)])
+@pytest.mark.parametrize("first,last", [(0, 5000), (1, 4999), (2047, 2049), (4998, 5000),
+                                        (333, 334), (17, 17)])
 def test_packed_rows_in_the_middle(F, dtype, inter, first, last):  # noqa: F811
     log("rope packed rows %d to %d, %s" % (first, last, dtype))
     gen = torch.Generator().manual_seed(98)
@@ -71,8 +71,8 @@ def test_packed_rows_in_the_middle(F, dtype, inter, first, last):  # noqa: F811
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("n", [3, 2500])
-@pytest.mark.parametrize("D,pairs", [(1024, (512,)), (1024, (100, 0, 21)), (1022, (511,)), (2, (1,)),
-                                     (256, (1, 1, 1, 1))])
+@pytest.mark.parametrize("D,pairs", [(1024, (512,)), (1024, (100, 0, 21)), (1022, (511,)),
+                                     (2, (1,)), (256, (1, 1, 1, 1))])
 def test_largest_and_smallest_heads(F, dtype, inter, n, D, pairs):  # noqa: F811
     log("rope %d rows of %d, pairs %s, %s" % (n, D, pairs, dtype))
     gen = torch.Generator().manual_seed(99)
