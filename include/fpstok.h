@@ -489,6 +489,122 @@ fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_params* par
                           const fpstok_heads* q_out, const fpstok_heads* k_in,
                           const fpstok_heads* k_out, void* stream);
 
+/* ------------------------------------ the step between two blocks -- */
+
+#define FPSTOK_HAS_RESIDUAL 1 /* fpstok_residual and its gradients          */
+#define FPSTOK_MAX_WIDTH 8192 /* largest width of the residual step           */
+
+typedef enum { FPSTOK_NORM_NONE = 0, FPSTOK_NORM_RMS = 1, FPSTOK_NORM_LAYER = 2 } fpstok_norm;
+typedef enum {
+    FPSTOK_GATE_NONE = 0,
+    FPSTOK_GATE_ROW = 1,     /* gate [num_rows][C]                                  */
+    FPSTOK_GATE_SEQUENCE = 2 /* gate [num_seqs][C]: one row for all of a sequence   */
+} fpstok_gate;
+typedef enum { FPSTOK_ACT_NONE = 0, FPSTOK_ACT_SIGMOID = 1, FPSTOK_ACT_SILU = 2 } fpstok_act;
+
+/* A [rows][C] view: row r starts at data + r*row_stride (elements), its
+ * elements are adjacent.  Inputs may use any stride >= 0 (0: the same row
+ * again), outputs' rows must not overlap.  A row_stride above 2^23 is refused
+ * (EUNSUPPORTED).  16-byte aligned data and strides and a width that is a
+ * multiple of 8 are faster, everywhere or nowhere in a call. */
+typedef struct {
+    void* data;
+    int64_t row_stride;
+} fpstok_rows;
+
+typedef struct {
+    int32_t width;        /* C: 1 .. FPSTOK_MAX_WIDTH                                */
+    int32_t stream_dtype; /* of x, x_out and their gradients: FPSTOK_F32 or ...      */
+    int32_t branch_dtype; /* ... that of y, gate, h and their gradients: FPSTOK_F32, */
+                          /* FPSTOK_F16 or FPSTOK_BF16                               */
+    int32_t post_norm;    /* fpstok_norm of the block's result y                     */
+    int32_t pre_norm;     /* fpstok_norm of the sum, for the next block: NONE: no h  */
+    int32_t gate_per;     /* fpstok_gate                                             */
+    int32_t activation;   /* fpstok_act of the gate                                  */
+    float eps;            /* of both norms, > 0                                      */
+} fpstok_residual_params;
+
+/* [C] float32 each; NULL: ones, zeros for a bias.  A weight or bias belongs to
+ * its norm, the scale to y. */
+typedef struct {
+    const float* post_weight;
+    const float* post_bias;
+    const float* scale;
+    const float* pre_weight;
+    const float* pre_bias;
+} fpstok_residual_weights;
+
+/* [C] float32 each, where the weight of that name is given; NULL: not formed. */
+typedef struct {
+    float* post_weight;
+    float* post_bias;
+    float* scale;
+    float* pre_weight;
+    float* pre_bias;
+} fpstok_residual_weight_grads;
+
+/* The step between two blocks of an encoder over the tokens (graphnet PR #923,
+ * "What is added": RotaryTransformerBlock and its norms; norms on both sides of a
+ * block as in the set transformer of the neighbouring pages): for every row
+ * of a sequence
+ *   u = post_norm(y),  z = u * activation(gate)  (z = u without a gate),
+ *   x_out = x + scale * z,  h = pre_norm(x_out).
+ * RMS: v / sqrt(mean(v^2) + eps) * weight + bias.  LAYER: (v - mean(v)) /
+ * sqrt(mean((v - mean(v))^2) + eps) * weight + bias.  Everything between the
+ * loads and the stores is float32: h comes from the sum before x_out is rounded.
+ * (Sums of squares are float32 too: a row whose squares pass 3.4e38 norms to 0.)
+ *   x      [rows][C] in, stream_dtype
+ *   y      [rows][C] in, branch_dtype; NULL: no block before (x_out = x, h its
+ *          norm), then no post norm, gate or scale
+ *   gate   [rows][C] or [num_seqs][C] in, branch_dtype (NULL without gate_per)
+ *   x_out  [rows][C] out, stream_dtype, or NULL if there is h; may be x itself
+ *   h      [rows][C] out, branch_dtype (NULL without pre_norm); may be y itself
+ *   stats  [rows][4] f32 out, 16-byte aligned, for the gradients: mean and
+ *          1/std of the post norm, then of the pre norm; or NULL
+ * Rows behind the last packed sequence (and ahead of the first) are left as they
+ * were; the free slots of padded ones get 0.  No other output may overlap
+ * an input.  Errors: EINVAL, EUNSUPPORTED, EHIP. */
+fpstok_status fpstok_residual(const fpstok_seqs* seqs, const fpstok_residual_params* params,
+                              const fpstok_residual_weights* weights, const fpstok_rows* x,
+                              const fpstok_rows* y, const fpstok_rows* gate,
+                              const fpstok_rows* x_out, const fpstok_rows* h, float* stats,
+                              void* stream);
+
+/* Gradients of fpstok_residual.  With the rows of the forward call formed again
+ * in float32, xh and yh the normed x_out and y (before weight and bias), a =
+ * activation(gate), mean() over a row's columns, and gh = grad_h:
+ *   p = gh pre_weight,  gx = grad_x_out + (p - mean(p) - xh mean(p xh)) / std,
+ *   grad_x = gx,  grad_gate = gx scale u a',  gu = gx scale a,
+ *   q = gu post_weight,  grad_y = (q - mean(q) - yh mean(q yh)) / std
+ * (mean(p) and mean(q) for LAYER only; grad_y = gu without a post norm), and,
+ * summed over the rows of all sequences,
+ *   pre_weight: gh xh,  pre_bias: gh,  scale: gx a u,  post_weight: gu yh,
+ *   post_bias: gu;
+ * grad_gate of FPSTOK_GATE_SEQUENCE is summed over the sequence's rows.  Sums are
+ * held in float32 or float64 in a fixed order (no floating-point atomics).
+ *   x, y, gate, stats   as given to, and written by, the forward call (stats
+ *                       may be NULL if there is no norm)
+ *   grad_x_out          [rows][C] in, stream_dtype, or NULL (x_out was not used)
+ *   grad_h              [rows][C] in, branch_dtype, or NULL (h was not used)
+ *   grad_x              [rows][C] out, or NULL; may be grad_x_out itself
+ *   grad_y, grad_gate   out, as y and gate, or NULL
+ *   grads               the weights' gradients, or NULL
+ *   ws  fpstok_residual_workspace_size(seqs, params) bytes, 256-byte aligned
+ * Rows of no sequence as in the forward call; a sequence without rows gets a
+ * gate gradient of 0.  Errors: EINVAL, EWORKSPACE, EUNSUPPORTED, EHIP. */
+fpstok_status fpstok_residual_backward(
+    const fpstok_seqs* seqs, const fpstok_residual_params* params,
+    const fpstok_residual_weights* weights, const fpstok_rows* x, const fpstok_rows* y,
+    const fpstok_rows* gate, const float* stats, const fpstok_rows* grad_x_out,
+    const fpstok_rows* grad_h, const fpstok_rows* grad_x, const fpstok_rows* grad_y,
+    const fpstok_rows* grad_gate, const fpstok_residual_weight_grads* grads, void* ws,
+    size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of fpstok_residual_backward.  Host-only; 0 for arguments
+ * it would refuse (the reason is in fpstok_last_error()). */
+size_t fpstok_residual_workspace_size(const fpstok_seqs* seqs,
+                                      const fpstok_residual_params* params);
+
 /* Device-side status of the last fpstok_sample or fpstok_tokenize call on
  * the workspace `ws` (its first ws_bytes bytes; at least the 256-byte
  * header).  An event of more than 4096 pulses is split over a gang of

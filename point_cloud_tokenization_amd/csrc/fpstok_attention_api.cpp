@@ -5,15 +5,13 @@
 
 #include <cmath>
 
-#include "fpstok_host.h"
+#include "fpstok_seqs_host.h"
 
 namespace fpstok {
 
 static_assert(kMaxAxes == FPSTOK_MAX_AXES, "axes of the rotary positions");
 
-static int elem_bytes(int dtype) { return dtype == FPSTOK_F32 ? 4 : 2; }
-
-static fpstok_status check_seqs(const fpstok_seqs* s, const char* what) {
+fpstok_status check_seqs(const fpstok_seqs* s, const char* what) {
     if (!s) return fail(FPSTOK_EINVAL, "%s is NULL", what);
     if (s->num_seqs < 0) return fail(FPSTOK_EINVAL, "%s: num_seqs < 0", what);
     if (s->num_rows < 0) return fail(FPSTOK_EINVAL, "%s: num_rows < 0", what);
@@ -104,7 +102,7 @@ static fpstok_status check_heads(const fpstok_heads* v, const char* what, int64_
     return FPSTOK_OK;
 }
 
-static SeqArgs seq_args(const fpstok_seqs* s) {
+SeqArgs seq_args(const fpstok_seqs* s) {
     return SeqArgs{s->cu_seqlens, s->token_count, s->num_rows, (int32_t)s->num_seqs, s->capacity};
 }
 
@@ -139,8 +137,6 @@ static int32_t likely_len(const fpstok_seqs* s) {
     if (s->token_count) return s->capacity;
     return s->num_seqs > 0 ? (int32_t)((s->num_rows + s->num_seqs - 1) / s->num_seqs) : 0;
 }
-
-static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Plans a call and lays out its workspace (pointers are offsets from `ws`);
 // returns the bytes it needs.
@@ -188,7 +184,7 @@ static fpstok_status check_grid(const AttnPlan& plan) {
     return FPSTOK_OK;
 }
 
-static fpstok_status check_attn_ws(size_t need, void* ws, size_t ws_bytes) {
+fpstok_status check_ws(size_t need, void* ws, size_t ws_bytes) {
     if (need == 0) return FPSTOK_OK;
     if (!ws) return fail(FPSTOK_EWORKSPACE, "workspace is NULL (need %zu bytes)", need);
     if (ws_bytes < need)
@@ -232,7 +228,7 @@ FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_se
     AttnPlan plan;
     const size_t need = lay_out(qs, ks, false, ws, a, plan);
     if ((st = check_grid(plan)) != FPSTOK_OK ||
-        (st = check_attn_ws(need, ws, ws_bytes)) != FPSTOK_OK)
+        (st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;
     if (qs->num_seqs == 0 || nq == 0) return ok();
     a.q = heads_arg(q);
@@ -271,7 +267,7 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
     AttnPlan plan;
     const size_t need = lay_out(qs, ks, true, ws, a, plan);
     if ((st = check_grid(plan)) != FPSTOK_OK ||
-        (st = check_attn_ws(need, ws, ws_bytes)) != FPSTOK_OK)
+        (st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;
     if (qs->num_seqs == 0 || nq + nk == 0) return ok();
     a.q = heads_arg(q);

@@ -1,0 +1,41 @@
+// Internal interface between the C ABI (fpstok_residual_api.cpp) and the gfx950
+// kernels of the residual step (fpstok_residual.hip).  Not installed; not part
+// of the ABI.
+#pragma once
+
+#include "fpstok_attention.h"
+
+namespace fpstok {
+
+struct RowsArg {
+    void* data;  // null: not given
+    int64_t row;  // stride in elements
+};
+
+constexpr int kResidualWeights = 5;  // post weight, post bias, scale, pre weight, pre bias
+
+struct ResidualArgs {
+    SeqArgs seqs;
+    RowsArg x, y, gate, x_out, h;
+    RowsArg grad_x_out, grad_h, grad_x, grad_y, grad_gate;
+    const float* weights[kResidualWeights];  // null: ones, or zeros for a bias
+    float* weight_grads[kResidualWeights];   // null: not formed
+    float* stats;                            // [rows][4]: post mean, 1/std, pre mean, 1/std
+    int32_t C, stream, branch;               // width, dtypes
+    int32_t post, pre, gate_per, act;        // as in fpstok_residual_params
+    float eps;
+    int32_t vec;    // 16-byte accesses fit every operand
+    int32_t shift;  // a run is 2^shift rows
+    // backward: the workgroups' parts of the weights' gradients, [workgroups][given
+    // weights][C], and of the gates of sequences, [runs + sequences][C]
+    float* part;
+    float* gate_part;
+};
+
+// Workgroups of the launch over runs of 2^shift rows.
+int64_t residual_blocks(const ResidualArgs& a);
+int residual_shift(const ResidualArgs& a, bool backward);
+hipError_t launch_residual(const ResidualArgs& a, hipStream_t s);
+hipError_t launch_residual_backward(const ResidualArgs& a, hipStream_t s);
+
+}  // namespace fpstok

@@ -21,6 +21,10 @@ F32, F16, BF16, I32 = 0, 1, 2, 3  # fpstok_dtype
 MAX_PATCHES, MAX_K, MAX_LLOYD = 1024, 64, 1000
 NOALLOC_MAX_WORKSPACE = 64 << 20  # FPSTOK_NOALLOC_MAX_WORKSPACE
 MAX_HEAD_DIM, MAX_SINKS, MAX_AXES = 128, 64, 4
+MAX_WIDTH = 8192
+NORMS = {"none": 0, "rms": 1, "layer": 2}  # fpstok_norm
+GATES = {"none": 0, "row": 1, "sequence": 2}  # fpstok_gate
+ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}  # fpstok_act
 
 
 class FpstokError(RuntimeError):
@@ -74,6 +78,24 @@ class RopeParams(ctypes.Structure):
                 ("inverse", ctypes.c_int32)]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64)]
+
+
+class ResidualParams(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("stream_dtype", ctypes.c_int32),
+                ("branch_dtype", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("pre_norm", ctypes.c_int32), ("gate_per", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class ResidualWeights(ctypes.Structure):
+    """fpstok_residual_weights, and with the gradients' pointers
+    fpstok_residual_weight_grads."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("post_weight", "post_bias", "scale", "pre_weight",
+                                               "pre_bias")]
+
+
 _lib = None
 
 
@@ -114,7 +136,15 @@ def lib():
         L.fpstok_attention_workspace_size.restype = sz
         L.fpstok_rope.argtypes = [S, ctypes.POINTER(RopeParams), vp, vp] + \
             [ctypes.POINTER(Heads)] * 4 + [vp]
+        RP, RW = ctypes.POINTER(ResidualParams), ctypes.POINTER(ResidualWeights)
+        R = ctypes.POINTER(Rows)
+        L.fpstok_residual.argtypes = [S, RP, RW] + [R] * 5 + [vp, vp]
+        L.fpstok_residual_backward.argtypes = [S, RP, RW] + [R] * 3 + [vp] + [R] * 5 + \
+            [RW, vp, sz, vp]
+        L.fpstok_residual_workspace_size.argtypes = [S, RP]
+        L.fpstok_residual_workspace_size.restype = sz
         for f in ("fpstok_attention", "fpstok_attention_backward", "fpstok_rope",
+                  "fpstok_residual", "fpstok_residual_backward",
                   "fpstok_sample", "fpstok_assign", "fpstok_knn", "fpstok_lloyd",
                   "fpstok_pool", "fpstok_tokenize", "fpstok_validate", "fpstok_pack",
                   "fpstok_unpack", "fpstok_pool_backward", "fpstok_random_start",
@@ -726,3 +756,138 @@ class Rope(_DeviceCall):
         """fpstok_rope; inverse=True turns back (the gradient)."""
         self._call(self._fn, "fpstok_rope", self._args[1 if inverse else 0], stream)
         return self.q_out, self.k_out
+
+
+def make_rows(t, name, rows=None, width=None, dtype=None, device=None):
+    """A Rows struct over a [rows, C] device tensor (any row stride, adjacent
+    elements), which the caller keeps alive."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be [rows, C] with adjacent elements" % name)
+    if (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
+        raise ValueError("%s must hold %s rows of %s elements, got %s" % (name, rows, width,
+                                                                        tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    # (the stride of a single row is not used, and may be anything)
+    return Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0)
+
+
+class Residual(_DeviceCall):
+    """fpstok_residual on given tensors, with its outputs allocated once, and
+    with training=True fpstok_residual_backward.
+
+    x [rows, C] the stream; y [rows, C] the block's result, or None; gate
+    [rows, C] (gate_per="row") or [sequences, C] (gate_per="sequence");
+    post_norm, pre_norm: "none", "rms" or "layer"; activation of the gate:
+    "none", "sigmoid" or "silu"; the weights [C] float32 or None.  A call takes
+    what the tensors hold by then; it returns (x_out, h), the same buffers each
+    time (h None without pre_norm); rows behind the last packed sequence keep
+    what they held (0 after construction).  x_out=x and h=y work in place."""
+
+    def __init__(self, x, y, seqs, gate=None, gate_per="none", activation="none",
+                 post_norm="none", pre_norm="rms", post_weight=None, post_bias=None, scale=None,
+                 pre_weight=None, pre_bias=None, eps=1e-6, training=False, x_out=None, h=None):
+        import torch
+
+        super().__init__(x.device)
+        for value, known, name in ((post_norm, NORMS, "post_norm"), (pre_norm, NORMS, "pre_norm"),
+                                   (gate_per, GATES, "gate_per"),
+                                   (activation, ACTIVATIONS, "activation")):
+            if value not in known:
+                raise ValueError("%s must be one of %s" % (name, ", ".join(known)))
+        n, dev = seqs.num_rows, x.device
+        if seqs.tensor.device != dev:
+            raise ValueError("the sequences are on %s, expected %s" % (seqs.tensor.device, dev))
+        xr = make_rows(x, "x", rows=n)
+        C = x.shape[1]
+        branch = y if y is not None else h
+        bd = x.dtype if branch is None else branch.dtype
+        yr = None if y is None else make_rows(y, "y", n, C, bd, dev)
+        if (gate is None) != (gate_per == "none"):
+            raise ValueError("give gate with gate_per, or neither")
+        gate_rows = n if gate_per == "row" else seqs.num_seqs
+        gr = None if gate is None else make_rows(gate, "gate", gate_rows, C, bd, dev)
+        weights = dict(post_weight=post_weight, post_bias=post_bias, scale=scale,
+                       pre_weight=pre_weight, pre_bias=pre_bias)
+        for name, w in weights.items():
+            if w is not None:
+                _need(w, torch.float32, name, dev)
+                if tuple(w.shape) != (C,):
+                    raise ValueError("%s must be [%d]" % (name, C))
+        self._rows, self._C, self._sd, self._bd = n, C, x.dtype, bd
+        own = []
+
+        def buffer(given, name, shape, dtype):
+            if given is not None:
+                return given, make_rows(given, name, shape[0], shape[1], dtype, dev)
+            t = torch.zeros(shape, dtype=dtype, device=dev)
+            own.append(t)
+            return t, make_rows(t, name)
+
+        self.x_out, xo = buffer(x_out, "x_out", (n, C), x.dtype)
+        self.h = ho = None
+        if pre_norm != "none":
+            self.h, ho = buffer(h, "h", (n, C), bd)
+        elif h is not None:
+            raise ValueError("h without pre_norm")
+        self.stats = None
+        if training:
+            self.stats = torch.zeros((n, 4), dtype=torch.float32, device=dev)
+            own.append(self.stats)
+        self.params = ResidualParams(C, _dtype_code(x, "x"),
+                                     _dtype_code(x if branch is None else branch, "y"),
+                                     NORMS[post_norm], NORMS[pre_norm], GATES[gate_per],
+                                     ACTIVATIONS[activation], float(eps))
+        self._keep = (x, y, gate, seqs, weights)
+        view = lambda r: None if r is None else ctypes.byref(r)  # noqa: E731
+        w = ResidualWeights(*[_ptr(weights[k]) for k, _ in ResidualWeights._fields_])
+        self._head = (ctypes.byref(seqs), ctypes.byref(self.params), ctypes.byref(w), view(xr),
+                      view(yr), view(gr))
+        self._out = (view(xo), view(ho), _ptr(self.stats))
+        self._fwd, self._bwd = lib().fpstok_residual, lib().fpstok_residual_backward
+        self.grads = None
+        if training:
+            grads = {"x": torch.zeros((n, C), dtype=x.dtype, device=dev)}
+            if y is not None:
+                grads["y"] = torch.zeros((n, C), dtype=bd, device=dev)
+            if gate is not None:
+                grads["gate"] = torch.zeros((gate_rows, C), dtype=bd, device=dev)
+            for name, t in weights.items():
+                if t is not None:
+                    grads[name] = torch.zeros(C, dtype=torch.float32, device=dev)
+            need = lib().fpstok_residual_workspace_size(*self._head[:2])
+            self.ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            out = [None if grads.get(k) is None else make_rows(grads[k], k)
+                   for k in ("x", "y", "gate")]
+            gw = ResidualWeights(*[_ptr(grads.get(k)) for k, _ in ResidualWeights._fields_])
+            self._tail = tuple(view(r) for r in out) + (
+                ctypes.byref(gw), _ptr(self.ws), 0 if self.ws is None else self.ws.numel())
+            self.grads = grads
+            own += list(grads.values()) + ([] if self.ws is None else [self.ws])
+        if own:
+            self._allocated(*own)
+
+    def __call__(self, stream=None):
+        """fpstok_residual: (x_out, h)."""
+        self._call(self._fwd, "fpstok_residual", self._head + self._out, stream)
+        return self.x_out, self.h
+
+    def backward(self, grad_x_out=None, grad_h=None, stream=None):
+        """fpstok_residual_backward after a call on the same inputs: a dict of
+        the gradients of x, y, gate and the weights that are given (a gradient
+        that is None counts as 0)."""
+        if self.grads is None:
+            raise ValueError("construct with training=True")
+        gx = gh = None
+        if grad_x_out is not None:
+            gx = make_rows(grad_x_out, "grad_x_out", self._rows, self._C, self._sd, self.device)
+        if grad_h is not None:
+            gh = make_rows(grad_h, "grad_h", self._rows, self._C, self._bd, self.device)
+        view = lambda r: None if r is None else ctypes.byref(r)  # noqa: E731
+        self._call(self._bwd, "fpstok_residual_backward",
+                   self._head + (self._out[2], view(gx), view(gh)) + self._tail, stream)
+        return self.grads
