@@ -489,6 +489,73 @@ fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_params* par
                           const fpstok_heads* q_out, const fpstok_heads* k_in,
                           const fpstok_heads* k_out, void* stream);
 
+/* ------------------------------------ attention with a learned bias -- */
+
+#define FPSTOK_HAS_ATTENTION_BIAS 1 /* fpstok_attention_bias and its gradients */
+#define FPSTOK_MAX_BUCKETS 128      /* most buckets of all axes together          */
+
+/* A learned bias of the scores by the rows' distance, axis by axis.  Axis a
+ * sorts the distance D of a key from a query into buckets[a] buckets; table
+ * [num_heads][sum of buckets] holds a value for each, axis after axis.  Each
+ * float32 operation below is rounded by itself:
+ *   FPSTOK_F32 positions: D = fl(x_k - x_q), x = fl(position * rate[a])
+ *   FPSTOK_I32 positions: D = fl(fl(p_k - p_q) * rate[a]), the difference taken
+ *                         as int32 (it has to fit) and then rounded to float32
+ *   log_steps[a] = 0, linear: bucket = floor(fl(D + shift[a])): buckets of one
+ *     unit, distance 0 in bucket floor(shift[a])
+ *   log_steps[a] = g, a power of two up to 16: bucket = shift[a] + L, or
+ *     shift[a] - L if D < 0, with fl(1 + |D|) = 2^E (1 + F), L = floor(g (E + F)):
+ *     g buckets of one width up to |D| = 1, then g for every doubling of 1 + |D|;
+ *     shift[a] is a whole number of at most 2^20 in absolute value
+ * clamped to [0, buckets[a] - 1].  A distance that is not a number falls into
+ * one of the axis's buckets.  (Integer places with exact buckets up to 7 and
+ * growing ones behind: rate 1/8, g = 8.) */
+typedef struct {
+    const void* q_positions; /* [q rows][num_axes], contiguous                     */
+    const void* k_positions; /* [k rows][num_axes]; NULL without k_seqs: the       */
+                             /* queries'                                           */
+    const float* table;      /* [num_heads][sum of buckets]                        */
+    int32_t positions_dtype; /* FPSTOK_F32 or FPSTOK_I32                           */
+    int32_t num_axes;        /* 1 .. FPSTOK_MAX_AXES                               */
+    int32_t buckets[4];      /* >= 1 each, at most FPSTOK_MAX_BUCKETS together     */
+    int32_t log_steps[4];
+    float rate[4];           /* finite                                             */
+    float shift[4];          /* finite                                             */
+} fpstok_rel_bias;
+
+/* fpstok_attention with s_ij = scale * sum_d q_i[d] k_j[d] + sum over the axes of
+ * table[head][bucket].  A table entry of -1e30 or less counts as -infinity: a
+ * pair with such an entry has weight 0, and a query whose every visible pair has
+ * one gets out = 0 and lse = -inf.  (Only the window keeps what is not finite
+ * away: an infinite value times such a weight is not a number.)  Everything
+ * else as there, the workspace of fpstok_attention_bias_workspace_size(...,
+ * 0).  Errors: as there; EINVAL for the bias, EUNSUPPORTED if num_heads /
+ * num_kv_heads times the buckets passes 4096. */
+fpstok_status fpstok_attention_bias(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
+                                    const fpstok_attn_params* params, const fpstok_rel_bias* bias,
+                                    const fpstok_heads* q, const fpstok_heads* k,
+                                    const fpstok_heads* v, const fpstok_heads* out, float* lse,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of fpstok_attention_bias: as fpstok_attention_backward, and
+ *   grad_table [num_heads][sum of buckets] f32 out, or NULL: the sum of ds_ij over
+ *   the visible pairs of all sequences that fall into the bucket, written whole
+ *   (0 for a bucket without pairs).  It is held in float32 per tile of rows and
+ *   float64 across them, from weights and ds that are not rounded, in a fixed
+ *   order. */
+fpstok_status fpstok_attention_bias_backward(
+    const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs, const fpstok_attn_params* params,
+    const fpstok_rel_bias* bias, const fpstok_heads* q, const fpstok_heads* k,
+    const fpstok_heads* v, const fpstok_heads* out, const float* lse,
+    const fpstok_heads* grad_out, const fpstok_heads* grad_q, const fpstok_heads* grad_k,
+    const fpstok_heads* grad_v, float* grad_table, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of fpstok_attention_bias (backward = 0) or its gradients
+ * (1).  Host-only; 0 for arguments the call would refuse. */
+size_t fpstok_attention_bias_workspace_size(const fpstok_seqs* q_seqs, const fpstok_seqs* k_seqs,
+                                            const fpstok_attn_params* params,
+                                            const fpstok_rel_bias* bias, int32_t backward);
+
 /* ------------------------------------ the step between two blocks -- */
 
 #define FPSTOK_HAS_RESIDUAL 1 /* fpstok_residual and its gradients          */

@@ -53,6 +53,24 @@ struct AttnArgs {
     float* sink_part;
 };
 
+// A learned bias of the scores by buckets of distance (fpstok_rel_bias).
+struct BiasArgs {
+    const void* q_pos;  // [q rows][axes], float32 or (ints) int32
+    const void* k_pos;
+    const float* table;  // [H][entries]
+    int32_t axes, ints, entries;
+    int32_t first[kMaxAxes], top[kMaxAxes];  // an axis's first entry and its last bucket
+    int32_t log_shift[kMaxAxes];             // bits below a step of a log axis, -1: linear
+    float rate[kMaxAxes], shift[kMaxAxes];
+    // gradient: the entries from .. from + count - 1 (all there are, or a part of
+    // many), and the workgroups' parts, [row tiles][Hk][G][count]
+    int32_t from, count;
+    float* grad;  // [H][entries], or null
+    float* part;
+};
+constexpr int kGroupEntries = 4096;  // table entries of one key head's query heads (16 KB of LDS)
+constexpr int kTableEntries = 64;  // entries whose gradients one launch forms
+
 // How a call is laid out on the device, from the shapes alone.
 struct AttnPlan {
     bool few;        // at most 32 rows per sequence and key head: waves split the keys
@@ -78,6 +96,13 @@ int plan_key_parts(const AttnArgs& a, int32_t q_len);
 AttnPlan plan_attention(const AttnArgs& a, int32_t q_len, int32_t k_len);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);
+// The same with a bias (fpstok_attention_bias.hip).
+hipError_t launch_attention_bias(const AttnArgs& a, const BiasArgs& b, const AttnPlan& plan,
+                                 hipStream_t s);
+hipError_t launch_attention_bias_backward(const AttnArgs& a, const BiasArgs& b, hipStream_t s);
+// Joins of split walks.
+void launch_join(const AttnArgs& a, hipStream_t s);
+void launch_join_dkv(const AttnArgs& a, hipStream_t s);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
 
 }  // namespace fpstok

@@ -138,16 +138,73 @@ static int32_t likely_len(const fpstok_seqs* s) {
     return s->num_seqs > 0 ? (int32_t)((s->num_rows + s->num_seqs - 1) / s->num_seqs) : 0;
 }
 
+// The bias of a call, checked, as the kernels take it (`b`; its positions and
+// table may still be NULL: check_bias_data).
+static fpstok_status check_bias(const fpstok_rel_bias* r, const fpstok_attn_params* p,
+                                BiasArgs& b) {
+    if (!r) return fail(FPSTOK_EINVAL, "bias is NULL");
+    if (r->positions_dtype != FPSTOK_F32 && r->positions_dtype != FPSTOK_I32)
+        return fail(FPSTOK_EINVAL, "positions_dtype must be FPSTOK_F32 or FPSTOK_I32");
+    if (r->num_axes < 1 || r->num_axes > FPSTOK_MAX_AXES)
+        return fail(FPSTOK_EINVAL, "num_axes must be in [1, %d]", FPSTOK_MAX_AXES);
+    b = BiasArgs{};
+    b.q_pos = r->q_positions;
+    b.k_pos = r->k_positions;
+    b.table = r->table;
+    b.axes = r->num_axes;
+    b.ints = r->positions_dtype == FPSTOK_I32;
+    for (int i = 0; i < b.axes; ++i) {
+        const int steps = r->log_steps[i];
+        if (r->buckets[i] < 1 || r->buckets[i] > FPSTOK_MAX_BUCKETS - b.entries)
+            return fail(FPSTOK_EINVAL, "buckets[%d]: at least 1 an axis, at most %d together", i,
+                        FPSTOK_MAX_BUCKETS);
+        if (steps < 0 || steps > 16 || (steps & (steps - 1)) != 0)
+            return fail(FPSTOK_EINVAL, "log_steps[%d] must be 0, 1, 2, 4, 8 or 16", i);
+        if (!std::isfinite(r->rate[i]) || !std::isfinite(r->shift[i]))
+            return fail(FPSTOK_EINVAL, "rate[%d] and shift[%d] must be finite", i, i);
+        if (steps > 0 && (r->shift[i] != std::floor(r->shift[i]) ||
+                          std::fabs(r->shift[i]) > 1048576.0f))
+            return fail(FPSTOK_EINVAL, "shift[%d] of a log axis: a whole number up to 2^20", i);
+        b.first[i] = b.entries;
+        b.top[i] = r->buckets[i] - 1;
+        b.log_shift[i] = steps > 0 ? 23 - __builtin_ctz((unsigned)steps) : -1;
+        b.rate[i] = r->rate[i];
+        b.shift[i] = r->shift[i];
+        b.entries += r->buckets[i];
+    }
+    b.count = b.entries;
+    if ((int64_t)(p->num_heads / p->num_kv_heads) * b.entries > kGroupEntries)
+        return fail(FPSTOK_EUNSUPPORTED, "query heads per key head times buckets > %d",
+                    kGroupEntries);
+    return FPSTOK_OK;
+}
+
+static fpstok_status check_bias_data(const fpstok_seqs* qs, const fpstok_seqs* ks, BiasArgs& b) {
+    if (!b.k_pos && qs == ks) b.k_pos = b.q_pos;
+    if (!b.table) return fail(FPSTOK_EINVAL, "table is NULL");
+    if ((qs->num_rows > 0 && !b.q_pos) || (ks->num_rows > 0 && !b.k_pos))
+        return fail(FPSTOK_EINVAL, "q_positions or k_positions is NULL");
+    if (((uintptr_t)b.table & 3u) != 0 || ((uintptr_t)b.q_pos & 3u) != 0 ||
+        ((uintptr_t)b.k_pos & 3u) != 0)
+        return fail(FPSTOK_EINVAL, "table and positions must be 4-byte aligned");
+    return FPSTOK_OK;
+}
+
 // Plans a call and lays out its workspace (pointers are offsets from `ws`);
-// returns the bytes it needs.
+// returns the bytes it needs.  `b`: NULL without a bias.
 static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backward, void* ws,
-                      AttnArgs& a, AttnPlan& plan) {
+                      AttnArgs& a, BiasArgs* b, AttnPlan& plan) {
     const size_t rows = (size_t)qs->num_rows * a.H;
     char* at = (char*)ws;
     if (backward) {
         a.lse2 = (float*)at;
         a.delta = (float*)(at + align256(rows * sizeof(float)));
         size_t need = 2 * align256(rows * sizeof(float));
+        if (b) {
+            b->part = (float*)(at + need);
+            const int entries = b->entries < kTableEntries ? b->entries : kTableEntries;
+            need += align256((size_t)row_slots(a.qs, a.G, 7) * a.H * entries * sizeof(float));
+        }
         a.k_splits = plan_key_parts(a, likely_len(qs));
         if (a.k_splits > 1) {
             a.k_part = (float*)(at + need);
@@ -198,21 +255,25 @@ fpstok_status check_ws(size_t need, void* ws, size_t ws_bytes) {
 
 using namespace fpstok;
 
-FPSTOK_API size_t fpstok_attention_workspace_size(const fpstok_seqs* qs, const fpstok_seqs* ks,
-                                                  const fpstok_attn_params* p, int32_t backward) {
+// The calls with a bias (`r`) and without (`biased` false).
+static size_t workspace_size(const fpstok_seqs* qs, const fpstok_seqs* ks,
+                             const fpstok_attn_params* p, bool biased, const fpstok_rel_bias* r,
+                             bool backward) {
     if (!ks) ks = qs;
+    BiasArgs b{};
     if (check_attn(qs, ks, p) != FPSTOK_OK) return 0;
+    if (biased && check_bias(r, p, b) != FPSTOK_OK) return 0;
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    const size_t need = lay_out(qs, ks, backward != 0, nullptr, a, plan);
+    const size_t need = lay_out(qs, ks, backward, nullptr, a, biased ? &b : nullptr, plan);
     return check_grid(plan) == FPSTOK_OK ? need : 0;
 }
 
-FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_seqs* ks,
-                                          const fpstok_attn_params* p, const fpstok_heads* q,
-                                          const fpstok_heads* k, const fpstok_heads* v,
-                                          const fpstok_heads* out, float* lse, void* ws,
-                                          size_t ws_bytes, void* stream) {
+static fpstok_status attend(const fpstok_seqs* qs, const fpstok_seqs* ks,
+                            const fpstok_attn_params* p, bool biased, const fpstok_rel_bias* r,
+                            const fpstok_heads* q, const fpstok_heads* k, const fpstok_heads* v,
+                            const fpstok_heads* out, float* lse, void* ws, size_t ws_bytes,
+                            void* stream) {
     if (!ks) ks = qs;
     fpstok_status st = check_attn(qs, ks, p);
     if (st != FPSTOK_OK) return st;
@@ -224,9 +285,13 @@ FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_se
         (st = check_heads(out, "out", nq, H, D, dt, 16, true)) != FPSTOK_OK)
         return st;
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
+    BiasArgs b{};
+    if (biased && ((st = check_bias(r, p, b)) != FPSTOK_OK ||
+                   (st = check_bias_data(qs, ks, b)) != FPSTOK_OK))
+        return st;
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    const size_t need = lay_out(qs, ks, false, ws, a, plan);
+    const size_t need = lay_out(qs, ks, false, ws, a, nullptr, plan);
     if ((st = check_grid(plan)) != FPSTOK_OK ||
         (st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;
@@ -236,17 +301,18 @@ FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_se
     a.v = heads_arg(v);
     a.out = heads_arg(out);
     a.lse = lse;
-    const hipError_t e = launch_attention(a, plan, (hipStream_t)stream);
+    const hipError_t e = biased ? launch_attention_bias(a, b, plan, (hipStream_t)stream)
+                                : launch_attention(a, plan, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "attention kernel launch");
     return ok();
 }
 
-FPSTOK_API fpstok_status fpstok_attention_backward(
-    const fpstok_seqs* qs, const fpstok_seqs* ks, const fpstok_attn_params* p,
-    const fpstok_heads* q, const fpstok_heads* k, const fpstok_heads* v, const fpstok_heads* out,
-    const float* lse, const fpstok_heads* grad_out, const fpstok_heads* grad_q,
-    const fpstok_heads* grad_k, const fpstok_heads* grad_v, void* ws, size_t ws_bytes,
-    void* stream) {
+static fpstok_status attend_backward(
+    const fpstok_seqs* qs, const fpstok_seqs* ks, const fpstok_attn_params* p, bool biased,
+    const fpstok_rel_bias* r, const fpstok_heads* q, const fpstok_heads* k, const fpstok_heads* v,
+    const fpstok_heads* out, const float* lse, const fpstok_heads* grad_out,
+    const fpstok_heads* grad_q, const fpstok_heads* grad_k, const fpstok_heads* grad_v,
+    float* grad_table, void* ws, size_t ws_bytes, void* stream) {
     if (!ks) ks = qs;
     fpstok_status st = check_attn(qs, ks, p);
     if (st != FPSTOK_OK) return st;
@@ -263,13 +329,22 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
         return st;
     if (nq > 0 && !lse) return fail(FPSTOK_EINVAL, "lse is NULL");
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
+    BiasArgs b{};
+    if (biased && ((st = check_bias(r, p, b)) != FPSTOK_OK ||
+                   (st = check_bias_data(qs, ks, b)) != FPSTOK_OK))
+        return st;
+    if (((uintptr_t)grad_table & 3u) != 0)
+        return fail(FPSTOK_EINVAL, "grad_table must be 4-byte aligned");
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    const size_t need = lay_out(qs, ks, true, ws, a, plan);
+    const size_t need = lay_out(qs, ks, true, ws, a, biased ? &b : nullptr, plan);
     if ((st = check_grid(plan)) != FPSTOK_OK ||
         (st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;
-    if (qs->num_seqs == 0 || nq + nk == 0) return ok();
+    b.grad = grad_table;
+    // (without a row the table's gradient is still written: 0)
+    if (qs->num_seqs == 0) a.qs.rows = a.ks.rows = 0;
+    if (a.qs.rows + a.ks.rows == 0 && !b.grad) return ok();
     a.q = heads_arg(q);
     a.k = heads_arg(k);
     a.v = heads_arg(v);
@@ -279,9 +354,60 @@ FPSTOK_API fpstok_status fpstok_attention_backward(
     a.grad_k = heads_arg(grad_k);
     a.grad_v = heads_arg(grad_v);
     a.lse = const_cast<float*>(lse);
-    const hipError_t e = launch_attention_backward(a, (hipStream_t)stream);
+    const hipError_t e = biased ? launch_attention_bias_backward(a, b, (hipStream_t)stream)
+                                : launch_attention_backward(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "attention gradient kernel launch");
     return ok();
+}
+
+FPSTOK_API size_t fpstok_attention_workspace_size(const fpstok_seqs* qs, const fpstok_seqs* ks,
+                                                  const fpstok_attn_params* p, int32_t backward) {
+    return workspace_size(qs, ks, p, false, nullptr, backward != 0);
+}
+
+FPSTOK_API size_t fpstok_attention_bias_workspace_size(const fpstok_seqs* qs,
+                                                       const fpstok_seqs* ks,
+                                                       const fpstok_attn_params* p,
+                                                       const fpstok_rel_bias* bias,
+                                                       int32_t backward) {
+    return workspace_size(qs, ks, p, true, bias, backward != 0);
+}
+
+FPSTOK_API fpstok_status fpstok_attention(const fpstok_seqs* qs, const fpstok_seqs* ks,
+                                          const fpstok_attn_params* p, const fpstok_heads* q,
+                                          const fpstok_heads* k, const fpstok_heads* v,
+                                          const fpstok_heads* out, float* lse, void* ws,
+                                          size_t ws_bytes, void* stream) {
+    return attend(qs, ks, p, false, nullptr, q, k, v, out, lse, ws, ws_bytes, stream);
+}
+
+FPSTOK_API fpstok_status fpstok_attention_bias(const fpstok_seqs* qs, const fpstok_seqs* ks,
+                                               const fpstok_attn_params* p,
+                                               const fpstok_rel_bias* bias, const fpstok_heads* q,
+                                               const fpstok_heads* k, const fpstok_heads* v,
+                                               const fpstok_heads* out, float* lse, void* ws,
+                                               size_t ws_bytes, void* stream) {
+    return attend(qs, ks, p, true, bias, q, k, v, out, lse, ws, ws_bytes, stream);
+}
+
+FPSTOK_API fpstok_status fpstok_attention_backward(
+    const fpstok_seqs* qs, const fpstok_seqs* ks, const fpstok_attn_params* p,
+    const fpstok_heads* q, const fpstok_heads* k, const fpstok_heads* v, const fpstok_heads* out,
+    const float* lse, const fpstok_heads* grad_out, const fpstok_heads* grad_q,
+    const fpstok_heads* grad_k, const fpstok_heads* grad_v, void* ws, size_t ws_bytes,
+    void* stream) {
+    return attend_backward(qs, ks, p, false, nullptr, q, k, v, out, lse, grad_out, grad_q, grad_k,
+                           grad_v, nullptr, ws, ws_bytes, stream);
+}
+
+FPSTOK_API fpstok_status fpstok_attention_bias_backward(
+    const fpstok_seqs* qs, const fpstok_seqs* ks, const fpstok_attn_params* p,
+    const fpstok_rel_bias* bias, const fpstok_heads* q, const fpstok_heads* k,
+    const fpstok_heads* v, const fpstok_heads* out, const float* lse, const fpstok_heads* grad_out,
+    const fpstok_heads* grad_q, const fpstok_heads* grad_k, const fpstok_heads* grad_v,
+    float* grad_table, void* ws, size_t ws_bytes, void* stream) {
+    return attend_backward(qs, ks, p, true, bias, q, k, v, out, lse, grad_out, grad_q, grad_k,
+                           grad_v, grad_table, ws, ws_bytes, stream);
 }
 
 FPSTOK_API fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_params* p,

@@ -1,0 +1,62 @@
+// Attention with a learned bias of the scores: the kernels of
+// fpstok_attention_kernels.h with BIAS, and the sum of the tiles' parts of the
+// table's gradient.
+#include "fpstok_attention_kernels.h"
+
+namespace fpstok {
+
+// grad_table: the row tiles' parts in order, in 64 bits (a sum over every pair of
+// the batch): 32 entries of one head per workgroup, 32 threads an entry.
+__global__ __launch_bounds__(1024) void bias_table_kernel(BiasArgs b, int Hk, int G, int tiles) {
+    __shared__ double sums[32][33];
+    const int lane = threadIdx.x & 31, turn = threadIdx.x >> 5;
+    const int h = blockIdx.x, hk = h / G, e = blockIdx.y * 32 + lane;
+    const float* part =
+        b.part + ((int64_t)hk * G + (h - hk * G)) * b.count + (e < b.count ? e : 0);
+    const int64_t step = (int64_t)Hk * G * b.count;
+    double sum = 0.0;
+#pragma unroll 8
+    for (int i = turn; i < tiles; i += 32) sum += (double)part[i * step];
+    sums[turn][lane] = sum;
+    __syncthreads();
+    if (turn != 0 || e >= b.count) return;
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total += sums[i][lane];
+    b.grad[(int64_t)h * b.entries + b.from + e] = (float)total;
+}
+
+template <class T>
+static hipError_t backward(const AttnArgs& a, BiasArgs b, hipStream_t s) {
+    const bool rows = a.qs.rows > 0;
+    if (!b.grad) {
+        b.part = nullptr;
+        if (rows) backward_q<T, true>(a, b, s);
+    } else {
+        // more than kTableEntries entries: a walk for each part of them
+        const int tiles = rows ? (int)row_slots(a.qs, a.G, 7) : 0;
+        for (b.from = 0; b.from < b.entries; b.from += b.count) {
+            const int left = b.entries - b.from;
+            b.count = left < kTableEntries ? left : kTableEntries;
+            if (rows) backward_q<T, true>(a, b, s);
+            bias_table_kernel<<<dim3((unsigned)a.H, (unsigned)((b.count + 31) / 32)), 1024, 0, s>>>(
+                b, a.Hk, a.G, tiles);
+        }
+    }
+    backward_kv<T, true>(a, b, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_attention_bias(const AttnArgs& a, const BiasArgs& b, const AttnPlan& plan,
+                                 hipStream_t s) {
+    return a.dtype == 0   ? forward<float, true>(a, b, plan, s)
+           : a.dtype == 1 ? forward<_Float16, true>(a, b, plan, s)
+                          : forward<__bf16, true>(a, b, plan, s);
+}
+
+hipError_t launch_attention_bias_backward(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
+    return a.dtype == 0 ? backward<float>(a, b, s)
+                        : a.dtype == 1 ? backward<_Float16>(a, b, s) : backward<__bf16>(a, b, s);
+}
+
+}  // namespace fpstok

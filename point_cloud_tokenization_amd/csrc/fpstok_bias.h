@@ -1,0 +1,175 @@
+// A learned bias of the scores by buckets of the rows' distance, for the
+// attention kernels: per axis a of up to four,
+//   D = x_key - x_query,  linear: clamp(floor(D + shift), 0, n - 1),
+//   log: clamp(shift + sign(D) L, 0, n - 1), L = floor(g (E + F)) of
+//        1 + |D| = 2^E (1 + F),
+// each float32 operation rounded by itself, and the score gets table[head]
+// [first[a] + bucket].  For g a power of two, L is 1 + |D|'s bits less those of
+// 1.0, shifted: exponent and leading bits of the fraction.
+#pragma once
+
+#include <type_traits>
+
+#include "fpstok_attention.h"
+#include "fpstok_mma.h"
+
+namespace fpstok {
+
+struct NoBias {};
+template <bool BIAS>
+using BiasParam = std::conditional_t<BIAS, BiasArgs, NoBias>;
+
+// Positions of a tile's rows in LDS, and of the rows across the lanes: float32
+// times the axis's rate, or the int32 as they are.  [axis][row]
+template <bool BIAS, int OWN, int ROWS>
+struct BiasPos {
+    uint32_t own[kMaxAxes][OWN];
+    uint32_t tile[2][kMaxAxes][ROWS];
+};
+template <int OWN, int ROWS>
+struct BiasPos<false, OWN, ROWS> {};
+
+// The element of a small array in registers at a place that is the same in
+// every lane.
+template <class V>
+__device__ __forceinline__ V pick(const V (&v)[kMaxAxes], int a) {
+    return a == 0 ? v[0] : a == 1 ? v[1] : a == 2 ? v[2] : v[3];
+}
+
+// Positions of a tile's ROWS rows on their way to LDS, by THREADS threads.
+template <int ROWS, int THREADS>
+struct PosStage {
+    static constexpr int kPer = ROWS * kMaxAxes > THREADS ? ROWS * kMaxAxes / THREADS : 1;
+    uint32_t x[kPer];
+    int row[kPer], axis[kPer];
+    float rate[kPer];
+    __device__ __forceinline__ PosStage(const BiasArgs& b, int tid) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = tid + i * THREADS;
+            row[i] = (int)((uint32_t)at / (uint32_t)b.axes);
+            axis[i] = at - row[i] * b.axes;
+            rate[i] = pick(b.rate, axis[i]);
+        }
+    }
+    // Rows at or past `rows` (at least 1) hold the last one's.
+    __device__ __forceinline__ void load(const BiasArgs& b, const void* pos, int64_t row0,
+                                         int rows) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = row[i] < rows ? row[i] : rows - 1;
+            x[i] = ((const uint32_t*)pos)[(row0 + r) * b.axes + axis[i]];
+        }
+    }
+    __device__ __forceinline__ void store(const BiasArgs& b, uint32_t (*tile)[ROWS]) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (row[i] < ROWS)
+                tile[axis[i]][row[i]] =
+                    b.ints ? x[i] : __float_as_uint(__uint_as_float(x[i]) * rate[i]);
+    }
+};
+
+// Positions of the rows across a wave's lanes (lanes 0-31 write): row `row` of
+// the buffer, or, not `live`, one that exists.
+template <int OWN>
+__device__ __forceinline__ void own_positions(const BiasArgs& b, uint32_t (*own)[OWN], int at,
+                                              const void* pos, int64_t row, bool live, int half) {
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) {
+        if (a >= b.axes) break;
+        const uint32_t x = ((const uint32_t*)pos)[(live ? row : 0) * b.axes + a];
+        if (half == 0)
+            own[a][at] = b.ints ? x : __float_as_uint(__uint_as_float(x) * b.rate[a]);
+    }
+}
+
+// The group's tables in LDS, in units of log2; -1e30 and less hides a pair.
+__device__ __forceinline__ void load_table(const BiasArgs& b, float* lds, int hk, int G, int tid) {
+    const float* from = b.table + (int64_t)hk * G * b.entries;
+    for (int i = tid; i < G * b.entries; i += 256) {
+        const float x = from[i];
+        lds[i] = x <= -1e30f ? -INFINITY : x * 1.44269504088896f;
+    }
+}
+
+// LDS that the launch adds to a kernel's own: the tables, then the sums of
+// their gradients.
+__device__ __forceinline__ float* bias_lds() {
+    extern __shared__ __attribute__((aligned(256))) float fpstok_bias_lds[];
+    return fpstok_bias_lds;
+}
+__host__ __device__ inline int table_slots(const BiasArgs& b) {
+    return b.count + (b.count != b.entries);
+}
+inline size_t bias_lds_bytes(const BiasArgs& b, int G, bool sums) {
+    const size_t table = ((size_t)G * b.entries + 63) & ~(size_t)63;
+    return (table + (sums ? (size_t)4 * table_slots(b) * 64 : 0)) * sizeof(float);
+}
+
+__device__ __forceinline__ void lds_add(FPSTOK_LDS float* p, float x) {
+    __hip_atomic_fetch_add(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+}
+
+using u32x16 = uint32_t __attribute__((ext_vector_type(16)));
+
+// Adds the bias of a block of 32 x 32 pairs to its scores (in units of log2): a
+// lane's own row against the block's rows in its registers.  own: this lane's
+// place in own[0], tile: that of the block's row 4 half in tile[0].
+// KEY: the own row is the key.  PACK: entries, byte a of a pair's: the entry of
+// axis a.
+template <bool KEY, bool PACK, int OWN, int ROWS>
+__device__ __forceinline__ void add_bias(f32x16& s, u32x16* entries, const BiasArgs& b,
+                                         const FPSTOK_LDS float* table,
+                                         const FPSTOK_LDS uint32_t* own,
+                                         const FPSTOK_LDS uint32_t* tile) {
+    if constexpr (PACK) *entries = 0;
+#pragma unroll 1
+    for (int a = 0; a < b.axes; ++a) {
+        const uint32_t mine = own[a * OWN];
+        const int first = pick(b.first, a), top = pick(b.top, a), shift = pick(b.log_shift, a);
+        const float rate = pick(b.rate, a), zero = pick(b.shift, a);
+        const FPSTOK_LDS float* tab = table + first;
+        auto each = [&](auto ints, auto log) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const u32x4 other = *(const FPSTOK_LDS u32x4*)(tile + a * ROWS + g * 8);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t k = KEY ? mine : other[e], q = KEY ? other[e] : mine;
+                    float d;
+                    if constexpr (decltype(ints)::value)
+                        d = (float)(int)(k - q) * rate;
+                    else
+                        d = __uint_as_float(k) - __uint_as_float(q);
+                    int bucket;
+                    if constexpr (decltype(log)::value) {
+                        const int steps =
+                            (int)((__float_as_uint(1.0f + fabsf(d)) - 0x3f800000u) >> shift);
+                        const int sign = (int)__float_as_uint(d) >> 31;
+                        bucket = (steps ^ sign) + ((int)zero - sign);
+                        bucket = bucket < 0 ? 0 : bucket > top ? top : bucket;
+                    } else {
+                        // (0 where d is not a number)
+                        bucket = (int)__builtin_amdgcn_fmed3f(d + zero, 0.0f, (float)top);
+                    }
+                    s[g * 4 + e] += tab[bucket];
+                    if constexpr (PACK) (*entries)[g * 4 + e] += (uint32_t)(first + bucket) << 8 * a;
+                }
+            }
+        };
+        if (b.ints) {
+            if (shift >= 0)
+                each(std::true_type{}, std::true_type{});
+            else
+                each(std::true_type{}, std::false_type{});
+        } else {
+            if (shift >= 0)
+                each(std::false_type{}, std::true_type{});
+            else
+                each(std::false_type{}, std::false_type{});
+        }
+    }
+}
+
+}  // namespace fpstok

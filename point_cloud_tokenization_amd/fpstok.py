@@ -21,7 +21,7 @@ F32, F16, BF16, I32 = 0, 1, 2, 3  # fpstok_dtype
 MAX_PATCHES, MAX_K, MAX_LLOYD = 1024, 64, 1000
 NOALLOC_MAX_WORKSPACE = 64 << 20  # FPSTOK_NOALLOC_MAX_WORKSPACE
 MAX_HEAD_DIM, MAX_SINKS, MAX_AXES = 128, 64, 4
-MAX_WIDTH = 8192
+MAX_WIDTH, MAX_BUCKETS = 8192, 128
 NORMS = {"none": 0, "rms": 1, "layer": 2}  # fpstok_norm
 GATES = {"none": 0, "row": 1, "sequence": 2}  # fpstok_gate
 ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2}  # fpstok_act
@@ -76,6 +76,14 @@ class RopeParams(ctypes.Structure):
                 ("positions_dtype", ctypes.c_int32), ("num_axes", ctypes.c_int32),
                 ("pairs", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32),
                 ("inverse", ctypes.c_int32)]
+
+
+class RelBias(ctypes.Structure):
+    _fields_ = [("q_positions", ctypes.c_void_p), ("k_positions", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("positions_dtype", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("buckets", ctypes.c_int32 * 4),
+                ("log_steps", ctypes.c_int32 * 4), ("rate", ctypes.c_float * 4),
+                ("shift", ctypes.c_float * 4)]
 
 
 class Rows(ctypes.Structure):
@@ -136,6 +144,13 @@ def lib():
         L.fpstok_attention_workspace_size.restype = sz
         L.fpstok_rope.argtypes = [S, ctypes.POINTER(RopeParams), vp, vp] + \
             [ctypes.POINTER(Heads)] * 4 + [vp]
+        RB = ctypes.POINTER(RelBias)
+        L.fpstok_attention_bias.argtypes = [S, S, A, RB] + [ctypes.POINTER(Heads)] * 4 + \
+            [vp, vp, sz, vp]
+        L.fpstok_attention_bias_backward.argtypes = [S, S, A, RB] + \
+            [ctypes.POINTER(Heads)] * 4 + [vp] + [ctypes.POINTER(Heads)] * 4 + [vp, vp, sz, vp]
+        L.fpstok_attention_bias_workspace_size.argtypes = [S, S, A, RB, i32]
+        L.fpstok_attention_bias_workspace_size.restype = sz
         RP, RW = ctypes.POINTER(ResidualParams), ctypes.POINTER(ResidualWeights)
         R = ctypes.POINTER(Rows)
         L.fpstok_residual.argtypes = [S, RP, RW] + [R] * 5 + [vp, vp]
@@ -144,6 +159,7 @@ def lib():
         L.fpstok_residual_workspace_size.argtypes = [S, RP]
         L.fpstok_residual_workspace_size.restype = sz
         for f in ("fpstok_attention", "fpstok_attention_backward", "fpstok_rope",
+                  "fpstok_attention_bias", "fpstok_attention_bias_backward",
                   "fpstok_residual", "fpstok_residual_backward",
                   "fpstok_sample", "fpstok_assign", "fpstok_knn", "fpstok_lloyd",
                   "fpstok_pool", "fpstok_tokenize", "fpstok_validate", "fpstok_pack",
@@ -602,9 +618,53 @@ class _DeviceCall:
             _check(rc, where)
 
 
+class BiasAxis:
+    """One axis of a RelativeBias: its buckets, the rate that turns positions
+    into units, the shift, and the buckets per doubling of a log axis (0:
+    linear).  Without a shift distance 0 is in the middle."""
+
+    def __init__(self, buckets, rate=1.0, shift=None, log_steps=0):
+        self.buckets, self.rate, self.log_steps = int(buckets), float(rate), int(log_steps)
+        if shift is None:
+            shift = self.buckets // 2 if self.log_steps else self.buckets / 2
+        self.shift = float(shift)
+
+
+class RelativeBias:
+    """A learned bias for Attention (fpstok_rel_bias): table [H, buckets of all
+    axes] float32, and the rows' positions [rows, axes], float32 or int32
+    (k_positions None: the queries')."""
+
+    def __init__(self, table, axes, q_positions, k_positions=None):
+        import torch
+
+        A = len(axes)
+        if not 1 <= A <= MAX_AXES:
+            raise ValueError("axes must name 1 to %d axes" % MAX_AXES)
+        _need(table, torch.float32, "table")
+        if table.dim() != 2 or table.shape[1] != sum(a.buckets for a in axes):
+            raise ValueError("table must be [heads, %d]" % sum(a.buckets for a in axes))
+        if q_positions.dtype not in (torch.float32, torch.int32):
+            raise TypeError("positions must be float32 or int32, got %s" % q_positions.dtype)
+        for name, p in (("q_positions", q_positions), ("k_positions", k_positions)):
+            if p is not None:
+                _need(p, q_positions.dtype, name, table.device)
+                if p.dim() != 2 or p.shape[1] != A:
+                    raise ValueError("%s must be [rows, %d]" % (name, A))
+        self.table, self.q_positions, self.k_positions = table, q_positions, k_positions
+        pad = lambda v: list(v) + [0] * (4 - A)  # noqa: E731
+        i4, f4 = ctypes.c_int32 * 4, ctypes.c_float * 4
+        self.struct = RelBias(
+            q_positions.data_ptr(), None if k_positions is None else k_positions.data_ptr(),
+            table.data_ptr(), I32 if q_positions.dtype == torch.int32 else F32, A,
+            i4(*pad(a.buckets for a in axes)), i4(*pad(a.log_steps for a in axes)),
+            f4(*pad(a.rate for a in axes)), f4(*pad(a.shift for a in axes)))
+
+
 class Attention(_DeviceCall):
     """fpstok_attention on given tensors, with its outputs and workspace
-    allocated once, and with training=True fpstok_attention_backward.
+    allocated once, and with training=True fpstok_attention_backward; with a bias
+    (RelativeBias) fpstok_attention_bias and fpstok_attention_bias_backward.
 
     q [q rows, H, D]; k, v [k rows, Hk, D] (float32, float16 or bfloat16, any
     row and head stride); q_seqs, k_seqs: make_seqs (k_seqs None: q_seqs).
@@ -613,10 +673,11 @@ class Attention(_DeviceCall):
     buffers each time, and rows behind the last packed sequence keep what they
     held (0 after construction).  out and, in training, grads = (grad_q, grad_k,
     grad_v) may be given; other buffers assigned to .grads take the place of
-    those before."""
+    those before.  With a bias, grads ends with grad_table (None: the table
+    gets no gradient)."""
 
     def __init__(self, q, k, v, q_seqs, k_seqs=None, window=(-1, -1), num_sinks=0, scale=None,
-                 training=False, out=None, grads=None):
+                 training=False, out=None, grads=None, bias=None):
         import torch
 
         super().__init__(q.device)
@@ -636,27 +697,49 @@ class Attention(_DeviceCall):
         self.out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if out is None else out
         self.lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
         oh = make_heads(self.out, "out", rows=q.shape[0], heads=q.shape[1], like=q)
-        self._head = (ctypes.byref(q_seqs), None if k_seqs is None else ctypes.byref(k_seqs),
-                      ctypes.byref(self.params), ctypes.byref(qh), ctypes.byref(kh),
-                      ctypes.byref(vh), ctypes.byref(oh), _ptr(self.lse))
-        need = [lib().fpstok_attention_workspace_size(*self._head[:3], b)
-                for b in ((0, 1) if training else (0,))]
+        self.bias, name, fixed = bias, "fpstok_attention", 3
+        call = (ctypes.byref(q_seqs), None if k_seqs is None else ctypes.byref(k_seqs),
+                ctypes.byref(self.params))
+        if bias is not None:
+            self._check_bias(bias, ks)
+            name, fixed = "fpstok_attention_bias", 4
+            call += (ctypes.byref(bias.struct),)
+        self._head = call + (ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh),
+                             ctypes.byref(oh), _ptr(self.lse))
+        size = getattr(lib(), name + "_workspace_size")
+        need = [size(*self._head[:fixed], b) for b in ((0, 1) if training else (0,))]
         self.ws = torch.empty(max(need), dtype=torch.uint8, device=q.device) if max(need) else None
         self._ws = (_ptr(self.ws), 0 if self.ws is None else self.ws.numel())
-        self._fwd, self._bwd = lib().fpstok_attention, lib().fpstok_attention_backward
+        self._name, self._fwd = name, getattr(lib(), name)
+        self._bwd = getattr(lib(), name + "_backward")
         self._training, self._grads = bool(training), None
         own = [t for t in (self.lse, self.ws, self.out if out is None else None) if t is not None]
         if grads is not None:
             self.grads = grads
         elif training:
+            leaves = (q, k, v) if bias is None else (q, k, v, bias.table)
             self.grads = tuple(torch.zeros(t.shape, dtype=t.dtype, device=t.device)
-                               for t in (q, k, v))
+                               for t in leaves)
             own += self.grads
         self._allocated(*own)
 
+    def _check_bias(self, bias, ks):
+        q = self.q
+        if bias.table.device != q.device:
+            raise ValueError("the bias is on %s, expected %s" % (bias.table.device, q.device))
+        if bias.table.shape[0] != q.shape[1]:
+            raise ValueError("the bias's table must hold %d heads" % q.shape[1])
+        if bias.q_positions.shape[0] != q.shape[0]:
+            raise ValueError("q_positions must hold %d rows" % q.shape[0])
+        if bias.k_positions is None and ks is not self.q_seqs:
+            raise ValueError("k_seqs need k_positions")
+        if bias.k_positions is not None and bias.k_positions.shape[0] != ks.num_rows:
+            raise ValueError("k_positions must hold %d rows" % ks.num_rows)
+
     @property
     def grads(self):
-        """(grad_q, grad_k, grad_v), where backward writes; None if not training."""
+        """(grad_q, grad_k, grad_v), with a bias also grad_table, where backward
+        writes; None if not training."""
         return self._grads
 
     @grads.setter
@@ -664,26 +747,35 @@ class Attention(_DeviceCall):
         if not self._training:
             raise ValueError("construct with training=True")
         grads = tuple(grads)
-        if len(grads) != 3:
-            raise ValueError("grads must be (grad_q, grad_k, grad_v)")
+        if len(grads) != (3 if self.bias is None else 4):
+            raise ValueError("grads must be (grad_q, grad_k, grad_v%s)" % (
+                "" if self.bias is None else ", grad_table"))
+        table = ()
+        if self.bias is not None:
+            if grads[3] is not None:
+                _need(grads[3], self.bias.table.dtype, "grad_table", self.device)
+                if grads[3].shape != self.bias.table.shape:
+                    raise ValueError("grad_table must be %s" % (tuple(self.bias.table.shape),))
+            table = (_ptr(grads[3]),)
         views = [make_heads(g, name, rows=t.shape[0], heads=t.shape[1], like=t)
                  for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads,
                                        (self.q, self.k, self.v))]
-        self._grads, self._tail = grads, tuple(ctypes.byref(h) for h in views) + self._ws
+        self._grads = grads
+        self._tail = tuple(ctypes.byref(h) for h in views) + table + self._ws
 
     def __call__(self, stream=None):
-        """fpstok_attention: (out, lse)."""
-        self._call(self._fwd, "fpstok_attention", self._head + self._ws, stream)
+        """fpstok_attention (with a bias fpstok_attention_bias): (out, lse)."""
+        self._call(self._fwd, self._name, self._head + self._ws, stream)
         return self.out, self.lse
 
     def backward(self, grad_out, stream=None):
         """fpstok_attention_backward after a call on the same inputs:
-        (grad_q, grad_k, grad_v)."""
+        (grad_q, grad_k, grad_v), with a bias also grad_table."""
         if self._grads is None:
             raise ValueError("construct with training=True")
         gh = make_heads(grad_out, "grad_out", rows=self.q.shape[0], heads=self.q.shape[1],
                         like=self.q)
-        self._call(self._bwd, "fpstok_attention_backward",
+        self._call(self._bwd, self._name + "_backward",
                    self._head + (ctypes.byref(gh),) + self._tail, stream)
         return self._grads
 
