@@ -414,29 +414,59 @@ struct BiasTile<true, ROWS, THREADS> {
     }
 };
 
-// The sums of dS and of the weights by entry: [wave][entry][dS, weight][lane & 31],
-// behind the tables in LDS; one entry more takes those that are another
-// launch's.
+// The sums of dS and of the weights of a row by entry: [wave][entry][lane & 31]
+// behind the tables in LDS; one entry more takes those that are another launch's.
+// A place holds both as whole numbers: dS in units of 2^-35 of the row's `cap` in
+// the upper 38 bits, the weights in units of 2^-25 in the lower 26.  Whole numbers
+// add up to the same in any order, and by LDS's integer atomics (7 cycles for
+// the 64 lanes' 8 bytes; float32 ones take 3 cycles a lane, 192).  The cap is
+// a power of two that |dP - delta| stays below, so a sum does too, its weights
+// adding up to 1; where it grows, by more than a factor of 4 over what came
+// before, the sums are shifted.
 template <bool BIAS>
 struct TableSums {
     __device__ __forceinline__ TableSums(const NoBias&, int, int, int, int) {}
 };
 template <>
 struct TableSums<true> {
-    FPSTOK_LDS float* lane_sums;
-    float* all;
+    using u64 = unsigned long long;
+    static constexpr int kWeightBits = 26;
+    FPSTOK_LDS u64* lane_sums;
+    u64* all;
     int slots;
+    uint32_t cap = 0x0d800000u;  // 2^-100
     bool on;
     __device__ __forceinline__ TableSums(const BiasArgs& b, int G, int wave, int lane, int tid) {
         on = b.part != nullptr;
         if (!on) return;
         slots = table_slots(b);
-        all = bias_lds() + ((G * b.entries + 63) & ~63);
-        lane_sums = (FPSTOK_LDS float*)all + wave * slots * 64 + (lane & 31);
-        for (int i = tid; i < 4 * slots * 64; i += 256) all[i] = 0.0f;
+        all = (u64*)(bias_lds() + ((G * b.entries + 63) & ~63));
+        lane_sums = (FPSTOK_LDS u64*)all + wave * slots * 32 + (lane & 31);
+        for (int i = tid; i < 4 * slots * 32; i += 256) all[i] = 0;
     }
-    __device__ __forceinline__ void add(const BiasArgs& b, const u32x16& entries, const f32x16& ds,
-                                        const f32x16& w, bool counts, int half) const {
+    // 16 pairs of this lane's row: t = dP - delta, weights w (both 0 where hidden)
+    // and dS = w t.
+    __device__ __forceinline__ void add(const BiasArgs& b, const u32x16& entries, const f32x16& t,
+                                        const f32x16& w, const f32x16& ds, bool counts, int half) {
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(t[e]));
+        top = pair_max(counts ? top : 0.0f);  // (both lanes of a row keep one cap)
+        if (__any(top > __uint_as_float(cap))) grow(top, half);
+        if (!counts) return;
+        // 2^35 / cap, and what makes a double's last bit 1
+        const double units =
+            __builtin_bit_cast(double, (u64)(uint32_t)(1023 + 35 + 127 - (cap >> 23)) << 52);
+        constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52
+        u64 x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const u64 bits = __builtin_bit_cast(u64, __builtin_fma((double)ds[e], units, kWhole));
+            const uint32_t lo = (uint32_t)bits, hi = (uint32_t)(bits >> 32) - 0x43380000u;
+            const uint32_t weight = (uint32_t)(w[e] * 33554432.0f);
+            x[e] = (u64)__builtin_amdgcn_alignbit(hi, lo, 32 - kWeightBits) << 32 |
+                   ((lo << kWeightBits) + weight);
+        }
         auto each = [&](auto parts) {
 #pragma unroll 1
             for (int a = 0; a < b.axes; ++a) {
@@ -447,27 +477,47 @@ struct TableSums<true> {
                         at -= (uint32_t)b.from;
                         at = at < (uint32_t)b.count ? at : (uint32_t)b.count;
                     }
-                    lds_add(lane_sums + at * 64, ds[e]);
-                    lds_add(lane_sums + at * 64 + 32, w[e]);
+                    __hip_atomic_fetch_add(lane_sums + at * 32, x[e], __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_WAVEFRONT);
                 }
             }
         };
-        auto halves = [&](auto parts) {
-            if (half == 0 && counts) each(parts);
-            if (half == 1 && counts) each(parts);
-        };
         if (b.count != b.entries)
-            halves(std::true_type{});
+            each(std::true_type{});
         else
-            halves(std::false_type{});
+            each(std::false_type{});
     }
-    // The workgroup's part: per head of the group and entry, its rows in a fixed
+    // A cap of 4 times `top` or more; the row's first lane shifts its sums.
+    __device__ __forceinline__ void grow(float top, int half) {
+        const bool more = top > __uint_as_float(cap);
+        uint32_t to = (__float_as_uint(top) & 0x7f800000u) + (3u << 23);
+        to = to < 0x7f000000u ? to : 0x7f000000u;
+        const int by = more ? (int)((to - cap) >> 23) : 0;
+        const bool started = cap != 0x0d800000u;
+        cap = more ? to : cap;
+        if (!__any(more && started)) return;
+        if (half == 0 && by > 0) {
+            const int n = by < 63 ? by : 63;
+#pragma unroll 1
+            for (int i = 0; i < slots; ++i) {
+                FPSTOK_LDS u64* p = lane_sums + i * 32;
+                const u64 x = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+                const long long sum = ((long long)x >> kWeightBits) >> n;
+                __hip_atomic_store(p, ((u64)sum << kWeightBits) | (x & ((1u << kWeightBits) - 1)),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+            }
+        }
+        wave_sync();
+    }
+    // The workgroup's part: per head of the group and entry, the rows' sums of dS
+    // less `off` (what dS of all the row's keys is off 0 by) times its weights', in a fixed
     // order that starts elsewhere in every thread (threads of one entry after another
-    // would all read one bank).
+    // would all read one bank).  A row whose dS is not finite has an `off` that is
+    // not: nor are the entries it adds to.
     __device__ __forceinline__ void store(const BiasArgs& b, int G, const RowTile& t, float off,
                                           int row, int half, int tid) const {
-        __shared__ float offs[128];
-        if (half == 0) offs[row] = off;
+        __shared__ float2 rows[128];  // off and cap
+        if (half == 0) rows[row] = make_float2(off, __uint_as_float(cap));
         __syncthreads();
         float* part = b.part + (int64_t)blockIdx.x * G * b.count;
         for (int i = tid; i < G * b.count; i += 256) {
@@ -475,15 +525,19 @@ struct TableSums<true> {
             // rows of the tile in this head: the first, and every G-th after it
             const int first = (int)((uint32_t)(g + G - t.row0 % G) % (uint32_t)G);
             const int n = first < t.rows ? (t.rows - first - 1) / G + 1 : 0;
-            float sum = 0.0f;
+            double sum = 0.0;
             int x = n > 0 ? tid % n : 0;
             for (int k = 0; k < n; ++k) {
                 const int r = first + x * G;
-                const float* p = all + ((r >> 5) * slots + e) * 64 + (r & 31);
-                sum += __builtin_fmaf(-offs[r], p[32], p[0]);
+                const u64 s = all[((r >> 5) * slots + e) * 32 + (r & 31)];
+                const float2 row_is = rows[r];
+                const double value = (double)((long long)s >> kWeightBits) *
+                                     ((double)row_is.y * 0x1p-35);
+                const double weight = (double)(uint32_t)(s & ((1u << kWeightBits) - 1)) * 0x1p-25;
+                if (s != 0) sum += value - (double)row_is.x * weight;
                 if (++x == n) x = 0;
             }
-            part[i] = sum;
+            part[i] = (float)sum;
         }
     }
 };
@@ -866,14 +920,12 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // its whole gradient.  So the scores of such keys are set to -infinity, and 0
 // times the lost element, which is not a number, is added after the walk.
 //
-// The bias's gradient is dS summed by the pairs' entries.  Every lane adds to
-// copies of its own in LDS (32 of each entry and wave; the two lanes of a row take
-// turns), so no two add to one place at a time and the order of the sums is the
-// walk's.  It is a float32 result of up to all pairs, for which the delta of the
-// rounded out is not good enough; so the weights are summed by entry too, and
-// what dS summed over the keys is off by is taken back at the end: sum over the
-// rows of (sum dS) - off * (sum of weights).  The tiles' parts are added in order
-// by a kernel of their own.
+// The bias's gradient is dS summed by the pairs' entries (TableSums).  It is a
+// float32 result of up to all pairs, for which the delta of the rounded out is
+// not good enough; so the weights are summed by entry too, and what dS summed
+// over the keys is off by is taken back at the end: sum over the rows of (sum dS) -
+// off * (sum of weights).  The tiles' parts are added in order by a kernel of
+// their own.
 template <class T, int DP, int BN, bool TWICE, bool BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BIAS && DP > 64) ? 2 : 1)
 void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
@@ -971,6 +1023,12 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             x = Elem<T>::mma(Tl::row_frag(kbuf, row, st, half), qf[st], x);
             y = Elem<T>::mma(Tl::row_frag(kbuf + BN * Tl::kPitch, row, st, half), gf[st], y);
         }
+        if constexpr (BIAS) {
+            x *= cs;
+            add_bias<false, false, 128, BN>(
+                x, nullptr, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]);
+        }
         if (holes) hide_lost(x, b, i);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -998,20 +1056,21 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if (holes) hide_lost(x, b * 32, i);
         f32x16 ds;
         if constexpr (BIAS) {
-            f32x16 w;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                w[e] = __builtin_amdgcn_exp2f(x[e] - lse2);
-                ds[e] = w[e] * (y[e] - delta);
+                x[e] = __builtin_amdgcn_exp2f(x[e] - lse2);
+                y[e] -= delta;
             }
             if (mask) {
-                win.mask(w, j0 + b * 32, half, a.sinks, 0.0f);
-                win.mask(ds, j0 + b * 32, half, a.sinks, 0.0f);
+                win.mask(x, j0 + b * 32, half, a.sinks, 0.0f);
+                win.mask(y, j0 + b * 32, half, a.sinks, 0.0f);
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ds[e] = x[e] * y[e];
             if (sums.on) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) off_by += ds[e];
-                sums.add(bias, entries, ds, w, counts, half);
+                sums.add(bias, entries, y, x, ds, counts, half);
             }
         } else {
 #pragma unroll
@@ -1044,13 +1103,14 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     counts = q.live && some;
     if (n > 0) arrive(0);
     __syncthreads();
-    if (!BIAS && !TWICE && sizeof(T) == 2 && n == 1 && wave_live) {
+    if (!TWICE && sizeof(T) == 2 && n == 1 && wave_live) {
 #pragma unroll 1
         for (int b = 0; b < BN; b += 32) {
             const int view = mine.of(a, jn + b);
             if (view != 0) add_delta(lds, b, jn, view == 1, lost_in(0), 0, off_by);
         }
         delta += pair_sum(off_by);
+        off_by = 0.0f;
     }
     if constexpr (TWICE) {
         for (int i = 0; i < n; ++i) {
@@ -1068,6 +1128,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             __syncthreads();
         }
         delta += pair_sum(off_by);
+        off_by = 0.0f;
         jn = n > 0 ? kt.tile(0) * BN : 0;
         kp = kb + jn * a.k.row;
         vp = vb + jn * a.v.row;
@@ -1634,19 +1695,19 @@ static hipError_t forward(const AttnArgs& a, const BiasParam<BIAS>& b, const Att
 // grad_q and the rows' statistics (and, with a bias, the sums of its gradient).
 template <class T, bool BIAS>
 static void backward_q(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t s) {
-    constexpr bool k16 = sizeof(T) == 2, twice = k16 && !BIAS;
+    constexpr bool k16 = sizeof(T) == 2;
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
-    const bool narrow = twice && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
+    const bool narrow = k16 && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
     size_t lds = 0;
     if constexpr (BIAS) lds = bias_lds_bytes(b, a.G, b.part != nullptr);
     if (a.D <= 64) {
         if (narrow)
-            attention_dq_kernel<T, 64, 64, twice, BIAS><<<q, 256, lds, s>>>(a, b);
+            attention_dq_kernel<T, 64, 64, k16, BIAS><<<q, 256, lds, s>>>(a, b);
         else
             attention_dq_kernel<T, 64, 64, false, BIAS><<<q, 256, lds, s>>>(a, b);
     } else {
         if (narrow)
-            attention_dq_kernel<T, 128, k16 ? 64 : 32, twice, BIAS><<<q, 256, lds, s>>>(a, b);
+            attention_dq_kernel<T, 128, k16 ? 64 : 32, k16, BIAS><<<q, 256, lds, s>>>(a, b);
         else
             attention_dq_kernel<T, 128, k16 ? 64 : 32, false, BIAS><<<q, 256, lds, s>>>(a, b);
     }

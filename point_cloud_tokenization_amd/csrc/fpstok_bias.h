@@ -107,10 +107,6 @@ inline size_t bias_lds_bytes(const BiasArgs& b, int G, bool sums) {
     return (table + (sums ? (size_t)4 * table_slots(b) * 64 : 0)) * sizeof(float);
 }
 
-__device__ __forceinline__ void lds_add(FPSTOK_LDS float* p, float x) {
-    __hip_atomic_fetch_add(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
-}
-
 using u32x16 = uint32_t __attribute__((ext_vector_type(16)));
 
 // Adds the bias of a block of 32 x 32 pairs to its scores (in units of log2): a
