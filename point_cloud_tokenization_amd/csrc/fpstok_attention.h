@@ -67,9 +67,16 @@ struct BiasArgs {
     int32_t from, count;
     float* grad;  // [H][entries], or null
     float* part;
+    // the pairs' entries, found once for all heads: 4 times the entry of axis a in
+    // byte a of plane[q row * pitch + key], for sequences of up to `pitch` keys
+    uint32_t* plane;  // null: every head finds its own
+    int32_t pitch;
 };
 constexpr int kGroupEntries = 4096;  // table entries of one key head's query heads (16 KB of LDS)
 constexpr int kTableEntries = 64;  // entries whose gradients one launch forms
+
+// The pitch of the entries' plane, 0 without one.
+int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len);
 
 // How a call is laid out on the device, from the shapes alone.
 struct AttnPlan {

@@ -196,6 +196,12 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
                       AttnArgs& a, BiasArgs* b, AttnPlan& plan) {
     const size_t rows = (size_t)qs->num_rows * a.H;
     char* at = (char*)ws;
+    if (!backward) plan = plan_attention(a, likely_len(qs), likely_len(ks));
+    if (b && (b->pitch = plan_plane(a, *b, !backward && plan.few, likely_len(ks))) > 0) {
+        b->plane = (uint32_t*)at;
+        at += align256((size_t)qs->num_rows * b->pitch * sizeof(uint32_t));
+    }
+    const size_t plane = (size_t)(at - (char*)ws);
     if (backward) {
         a.lse2 = (float*)at;
         a.delta = (float*)(at + align256(rows * sizeof(float)));
@@ -213,7 +219,7 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
         const int64_t q_blocks = row_slots(a.qs, a.G, 7) * a.Hk;
         const int64_t k_blocks = row_slots(a.ks, 1, 7) * a.Hk * a.k_splits;
         plan.blocks = q_blocks > k_blocks ? q_blocks : k_blocks;
-        if (a.left < 0 || a.sinks == 0) return need;
+        if (a.left < 0 || a.sinks == 0) return plane + need;
         // about 512 workgroups of queries past the sinks, of 128 queries or more
         // (883 + 300 pulses, 16 heads on 4: 74 us a training step, of 256: 80)
         a.sink_shift = 7;
@@ -221,16 +227,15 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
         a.sink_part = (float*)(at + need);
         const int64_t chunks = row_slots(a.qs, 1, a.sink_shift) * a.Hk;
         if (chunks > plan.blocks) plan.blocks = chunks;
-        return need + align256((size_t)chunks * 2 * a.sinks * a.D * sizeof(float));
+        return plane + need + align256((size_t)chunks * 2 * a.sinks * a.D * sizeof(float));
     }
-    plan = plan_attention(a, likely_len(qs), likely_len(ks));
     a.splits = plan.splits;
     plan.blocks = row_slots(a.qs, a.G, plan.few ? 5 : 7) * a.Hk * a.splits;
-    if (plan.splits == 1) return 0;
+    if (plan.splits == 1) return plane;
     const size_t ml = align256(rows * plan.splits * sizeof(float2));
     a.part_ml = (float2*)at;
     a.part = (float*)(at + ml);
-    return ml + align256(rows * plan.splits * a.D * sizeof(float));
+    return plane + ml + align256(rows * plan.splits * a.D * sizeof(float));
 }
 
 // A launch holds less than 2^32 threads, 256 a workgroup.
@@ -291,7 +296,7 @@ static fpstok_status attend(const fpstok_seqs* qs, const fpstok_seqs* ks,
         return st;
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
-    const size_t need = lay_out(qs, ks, false, ws, a, nullptr, plan);
+    const size_t need = lay_out(qs, ks, false, ws, a, biased ? &b : nullptr, plan);
     if ((st = check_grid(plan)) != FPSTOK_OK ||
         (st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK)
         return st;

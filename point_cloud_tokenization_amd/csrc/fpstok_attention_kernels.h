@@ -405,6 +405,7 @@ struct BiasTile {
 template <int ROWS, int THREADS>
 struct BiasTile<true, ROWS, THREADS> {
     const FPSTOK_LDS float* table;  // of head `head` of the group
+    bool planed = false;            // the pairs' entries are in the plane
     PosStage<ROWS, THREADS> stage;
     __device__ __forceinline__ BiasTile(const BiasArgs& b, int hk, int G, int head, int tid)
         : stage(b, tid % THREADS) {
@@ -413,6 +414,18 @@ struct BiasTile<true, ROWS, THREADS> {
         table = (const FPSTOK_LDS float*)lds + head * b.entries;
     }
 };
+
+// A block's entries from the plane: the keys p + 8 g + 0 .. 3 of one query.
+__device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
+    u32x16 x;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const u32x4 y = *(const u32x4*)(p + g * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[g * 4 + e] = y[e];
+    }
+    return x;
+}
 
 // The sums of dS and of the weights of a row by entry: [wave][entry][lane & 31]
 // behind the tables in LDS; one entry more takes those that are another launch's.
@@ -434,6 +447,7 @@ struct TableSums<true> {
     FPSTOK_LDS u64* lane_sums;
     u64* all;
     int slots;
+    int byte_shift;              // from a pair's byte to bytes of a place
     uint32_t cap = 0x0d800000u;  // 2^-100
     bool on;
     __device__ __forceinline__ TableSums(const BiasArgs& b, int G, int wave, int lane, int tid) {
@@ -467,25 +481,28 @@ struct TableSums<true> {
             x[e] = (u64)__builtin_amdgcn_alignbit(hi, lo, 32 - kWeightBits) << 32 |
                    ((lo << kWeightBits) + weight);
         }
-        auto each = [&](auto parts) {
+        if (b.count == b.entries) {
+#pragma unroll
+            for (int a = 0; a < kMaxAxes; ++a) {
+                if (a >= b.axes) break;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    put(entries[e] >> 8 * a & 255u, byte_shift, x[e]);
+            }
+        } else {
 #pragma unroll 1
             for (int a = 0; a < b.axes; ++a) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    uint32_t at = entries[e] >> 8 * a & 255u;
-                    if constexpr (decltype(parts)::value) {
-                        at -= (uint32_t)b.from;
-                        at = at < (uint32_t)b.count ? at : (uint32_t)b.count;
-                    }
-                    __hip_atomic_fetch_add(lane_sums + at * 32, x[e], __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_WAVEFRONT);
+                    const uint32_t at = (entries[e] >> 8 * a & 255u) - (uint32_t)b.from;
+                    put(at < (uint32_t)b.count ? at : (uint32_t)b.count, 8, x[e]);
                 }
             }
-        };
-        if (b.count != b.entries)
-            each(std::true_type{});
-        else
-            each(std::false_type{});
+        }
+    }
+    __device__ __forceinline__ void put(uint32_t at, int shift, u64 x) const {
+        __hip_atomic_fetch_add((FPSTOK_LDS u64*)((FPSTOK_LDS char*)lane_sums + (at << shift)), x,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     }
     // A cap of 4 times `top` or more; the row's first lane shifts its sums.
     __device__ __forceinline__ void grow(float top, int half) {
@@ -561,7 +578,7 @@ struct TableSums<true> {
 // 128 tokens, 12 heads: 14 us (7 us of bytes).  A third buffer cost 5 %, scores
 // formed one tile ahead 5 to 15 % (and spills at D = 128).
 template <class T, int DP, int BN, bool BIAS>
-__global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)))
+__global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) - (BIAS && DP * sizeof(T) == 128))
 void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     constexpr int DB = DP / 32, STEPS = DP / 16;
     using Tl = Tile<T, DP>;
@@ -581,8 +598,12 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
     BiasTile<BIAS, BN> scores(bias, t.hk, G, q.h - t.hk * G, tid);
-    if constexpr (BIAS)
+    const uint32_t* entry_row = nullptr;
+    if constexpr (BIAS) {
         own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
+        scores.planed = bias.plane && t.tk <= bias.pitch;
+        entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+    }
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
     const int n = t.rows > 0 ? kt.part(t.part, a.splits) : 0;
@@ -634,16 +655,23 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             f32x16 x = 0.0f;
+            u32x16 entries;
+            if constexpr (BIAS) {
+                if (scores.planed) entries = load_entries(entry_row + j0 + b * 32);
+            }
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
                 if (sizeof(T) == 2 || st * 16 < a.D)  // (float32: a step is 8 instructions)
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             if constexpr (BIAS) {
                 x *= cs;
-                add_bias<false, false, 128, BN>(
-                    x, nullptr, bias, scores.table,
-                    (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
-                    (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
+                if (scores.planed)
+                    add_entries(x, entries, bias.axes, scores.table);
+                else
+                    add_bias<false, false, 128, BN>(
+                        x, nullptr, bias, scores.table,
+                        (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                        (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
             }
             s[b] = x;
         }
@@ -954,8 +982,13 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const bool wave_live = wave * 32 < t.rows;
     BiasTile<BIAS, BN> scores(bias, t.hk, a.G, q.h - t.hk * a.G, tid);
     TableSums<BIAS> sums(bias, a.G, wave, lane, tid);
-    if constexpr (BIAS)
+    const uint32_t* entry_row = nullptr;
+    if constexpr (BIAS) {
         own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
+        scores.planed = bias.plane && t.tk <= bias.pitch;
+        sums.byte_shift = scores.planed ? 6 : 8;
+        entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+    }
     Frag qf[STEPS], gf[STEPS], of[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
     q.load<T, STEPS>(gf, a.grad_out, a.D, half);
@@ -1025,9 +1058,12 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         if constexpr (BIAS) {
             x *= cs;
-            add_bias<false, false, 128, BN>(
-                x, nullptr, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
-                (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]);
+            if (scores.planed)
+                add_entries(x, load_entries(entry_row + j0 + b), bias.axes, scores.table);
+            else
+                add_bias<false, false, 128, BN>(
+                    x, nullptr, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]);
         }
         if (holes) hide_lost(x, b, i);
 #pragma unroll
@@ -1041,17 +1077,23 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     auto block = [&](const FPSTOK_LDS char* kbuf, int b, int j0, bool mask, bool holes, int i) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
+        u32x16 entries;
+        if constexpr (BIAS) {
+            if (scores.planed) entries = load_entries(entry_row + j0 + b * 32);
+        }
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
         }
-        u32x16 entries;
         if constexpr (BIAS) {
             x *= cs;
-            add_bias<false, true, 128, BN>(
-                x, &entries, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
-                (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
+            if (scores.planed)
+                add_entries(x, entries, bias.axes, scores.table);
+            else
+                add_bias<false, true, 128, BN>(
+                    x, &entries, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
         }
         if (holes) hide_lost(x, b * 32, i);
         f32x16 ds;
@@ -1395,8 +1437,12 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         load_row<T, STEPS>(vf, (const T*)a.v.data + krow * a.v.row + t.hk * a.v.head, live,
                            (const T*)a.v.data, a.D, half);
     BiasTile<BIAS, BQ> scores(bias, t.hk, G, 0, tid);
-    if constexpr (BIAS)
+    const uint32_t* entry_col = nullptr;
+    if constexpr (BIAS) {
         own_positions(bias, pos.own, r, bias.k_pos, krow, live, half);
+        scores.planed = bias.plane && t.tk <= bias.pitch;
+        entry_col = bias.plane + t.q0 * bias.pitch + (live ? t.row0 + r : 0);
+    }
     // queries i0 .. i1 see some key of the tile (of the rows past its window,
     // the tile with the sinks gets their gradients from the kernel above), e0 ..
     // e1 of them this lane's key
@@ -1507,6 +1553,16 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                      bool mask, int turn, int head) {
         const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
+        u32x16 entries;
+        if constexpr (BIAS) {
+            if (scores.planed) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int i = x0 + b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
+                    entries[e] = entry_col[(int64_t)(i < i1 ? i : i1) * bias.pitch];
+                }
+            }
+        }
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             Frag v;
@@ -1520,10 +1576,13 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         f32x16 w, ds;
         if constexpr (BIAS) {
             x *= c;
-            add_bias<true, false, 128, BQ>(
-                x, nullptr, bias, scores.table + head * bias.entries,
-                (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
-                (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
+            if (scores.planed)
+                add_entries(x, entries, bias.axes, scores.table + head * bias.entries);
+            else
+                add_bias<true, false, 128, BQ>(
+                    x, nullptr, bias, scores.table + head * bias.entries,
+                    (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
+                    (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -1702,9 +1761,9 @@ static void backward_q(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t 
     if constexpr (BIAS) lds = bias_lds_bytes(b, a.G, b.part != nullptr);
     if (a.D <= 64) {
         if (narrow)
-            attention_dq_kernel<T, 64, 64, k16, BIAS><<<q, 256, lds, s>>>(a, b);
+            attention_dq_kernel<T, 64, BIAS ? 32 : 64, k16, BIAS><<<q, 256, lds, s>>>(a, b);
         else
-            attention_dq_kernel<T, 64, 64, false, BIAS><<<q, 256, lds, s>>>(a, b);
+            attention_dq_kernel<T, 64, BIAS ? 32 : 64, false, BIAS><<<q, 256, lds, s>>>(a, b);
     } else {
         if (narrow)
             attention_dq_kernel<T, 128, k16 ? 64 : 32, k16, BIAS><<<q, 256, lds, s>>>(a, b);

@@ -109,6 +109,55 @@ inline size_t bias_lds_bytes(const BiasArgs& b, int G, bool sums) {
 
 using u32x16 = uint32_t __attribute__((ext_vector_type(16)));
 
+// The bucket of a distance, from the own row's and another's position as they
+// are in LDS.
+template <bool INTS, bool LOG>
+__device__ __forceinline__ int bucket_of(uint32_t k, uint32_t q, float rate, float zero, int top,
+                                         int shift) {
+    float d;
+    if constexpr (INTS)
+        d = (float)(int)(k - q) * rate;
+    else
+        d = __uint_as_float(k) - __uint_as_float(q);
+    if constexpr (LOG) {
+        const int steps = (int)((__float_as_uint(1.0f + fabsf(d)) - 0x3f800000u) >> shift);
+        const int sign = (int)__float_as_uint(d) >> 31;
+        const int bucket = (steps ^ sign) + ((int)zero - sign);
+        return bucket < 0 ? 0 : bucket > top ? top : bucket;
+    }
+    // (0 where d is not a number)
+    return (int)__builtin_amdgcn_fmed3f(d + zero, 0.0f, (float)top);
+}
+
+// Calls f(INTS, LOG) with what an axis is.
+template <class F>
+__device__ __forceinline__ void by_kind(bool ints, bool log, F f) {
+    if (ints) {
+        if (log)
+            f(std::true_type{}, std::true_type{});
+        else
+            f(std::true_type{}, std::false_type{});
+    } else {
+        if (log)
+            f(std::false_type{}, std::true_type{});
+        else
+            f(std::false_type{}, std::false_type{});
+    }
+}
+
+// The same from the pairs' entries as they are in the plane.
+__device__ __forceinline__ void add_entries(f32x16& s, const u32x16& entries, int axes,
+                                            const FPSTOK_LDS float* table) {
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) {
+        if (a >= axes) break;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            s[e] += *(const FPSTOK_LDS float*)((const FPSTOK_LDS char*)table +
+                                               (entries[e] >> 8 * a & 255u));
+    }
+}
+
 // Adds the bias of a block of 32 x 32 pairs to its scores (in units of log2): a
 // lane's own row against the block's rows in its registers.  own: this lane's
 // place in own[0], tile: that of the block's row 4 half in tile[0].
@@ -126,45 +175,19 @@ __device__ __forceinline__ void add_bias(f32x16& s, u32x16* entries, const BiasA
         const int first = pick(b.first, a), top = pick(b.top, a), shift = pick(b.log_shift, a);
         const float rate = pick(b.rate, a), zero = pick(b.shift, a);
         const FPSTOK_LDS float* tab = table + first;
-        auto each = [&](auto ints, auto log) {
+        by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const u32x4 other = *(const FPSTOK_LDS u32x4*)(tile + a * ROWS + g * 8);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t k = KEY ? mine : other[e], q = KEY ? other[e] : mine;
-                    float d;
-                    if constexpr (decltype(ints)::value)
-                        d = (float)(int)(k - q) * rate;
-                    else
-                        d = __uint_as_float(k) - __uint_as_float(q);
-                    int bucket;
-                    if constexpr (decltype(log)::value) {
-                        const int steps =
-                            (int)((__float_as_uint(1.0f + fabsf(d)) - 0x3f800000u) >> shift);
-                        const int sign = (int)__float_as_uint(d) >> 31;
-                        bucket = (steps ^ sign) + ((int)zero - sign);
-                        bucket = bucket < 0 ? 0 : bucket > top ? top : bucket;
-                    } else {
-                        // (0 where d is not a number)
-                        bucket = (int)__builtin_amdgcn_fmed3f(d + zero, 0.0f, (float)top);
-                    }
+                    const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                        KEY ? mine : other[e], KEY ? other[e] : mine, rate, zero, top, shift);
                     s[g * 4 + e] += tab[bucket];
                     if constexpr (PACK) (*entries)[g * 4 + e] += (uint32_t)(first + bucket) << 8 * a;
                 }
             }
-        };
-        if (b.ints) {
-            if (shift >= 0)
-                each(std::true_type{}, std::true_type{});
-            else
-                each(std::true_type{}, std::false_type{});
-        } else {
-            if (shift >= 0)
-                each(std::false_type{}, std::true_type{});
-            else
-                each(std::false_type{}, std::false_type{});
-        }
+        });
     }
 }
 
