@@ -572,8 +572,8 @@ typedef enum { FPSTOK_ACT_NONE = 0, FPSTOK_ACT_SIGMOID = 1, FPSTOK_ACT_SILU = 2 
 /* A [rows][C] view: row r starts at data + r*row_stride (elements), its
  * elements are adjacent.  Inputs may use any stride >= 0 (0: the same row
  * again), outputs' rows must not overlap.  A row_stride above 2^23 is refused
- * (EUNSUPPORTED).  16-byte aligned data and strides and a width that is a
- * multiple of 8 are faster, everywhere or nowhere in a call. */
+ * (EUNSUPPORTED).  Data is aligned to its element; 16-byte aligned data and
+ * strides are a little faster. */
 typedef struct {
     void* data;
     int64_t row_stride;
@@ -588,7 +588,7 @@ typedef struct {
     int32_t pre_norm;     /* fpstok_norm of the sum, for the next block: NONE: no h  */
     int32_t gate_per;     /* fpstok_gate                                             */
     int32_t activation;   /* fpstok_act of the gate                                  */
-    float eps;            /* of both norms, > 0                                      */
+    float eps;            /* of both norms: finite, a normal number > 0              */
 } fpstok_residual_params;
 
 /* [C] float32 each; NULL: ones, zeros for a bias.  A weight or bias belongs to

@@ -24,17 +24,17 @@ struct ResidualArgs {
     int32_t C, stream, branch;               // width, dtypes
     int32_t post, pre, gate_per, act;        // as in fpstok_residual_params
     float eps;
-    int32_t vec;    // 16-byte accesses fit every operand
-    int32_t shift;  // a run is 2^shift rows
+    // plan_residual: elements of a row that a thread holds, threads of a row, and
+    // in how many runs of adjacent rows the rows are shared out
+    int32_t elements, threads, runs;
     // backward: the workgroups' parts of the weights' gradients, [workgroups][given
     // weights][C], and of the gates of sequences, [runs + sequences][C]
     float* part;
     float* gate_part;
 };
 
-// Workgroups of the launch over runs of 2^shift rows.
-int64_t residual_blocks(const ResidualArgs& a);
-int residual_shift(const ResidualArgs& a, bool backward);
+void plan_residual(ResidualArgs& a, bool backward);
+int64_t residual_blocks(const ResidualArgs& a);  // workgroups
 hipError_t launch_residual(const ResidualArgs& a, hipStream_t s);
 hipError_t launch_residual_backward(const ResidualArgs& a, hipStream_t s);
 

@@ -6,83 +6,91 @@
 
 namespace fpstok {
 
-// A row of C <= 8192 elements belongs to T threads (64 to 1024), 8 elements to
-// each: 8 adjacent ones (VEC = 8: 16-byte accesses), or every T-th one where
-// width, pointers or strides do not allow that (VEC = 1).
-constexpr int kEl = 8;
+// A row of C elements belongs to T threads (64 to 1024, whole waves), EL adjacent
+// elements to each, which come and go by 8- or 16-byte accesses (of any
+// alignment).  Where EL does not divide C the last thread takes the row's last
+// EL elements and leaves out the first of them, which are its neighbour's.
+enum Fit {
+    kNarrow,  // C < EL: elements one by one
+    kTail,    // C > EL is no multiple of EL
+    kWhole    // C is one
+};
 
-template <int VEC, int T>
-__device__ __forceinline__ int col(int t, int e) {
-    return VEC == 8 ? t * 8 + e : t + e * T;
-}
-
-// A thread's elements of a row as they came from memory.  Threads and elements
-// past the width load an element that exists (a load under a divergent branch
-// would be waited for before the branch ends) and count as 0.
-template <class E, int VEC, int T>
-struct Raw {
-    using V = uint32_t __attribute__((ext_vector_type(4)));
-    V v[VEC == 8 ? sizeof(E) / 2 : 1];
-    E e[VEC == 8 ? 1 : kEl];
-    __device__ __forceinline__ void load(const E* p, int C, int t) {
-        if constexpr (VEC == 8) {
-            const int c = t * 8 < C ? t * 8 : 0;
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(E) / 2; ++i) v[i] = ((const V*)(p + c))[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEl; ++i) {
-                const int c = col<VEC, T>(t, i);
-                e[i] = p[c < C ? c : 0];
-            }
+template <Fit FIT, int EL>
+struct Cols {
+    int C, base;  // this thread's first element
+    int skip;     // of its EL elements, those that are not its own (EL: all)
+    __device__ __forceinline__ Cols(int C, int t) : C(C) {
+        base = t * EL < C ? t * EL : 0;
+        skip = t * EL < C ? 0 : EL;
+        if (FIT == kTail && skip == 0 && base + EL > C) {
+            skip = base + EL - C;
+            base = C - EL;
         }
     }
-    __device__ __forceinline__ void get(float* f, int C, int t) const {
-        if constexpr (VEC == 8) {
-            using E8 = E __attribute__((ext_vector_type(8)));
-            const E8 x = *(const E8*)v;
-            const bool in = t * 8 < C;
-#pragma unroll
-            for (int i = 0; i < kEl; ++i) f[i] = in ? (float)x[i] : 0.0f;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEl; ++i) f[i] = col<VEC, T>(t, i) < C ? (float)e[i] : 0.0f;
-        }
+    __device__ __forceinline__ bool own(int e) const {
+        return FIT == kNarrow ? skip == 0 && e < C : FIT == kTail ? e >= skip : skip == 0;
+    }
+    // What a thread adds to a sum over the row: threads past the width hold a
+    // copy of the row's first elements.
+    __device__ __forceinline__ float part(float x) const {
+        return FIT != kWhole || skip == 0 ? x : 0.0f;
+    }
+    // An element that is not the thread's own counts as 0 in a sum over the row
+    // where a thread may hold some of both.
+    __device__ __forceinline__ float keep(float x, int e) const {
+        return FIT == kWhole || own(e) ? x : 0.0f;
     }
 };
 
-template <class E, int VEC, int T>
-__device__ __forceinline__ void store(E* p, const float* f, int C, int t) {
-    if constexpr (VEC == 8) {
-        using V = uint32_t __attribute__((ext_vector_type(4)));
-        using E8 = E __attribute__((ext_vector_type(8)));
-        E8 x;
+// A thread's elements of a row as they came from memory.  Threads past the
+// width load elements that exist (a load under a divergent branch would be
+// waited for before the branch ends).
+template <class E, Fit FIT, int EL>
+struct Raw {
+    using Vec = E __attribute__((ext_vector_type(EL)));
+    using Loose = Vec __attribute__((aligned(sizeof(E))));  // of any alignment
+    Vec v;
+    __device__ __forceinline__ void load(const E* p, const Cols<FIT, EL>& c) {
+        if constexpr (FIT != kNarrow) {
+            v = *(const Loose*)(p + c.base);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kEl; ++i) x[i] = (E)f[i];
-        if (t * 8 < C) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(E) / 2; ++i)
-                ((V*)(p + t * 8))[i] = ((const V*)&x)[i];
+            for (int i = 0; i < EL; ++i) v[i] = p[i < c.C ? i : 0];
         }
-    } else {
+    }
+    __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
-        for (int i = 0; i < kEl; ++i) {
-            const int c = col<VEC, T>(t, i);
-            if (c < C) p[c] = (E)f[i];
-        }
+        for (int i = 0; i < EL; ++i) f[i] = (float)v[i];
+    }
+};
+
+template <class E, Fit FIT, int EL>
+__device__ __forceinline__ void store(E* p, const float* f, const Cols<FIT, EL>& c) {
+    using R = Raw<E, FIT, EL>;
+    typename R::Vec x;
+#pragma unroll
+    for (int i = 0; i < EL; ++i) x[i] = (E)f[i];
+    if (FIT != kNarrow && c.skip == 0) {
+        *(typename R::Loose*)(p + c.base) = x;
+    } else if (FIT != kWhole && c.skip < EL) {
+#pragma unroll
+        for (int i = 0; i < EL; ++i)
+            if (c.own(i)) p[c.base + i] = x[i];
     }
 }
 
-template <int VEC, int T>
-__device__ __forceinline__ void load_weight(float* f, const float* w, float none, int C, int t) {
+template <Fit FIT, int EL>
+__device__ __forceinline__ void load_weight(float* f, const float* w, float none,
+                                            const Cols<FIT, EL>& c) {
     if (w == nullptr) {
 #pragma unroll
-        for (int i = 0; i < kEl; ++i) f[i] = none;
+        for (int i = 0; i < EL; ++i) f[i] = none;
         return;
     }
-    Raw<float, VEC, T> r;
-    r.load(w, C, t);
-    r.get(f, C, t);
+    Raw<float, FIT, EL> r;
+    r.load(w, c);
+    r.get(f);
 }
 
 template <int CTRL>
@@ -106,26 +114,32 @@ __device__ __forceinline__ float wave_sum(float x) {
 // sums in LDS, in one of two places in turn: a wave that writes the third sum
 // has passed the barrier of the second, which every wave reaches only after it
 // has read the first.
-template <int T>
 struct RowSum {
     float (*lds)[2][16];
-    int turn = 0;
+    int waves, turn = 0;
+    __device__ __forceinline__ RowSum(float (*lds)[2][16], int T) : lds(lds), waves(T >> 6) {}
     __device__ __forceinline__ void operator()(float& a, float& b) {
         a = wave_sum(a);
         b = wave_sum(b);
-        if constexpr (T > 64) {
+        if (waves > 1) {
             const int wave = threadIdx.x >> 6;
             if ((threadIdx.x & 63) == 0) lds[turn][0][wave] = a, lds[turn][1][wave] = b;
             __syncthreads();
             a = 0.0f, b = 0.0f;
-#pragma unroll
-            for (int w = 0; w < T / 64; ++w) a += lds[turn][0][w], b += lds[turn][1][w];
+            for (int w = 0; w < waves; ++w) a += lds[turn][0][w], b += lds[turn][1][w];
             turn ^= 1;
         }
     }
     __device__ __forceinline__ void operator()(float& a) {
-        float none = 0.0f;
-        (*this)(a, none);
+        a = wave_sum(a);
+        if (waves > 1) {
+            const int wave = threadIdx.x >> 6;
+            if ((threadIdx.x & 63) == 0) lds[turn][0][wave] = a;
+            __syncthreads();
+            a = 0.0f;
+            for (int w = 0; w < waves; ++w) a += lds[turn][0][w];
+            turn ^= 1;
+        }
     }
 };
 
@@ -145,6 +159,19 @@ __device__ __forceinline__ int seq_of_row(const SeqArgs& s, int64_t row) {
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// How the rows are shared out: packed ones from the first sequence's first to
+// the last one's last, padded ones all, in a.runs runs of as many adjacent rows.
+struct Runs {
+    int64_t first, last;
+    int rows;  // of a run
+    __device__ __forceinline__ Runs(const ResidualArgs& a) {
+        first = a.seqs.cu ? cu_at(a.seqs, 0) : 0;
+        last = a.seqs.cu ? cu_at(a.seqs, a.seqs.B) : a.seqs.rows;
+        const uint32_t n = last > first ? (uint32_t)(last - first) : 0;
+        rows = n > 0 ? (int)((n + (uint32_t)a.runs - 1) / (uint32_t)a.runs) : 1;
+    }
+};
+
 // The rows of a run in order, and what is known of each: its sequence (packed:
 // only if SEQ asks for it) and whether it is one of it.
 struct RunRows {
@@ -152,22 +179,19 @@ struct RunRows {
     bool seq;
     int b = 0;
     int64_t lo, hi, end, live_end;  // rows of the run; where the sequence's slots and rows end
-    __device__ __forceinline__ RunRows(const SeqArgs& s, int64_t run, int shift, bool seq)
-        : s(s), seq(seq) {
-        lo = run << shift;
-        hi = lo + ((int64_t)1 << shift);
-        if (hi > s.rows) hi = s.rows;
-        if (s.cu) {
-            const int64_t first = cu_at(s, 0), last = cu_at(s, s.B);
-            if (lo < first) lo = first;
-            if (hi > last) hi = last;
-            end = live_end = hi;
-            if (seq && lo < hi) {
-                b = seq_of_row(s, lo);
-                end = live_end = cu_at(s, b + 1);
-            }
-        } else if (lo < hi) {
+    __device__ __forceinline__ RunRows(const ResidualArgs& a, int64_t run)
+        : s(a.seqs), seq(a.gate_per == 2) {
+        const Runs runs(a);
+        lo = runs.first + run * runs.rows;
+        hi = lo + runs.rows < runs.last ? lo + runs.rows : runs.last;
+        end = live_end = hi;
+        if (run >= a.runs) lo = hi;
+        if (lo >= hi) return;
+        if (!s.cu) {
             at_slot((int)((uint32_t)lo / (uint32_t)s.cap));
+        } else if (seq) {
+            b = seq_of_row(s, lo);
+            end = live_end = cu_at(s, b + 1);
         }
     }
     __device__ __forceinline__ void at_slot(int seq_no) {
@@ -189,71 +213,90 @@ struct RunRows {
     }
 };
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// Off by |g| half steps of float32 from the product's rounding and a few from
+// the instructions'.
+__device__ __forceinline__ float sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f));
+}
 
 // Norms a row in place: (x - mean) / std with LAYER, x / rms without; `mean`
 // and `r` = 1 / sqrt(mean square + eps) are returned.  The mean comes off
-// before the squares are summed, in 32 bits; elements past the width stay 0.
-template <int VEC, int T>
-__device__ __forceinline__ void norm_row(float* x, bool layer, float inv_c, float eps, int C, int t,
-                                         RowSum<T>& sum, float& mean, float& r) {
+// before the squares are summed, in 32 bits.
+template <Fit FIT, int EL>
+__device__ __forceinline__ void norm_row(float* x, bool layer, float inv_c, float eps,
+                                         const Cols<FIT, EL>& c, RowSum& sum, float& mean,
+                                         float& r) {
     mean = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EL; ++i) x[i] = c.keep(x[i], i);
     if (layer) {
 #pragma unroll
-        for (int i = 0; i < kEl; ++i) mean += x[i];
+        for (int i = 0; i < EL; ++i) mean += x[i];
+        mean = c.part(mean);
         sum(mean);
         mean *= inv_c;
 #pragma unroll
-        for (int i = 0; i < kEl; ++i) x[i] = col<VEC, T>(t, i) < C ? x[i] - mean : 0.0f;
+        for (int i = 0; i < EL; ++i) x[i] = c.keep(x[i] - mean, i);
     }
     float q = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kEl; ++i) q = __builtin_fmaf(x[i], x[i], q);
+    for (int i = 0; i < EL; ++i) q = __builtin_fmaf(x[i], x[i], q);
+    q = c.part(q);
     sum(q);
-    r = 1.0f / sqrtf(__builtin_fmaf(q, inv_c, eps));
+    r = __builtin_amdgcn_rsqf(__builtin_fmaf(q, inv_c, eps));
 #pragma unroll
-    for (int i = 0; i < kEl; ++i) x[i] *= r;
+    for (int i = 0; i < EL; ++i) x[i] *= r;
 }
 
-template <int T>
-constexpr int kThreads = T == 64 ? 256 : T;
+// A workgroup's rows and threads: rows of one wave share a workgroup of four.
+struct Threads {
+    int T, t, group;
+    int64_t run;
+    __device__ __forceinline__ Threads(const ResidualArgs& a) {
+        const int tid = threadIdx.x;
+        T = a.threads;
+        group = T == 64 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0;
+        t = T == 64 ? tid & 63 : tid;
+        run = T == 64 ? (int64_t)blockIdx.x * 4 + group : (int64_t)blockIdx.x;
+    }
+};
 
 // Forward.  The T threads of a row hold it in registers from the first load to
 // the last store, so every operand is read and every result written once; a
 // workgroup takes a run of adjacent rows, keeps the weights in registers and
 // has the next row's loads on their way while it works on one.
-template <class S, class B, int VEC, int T>
-__global__ __launch_bounds__(kThreads<T>) void residual_kernel(ResidualArgs a) {
+// PLAIN: RMS norms without biases.
+template <class S, class B, Fit FIT, int EL, int MAX_T, bool PLAIN>
+__global__ __launch_bounds__(MAX_T) void residual_kernel(ResidualArgs a) {
     __shared__ float lds[2][2][16];
-    const int tid = threadIdx.x, t = tid % T, C = a.C;
-    const int group = __builtin_amdgcn_readfirstlane(tid / T);
-    const int64_t run = (int64_t)blockIdx.x * (kThreads<T> / T) + group;
-    RowSum<T> sum{lds};
-    RunRows rows(a.seqs, run, a.shift, a.gate_per == 2);
+    const Threads th(a);
+    const Cols<FIT, EL> c(a.C, th.t);
+    RowSum sum(lds, th.T);
+    RunRows rows(a, th.run);
     if (rows.lo >= rows.hi) return;  // (the same for all threads of a row)
-    const float inv_c = 1.0f / (float)C;
+    const float inv_c = 1.0f / (float)a.C;
     const bool has_y = a.y.data != nullptr, gated = a.gate_per != 0;
-    float wp[kEl], bp[kEl], sc[kEl], wh[kEl], bh[kEl];
-    load_weight<VEC, T>(wp, a.weights[0], 1.0f, C, t);
-    load_weight<VEC, T>(bp, a.weights[1], 0.0f, C, t);
-    load_weight<VEC, T>(sc, a.weights[2], 1.0f, C, t);
-    load_weight<VEC, T>(wh, a.weights[3], 1.0f, C, t);
-    load_weight<VEC, T>(bh, a.weights[4], 0.0f, C, t);
-    Raw<S, VEC, T> rx;
-    Raw<B, VEC, T> ry, rg;
+    float wp[EL], bp[EL], sc[EL], wh[EL], bh[EL];
+    load_weight(wp, a.weights[0], 1.0f, c);
+    if (!PLAIN) load_weight(bp, a.weights[1], 0.0f, c);
+    load_weight(sc, a.weights[2], 1.0f, c);
+    load_weight(wh, a.weights[3], 1.0f, c);
+    if (!PLAIN) load_weight(bh, a.weights[4], 0.0f, c);
+    Raw<S, FIT, EL> rx;
+    Raw<B, FIT, EL> ry, rg;
     auto load = [&](int64_t r) {
-        rx.load((const S*)a.x.data + r * a.x.row, C, t);
-        if (has_y) ry.load((const B*)a.y.data + r * a.y.row, C, t);
+        rx.load((const S*)a.x.data + r * a.x.row, c);
+        if (has_y) ry.load((const B*)a.y.data + r * a.y.row, c);
         if (gated)
-            rg.load((const B*)a.gate.data + (a.gate_per == 2 ? rows.b : r) * a.gate.row, C, t);
+            rg.load((const B*)a.gate.data + (a.gate_per == 2 ? rows.b : r) * a.gate.row, c);
     };
     load(rows.lo);
     for (int64_t r = rows.lo; r < rows.hi; ++r) {
         const bool live = r < rows.live_end;
-        float x[kEl], y[kEl], g[kEl];
-        rx.get(x, C, t);
-        if (has_y) ry.get(y, C, t);
-        if (gated) rg.get(g, C, t);
+        float x[EL], y[EL], g[EL];
+        rx.get(x);
+        if (has_y) ry.get(y);
+        if (gated) rg.get(g);
         if (r + 1 < rows.hi) {
             rows.to(r + 1);
             load(r + 1);
@@ -263,39 +306,42 @@ __global__ __launch_bounds__(kThreads<T>) void residual_kernel(ResidualArgs a) {
         float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (!live) {
 #pragma unroll
-            for (int i = 0; i < kEl; ++i) x[i] = 0.0f;
-            if (xo) store<S, VEC, T>(xo, x, C, t);
-            if (h) store<B, VEC, T>(h, x, C, t);
-            if (a.stats && t == 0) ((float4*)a.stats)[r] = st;
+            for (int i = 0; i < EL; ++i) x[i] = 0.0f;
+            if (xo) store(xo, x, c);
+            if (h) store(h, x, c);
+            if (a.stats && th.t == 0) ((float4*)a.stats)[r] = st;
             continue;
         }
         if (has_y) {
             if (a.post != 0) {
-                norm_row<VEC, T>(y, a.post == 2, inv_c, a.eps, C, t, sum, st.x, st.y);
+                norm_row(y, !PLAIN && a.post == 2, inv_c, a.eps, c, sum, st.x, st.y);
 #pragma unroll
-                for (int i = 0; i < kEl; ++i) y[i] = __builtin_fmaf(y[i], wp[i], bp[i]);
+                for (int i = 0; i < EL; ++i)
+                    y[i] = PLAIN ? y[i] * wp[i] : __builtin_fmaf(y[i], wp[i], bp[i]);
             }
             if (gated) {
+                if (a.act != 0) {
 #pragma unroll
-                for (int i = 0; i < kEl; ++i) {
-                    if (a.act == 0)
-                        y[i] *= g[i];
-                    else
-                        y[i] *= a.act == 1 ? sigmoid(g[i]) : g[i] * sigmoid(g[i]);
+                    for (int i = 0; i < EL; ++i) {
+                        const float s = sigmoid(g[i]);
+                        g[i] = a.act == 1 ? s : g[i] * s;
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < EL; ++i) y[i] *= g[i];
             }
 #pragma unroll
-            for (int i = 0; i < kEl; ++i)
-                x[i] = col<VEC, T>(t, i) < C ? __builtin_fmaf(y[i], sc[i], x[i]) : 0.0f;
+            for (int i = 0; i < EL; ++i) x[i] = __builtin_fmaf(y[i], sc[i], x[i]);
         }
-        if (xo) store<S, VEC, T>(xo, x, C, t);
+        if (xo) store(xo, x, c);
         if (a.pre != 0) {
-            norm_row<VEC, T>(x, a.pre == 2, inv_c, a.eps, C, t, sum, st.z, st.w);
+            norm_row(x, !PLAIN && a.pre == 2, inv_c, a.eps, c, sum, st.z, st.w);
 #pragma unroll
-            for (int i = 0; i < kEl; ++i) x[i] = __builtin_fmaf(x[i], wh[i], bh[i]);
-            store<B, VEC, T>(h, x, C, t);
+            for (int i = 0; i < EL; ++i)
+                x[i] = PLAIN ? x[i] * wh[i] : __builtin_fmaf(x[i], wh[i], bh[i]);
+            store(h, x, c);
         }
-        if (a.stats && t == 0) ((float4*)a.stats)[r] = st;
+        if (a.stats && th.t == 0) ((float4*)a.stats)[r] = st;
     }
 }
 
@@ -309,40 +355,40 @@ __global__ __launch_bounds__(kThreads<T>) void residual_kernel(ResidualArgs a) {
 // A thread sums the weights' gradients of its columns over the rows of its
 // run, in order; the workgroup adds its waves' and leaves one part, which the
 // kernels below add in order: results are equal from run to run.
-template <class S, class B, int VEC, int T>
-__global__ __launch_bounds__(kThreads<T>) void residual_grad_kernel(ResidualArgs a) {
+// PLAIN: RMS norms without biases, which need neither means nor their sums.
+template <class S, class B, Fit FIT, int EL, int MAX_T, bool PLAIN>
+__global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
     __shared__ float lds[2][2][16];
-    __shared__ float cols[T == 64 ? 3 : 1][T == 64 ? 64 * kEl : 1];
-    const int tid = threadIdx.x, t = tid % T, C = a.C;
-    const int group = __builtin_amdgcn_readfirstlane(tid / T);
-    const int64_t run = (int64_t)blockIdx.x * (kThreads<T> / T) + group;
-    RowSum<T> sum{lds};
-    RunRows rows(a.seqs, run, a.shift, a.gate_per == 2);
-    const float inv_c = 1.0f / (float)C;
+    __shared__ float cols[3][64 * EL];
+    const Threads th(a);
+    const Cols<FIT, EL> c(a.C, th.t);
+    RowSum sum(lds, th.T);
+    RunRows rows(a, th.run);
+    const float inv_c = 1.0f / (float)a.C;
     const bool has_y = a.y.data != nullptr, gated = a.gate_per != 0;
     const bool has_gx = a.grad_x_out.data != nullptr, has_gh = a.grad_h.data != nullptr;
-    float wp[kEl], bp[kEl], sc[kEl], wh[kEl];
-    load_weight<VEC, T>(wp, a.weights[0], 1.0f, C, t);
-    load_weight<VEC, T>(bp, a.weights[1], 0.0f, C, t);
-    load_weight<VEC, T>(sc, a.weights[2], 1.0f, C, t);
-    load_weight<VEC, T>(wh, a.weights[3], 1.0f, C, t);
-    float acc[kResidualWeights][kEl], gate_acc[kEl];
+    float wp[EL], bp[EL], sc[EL], wh[EL];
+    load_weight(wp, a.weights[0], 1.0f, c);
+    if (!PLAIN) load_weight(bp, a.weights[1], 0.0f, c);
+    load_weight(sc, a.weights[2], 1.0f, c);
+    load_weight(wh, a.weights[3], 1.0f, c);
+    float acc[kResidualWeights][EL], gate_acc[EL];
 #pragma unroll
-    for (int i = 0; i < kEl; ++i) {
+    for (int i = 0; i < EL; ++i) {
 #pragma unroll
         for (int k = 0; k < kResidualWeights; ++k) acc[k][i] = 0.0f;
         gate_acc[i] = 0.0f;
     }
-    Raw<S, VEC, T> rx, rgx;
-    Raw<B, VEC, T> ry, rg, rgh;
+    Raw<S, FIT, EL> rx, rgx;
+    Raw<B, FIT, EL> ry, rg, rgh;
     float4 st_next = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto load = [&](int64_t r) {
-        rx.load((const S*)a.x.data + r * a.x.row, C, t);
-        if (has_y) ry.load((const B*)a.y.data + r * a.y.row, C, t);
+        rx.load((const S*)a.x.data + r * a.x.row, c);
+        if (has_y) ry.load((const B*)a.y.data + r * a.y.row, c);
         if (gated)
-            rg.load((const B*)a.gate.data + (a.gate_per == 2 ? rows.b : r) * a.gate.row, C, t);
-        if (has_gx) rgx.load((const S*)a.grad_x_out.data + r * a.grad_x_out.row, C, t);
-        if (has_gh) rgh.load((const B*)a.grad_h.data + r * a.grad_h.row, C, t);
+            rg.load((const B*)a.gate.data + (a.gate_per == 2 ? rows.b : r) * a.gate.row, c);
+        if (has_gx) rgx.load((const S*)a.grad_x_out.data + r * a.grad_x_out.row, c);
+        if (has_gh) rgh.load((const B*)a.grad_h.data + r * a.grad_h.row, c);
         if (a.stats) st_next = ((const float4*)a.stats)[r];
     };
     const bool gate_sums = a.gate_per == 2 && a.grad_gate.data != nullptr;
@@ -351,14 +397,14 @@ __global__ __launch_bounds__(kThreads<T>) void residual_grad_kernel(ResidualArgs
         const bool live = r < rows.live_end;
         const int b = rows.b;
         const float4 st = st_next;
-        float x[kEl], y[kEl], g[kEl], gx[kEl], gh[kEl];
-        rx.get(x, C, t);
-        if (has_y) ry.get(y, C, t);
-        if (gated) rg.get(g, C, t);
-        if (has_gh) rgh.get(gh, C, t);
+        float x[EL], y[EL], g[EL], gx[EL], gh[EL];
+        rx.get(x);
+        if (has_y) ry.get(y);
+        if (gated) rg.get(g);
+        if (has_gh) rgh.get(gh);
 #pragma unroll
-        for (int i = 0; i < kEl; ++i) gx[i] = 0.0f;
-        if (has_gx) rgx.get(gx, C, t);
+        for (int i = 0; i < EL; ++i) gx[i] = 0.0f;
+        if (has_gx) rgx.get(gx);
         const bool more = r + 1 < rows.hi;
         if (more) {
             rows.to(r + 1);
@@ -370,123 +416,145 @@ __global__ __launch_bounds__(kThreads<T>) void residual_grad_kernel(ResidualArgs
                     ? (B*)a.grad_gate.data + r * a.grad_gate.row
                     : nullptr;
         if (live) {
-            float u[kEl], act[kEl], slope[kEl];
+            float u[EL], act[EL], slope[EL];
             if (has_y) {
                 if (a.post != 0) {
 #pragma unroll
-                    for (int i = 0; i < kEl; ++i) {
-                        y[i] = col<VEC, T>(t, i) < C ? (y[i] - st.x) * st.y : 0.0f;
-                        u[i] = __builtin_fmaf(y[i], wp[i], bp[i]);
+                    for (int i = 0; i < EL; ++i) {
+                        y[i] = PLAIN ? y[i] * st.y : (y[i] - st.x) * st.y;
+                        u[i] = PLAIN ? y[i] * wp[i] : __builtin_fmaf(y[i], wp[i], bp[i]);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kEl; ++i) u[i] = y[i];
+                    for (int i = 0; i < EL; ++i) u[i] = y[i];
                 }
 #pragma unroll
-                for (int i = 0; i < kEl; ++i) {
-                    act[i] = 1.0f, slope[i] = 1.0f;
-                    if (gated && a.act == 0) act[i] = g[i];
-                    if (gated && a.act != 0) {
-                        const float s = sigmoid(g[i]);
-                        act[i] = a.act == 1 ? s : g[i] * s;
-                        slope[i] = s * (1.0f - s);
-                        // silu: s (1 + g (1 - s))
-                        if (a.act == 2) slope[i] = __builtin_fmaf(slope[i], g[i], s);
+                for (int i = 0; i < EL; ++i) act[i] = 1.0f, slope[i] = 1.0f;
+                if (gated) {
+                    if (a.act != 0) {
+#pragma unroll
+                        for (int i = 0; i < EL; ++i) {
+                            const float s = sigmoid(g[i]);
+                            act[i] = a.act == 1 ? s : g[i] * s;
+                            slope[i] = s * (1.0f - s);
+                            // silu: s (1 + g (1 - s))
+                            if (a.act == 2) slope[i] = __builtin_fmaf(slope[i], g[i], s);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < EL; ++i) act[i] = g[i];
                     }
-                    x[i] = __builtin_fmaf(u[i] * act[i], sc[i], x[i]);
                 }
+#pragma unroll
+                for (int i = 0; i < EL; ++i) x[i] = __builtin_fmaf(u[i] * act[i], sc[i], x[i]);
             }
             if (has_gh) {
                 float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kEl; ++i) {
-                    x[i] = col<VEC, T>(t, i) < C ? (x[i] - st.z) * st.w : 0.0f;
+                for (int i = 0; i < EL; ++i) {
+                    x[i] = PLAIN ? x[i] * st.w : (x[i] - st.z) * st.w;
+                    gh[i] = c.keep(gh[i], i);
                     const float p = gh[i] * wh[i];
                     c1 = __builtin_fmaf(p, x[i], c1);
-                    c2 += p;
                     acc[3][i] = __builtin_fmaf(gh[i], x[i], acc[3][i]);
-                    acc[4][i] += gh[i];
+                    if (!PLAIN) {
+                        c2 += p;
+                        acc[4][i] += gh[i];
+                    }
                 }
-                sum(c1, c2);
+                c1 = c.part(c1);
+                if (PLAIN) {
+                    sum(c1);
+                } else {
+                    c2 = c.part(c2);
+                    sum(c1, c2);
+                }
                 c1 *= inv_c;
                 c2 = a.pre == 2 ? c2 * inv_c : 0.0f;
 #pragma unroll
-                for (int i = 0; i < kEl; ++i)
-                    gx[i] = __builtin_fmaf(
-                        st.w, __builtin_fmaf(-x[i], c1, gh[i] * wh[i] - c2), gx[i]);
+                for (int i = 0; i < EL; ++i) {
+                    const float p = gh[i] * wh[i];
+                    gx[i] = __builtin_fmaf(st.w, __builtin_fmaf(-x[i], c1, PLAIN ? p : p - c2),
+                                           gx[i]);
+                }
             }
-            if (ox) store<S, VEC, T>(ox, gx, C, t);
+            if (ox) store(ox, gx, c);
             if (has_y) {
                 float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kEl; ++i) {
-                    // (past the width gx is not 0)
-                    const float d = col<VEC, T>(t, i) < C ? gx[i] : 0.0f;
+                for (int i = 0; i < EL; ++i) {
+                    const float d = c.keep(gx[i], i);
                     acc[2][i] = __builtin_fmaf(d, act[i] * u[i], acc[2][i]);
                     const float gz = d * sc[i];
                     g[i] = gz * u[i] * slope[i];
                     gx[i] = gz * act[i];
                     acc[0][i] = __builtin_fmaf(gx[i], y[i], acc[0][i]);
-                    acc[1][i] += gx[i];
+                    if (!PLAIN) acc[1][i] += gx[i];
                     if (a.post != 0) {
                         gx[i] *= wp[i];
                         c1 = __builtin_fmaf(gx[i], y[i], c1);
-                        c2 += gx[i];
+                        if (!PLAIN) c2 += gx[i];
                     }
                 }
-                if (og) store<B, VEC, T>(og, g, C, t);
+                if (og) store(og, g, c);
                 if (gate_sums) {
 #pragma unroll
-                    for (int i = 0; i < kEl; ++i) gate_acc[i] += g[i];
+                    for (int i = 0; i < EL; ++i) gate_acc[i] += g[i];
                 }
                 if (a.post != 0) {
-                    sum(c1, c2);
+                    c1 = c.part(c1);
+                    if (PLAIN) {
+                        sum(c1);
+                    } else {
+                        c2 = c.part(c2);
+                        sum(c1, c2);
+                    }
                     c1 *= inv_c;
                     c2 = a.post == 2 ? c2 * inv_c : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < kEl; ++i)
-                        gx[i] = st.y * __builtin_fmaf(-y[i], c1, gx[i] - c2);
+                    for (int i = 0; i < EL; ++i)
+                        gx[i] = st.y * __builtin_fmaf(-y[i], c1, PLAIN ? gx[i] : gx[i] - c2);
                 }
-                if (oy) store<B, VEC, T>(oy, gx, C, t);
+                if (oy) store(oy, gx, c);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kEl; ++i) gx[i] = 0.0f;
-            if (ox) store<S, VEC, T>(ox, gx, C, t);
-            if (oy) store<B, VEC, T>(oy, gx, C, t);
-            if (og) store<B, VEC, T>(og, gx, C, t);
+            for (int i = 0; i < EL; ++i) gx[i] = 0.0f;
+            if (ox) store(ox, gx, c);
+            if (oy) store(oy, gx, c);
+            if (og) store(og, gx, c);
         }
         if (gate_sums && (!more || rows.b != b)) {
             // run + sequence is a number of its own: along the rows one of both grows
-            store<float, VEC, T>(a.gate_part + (run + b) * C, gate_acc, C, t);
+            store(a.gate_part + (th.run + b) * a.C, gate_acc, c);
 #pragma unroll
-            for (int i = 0; i < kEl; ++i) gate_acc[i] = 0.0f;
+            for (int i = 0; i < EL; ++i) gate_acc[i] = 0.0f;
         }
     }
     // the workgroup's part of every gradient that is asked for
     int given = 0;
 #pragma unroll
     for (int k = 0; k < kResidualWeights; ++k) given += a.weight_grads[k] != nullptr;
-    float* part = a.part + (int64_t)blockIdx.x * given * C;
+    float* part = a.part + (int64_t)blockIdx.x * given * a.C;
 #pragma unroll
     for (int k = 0; k < kResidualWeights; ++k) {
         if (a.weight_grads[k] == nullptr) continue;
-        if constexpr (T == 64) {
+        if (th.T == 64) {
             __syncthreads();
-            if (group > 0) {
+            if (th.group > 0) {
 #pragma unroll
-                for (int i = 0; i < kEl; ++i) cols[group - 1][i * 64 + t] = acc[k][i];
+                for (int i = 0; i < EL; ++i) cols[th.group - 1][i * 64 + th.t] = acc[k][i];
             }
             __syncthreads();
-            if (group == 0) {
+            if (th.group == 0) {
 #pragma unroll
-                for (int i = 0; i < kEl; ++i)
-                    acc[k][i] = ((acc[k][i] + cols[0][i * 64 + t]) + cols[1][i * 64 + t]) +
-                                cols[2][i * 64 + t];
+                for (int i = 0; i < EL; ++i)
+                    acc[k][i] = ((acc[k][i] + cols[0][i * 64 + th.t]) + cols[1][i * 64 + th.t]) +
+                                cols[2][i * 64 + th.t];
             }
         }
-        if (group == 0) store<float, VEC, T>(part, acc[k], C, t);
-        part += C;
+        if (th.group == 0) store(part, acc[k], c);
+        part += a.C;
     }
 }
 
@@ -524,14 +592,16 @@ __global__ __launch_bounds__(256) void residual_gates_kernel(ResidualArgs a) {
     __shared__ float sums[8][32];
     const int lane = threadIdx.x & 31, turn = threadIdx.x >> 5;
     const int c = blockIdx.y * 32 + lane;
+    const Runs runs(a);
     for (int b = blockIdx.x; b < a.seqs.B; b += gridDim.x) {
         int64_t start;
         int len;
         seq_rows(a.seqs, b, start, len);
         float sum = 0.0f;
         if (len > 0) {
-            const int64_t first = (start >> a.shift) + b;
-            const int n = (int)(((start + len - 1) >> a.shift) + b - first) + 1;
+            const uint32_t from = (uint32_t)(start - runs.first), run = (uint32_t)runs.rows;
+            const int64_t first = (int64_t)(from / run) + b;
+            const int n = (int)((from + (uint32_t)len - 1) / run - from / run) + 1;
             const float* part = a.gate_part + first * a.C + (c < a.C ? c : 0);
 #pragma unroll 4
             for (int i = turn; i < n; i += 8) sum += part[(int64_t)i * a.C];
@@ -548,63 +618,88 @@ __global__ __launch_bounds__(256) void residual_gates_kernel(ResidualArgs a) {
     }
 }
 
-static int row_threads(int C) {
-    int threads = 64;
-    while (threads * kEl < C) threads *= 2;
-    return threads;
+// 4 elements a thread for gradients and a float32 stream, 8 else, and where a row
+// needs more than 512 threads.  (float32 stream, 38,600 rows of 768: 4 elements 87 us
+// forward and 140 backward, 8 elements 102 and 197: half the registers, and 8 leave a
+// quarter of the threads idle.  bfloat16, 34,000 of 512: 49 and 105 against 39 and 113.)
+static int residual_elements(const ResidualArgs& a, bool backward) {
+    return a.C >= 4 && a.C <= 2048 && (a.stream == 0 || backward) ? 4 : 8;
 }
 
 int64_t residual_blocks(const ResidualArgs& a) {
-    const int per = row_threads(a.C) == 64 ? 4 : 1;
-    const int64_t runs = (a.seqs.rows + ((int64_t)1 << a.shift) - 1) >> a.shift;
-    return (runs + per - 1) / per;
+    const int per = a.threads == 64 ? 4 : 1;
+    return (a.runs + per - 1) / per;
 }
 
-int residual_shift(const ResidualArgs& a, bool backward) {
-    const int64_t runs = (backward ? 2048 : 4096) * 128 / row_threads(a.C);
-    int shift = 0;
-    while (shift < 20 && a.seqs.rows >> (shift + 1) >= runs) ++shift;
-    return shift;
+bool residual_plain(const ResidualArgs& a) {
+    return a.post != 2 && a.pre != 2 && !a.weights[1] && !a.weights[4];
 }
 
-template <class S, class B, int VEC, int T>
+void plan_residual(ResidualArgs& a, bool backward) {
+    a.elements = residual_elements(a, backward);
+    a.threads = (a.C + 64 * a.elements - 1) / (64 * a.elements) * 64;
+    // as many runs as the kernel's registers let run at once on 256 compute units
+    const int waves = !backward             ? 20
+                      : a.threads > 768     ? 16
+                      : a.threads > 512     ? 12
+                      : a.elements == 8     ? 8
+                      : residual_plain(a)   ? 16
+                                            : 12;
+    const int per_unit = waves / (a.threads / 64);
+    // (free slots leave some runs of padded rows little to do: shorter ones even that
+    // out.  Backward a run leaves a part of the weights' gradients: 400 padded events, 512
+    // wide, 102 us, with twice the runs 112)
+    const int times = a.seqs.cu || backward ? 1 : 4;
+    const int64_t runs = 256 * (int64_t)times * (per_unit < 1 ? 1 : per_unit);
+    a.runs = (int32_t)(runs < a.seqs.rows ? runs : a.seqs.rows);
+}
+
+template <class S, class B, Fit FIT, int EL, int MAX_T>
 static void launch(const ResidualArgs& a, bool backward, hipStream_t s) {
-    const dim3 grid((unsigned)residual_blocks(a));
-    if (backward)
-        residual_grad_kernel<S, B, VEC, T><<<grid, kThreads<T>, 0, s>>>(a);
+    const dim3 grid((unsigned)residual_blocks(a)), block(a.threads == 64 ? 256 : a.threads);
+    const bool plain = residual_plain(a);
+    if (!backward && plain)
+        residual_kernel<S, B, FIT, EL, MAX_T, true><<<grid, block, 0, s>>>(a);
+    else if (!backward)
+        residual_kernel<S, B, FIT, EL, MAX_T, false><<<grid, block, 0, s>>>(a);
+    else if (plain)
+        residual_grad_kernel<S, B, FIT, EL, MAX_T, true><<<grid, block, 0, s>>>(a);
     else
-        residual_kernel<S, B, VEC, T><<<grid, kThreads<T>, 0, s>>>(a);
+        residual_grad_kernel<S, B, FIT, EL, MAX_T, false><<<grid, block, 0, s>>>(a);
 }
 
-template <class S, class B, int VEC>
+template <class S, class B, Fit FIT>
 static void by_width(const ResidualArgs& a, bool backward, hipStream_t s) {
-    switch (row_threads(a.C)) {
-        case 64: return launch<S, B, VEC, 64>(a, backward, s);
-        case 128: return launch<S, B, VEC, 128>(a, backward, s);
-        case 256: return launch<S, B, VEC, 256>(a, backward, s);
-        case 512: return launch<S, B, VEC, 512>(a, backward, s);
-        default: return launch<S, B, VEC, 1024>(a, backward, s);
-    }
+    if (a.elements == 4)
+        launch<S, B, FIT, 4, 512>(a, backward, s);
+    else if (a.threads <= 512)
+        launch<S, B, FIT, 8, 512>(a, backward, s);
+    else if (a.threads <= 768)
+        launch<S, B, FIT, 8, 768>(a, backward, s);
+    else
+        launch<S, B, FIT, 8, 1024>(a, backward, s);
 }
 
 template <class S, class B>
-static void by_alignment(const ResidualArgs& a, bool backward, hipStream_t s) {
-    if (a.vec)
-        by_width<S, B, 8>(a, backward, s);
+static void by_fit(const ResidualArgs& a, bool backward, hipStream_t s) {
+    if (a.C < a.elements)
+        launch<S, B, kNarrow, 8, 512>(a, backward, s);
+    else if (a.C % a.elements != 0)
+        by_width<S, B, kTail>(a, backward, s);
     else
-        by_width<S, B, 1>(a, backward, s);
+        by_width<S, B, kWhole>(a, backward, s);
 }
 
 static void by_type(const ResidualArgs& a, bool backward, hipStream_t s) {
     const bool wide = a.stream == 0;
     switch (a.branch) {
-        case 0: return by_alignment<float, float>(a, backward, s);
+        case 0: return by_fit<float, float>(a, backward, s);
         case 1:
-            return wide ? by_alignment<float, _Float16>(a, backward, s)
-                        : by_alignment<_Float16, _Float16>(a, backward, s);
+            return wide ? by_fit<float, _Float16>(a, backward, s)
+                        : by_fit<_Float16, _Float16>(a, backward, s);
         default:
-            return wide ? by_alignment<float, __bf16>(a, backward, s)
-                        : by_alignment<__bf16, __bf16>(a, backward, s);
+            return wide ? by_fit<float, __bf16>(a, backward, s)
+                        : by_fit<__bf16, __bf16>(a, backward, s);
     }
 }
 

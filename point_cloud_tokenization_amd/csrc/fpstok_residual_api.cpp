@@ -26,14 +26,14 @@ static fpstok_status check_residual(const fpstok_seqs* s, const fpstok_residual_
         return fail(FPSTOK_EINVAL, "gate_per must be FPSTOK_GATE_*");
     if (p->activation < FPSTOK_ACT_NONE || p->activation > FPSTOK_ACT_SILU)
         return fail(FPSTOK_EINVAL, "activation must be FPSTOK_ACT_*");
-    if (!(p->eps > 0.0f) || !std::isfinite(p->eps))
-        return fail(FPSTOK_EINVAL, "eps must be > 0 and finite");
+    if (!(p->eps >= 1.17549435e-38f) || !std::isfinite(p->eps))
+        return fail(FPSTOK_EINVAL, "eps must be finite and at least 1.2e-38");
     return FPSTOK_OK;
 }
 
-// One [rows][width] view; `vec` stays set while 16-byte accesses fit it.
+// One [rows][width] view.
 static fpstok_status check_rows(const fpstok_rows* v, const char* what, int64_t rows, int C,
-                                int dtype, bool output, int32_t& vec, RowsArg& to) {
+                                int dtype, bool output, RowsArg& to) {
     if (!v) return fail(FPSTOK_EINVAL, "%s is NULL", what);
     to = RowsArg{v->data, rows > 1 ? v->row_stride : 0};
     if (rows == 0) return FPSTOK_OK;
@@ -45,14 +45,12 @@ static fpstok_status check_rows(const fpstok_rows* v, const char* what, int64_t 
     if (to.row > ((int64_t)1 << 23))
         return fail(FPSTOK_EUNSUPPORTED, "%s: row_stride > 2^23", what);
     if (output && rows > 1 && to.row < C) return fail(FPSTOK_EINVAL, "%s: rows overlap", what);
-    if (((uintptr_t)v->data % 16) != 0 || ((uintptr_t)(to.row * w) % 16) != 0) vec = 0;
     return FPSTOK_OK;
 }
 
-static fpstok_status check_weight(const float* w, const char* what, bool fits, int32_t& vec) {
+static fpstok_status check_weight(const float* w, const char* what, bool fits) {
     if (w && !fits) return fail(FPSTOK_EINVAL, "%s without what it belongs to", what);
     if (((uintptr_t)w & 3u) != 0) return fail(FPSTOK_EINVAL, "%s must be 4-byte aligned", what);
-    if (((uintptr_t)w & 15u) != 0) vec = 0;
     return FPSTOK_OK;
 }
 
@@ -72,10 +70,9 @@ static fpstok_status check_inputs(const fpstok_seqs* s, const fpstok_residual_pa
     a.gate_per = p->gate_per;
     a.act = p->activation;
     a.eps = p->eps;
-    a.vec = p->width % 8 == 0;
-    if ((st = check_rows(x, "x", n, a.C, a.stream, false, a.vec, a.x)) != FPSTOK_OK) return st;
+    if ((st = check_rows(x, "x", n, a.C, a.stream, false, a.x)) != FPSTOK_OK) return st;
     if (y) {
-        if ((st = check_rows(y, "y", n, a.C, a.branch, false, a.vec, a.y)) != FPSTOK_OK) return st;
+        if ((st = check_rows(y, "y", n, a.C, a.branch, false, a.y)) != FPSTOK_OK) return st;
     } else if (a.post != FPSTOK_NORM_NONE || a.gate_per != FPSTOK_GATE_NONE) {
         return fail(FPSTOK_EINVAL, "post_norm or gate_per without y");
     }
@@ -85,7 +82,7 @@ static fpstok_status check_inputs(const fpstok_seqs* s, const fpstok_residual_pa
         return fail(FPSTOK_EINVAL, "activation without a gate");
     if (gate && (st = check_rows(gate, "gate",
                                  a.gate_per == FPSTOK_GATE_ROW ? n : s->num_seqs, a.C, a.branch,
-                                 false, a.vec, a.gate)) != FPSTOK_OK)
+                                 false, a.gate)) != FPSTOK_OK)
         return st;
     if (!w) return FPSTOK_OK;
     const float* weights[kResidualWeights] = {w->post_weight, w->post_bias, w->scale,
@@ -95,7 +92,7 @@ static fpstok_status check_inputs(const fpstok_seqs* s, const fpstok_residual_pa
     const bool fits[kResidualWeights] = {a.post != 0, a.post != 0, y != nullptr, a.pre != 0,
                                          a.pre != 0};
     for (int k = 0; k < kResidualWeights; ++k) {
-        if ((st = check_weight(weights[k], names[k], fits[k], a.vec)) != FPSTOK_OK) return st;
+        if ((st = check_weight(weights[k], names[k], fits[k])) != FPSTOK_OK) return st;
         a.weights[k] = weights[k];
     }
     return FPSTOK_OK;
@@ -104,8 +101,7 @@ static fpstok_status check_inputs(const fpstok_seqs* s, const fpstok_residual_pa
 // Lays out the workspace of the gradients and returns its bytes; `given`: the
 // weights whose gradients are formed.
 static size_t lay_out(ResidualArgs& a, int given, bool gates, void* ws) {
-    const int64_t blocks = residual_blocks(a);
-    const int64_t runs = (a.seqs.rows + ((int64_t)1 << a.shift) - 1) >> a.shift;
+    const int64_t blocks = residual_blocks(a), runs = a.runs;
     const size_t row = (size_t)a.C * sizeof(float);
     a.part = (float*)ws;
     size_t need = align256((size_t)blocks * given * row);
@@ -126,7 +122,9 @@ FPSTOK_API size_t fpstok_residual_workspace_size(const fpstok_seqs* s,
     ResidualArgs a{};
     a.seqs = seq_args(s);
     a.C = p->width;
-    a.shift = residual_shift(a, true);
+    a.stream = p->stream_dtype;
+    a.post = a.pre = FPSTOK_NORM_RMS;  // (the most runs there can be)
+    plan_residual(a, true);
     return lay_out(a, kResidualWeights, p->gate_per == FPSTOK_GATE_SEQUENCE, nullptr);
 }
 
@@ -145,9 +143,9 @@ FPSTOK_API fpstok_status fpstok_residual(const fpstok_seqs* s, const fpstok_resi
     if ((h != nullptr) != (a.pre != FPSTOK_NORM_NONE))
         return fail(FPSTOK_EINVAL, "give h with pre_norm, or neither");
     if (x_out &&
-        (st = check_rows(x_out, "x_out", n, a.C, a.stream, true, a.vec, a.x_out)) != FPSTOK_OK)
+        (st = check_rows(x_out, "x_out", n, a.C, a.stream, true, a.x_out)) != FPSTOK_OK)
         return st;
-    if (h && (st = check_rows(h, "h", n, a.C, a.branch, true, a.vec, a.h)) != FPSTOK_OK) return st;
+    if (h && (st = check_rows(h, "h", n, a.C, a.branch, true, a.h)) != FPSTOK_OK) return st;
     const RowsArg* in[2] = {&a.x, &a.y};
     const RowsArg* out[2] = {&a.x_out, &a.h};
     for (int i = 0; i < 2; ++i)
@@ -157,7 +155,7 @@ FPSTOK_API fpstok_status fpstok_residual(const fpstok_seqs* s, const fpstok_resi
         return fail(FPSTOK_EINVAL, "stats must be 16-byte aligned");
     if (s->num_seqs == 0 || n == 0) return ok();
     a.stats = stats;
-    a.shift = residual_shift(a, false);
+    plan_residual(a, false);
     const hipError_t e = launch_residual(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "residual step kernel launch");
     return ok();
@@ -193,7 +191,7 @@ FPSTOK_API fpstok_status fpstok_residual_backward(
                  {grad_y, "grad_y", n, a.branch, true, &a.grad_y},
                  {grad_gate, "grad_gate", gate_rows, a.branch, true, &a.grad_gate}};
     for (const auto& v : views)
-        if (v.v && (st = check_rows(v.v, v.name, v.rows, a.C, v.dtype, v.output, a.vec, *v.to)) !=
+        if (v.v && (st = check_rows(v.v, v.name, v.rows, a.C, v.dtype, v.output, *v.to)) !=
                        FPSTOK_OK)
             return st;
     if (n > 1 && a.grad_x.data && a.grad_x.data == a.grad_x_out.data &&
@@ -207,7 +205,7 @@ FPSTOK_API fpstok_status fpstok_residual_backward(
                                                "grad of scale", "grad of pre_weight",
                                                "grad of pre_bias"};
         for (int k = 0; k < kResidualWeights; ++k) {
-            if ((st = check_weight(to[k], names[k], a.weights[k] != nullptr, a.vec)) != FPSTOK_OK)
+            if ((st = check_weight(to[k], names[k], a.weights[k] != nullptr)) != FPSTOK_OK)
                 return st;
             a.weight_grads[k] = to[k];
             given += to[k] != nullptr;
@@ -219,12 +217,12 @@ FPSTOK_API fpstok_status fpstok_residual_backward(
     if (((uintptr_t)stats & 15u) != 0)
         return fail(FPSTOK_EINVAL, "stats must be 16-byte aligned");
     a.stats = const_cast<float*>(stats);
-    a.shift = residual_shift(a, true);
+    plan_residual(a, true);
     const bool gates = a.gate_per == FPSTOK_GATE_SEQUENCE;
     const size_t need = lay_out(a, kResidualWeights, gates, ws);
     if ((st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK) return st;
     lay_out(a, given, gates, ws);
-    if (s->num_seqs == 0) a.seqs.rows = 0;  // no row is one of a sequence: zeros
+    if (s->num_seqs == 0) a.runs = 0;  // no row is one of a sequence: zeros
     const hipError_t e = launch_residual_backward(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "residual step gradient kernel launch");
     return ok();

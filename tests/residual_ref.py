@@ -35,12 +35,14 @@ def _norm_grad(p, xh, r, kind):
 
 
 def _act(g, name):
-    """The gate and its derivative: exp off by two steps, a sum and a quotient."""
+    """The gate and its derivative.  exp(-g) as 2^x with x = -g log2(e) rounded is off
+    by |g| f, exp2 by a step, the sum by half a step, the reciprocal by a step:
+    (|g| + 6) f at most; a result below 2^-126 may come out as 0."""
     if name == "none":
         return Val(g), Val(np.ones_like(g))
     with np.errstate(over="ignore"):
         s = 1.0 / (1.0 + np.exp(-g))
-    s = Val(s, 8 * F * s + 2.0 ** -149)
+    s = Val(s, (np.abs(np.clip(g, -200, 200)) + 6) * F * s + 2.0 ** -126)
     d = s * (Val(1.0) - s)
     if name == "sigmoid":
         return s, d

@@ -125,7 +125,7 @@ BOTH = [
     (dict(p=_params(stream_dtype=F.F16)), F.EINVAL),
     (dict(p=_params(post_norm=3)), F.EINVAL), (dict(p=_params(pre_norm=-1)), F.EINVAL),
     (dict(p=_params(gate_per=3)), F.EINVAL), (dict(p=_params(activation=3)), F.EINVAL),
-    (dict(p=_params(eps=0.0)), F.EINVAL), (dict(p=_params(eps=float("nan"))), F.EINVAL),
+    (dict(p=_params(eps=0.0)), F.EINVAL), (dict(p=_params(eps=1e-40)), F.EINVAL), (dict(p=_params(eps=float("nan"))), F.EINVAL),
     (dict(p=_params(eps=float("inf"))), F.EINVAL),
     (dict(s=_seqs(B=-1)), F.EINVAL), (dict(s=_seqs(cu=None)), F.EINVAL),
     (dict(s=_seqs(rows=1 << 31)), F.EUNSUPPORTED),
