@@ -93,6 +93,49 @@ __device__ __forceinline__ void load_weight(float* f, const float* w, float none
     r.get(f);
 }
 
+// A workgroup's rows and threads: rows of one wave share a workgroup of four.
+struct Threads {
+    int T, t, group;
+    int64_t run;
+    __device__ __forceinline__ Threads(const ResidualArgs& a) {
+        const int tid = threadIdx.x;
+        T = a.threads;
+        group = T == 64 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0;
+        t = T == 64 ? tid & 63 : tid;
+        run = T == 64 ? (int64_t)blockIdx.x * 4 + group : (int64_t)blockIdx.x;
+    }
+};
+
+// A thread's weights of its own elements in LDS, [weight][4 elements][thread]: what
+// is read again for every row need not stay in registers.
+template <Fit FIT, int EL>
+struct LdsWeights {
+    using f4 = float __attribute__((ext_vector_type(4)));
+    f4* at;
+    int T;
+    __device__ __forceinline__ LdsWeights(f4* lds, const Threads& th) : at(lds + th.t), T(th.T) {}
+    __device__ __forceinline__ void put(int k, const float* w, float none,
+                                        const Cols<FIT, EL>& c) {
+        float f[EL];
+        load_weight(f, w, none, c);
+#pragma unroll
+        for (int q = 0; q < EL / 4; ++q) {
+            f4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f[q * 4 + i];
+            at[(k * (EL / 4) + q) * T] = x;
+        }
+    }
+    __device__ __forceinline__ void get(float* f, int k) const {
+#pragma unroll
+        for (int q = 0; q < EL / 4; ++q) {
+            const f4 x = at[(k * (EL / 4) + q) * T];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[q * 4 + i] = x[i];
+        }
+    }
+};
+
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {
     return __uint_as_float(
@@ -248,19 +291,6 @@ __device__ __forceinline__ void norm_row(float* x, bool layer, float inv_c, floa
     for (int i = 0; i < EL; ++i) x[i] *= r;
 }
 
-// A workgroup's rows and threads: rows of one wave share a workgroup of four.
-struct Threads {
-    int T, t, group;
-    int64_t run;
-    __device__ __forceinline__ Threads(const ResidualArgs& a) {
-        const int tid = threadIdx.x;
-        T = a.threads;
-        group = T == 64 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0;
-        t = T == 64 ? tid & 63 : tid;
-        run = T == 64 ? (int64_t)blockIdx.x * 4 + group : (int64_t)blockIdx.x;
-    }
-};
-
 // Forward.  The T threads of a row hold it in registers from the first load to
 // the last store, so every operand is read and every result written once; a
 // workgroup takes a run of adjacent rows, keeps the weights in registers and
@@ -358,6 +388,9 @@ __global__ __launch_bounds__(MAX_T) void residual_kernel(ResidualArgs a) {
 // PLAIN: RMS norms without biases, which need neither means nor their sums.
 template <class S, class B, Fit FIT, int EL, int MAX_T, bool PLAIN>
 __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
+    // rows of more than 4096 elements leave few registers: the next row is called
+    // for when most of this one's are free again
+    constexpr bool kLate = MAX_T > 512;
     __shared__ float lds[2][2][16];
     __shared__ float cols[3][64 * EL];
     const Threads th(a);
@@ -367,11 +400,16 @@ __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
     const float inv_c = 1.0f / (float)a.C;
     const bool has_y = a.y.data != nullptr, gated = a.gate_per != 0;
     const bool has_gx = a.grad_x_out.data != nullptr, has_gh = a.grad_h.data != nullptr;
-    float wp[EL], bp[EL], sc[EL], wh[EL];
-    load_weight(wp, a.weights[0], 1.0f, c);
-    if (!PLAIN) load_weight(bp, a.weights[1], 0.0f, c);
-    load_weight(sc, a.weights[2], 1.0f, c);
-    load_weight(wh, a.weights[3], 1.0f, c);
+    extern __shared__ __attribute__((aligned(16))) float fpstok_residual_lds[];
+    enum { kPost, kScale, kPre, kPostBias };
+    LdsWeights<FIT, EL> weights((typename LdsWeights<FIT, EL>::f4*)fpstok_residual_lds, th);
+    if (th.group == 0) {
+        weights.put(kPost, a.weights[0], 1.0f, c);
+        weights.put(kScale, a.weights[2], 1.0f, c);
+        weights.put(kPre, a.weights[3], 1.0f, c);
+        if (!PLAIN) weights.put(kPostBias, a.weights[1], 0.0f, c);
+    }
+    __syncthreads();
     float acc[kResidualWeights][EL], gate_acc[EL];
 #pragma unroll
     for (int i = 0; i < EL; ++i) {
@@ -406,50 +444,66 @@ __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
         for (int i = 0; i < EL; ++i) gx[i] = 0.0f;
         if (has_gx) rgx.get(gx);
         const bool more = r + 1 < rows.hi;
-        if (more) {
+        bool called = false;
+        auto call_next = [&]() {  // for the next row
+            if (called || !more) return;
+            called = true;
             rows.to(r + 1);
             load(r + 1);
-        }
+        };
+        if (!kLate) call_next();
         S* ox = a.grad_x.data ? (S*)a.grad_x.data + r * a.grad_x.row : nullptr;
         B* oy = a.grad_y.data ? (B*)a.grad_y.data + r * a.grad_y.row : nullptr;
         B* og = a.grad_gate.data && a.gate_per == 1
                     ? (B*)a.grad_gate.data + r * a.grad_gate.row
                     : nullptr;
         if (live) {
-            float u[EL], act[EL], slope[EL];
-            if (has_y) {
+            // u = yh weight + bias, the gate and its derivative; formed twice, before and
+            // after the sums, so that they need no registers in between
+            auto branch = [&](float* u, float* act, float* slope) {
+                asm volatile("" ::: "memory");
                 if (a.post != 0) {
+                    float wp[EL], bp[EL];
+                    weights.get(wp, kPost);
+                    if (!PLAIN) weights.get(bp, kPostBias);
 #pragma unroll
-                    for (int i = 0; i < EL; ++i) {
-                        y[i] = PLAIN ? y[i] * st.y : (y[i] - st.x) * st.y;
+                    for (int i = 0; i < EL; ++i)
                         u[i] = PLAIN ? y[i] * wp[i] : __builtin_fmaf(y[i], wp[i], bp[i]);
-                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < EL; ++i) u[i] = y[i];
                 }
 #pragma unroll
                 for (int i = 0; i < EL; ++i) act[i] = 1.0f, slope[i] = 1.0f;
-                if (gated) {
-                    if (a.act != 0) {
+                if (!gated) return;
+                if (a.act != 0) {
 #pragma unroll
-                        for (int i = 0; i < EL; ++i) {
-                            const float s = sigmoid(g[i]);
-                            act[i] = a.act == 1 ? s : g[i] * s;
-                            slope[i] = s * (1.0f - s);
-                            // silu: s (1 + g (1 - s))
-                            if (a.act == 2) slope[i] = __builtin_fmaf(slope[i], g[i], s);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < EL; ++i) act[i] = g[i];
+                    for (int i = 0; i < EL; ++i) {
+                        const float s = sigmoid(g[i]);
+                        act[i] = a.act == 1 ? s : g[i] * s;
+                        slope[i] = s * (1.0f - s);
+                        // silu: s (1 + g (1 - s))
+                        if (a.act == 2) slope[i] = __builtin_fmaf(slope[i], g[i], s);
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < EL; ++i) act[i] = g[i];
                 }
+            };
+            if (has_y) {
+                if (a.post != 0) {
+#pragma unroll
+                    for (int i = 0; i < EL; ++i) y[i] = PLAIN ? y[i] * st.y : (y[i] - st.x) * st.y;
+                }
+                float u[EL], act[EL], slope[EL], sc[EL];
+                branch(u, act, slope);
+                weights.get(sc, kScale);
 #pragma unroll
                 for (int i = 0; i < EL; ++i) x[i] = __builtin_fmaf(u[i] * act[i], sc[i], x[i]);
             }
             if (has_gh) {
-                float c1 = 0.0f, c2 = 0.0f;
+                float c1 = 0.0f, c2 = 0.0f, wh[EL];
+                weights.get(wh, kPre);
 #pragma unroll
                 for (int i = 0; i < EL; ++i) {
                     x[i] = PLAIN ? x[i] * st.w : (x[i] - st.z) * st.w;
@@ -480,7 +534,10 @@ __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
             }
             if (ox) store(ox, gx, c);
             if (has_y) {
-                float c1 = 0.0f, c2 = 0.0f;
+                float c1 = 0.0f, c2 = 0.0f, sc[EL], wp[EL], u[EL], act[EL], slope[EL];
+                branch(u, act, slope);
+                weights.get(sc, kScale);
+                if (a.post != 0) weights.get(wp, kPost);
 #pragma unroll
                 for (int i = 0; i < EL; ++i) {
                     const float d = c.keep(gx[i], i);
@@ -496,6 +553,7 @@ __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
                         if (!PLAIN) c2 += gx[i];
                     }
                 }
+                if (kLate) call_next();
                 if (og) store(og, g, c);
                 if (gate_sums) {
 #pragma unroll
@@ -524,6 +582,7 @@ __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {
             if (oy) store(oy, gx, c);
             if (og) store(og, gx, c);
         }
+        call_next();
         if (gate_sums && (!more || rows.b != b)) {
             // run + sequence is a number of its own: along the rows one of both grows
             store(a.gate_part + (th.run + b) * a.C, gate_acc, c);
@@ -618,12 +677,15 @@ __global__ __launch_bounds__(256) void residual_gates_kernel(ResidualArgs a) {
     }
 }
 
-// 4 elements a thread for gradients and a float32 stream, 8 else, and where a row
-// needs more than 512 threads.  (float32 stream, 38,600 rows of 768: 4 elements 87 us
-// forward and 140 backward, 8 elements 102 and 197: half the registers, and 8 leave a
-// quarter of the threads idle.  bfloat16, 34,000 of 512: 49 and 105 against 39 and 113.)
+// 4 elements a thread for gradients and a float32 stream, 8 else and for wide
+// rows.  (float32 stream, 38,600 rows of 768: 4 elements 87 us forward and 140
+// backward, 8 elements 102 and 197: half the registers, and 8 leave a quarter of the
+// threads idle.  bfloat16, 34,000 of 512: 49 and 105 against 39 and 113; 11,700 of
+// 2560 backward: 144 against 206, with a float32 stream and layer norms 229 against
+// 189.)
 static int residual_elements(const ResidualArgs& a, bool backward) {
-    return a.C >= 4 && a.C <= 2048 && (a.stream == 0 || backward) ? 4 : 8;
+    const int most = backward && a.stream != 0 ? 4096 : 2048;
+    return a.C >= 4 && a.C <= most && (a.stream == 0 || backward) ? 4 : 8;
 }
 
 int64_t residual_blocks(const ResidualArgs& a) {
@@ -638,13 +700,15 @@ bool residual_plain(const ResidualArgs& a) {
 void plan_residual(ResidualArgs& a, bool backward) {
     a.elements = residual_elements(a, backward);
     a.threads = (a.C + 64 * a.elements - 1) / (64 * a.elements) * 64;
-    // as many runs as the kernel's registers let run at once on 256 compute units
-    const int waves = !backward             ? 20
-                      : a.threads > 768     ? 16
-                      : a.threads > 512     ? 12
-                      : a.elements == 8     ? 8
-                      : residual_plain(a)   ? 16
-                                            : 12;
+    // as many runs as the kernels' registers let run at once on 256 compute units
+    const bool plain = residual_plain(a);
+    int waves;
+    if (!backward)
+        waves = a.elements == 4 || plain ? 20 : 16;
+    else if (a.elements == 4)
+        waves = plain || a.stream != 0 ? 16 : 12;
+    else
+        waves = a.threads > 768 ? 16 : a.threads > 512 ? 12 : 8;
     const int per_unit = waves / (a.threads / 64);
     // (free slots leave some runs of padded rows little to do: shorter ones even that
     // out.  Backward a run leaves a part of the weights' gradients: 400 padded events, 512
@@ -663,15 +727,19 @@ static void launch(const ResidualArgs& a, bool backward, hipStream_t s) {
     else if (!backward)
         residual_kernel<S, B, FIT, EL, MAX_T, false><<<grid, block, 0, s>>>(a);
     else if (plain)
-        residual_grad_kernel<S, B, FIT, EL, MAX_T, true><<<grid, block, 0, s>>>(a);
+        residual_grad_kernel<S, B, FIT, EL, MAX_T, true>
+            <<<grid, block, 3 * a.threads * EL * sizeof(float), s>>>(a);
     else
-        residual_grad_kernel<S, B, FIT, EL, MAX_T, false><<<grid, block, 0, s>>>(a);
+        residual_grad_kernel<S, B, FIT, EL, MAX_T, false>
+            <<<grid, block, 4 * a.threads * EL * sizeof(float), s>>>(a);
 }
 
 template <class S, class B, Fit FIT>
 static void by_width(const ResidualArgs& a, bool backward, hipStream_t s) {
-    if (a.elements == 4)
+    if (a.elements == 4 && a.threads <= 512)
         launch<S, B, FIT, 4, 512>(a, backward, s);
+    else if (a.elements == 4)
+        launch<S, B, FIT, 4, 1024>(a, backward, s);
     else if (a.threads <= 512)
         launch<S, B, FIT, 8, 512>(a, backward, s);
     else if (a.threads <= 768)
