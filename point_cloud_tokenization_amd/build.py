@@ -12,10 +12,12 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfpstok.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "fpstok_kernels.hip", "fpstok_api.cpp", "fpstok_attention.hip", "fpstok_rope.hip",
-    "fpstok_attention_api.cpp", "fpstok_attention_bias.hip", "fpstok_residual.hip", "fpstok_residual_api.cpp")]
+    "fpstok_attention_api.cpp", "fpstok_attention_bias.hip", "fpstok_attention_plane.hip",
+    "fpstok_residual.hip", "fpstok_residual_api.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "fpstok.h")] + [os.path.join(CSRC, f) for f in (
     "fpstok_internal.h", "fpstok_host.h", "fpstok_attention.h", "fpstok_seqs.h", "fpstok_mma.h",
-    "fpstok_seqs_host.h", "fpstok_residual.h", "fpstok_attention_kernels.h", "fpstok_bias.h")]
+    "fpstok_seqs_host.h", "fpstok_residual.h", "fpstok_attention_kernels.h", "fpstok_bias.h",
+    "fpstok_attention_bias.h")]
 
 ARCH = "gfx950"
 # -ffp-contract=off: the squared distance is the exact float32 sequence

@@ -239,15 +239,15 @@ void launch_join_dkv(const AttnArgs& a, hipStream_t s) {
 
 template <class T>
 static hipError_t backward(const AttnArgs& a, hipStream_t s) {
-    if (a.qs.rows > 0) backward_q<T, false>(a, NoBias{}, s);
-    backward_kv<T, false>(a, NoBias{}, s);
+    if (a.qs.rows > 0) backward_q<T, kNoBias>(a, NoBias{}, s);
+    backward_kv<T, kNoBias>(a, NoBias{}, s);
     return hipGetLastError();
 }
 
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
-    return a.dtype == 0   ? forward<float, false>(a, NoBias{}, plan, s)
-           : a.dtype == 1 ? forward<_Float16, false>(a, NoBias{}, plan, s)
-                          : forward<__bf16, false>(a, NoBias{}, plan, s);
+    return a.dtype == 0   ? forward<float, kNoBias>(a, NoBias{}, plan, s)
+           : a.dtype == 1 ? forward<_Float16, kNoBias>(a, NoBias{}, plan, s)
+                          : forward<__bf16, kNoBias>(a, NoBias{}, plan, s);
 }
 
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s) {

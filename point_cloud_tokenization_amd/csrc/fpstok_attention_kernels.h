@@ -398,21 +398,21 @@ __device__ __forceinline__ float log_sum(float mc, float l) {
 // What a workgroup needs to form its scores' bias: the group's tables in LDS
 // (behind the kernel's own, in what the launch adds to it) and the positions of the
 // walk's next tile.
-template <bool BIAS, int ROWS, int THREADS = 256>
+template <BiasFrom BIAS, int ROWS, int THREADS = 256>
 struct BiasTile {
-    __device__ __forceinline__ BiasTile(const NoBias&, int, int, int, int) {}
-};
-template <int ROWS, int THREADS>
-struct BiasTile<true, ROWS, THREADS> {
     const FPSTOK_LDS float* table;  // of head `head` of the group
-    bool planed = false;            // the pairs' entries are in the plane
+    bool planed;                    // the sequence's entries are in the plane
     PosStage<ROWS, THREADS> stage;
-    __device__ __forceinline__ BiasTile(const BiasArgs& b, int hk, int G, int head, int tid)
-        : stage(b, tid % THREADS) {
+    __device__ __forceinline__ BiasTile(const BiasArgs& b, int hk, int G, int head, int tk, int tid)
+        : planed(BIAS == kPlane && tk <= b.pitch), stage(b, tid % THREADS) {
         float* lds = bias_lds();
         load_table(b, lds, hk, G, tid);
         table = (const FPSTOK_LDS float*)lds + head * b.entries;
     }
+};
+template <int ROWS, int THREADS>
+struct BiasTile<kNoBias, ROWS, THREADS> {
+    __device__ __forceinline__ BiasTile(const NoBias&, int, int, int, int, int) {}
 };
 
 // A block's entries from the plane: the keys p + 8 g + 0 .. 3 of one query.
@@ -427,6 +427,14 @@ __device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
     return x;
 }
 
+// The same, or, of a sequence that is longer than the plane, found here.
+template <int BN>
+__device__ __forceinline__ u32x16 plane_entries(const BiasArgs& b, bool planed, const uint32_t* p,
+                                                const FPSTOK_LDS uint32_t* own,
+                                                const FPSTOK_LDS uint32_t* tile) {
+    return planed ? load_entries(p) : find_entries<false, 128, BN>(b, own, tile);
+}
+
 // The sums of dS and of the weights of a row by entry: [wave][entry][lane & 31]
 // behind the tables in LDS; one entry more takes those that are another launch's.
 // A place holds both as whole numbers: dS in units of 2^-35 of the row's `cap` in
@@ -436,18 +444,13 @@ __device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
 // a power of two that |dP - delta| stays below, so a sum does too, its weights
 // adding up to 1; where it grows, by more than a factor of 4 over what came
 // before, the sums are shifted.
-template <bool BIAS>
+template <BiasFrom BIAS>
 struct TableSums {
-    __device__ __forceinline__ TableSums(const NoBias&, int, int, int, int) {}
-};
-template <>
-struct TableSums<true> {
     using u64 = unsigned long long;
     static constexpr int kWeightBits = 26;
     FPSTOK_LDS u64* lane_sums;
     u64* all;
     int slots;
-    int byte_shift;              // from a pair's byte to bytes of a place
     uint32_t cap = 0x0d800000u;  // 2^-100
     bool on;
     __device__ __forceinline__ TableSums(const BiasArgs& b, int G, int wave, int lane, int tid) {
@@ -487,7 +490,7 @@ struct TableSums<true> {
                 if (a >= b.axes) break;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    put(entries[e] >> 8 * a & 255u, byte_shift, x[e]);
+                    put(entries[e] >> 8 * a & 255u, BIAS == kPlane ? 6 : 8, x[e]);
             }
         } else {
 #pragma unroll 1
@@ -558,6 +561,10 @@ struct TableSums<true> {
         }
     }
 };
+template <>
+struct TableSums<kNoBias> {
+    __device__ __forceinline__ TableSums(const NoBias&, int, int, int, int) {}
+};
 
 // Forward.  A workgroup of 4 waves takes 128 rows (32 per wave) of one key
 // head and walks the tiles of BN keys they see.  Per tile a wave forms
@@ -577,7 +584,7 @@ struct TableSums<true> {
 // event.  84k pulses, window 257, 8 heads on 2: 0.14 ms; 64 events of at most
 // 128 tokens, 12 heads: 14 us (7 us of bytes).  A third buffer cost 5 %, scores
 // formed one tile ahead 5 to 15 % (and spills at D = 128).
-template <class T, int DP, int BN, bool BIAS>
+template <class T, int DP, int BN, BiasFrom BIAS>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) - (BIAS && DP * sizeof(T) == 128))
 void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     constexpr int DB = DP / 32, STEPS = DP / 16;
@@ -597,12 +604,12 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     q.load<T, STEPS>(qf, a.q, a.D, half);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
-    BiasTile<BIAS, BN> scores(bias, t.hk, G, q.h - t.hk * G, tid);
+    BiasTile<BIAS, BN> scores(bias, t.hk, G, q.h - t.hk * G, t.tk, tid);
     const uint32_t* entry_row = nullptr;
-    if constexpr (BIAS) {
+    if constexpr (BIAS != kNoBias) {
         own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
-        scores.planed = bias.plane && t.tk <= bias.pitch;
-        entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+        if (BIAS == kPlane)
+            entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
     }
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
@@ -625,13 +632,13 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
         dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
-        if constexpr (BIAS) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
+        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
     };
     const View<BN> all(a, q.pa, q.pb, t.tk);
     const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {  // this wave's part of it is there
         dma_wait();
-        if constexpr (BIAS) scores.stage.store(bias, pos.tile[i & 1]);
+        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos.tile[i & 1]);
         // a value that some row must not see meets a weight of 0 there: an
         // infinite one has to leave the product
         if (all.of(a, jn) == 1) {
@@ -656,16 +663,18 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         for (int b = 0; b < NB; ++b) {
             f32x16 x = 0.0f;
             u32x16 entries;
-            if constexpr (BIAS) {
-                if (scores.planed) entries = load_entries(entry_row + j0 + b * 32);
-            }
+            if constexpr (BIAS == kPlane)
+                entries = plane_entries<BN>(
+                    bias, scores.planed, entry_row + j0 + b * 32,
+                    (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
                 if (sizeof(T) == 2 || st * 16 < a.D)  // (float32: a step is 8 instructions)
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-            if constexpr (BIAS) {
+            if constexpr (BIAS != kNoBias) {
                 x *= cs;
-                if (scores.planed)
+                if constexpr (BIAS == kPlane)
                     add_entries(x, entries, bias.axes, scores.table);
                 else
                     add_bias<false, false, 128, BN>(
@@ -756,7 +765,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // workgroup per compute unit: 435 us there.  Sequences of more than 32 rows are
 // slower here (64 events of up to 128 tokens: 30 us against 14), for every 32
 // rows read all keys again.
-template <class T, int DP, int BN, bool BIAS>
+template <class T, int DP, int BN, BiasFrom BIAS>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) > 3 ? 3 : 512 / (DP * (int)sizeof(T)))
 void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     constexpr int BM = 32, DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
@@ -780,8 +789,8 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     Frag qf[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
-    BiasTile<BIAS, BN, 64> scores(bias, t.hk, G, q.h - t.hk * G, tid);
-    if constexpr (BIAS)
+    BiasTile<BIAS, BN, 64> scores(bias, t.hk, G, q.h - t.hk * G, t.tk, tid);
+    if constexpr (BIAS != kNoBias)
         own_positions(bias, pos[wave].own, q.r, bias.q_pos, q.row, q.live, half);
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
@@ -795,7 +804,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         const int64_t j0 = (int64_t)kt.tile(i) * BN;
         sk.load(kb + j0 * a.k.row, a.k.row, t.tk - (int)j0, a.D, lane);
         sv.load(vb + j0 * a.v.row, a.v.row, t.tk - (int)j0, a.D, lane);
-        if constexpr (BIAS) scores.stage.load(bias, bias.k_pos, t.k0 + j0, t.tk - (int)j0);
+        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.k_pos, t.k0 + j0, t.tk - (int)j0);
     };
 
     const View<BN> all(a, q.pa, q.pb, t.tk);
@@ -816,7 +825,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         wave_sync();  // the wave's reads of the last tile are done
         sk.store(kbuf, a.D, lane);
         sv.store(vbuf, a.D, lane);
-        if constexpr (BIAS) scores.stage.store(bias, pos[wave].tile[0]);
+        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos[wave].tile[0]);
         wave_sync();
         if (i + 4 < n) load(i + 4);
         f32x16 s[KB];
@@ -827,7 +836,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             for (int st = 0; st < STEPS; ++st)
                 if (sizeof(T) == 2 || st * 16 < a.D)  // (float32: a step is 8 instructions)
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-            if constexpr (BIAS) {
+            if constexpr (BIAS != kNoBias) {
                 x *= cs;
                 add_bias<false, false, BM, BN>(
                     x, nullptr, bias, scores.table,
@@ -954,7 +963,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // over the keys is off by is taken back at the end: sum over the rows of (sum dS) -
 // off * (sum of weights).  The tiles' parts are added in order by a kernel of
 // their own.
-template <class T, int DP, int BN, bool TWICE, bool BIAS>
+template <class T, int DP, int BN, bool TWICE, BiasFrom BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BIAS && DP > 64) ? 2 : 1)
 void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     constexpr int DB = DP / 32, KB = BN / 32, STEPS = DP / 16;
@@ -969,7 +978,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     RowTile t;
     if (!row_tile<7, false>(a, 1, t)) {
-        if constexpr (BIAS) {  // (the kernel that adds the parts does not know)
+        if constexpr (BIAS != kNoBias) {  // (the kernel that adds the parts does not know)
             const int size = a.G * bias.count;
             if (bias.part)
                 for (int i = tid; i < size; i += 256)
@@ -980,14 +989,13 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const QueryRows q(a, t, wave * 32, lane);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
-    BiasTile<BIAS, BN> scores(bias, t.hk, a.G, q.h - t.hk * a.G, tid);
+    BiasTile<BIAS, BN> scores(bias, t.hk, a.G, q.h - t.hk * a.G, t.tk, tid);
     TableSums<BIAS> sums(bias, a.G, wave, lane, tid);
     const uint32_t* entry_row = nullptr;
-    if constexpr (BIAS) {
+    if constexpr (BIAS != kNoBias) {
         own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
-        scores.planed = bias.plane && t.tk <= bias.pitch;
-        sums.byte_shift = scores.planed ? 6 : 8;
-        entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+        if (BIAS == kPlane)
+            entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
     }
     Frag qf[STEPS], gf[STEPS], of[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
@@ -1015,13 +1023,13 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
         dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
-        if constexpr (BIAS) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
+        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
     };
     const View<BN> all(a, q.pa, q.pb, t.tk);
     const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {
         dma_wait();
-        if constexpr (BIAS) scores.stage.store(bias, pos.tile[i & 1]);
+        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos.tile[i & 1]);
         if (all.of(a, jn) != 1) return;
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
         const uint32_t chunks = dma.clean(buf, tid);
@@ -1056,10 +1064,13 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             x = Elem<T>::mma(Tl::row_frag(kbuf, row, st, half), qf[st], x);
             y = Elem<T>::mma(Tl::row_frag(kbuf + BN * Tl::kPitch, row, st, half), gf[st], y);
         }
-        if constexpr (BIAS) {
+        if constexpr (BIAS != kNoBias) {
             x *= cs;
-            if (scores.planed)
-                add_entries(x, load_entries(entry_row + j0 + b), bias.axes, scores.table);
+            if constexpr (BIAS == kPlane)
+                add_entries(x, plane_entries<BN>(
+                bias, scores.planed, entry_row + j0 + b,
+                (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]), bias.axes, scores.table);
             else
                 add_bias<false, false, 128, BN>(
                     x, nullptr, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
@@ -1078,17 +1089,18 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
         u32x16 entries;
-        if constexpr (BIAS) {
-            if (scores.planed) entries = load_entries(entry_row + j0 + b * 32);
-        }
+        if constexpr (BIAS == kPlane) entries = plane_entries<BN>(
+                bias, scores.planed, entry_row + j0 + b * 32,
+                (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             y = Elem<T>::mma(Tl::row_frag(vbuf, b * 32 + (lane & 31), st, half), gf[st], y);
         }
-        if constexpr (BIAS) {
+        if constexpr (BIAS != kNoBias) {
             x *= cs;
-            if (scores.planed)
+            if constexpr (BIAS == kPlane)
                 add_entries(x, entries, bias.axes, scores.table);
             else
                 add_bias<false, true, 128, BN>(
@@ -1097,7 +1109,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         if (holes) hide_lost(x, b * 32, i);
         f32x16 ds;
-        if constexpr (BIAS) {
+        if constexpr (BIAS != kNoBias) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 x[e] = __builtin_amdgcn_exp2f(x[e] - lse2);
@@ -1198,7 +1210,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if (i + 1 < n) arrive(i + 1);
         __syncthreads();
     }
-    if constexpr (BIAS) {
+    if constexpr (BIAS != kNoBias) {
         if (sums.on) sums.store(bias, a.G, t, counts ? pair_sum(off_by) : 0.0f, q.r, half, tid);
     }
     T* out = (T*)a.grad_q.data + q.row * a.grad_q.row + q.h * a.grad_q.head;
@@ -1227,7 +1239,7 @@ __device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk)
 // are added in order by the kernel below.  (40k + 12k + 2.5k pulses, 4 sinks, 8
 // heads on 4: the walk in one workgroup 4 ms, in chunks 27 us.  At float32 and
 // D > 64 its two results and two operands pass the registers and spill.)
-template <class T, int DP, bool BIAS>
+template <class T, int DP, BiasFrom BIAS>
 __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 128 ? 2 : 1)
 void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     constexpr int DB = DP / 32, STEPS = DP / 16;
@@ -1271,8 +1283,8 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     FPSTOK_LDS char* qbuf = lds + wave * kWaveBytes;
     FPSTOK_LDS char* gbuf = qbuf + kTile;
     const float cs = a.scale * kLog2e;
-    BiasTile<BIAS, 32, 64> scores(bias, hk, G, 0, tid);
-    if constexpr (BIAS) __syncthreads();
+    BiasTile<BIAS, 32, 64> scores(bias, hk, G, 0, tk, tid);
+    if constexpr (BIAS != kNoBias) __syncthreads();
 
     for (int s0 = 0; s0 < sinks; s0 += 32) {
         const int j = s0 + (lane & 31);
@@ -1282,7 +1294,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                            (const T*)a.k.data, a.D, half);
         load_row<T, STEPS>(vf, (const T*)a.v.data + (k0 + j) * a.v.row + hk * a.v.head, live,
                            (const T*)a.v.data, a.D, half);
-        if constexpr (BIAS)
+        if constexpr (BIAS != kNoBias)
             own_positions(bias, pos[wave].own, lane & 31, bias.k_pos, k0 + j, live, half);
         f32x16 dk[DB], dv[DB];
 #pragma unroll
@@ -1297,7 +1309,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             const int64_t at = (int64_t)(hk * G + g) * a.qs.rows + row0 + x + (r < last ? r : last);
             st = make_float2(a.lse2[at], a.delta[at]);
             if (r > last) st = make_float2(INFINITY, 0.0f);
-            if constexpr (BIAS) scores.stage.load(bias, bias.q_pos, row0 + x, rows - x);
+            if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.q_pos, row0 + x, rows - x);
         };
         if (wave * 32 < rows) load(0, wave * 32);
         for (int g = 0, x = wave * 32; g < G && x < rows;) {
@@ -1313,7 +1325,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             sq.store(qbuf, a.D, lane);
             sg.store(gbuf, a.D, lane);
             if (half == 0) stat[wave][0][lane] = st.x, stat[wave][1][lane] = st.y;
-            if constexpr (BIAS) scores.stage.store(bias, pos[wave].tile[0]);
+            if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos[wave].tile[0]);
             wave_sync();
             const int head = g;
             x += 128;
@@ -1326,7 +1338,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                 y = Elem<T>::mma(Tl::row_frag(gbuf, lane & 31, e, half), vf[e], y);
             }
             f32x16 w, ds;
-            if constexpr (BIAS) {
+            if constexpr (BIAS != kNoBias) {
                 s *= cs;
                 add_bias<true, false, 32, 32>(
                     s, nullptr, bias, scores.table + head * bias.entries,
@@ -1406,7 +1418,7 @@ __device__ __forceinline__ int64_t k_part_at(const AttnArgs& a, int split, int h
 // term of a score that was -infinity stays so, or is finite) and takes 0 for
 // their gradient and for infinite values (any other query that sees one of those has
 // a delta that is not finite).
-template <class T, int DP, int BQ, bool BIAS>
+template <class T, int DP, int BQ, BiasFrom BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BIAS && DP > 64) ? 2 : 1)
 void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     constexpr int DB = DP / 32, QB = BQ / 32, STEPS = DP / 16;
@@ -1436,12 +1448,12 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     if constexpr (!kVLds)
         load_row<T, STEPS>(vf, (const T*)a.v.data + krow * a.v.row + t.hk * a.v.head, live,
                            (const T*)a.v.data, a.D, half);
-    BiasTile<BIAS, BQ> scores(bias, t.hk, G, 0, tid);
+    BiasTile<BIAS, BQ> scores(bias, t.hk, G, 0, t.tk, tid);
     const uint32_t* entry_col = nullptr;
-    if constexpr (BIAS) {
+    if constexpr (BIAS != kNoBias) {
         own_positions(bias, pos.own, r, bias.k_pos, krow, live, half);
-        scores.planed = bias.plane && t.tk <= bias.pitch;
-        entry_col = bias.plane + t.q0 * bias.pitch + (live ? t.row0 + r : 0);
+        if (BIAS == kPlane)
+            entry_col = bias.plane + t.q0 * bias.pitch + (live ? t.row0 + r : 0);
     }
     // queries i0 .. i1 see some key of the tile (of the rows past its window,
     // the tile with the sinks gets their gradients from the kernel above), e0 ..
@@ -1515,7 +1527,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                 qp += a.q.head - back * a.q.row;
                 gp += a.grad_out.head - back * a.grad_out.row;
                 stat_at += a.qs.rows - back;
-                if constexpr (BIAS) ++group_n;
+                if constexpr (BIAS != kNoBias) ++group_n;
             }
         }
         const int rows = i1 - xn + 1;
@@ -1527,11 +1539,11 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             dma4(src, (uint32_t)(lane < rows ? lane : rows - 1) * 4u,
                  (uint32_t)(uintptr_t)(FPSTOK_LDS float*)stat[i & 1][wave]);
         }
-        if constexpr (BIAS) scores.stage.load(bias, bias.q_pos, t.q0 + xn, rows);
+        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.q_pos, t.q0 + xn, rows);
     };
     auto arrive = [&](int i) {
         dma_wait();
-        if constexpr (BIAS) scores.stage.store(bias, pos.tile[i & 1]);
+        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos.tile[i & 1]);
         if (!tile_all.has(xn)) {
             FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
             // (a query with infinite elements has no finite score: its weights are
@@ -1554,13 +1566,17 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         const FPSTOK_LDS char* gbuf = qbuf + BQ * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
         u32x16 entries;
-        if constexpr (BIAS) {
+        if constexpr (BIAS == kPlane) {
             if (scores.planed) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int i = x0 + b * 32 + (e >> 2) * 8 + half * 4 + (e & 3);
                     entries[e] = entry_col[(int64_t)(i < i1 ? i : i1) * bias.pitch];
                 }
+            } else {
+                entries = find_entries<true, 128, BQ>(
+                    bias, (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
+                    (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
             }
         }
 #pragma unroll
@@ -1574,9 +1590,9 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             y = Elem<T>::mma(Tl::row_frag(gbuf, b * 32 + (lane & 31), st, half), v, y);
         }
         f32x16 w, ds;
-        if constexpr (BIAS) {
+        if constexpr (BIAS != kNoBias) {
             x *= c;
-            if (scores.planed)
+            if constexpr (BIAS == kPlane)
                 add_entries(x, entries, bias.axes, scores.table + head * bias.entries);
             else
                 add_bias<true, false, 128, BQ>(
@@ -1728,19 +1744,21 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     if (bad.tiles != 0) add_hidden(ov);
 }
 
-template <class T, bool BIAS>
+template <class T, BiasFrom BIAS>
 static hipError_t forward(const AttnArgs& a, const BiasParam<BIAS>& b, const AttnPlan& plan,
                           hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const int64_t blocks = row_slots(a.qs, a.G, plan.few ? 5 : 7) * a.Hk;
     const dim3 grid((unsigned)(blocks * a.splits));
     size_t lds = 0;
-    if constexpr (BIAS) lds = bias_lds_bytes(b, a.G, false);
-    if (plan.few) {
-        if (a.D <= 64)
-            attention_few_kernel<T, 64, 32, BIAS><<<grid, 256, lds, s>>>(a, b);
-        else
-            attention_few_kernel<T, 128, 32, BIAS><<<grid, 256, lds, s>>>(a, b);
+    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, false);
+    if (BIAS != kPlane && plan.few) {
+        if constexpr (BIAS != kPlane) {  // (few queries have no plane)
+            if (a.D <= 64)
+                attention_few_kernel<T, 64, 32, BIAS><<<grid, 256, lds, s>>>(a, b);
+            else
+                attention_few_kernel<T, 128, 32, BIAS><<<grid, 256, lds, s>>>(a, b);
+        }
     } else {
         if (a.D <= 64)
             attention_kernel<T, 64, 64, BIAS><<<grid, 256, lds, s>>>(a, b);
@@ -1752,13 +1770,13 @@ static hipError_t forward(const AttnArgs& a, const BiasParam<BIAS>& b, const Att
 }
 
 // grad_q and the rows' statistics (and, with a bias, the sums of its gradient).
-template <class T, bool BIAS>
+template <class T, BiasFrom BIAS>
 static void backward_q(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
     const bool narrow = k16 && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
     size_t lds = 0;
-    if constexpr (BIAS) lds = bias_lds_bytes(b, a.G, b.part != nullptr);
+    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, b.part != nullptr);
     if (a.D <= 64) {
         if (narrow)
             attention_dq_kernel<T, 64, BIAS ? 32 : 64, k16, BIAS><<<q, 256, lds, s>>>(a, b);
@@ -1773,12 +1791,12 @@ static void backward_q(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t 
 }
 
 // grad_k and grad_v, from the statistics.
-template <class T, bool BIAS>
+template <class T, BiasFrom BIAS>
 static void backward_kv(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk * a.k_splits));
     size_t lds = 0;
-    if constexpr (BIAS) lds = bias_lds_bytes(b, a.G, false);
+    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, false);
     if (a.sink_part && a.qs.rows > 0) {
         const dim3 c((unsigned)(row_slots(a.qs, 1, a.sink_shift) * a.Hk));
         if (a.D <= 64)

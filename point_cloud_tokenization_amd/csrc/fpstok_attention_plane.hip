@@ -1,0 +1,92 @@
+// Attention with a learned bias whose pairs' entries are found once for all heads:
+// the plane that holds them, and the kernels that read it.
+#include "fpstok_attention_bias.h"
+
+namespace fpstok {
+
+// The plane of the pairs' entries: a workgroup takes 32 queries of a sequence, a
+// thread a key at a time, up to the end of the last 32 keys (the last key again
+// past the end, so every place that a block of 32 x 32 pairs reads holds an entry).
+__global__ __launch_bounds__(256) void bias_plane_kernel(AttnArgs a, BiasArgs b) {
+    __shared__ uint32_t own[kMaxAxes][32];
+    const int tid = threadIdx.x;
+    int64_t q0, k0, tile;
+    int tq, tk, seq;
+    const uint32_t slot = blockIdx.x;
+    if (a.qs.cu) {
+        seq = find_seq(a.qs, slot, 1, 5, q0, tq, tile);
+        if (tile < 0) return;
+    } else {
+        const uint32_t per = (uint32_t)((a.qs.cap + 31) >> 5);
+        seq = (int)(slot / per);
+        tile = slot % per;
+        seq_rows(a.qs, seq, q0, tq);
+    }
+    const int64_t left = tq - (tile << 5);
+    if (a.same_seqs)
+        k0 = q0, tk = tq;
+    else
+        seq_rows(a.ks, seq, k0, tk);
+    if (left <= 0 || tk <= 0 || tk > b.pitch) return;
+    const int rows = left < 32 ? (int)left : 32;
+    const int64_t row0 = q0 + (tile << 5);
+    for (int i = tid; i < 32 * kMaxAxes; i += 256) {
+        const int r = i & 31, axis = i >> 5;
+        if (axis < b.axes && r < rows) {
+            const uint32_t x = ((const uint32_t*)b.q_pos)[(row0 + r) * b.axes + axis];
+            own[axis][r] =
+                b.ints ? x : __float_as_uint(__uint_as_float(x) * pick(b.rate, axis));
+        }
+    }
+    __syncthreads();
+    // 64 keys and every 4th row a wave
+    const int lane = tid & 63, wave = tid >> 6;
+    for (int j = lane; j < ((tk + 31) & ~31); j += 64) {
+        uint32_t key[kMaxAxes];
+#pragma unroll
+        for (int axis = 0; axis < kMaxAxes; ++axis) {
+            if (axis >= b.axes) break;
+            const uint32_t x =
+                ((const uint32_t*)b.k_pos)[(k0 + (j < tk ? j : tk - 1)) * b.axes + axis];
+            key[axis] = b.ints ? x : __float_as_uint(__uint_as_float(x) * b.rate[axis]);
+        }
+        for (int r = wave; r < rows; r += 4) {
+            uint32_t entries = 0;
+#pragma unroll
+            for (int axis = 0; axis < kMaxAxes; ++axis) {
+                if (axis >= b.axes) break;
+                by_kind(b.ints, b.log_shift[axis] >= 0, [&](auto ints, auto log) {
+                    const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                        key[axis], own[axis][r], b.rate[axis], b.shift[axis], b.top[axis],
+                        b.log_shift[axis]);
+                    entries |= (uint32_t)(b.first[axis] + bucket) << (8 * axis + 2);
+                });
+            }
+            b.plane[(row0 + r) * b.pitch + j] = entries;
+        }
+    }
+}
+
+static void fill_plane(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
+    if (!b.plane || a.qs.rows == 0) return;
+    bias_plane_kernel<<<dim3((unsigned)row_slots(a.qs, 1, 5)), 256, 0, s>>>(a, b);
+}
+
+int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len) {
+    if (few || b.entries > kTableEntries || a.H < 4 || k_len > 1024) return 0;
+    // a window that hides most pairs of the plane
+    if (a.left >= 0 && a.right >= 0 && 4 * ((int64_t)a.left + a.right + 1) < k_len) return 0;
+    return (k_len + 31) & ~31;
+}
+
+hipError_t launch_plane(const AttnArgs& a, const BiasArgs& b, const AttnPlan& plan, hipStream_t s) {
+    fill_plane(a, b, s);
+    return launch<kPlane>(a, b, plan, s);
+}
+
+hipError_t launch_plane_backward(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
+    fill_plane(a, b, s);
+    return launch_backward<kPlane>(a, b, s);
+}
+
+}  // namespace fpstok

@@ -15,19 +15,25 @@
 
 namespace fpstok {
 
+// Where a kernel's scores get their bias from.
+enum BiasFrom {
+    kNoBias,
+    kPositions,  // every head finds the pairs' entries itself
+    kPlane       // they were found once for all heads (bias_plane_kernel)
+};
 struct NoBias {};
-template <bool BIAS>
-using BiasParam = std::conditional_t<BIAS, BiasArgs, NoBias>;
+template <BiasFrom BIAS>
+using BiasParam = std::conditional_t<BIAS != kNoBias, BiasArgs, NoBias>;
 
 // Positions of a tile's rows in LDS, and of the rows across the lanes: float32
 // times the axis's rate, or the int32 as they are.  [axis][row]
-template <bool BIAS, int OWN, int ROWS>
+template <BiasFrom BIAS, int OWN, int ROWS>
 struct BiasPos {
     uint32_t own[kMaxAxes][OWN];
     uint32_t tile[2][kMaxAxes][ROWS];
 };
 template <int OWN, int ROWS>
-struct BiasPos<false, OWN, ROWS> {};
+struct BiasPos<kNoBias, OWN, ROWS> {};
 
 // The element of a small array in registers at a place that is the same in
 // every lane.
@@ -156,6 +162,29 @@ __device__ __forceinline__ void add_entries(f32x16& s, const u32x16& entries, in
             s[e] += *(const FPSTOK_LDS float*)((const FPSTOK_LDS char*)table +
                                                (entries[e] >> 8 * a & 255u));
     }
+}
+
+// Entries of a block's pairs as the plane would hold them (places as for add_bias).
+template <bool KEY, int OWN, int ROWS>
+__device__ __forceinline__ u32x16 find_entries(const BiasArgs& b, const FPSTOK_LDS uint32_t* own,
+                                               const FPSTOK_LDS uint32_t* tile) {
+    u32x16 entries = 0;
+#pragma unroll 1
+    for (int a = 0; a < b.axes; ++a) {
+        const uint32_t mine = own[a * OWN];
+        const int first = pick(b.first, a), top = pick(b.top, a), shift = pick(b.log_shift, a);
+        const float rate = pick(b.rate, a), zero = pick(b.shift, a);
+        by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t other = tile[a * ROWS + (e >> 2) * 8 + (e & 3)];
+                const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                    KEY ? mine : other, KEY ? other : mine, rate, zero, top, shift);
+                entries[e] |= (uint32_t)(first + bucket) << (8 * a + 2);
+            }
+        });
+    }
+    return entries;
 }
 
 // Adds the bias of a block of 32 x 32 pairs to its scores (in units of log2): a
