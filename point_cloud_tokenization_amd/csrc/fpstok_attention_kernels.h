@@ -403,11 +403,24 @@ struct BiasTile {
     const FPSTOK_LDS float* table;  // of head `head` of the group
     bool planed;                    // the sequence's entries are in the plane
     PosStage<ROWS, THREADS> stage;
+    const float* from;  // the group's tables, and how many values they are
+    int size;
+    float first;  // this thread's value of the first 256
     __device__ __forceinline__ BiasTile(const BiasArgs& b, int hk, int G, int head, int tk, int tid)
         : planed(BIAS == kPlane && tk <= b.pitch), stage(b, tid % THREADS) {
+        table = (const FPSTOK_LDS float*)bias_lds() + head * b.entries;
+        from = b.table + (int64_t)hk * G * b.entries;
+        size = G * b.entries;
+        first = from[tid < size ? tid : 0];
+    }
+    // Writes the tables to LDS, in units of log2; -1e30 and less hides a pair.
+    // (Their load is on its way since the constructor.)
+    __device__ __forceinline__ void finish(int tid) const {
         float* lds = bias_lds();
-        load_table(b, lds, hk, G, tid);
-        table = (const FPSTOK_LDS float*)lds + head * b.entries;
+        for (int i = tid; i < size; i += 256) {
+            const float x = i < 256 ? first : from[i];
+            lds[i] = x <= -1e30f ? -INFINITY : x * kLog2e;
+        }
     }
 };
 template <int ROWS, int THREADS>
@@ -427,13 +440,31 @@ __device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
     return x;
 }
 
-// The same, or, of a sequence that is longer than the plane, found here.
-template <int BN>
-__device__ __forceinline__ u32x16 plane_entries(const BiasArgs& b, bool planed, const uint32_t* p,
-                                                const FPSTOK_LDS uint32_t* own,
-                                                const FPSTOK_LDS uint32_t* tile) {
-    return planed ? load_entries(p) : find_entries<false, 128, BN>(b, own, tile);
-}
+// The entries of a walk's blocks, each called for one block ahead (a load and its
+// use in one block would wait for memory every time); of a sequence that is longer
+// than the plane they are found where they are used.
+struct EntryWalk {
+    const uint32_t* row;  // key 4 half of the query
+    u32x16 next;
+    int at = -1, last = 0;  // the block called for, and the last there is
+    __device__ __forceinline__ void begin(bool planed, int j) {
+        if (!planed || j > last) return;
+        at = j;
+        next = load_entries(row + j);
+    }
+    // Of the keys j .. j + 31; then_j: the block that may come next.
+    template <int BN>
+    __device__ __forceinline__ u32x16 take(const BiasArgs& b, bool planed, int j, int then_j,
+                                           const FPSTOK_LDS uint32_t* own,
+                                           const FPSTOK_LDS uint32_t* tile) {
+        if (!planed) return find_entries<false, 128, BN>(b, own, tile);
+        if (j != at) next = load_entries(row + j);
+        const u32x16 now = next;
+        at = then_j <= last ? then_j : last;
+        next = load_entries(row + at);
+        return now;
+    }
+};
 
 // The sums of dS and of the weights of a row by entry: [wave][entry][lane & 31]
 // behind the tables in LDS; one entry more takes those that are another launch's.
@@ -530,34 +561,54 @@ struct TableSums {
         wave_sync();
     }
     // The workgroup's part: per head of the group and entry, the rows' sums of dS
-    // less `off` (what dS of all the row's keys is off 0 by) times its weights', in a fixed
-    // order that starts elsewhere in every thread (threads of one entry after another
-    // would all read one bank).  A row whose dS is not finite has an `off` that is
-    // not: nor are the entries it adds to.
+    // less `off` (what dS of all the row's keys is off 0 by) times its weights'.  As many
+    // threads to an entry as there are, each with every so manieth row of it, from one
+    // that is elsewhere in every thread on (threads of one entry after another would all
+    // read one bank): the order is fixed.  A row whose dS is not finite has an `off` that
+    // is not: nor are the entries it adds to.
     __device__ __forceinline__ void store(const BiasArgs& b, int G, const RowTile& t, float off,
                                           int row, int half, int tid) const {
-        __shared__ float2 rows[128];  // off and cap
-        if (half == 0) rows[row] = make_float2(off, __uint_as_float(cap));
+        __shared__ float2 rows[128];  // off and cap, in the units of the sums
+        __shared__ float parts[256];
+        if (half == 0)
+            rows[row] = make_float2(off * 0x1p-25f, __uint_as_float(cap) * 0x1p-35f);
         __syncthreads();
-        float* part = b.part + (int64_t)blockIdx.x * G * b.count;
-        for (int i = tid; i < G * b.count; i += 256) {
-            const int g = i / b.count, e = i - g * b.count;
-            // rows of the tile in this head: the first, and every G-th after it
-            const int first = (int)((uint32_t)(g + G - t.row0 % G) % (uint32_t)G);
-            const int n = first < t.rows ? (t.rows - first - 1) / G + 1 : 0;
-            double sum = 0.0;
-            int x = n > 0 ? tid % n : 0;
-            for (int k = 0; k < n; ++k) {
-                const int r = first + x * G;
-                const u64 s = all[((r >> 5) * slots + e) * 32 + (r & 31)];
-                const float2 row_is = rows[r];
-                const double value = (double)((long long)s >> kWeightBits) *
-                                     ((double)row_is.y * 0x1p-35);
-                const double weight = (double)(uint32_t)(s & ((1u << kWeightBits) - 1)) * 0x1p-25;
-                if (s != 0) sum += value - (double)row_is.x * weight;
-                if (++x == n) x = 0;
+        const uint32_t all_entries = (uint32_t)(G * b.count);
+        const uint32_t share = all_entries < 256u ? 256u / all_entries : 1u;
+        float* part = b.part + (int64_t)blockIdx.x * all_entries;
+        for (uint32_t i0 = 0; i0 < all_entries; i0 += 256) {
+            const uint32_t mine = (uint32_t)tid / share, p = (uint32_t)tid - mine * share;
+            const uint32_t i = i0 + mine;
+            float sum = 0.0f;
+            if (i < all_entries) {
+                const int g = (int)(i / (uint32_t)b.count), e = (int)i - g * b.count;
+                // rows of the tile in this head: the first, and every G-th after it
+                const int first = (int)((uint32_t)(g + G - t.row0 % G) % (uint32_t)G);
+                const int in_head = first < t.rows ? (t.rows - first - 1) / G + 1 : 0;
+                const int n = in_head > (int)p ? (in_head - (int)p - 1) / (int)share + 1 : 0;
+                int x = n > 0 ? tid % n : 0;
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) {
+                    const int r = first + ((int)p + x * (int)share) * G;
+                    const u64 s = all[((r >> 5) * slots + e) * 32 + (r & 31)];
+                    const float2 is = rows[r];
+                    // (38 bits: 32 and 6, joined in one rounding)
+                    const float value =
+                        __builtin_fmaf((float)(int)(s >> 32), 64.0f,
+                                       (float)((uint32_t)s >> kWeightBits));
+                    const float weight = (float)((uint32_t)s & ((1u << kWeightBits) - 1));
+                    const float term = __builtin_fmaf(-is.x, weight, value * is.y);
+                    sum += s != 0 ? term : 0.0f;
+                    if (++x == n) x = 0;
+                }
             }
-            part[i] = (float)sum;
+            parts[tid] = sum;
+            __syncthreads();
+            if (p == 0 && i < all_entries) {
+                for (uint32_t k = 1; k < share; ++k) sum += parts[tid + k];
+                part[i] = sum;
+            }
+            __syncthreads();
         }
     }
 };
@@ -605,11 +656,14 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
     BiasTile<BIAS, BN> scores(bias, t.hk, G, q.h - t.hk * G, t.tk, tid);
-    const uint32_t* entry_row = nullptr;
+    EntryWalk walk;
     if constexpr (BIAS != kNoBias) {
-        own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
-        if (BIAS == kPlane)
-            entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+        if (!scores.planed)
+            own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
+        if (BIAS == kPlane) {
+            walk.row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+            walk.last = (t.tk - 1) & ~31;
+        }
     }
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
@@ -632,13 +686,17 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
         dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
-        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
+        if constexpr (BIAS != kNoBias) {
+            if (!scores.planed) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
+        }
     };
     const View<BN> all(a, q.pa, q.pb, t.tk);
     const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {  // this wave's part of it is there
         dma_wait();
-        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos.tile[i & 1]);
+        if constexpr (BIAS != kNoBias) {
+            if (!scores.planed) scores.stage.store(bias, pos.tile[i & 1]);
+        }
         // a value that some row must not see meets a weight of 0 there: an
         // infinite one has to leave the product
         if (all.of(a, jn) == 1) {
@@ -664,8 +722,8 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             f32x16 x = 0.0f;
             u32x16 entries;
             if constexpr (BIAS == kPlane)
-                entries = plane_entries<BN>(
-                    bias, scores.planed, entry_row + j0 + b * 32,
+                entries = walk.take<BN>(
+                    bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
                     (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
 #pragma unroll
@@ -700,10 +758,10 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     bad.clear(tid);
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
-    if (n > 0) {
-        load(0);
-        arrive(0);
-    }
+    if (n > 0) load(0);
+    if constexpr (BIAS == kPlane) walk.begin(scores.planed, jn);
+    if constexpr (BIAS != kNoBias) scores.finish(tid);
+    if (n > 0) arrive(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int j0 = jn;
@@ -812,6 +870,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const float cs = a.scale * kLog2e, c = BIAS ? 1.0f : cs;
     if (wave < n) load(wave);
     bad.clear(tid);
+    if constexpr (BIAS != kNoBias) scores.finish(tid);
     __syncthreads();
     for (int i = wave; i < n; i += 4) {
         const int j0 = kt.tile(i) * BN;
@@ -991,11 +1050,14 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const bool wave_live = wave * 32 < t.rows;
     BiasTile<BIAS, BN> scores(bias, t.hk, a.G, q.h - t.hk * a.G, t.tk, tid);
     TableSums<BIAS> sums(bias, a.G, wave, lane, tid);
-    const uint32_t* entry_row = nullptr;
+    EntryWalk walk;
     if constexpr (BIAS != kNoBias) {
-        own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
-        if (BIAS == kPlane)
-            entry_row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+        if (!scores.planed)
+            own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
+        if (BIAS == kPlane) {
+            walk.row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+            walk.last = (t.tk - 1) & ~31;
+        }
     }
     Frag qf[STEPS], gf[STEPS], of[STEPS];
     q.load<T, STEPS>(qf, a.q, a.D, half);
@@ -1023,13 +1085,17 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         dma.load(kp, off_k, a.k.row, t.tk - jn, buf, wave);
         dma.load(vp, off_v, a.v.row, t.tk - jn, buf + BN * Tl::kPitch, wave);
-        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
+        if constexpr (BIAS != kNoBias) {
+            if (!scores.planed) scores.stage.load(bias, bias.k_pos, t.k0 + jn, t.tk - jn);
+        }
     };
     const View<BN> all(a, q.pa, q.pb, t.tk);
     const View<32> mine(a, q.wa, q.wb, t.tk);
     auto arrive = [&](int i) {
         dma_wait();
-        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos.tile[i & 1]);
+        if constexpr (BIAS != kNoBias) {
+            if (!scores.planed) scores.stage.store(bias, pos.tile[i & 1]);
+        }
         if (all.of(a, jn) != 1) return;
         FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BN * Tl::kPitch;
         const uint32_t chunks = dma.clean(buf, tid);
@@ -1067,8 +1133,8 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if constexpr (BIAS != kNoBias) {
             x *= cs;
             if constexpr (BIAS == kPlane)
-                add_entries(x, plane_entries<BN>(
-                bias, scores.planed, entry_row + j0 + b,
+                add_entries(x, walk.take<BN>(
+                bias, scores.planed, j0 + b, j0 + b + 32,
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]), bias.axes, scores.table);
             else
@@ -1089,8 +1155,8 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
         u32x16 entries;
-        if constexpr (BIAS == kPlane) entries = plane_entries<BN>(
-                bias, scores.planed, entry_row + j0 + b * 32,
+        if constexpr (BIAS == kPlane) entries = walk.take<BN>(
+                bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
 #pragma unroll
@@ -1145,6 +1211,8 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     if (a.D < DP) dma.zero(lds, sizeof(smem), tid);
     __syncthreads();
     if (n > 0) load(0);
+    if constexpr (BIAS == kPlane) walk.begin(scores.planed, jn);
+    if constexpr (BIAS != kNoBias) scores.finish(tid);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -1284,7 +1352,10 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     FPSTOK_LDS char* gbuf = qbuf + kTile;
     const float cs = a.scale * kLog2e;
     BiasTile<BIAS, 32, 64> scores(bias, hk, G, 0, tk, tid);
-    if constexpr (BIAS != kNoBias) __syncthreads();
+    if constexpr (BIAS != kNoBias) {
+        scores.finish(tid);
+        __syncthreads();
+    }
 
     for (int s0 = 0; s0 < sinks; s0 += 32) {
         const int j = s0 + (lane & 31);
@@ -1451,7 +1522,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     BiasTile<BIAS, BQ> scores(bias, t.hk, G, 0, t.tk, tid);
     const uint32_t* entry_col = nullptr;
     if constexpr (BIAS != kNoBias) {
-        own_positions(bias, pos.own, r, bias.k_pos, krow, live, half);
+        if (!scores.planed) own_positions(bias, pos.own, r, bias.k_pos, krow, live, half);
         if (BIAS == kPlane)
             entry_col = bias.plane + t.q0 * bias.pitch + (live ? t.row0 + r : 0);
     }
@@ -1539,11 +1610,15 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             dma4(src, (uint32_t)(lane < rows ? lane : rows - 1) * 4u,
                  (uint32_t)(uintptr_t)(FPSTOK_LDS float*)stat[i & 1][wave]);
         }
-        if constexpr (BIAS != kNoBias) scores.stage.load(bias, bias.q_pos, t.q0 + xn, rows);
+        if constexpr (BIAS != kNoBias) {
+            if (!scores.planed) scores.stage.load(bias, bias.q_pos, t.q0 + xn, rows);
+        }
     };
     auto arrive = [&](int i) {
         dma_wait();
-        if constexpr (BIAS != kNoBias) scores.stage.store(bias, pos.tile[i & 1]);
+        if constexpr (BIAS != kNoBias) {
+            if (!scores.planed) scores.stage.store(bias, pos.tile[i & 1]);
+        }
         if (!tile_all.has(xn)) {
             FPSTOK_LDS char* buf = lds + (i & 1) * 2 * BQ * Tl::kPitch;
             // (a query with infinite elements has no finite score: its weights are
@@ -1637,8 +1712,9 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                        dma_v.offset(a.v.row), a.v.row, t.rows, lds + kV, wave);
         }
         load(0);
-        arrive(0);
     }
+    if constexpr (BIAS != kNoBias) scores.finish(tid);
+    if (n > 0) arrive(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
         const int x0 = xn, head = group_n;

@@ -4,45 +4,35 @@
 
 namespace fpstok {
 
-// The plane of the pairs' entries: a workgroup takes 32 queries of a sequence, a
+// The plane of the pairs' entries: a workgroup takes 16 queries of a sequence, a
 // thread a key at a time, up to the end of the last 32 keys (the last key again
 // past the end, so every place that a block of 32 x 32 pairs reads holds an entry).
 __global__ __launch_bounds__(256) void bias_plane_kernel(AttnArgs a, BiasArgs b) {
-    __shared__ uint32_t own[kMaxAxes][32];
+    __shared__ uint32_t own[kMaxAxes][16];
     const int tid = threadIdx.x;
     int64_t q0, k0, tile;
     int tq, tk, seq;
     const uint32_t slot = blockIdx.x;
     if (a.qs.cu) {
-        seq = find_seq(a.qs, slot, 1, 5, q0, tq, tile);
+        seq = find_seq(a.qs, slot, 1, 4, q0, tq, tile);
         if (tile < 0) return;
     } else {
-        const uint32_t per = (uint32_t)((a.qs.cap + 31) >> 5);
+        const uint32_t per = (uint32_t)((a.qs.cap + 15) >> 4);
         seq = (int)(slot / per);
         tile = slot % per;
         seq_rows(a.qs, seq, q0, tq);
     }
-    const int64_t left = tq - (tile << 5);
+    const int64_t left = tq - (tile << 4);
     if (a.same_seqs)
         k0 = q0, tk = tq;
     else
         seq_rows(a.ks, seq, k0, tk);
     if (left <= 0 || tk <= 0 || tk > b.pitch) return;
-    const int rows = left < 32 ? (int)left : 32;
-    const int64_t row0 = q0 + (tile << 5);
-    for (int i = tid; i < 32 * kMaxAxes; i += 256) {
-        const int r = i & 31, axis = i >> 5;
-        if (axis < b.axes && r < rows) {
-            const uint32_t x = ((const uint32_t*)b.q_pos)[(row0 + r) * b.axes + axis];
-            own[axis][r] =
-                b.ints ? x : __float_as_uint(__uint_as_float(x) * pick(b.rate, axis));
-        }
-    }
-    __syncthreads();
-    // 64 keys and every 4th row a wave
-    const int lane = tid & 63, wave = tid >> 6;
-    for (int j = lane; j < ((tk + 31) & ~31); j += 64) {
-        uint32_t key[kMaxAxes];
+    const int rows = left < 16 ? (int)left : 16;
+    const int64_t row0 = q0 + (tile << 4);
+    const int keys = (tk + 31) & ~31;
+    uint32_t key[kMaxAxes];
+    auto load_key = [&](int j) {
 #pragma unroll
         for (int axis = 0; axis < kMaxAxes; ++axis) {
             if (axis >= b.axes) break;
@@ -50,26 +40,45 @@ __global__ __launch_bounds__(256) void bias_plane_kernel(AttnArgs a, BiasArgs b)
                 ((const uint32_t*)b.k_pos)[(k0 + (j < tk ? j : tk - 1)) * b.axes + axis];
             key[axis] = b.ints ? x : __float_as_uint(__uint_as_float(x) * b.rate[axis]);
         }
-        for (int r = wave; r < rows; r += 4) {
-            uint32_t entries = 0;
+    };
+    load_key(tid);
+    if (tid < 16 * kMaxAxes) {
+        const int r = tid & 15, axis = tid >> 4;
+        if (axis < b.axes && r < rows) {
+            const uint32_t x = ((const uint32_t*)b.q_pos)[(row0 + r) * b.axes + axis];
+            own[axis][r] =
+                b.ints ? x : __float_as_uint(__uint_as_float(x) * pick(b.rate, axis));
+        }
+    }
+    __syncthreads();
+    for (int j = tid; j < keys; j += 256) {
+        if (j != tid) load_key(j);
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 4) {
+            uint32_t entries[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int axis = 0; axis < kMaxAxes; ++axis) {
                 if (axis >= b.axes) break;
                 by_kind(b.ints, b.log_shift[axis] >= 0, [&](auto ints, auto log) {
-                    const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
-                        key[axis], own[axis][r], b.rate[axis], b.shift[axis], b.top[axis],
-                        b.log_shift[axis]);
-                    entries |= (uint32_t)(b.first[axis] + bucket) << (8 * axis + 2);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                            key[axis], own[axis][r0 + r], b.rate[axis], b.shift[axis], b.top[axis],
+                            b.log_shift[axis]);
+                        entries[r] |= (uint32_t)(b.first[axis] + bucket) << (8 * axis + 2);
+                    }
                 });
             }
-            b.plane[(row0 + r) * b.pitch + j] = entries;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r0 + r < rows) b.plane[(row0 + r0 + r) * b.pitch + j] = entries[r];
         }
     }
 }
 
 static void fill_plane(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
     if (!b.plane || a.qs.rows == 0) return;
-    bias_plane_kernel<<<dim3((unsigned)row_slots(a.qs, 1, 5)), 256, 0, s>>>(a, b);
+    bias_plane_kernel<<<dim3((unsigned)row_slots(a.qs, 1, 4)), 256, 0, s>>>(a, b);
 }
 
 int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len) {

@@ -90,15 +90,6 @@ __device__ __forceinline__ void own_positions(const BiasArgs& b, uint32_t (*own)
     }
 }
 
-// The group's tables in LDS, in units of log2; -1e30 and less hides a pair.
-__device__ __forceinline__ void load_table(const BiasArgs& b, float* lds, int hk, int G, int tid) {
-    const float* from = b.table + (int64_t)hk * G * b.entries;
-    for (int i = tid; i < G * b.entries; i += 256) {
-        const float x = from[i];
-        lds[i] = x <= -1e30f ? -INFINITY : x * 1.44269504088896f;
-    }
-}
-
 // LDS that the launch adds to a kernel's own: the tables, then the sums of
 // their gradients.
 __device__ __forceinline__ float* bias_lds() {
