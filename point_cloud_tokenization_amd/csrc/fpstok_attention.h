@@ -67,10 +67,15 @@ struct BiasArgs {
     int32_t from, count;
     float* grad;  // [H][entries], or null
     float* part;
-    // the pairs' entries, found once for all heads: 4 times the entry of axis a in
-    // byte a of plane[q row * pitch + key], for sequences of up to `pitch` keys
+    // the pairs' entries, found once for all heads, at [q row * pitch + key] for
+    // sequences of up to `pitch` keys.  plane: two axes at a time, in bytes of a table of
+    // their sums ([bucket of the first * buckets of the second + that of the second]):
+    // axes 0 and 1 in the lower half of a word, 2 and 3, behind them in the table, in the
+    // upper one.  bytes: 4 times the entry of axis a in byte a (for the gradient).
     uint32_t* plane;  // null: every head finds its own
+    uint32_t* bytes;
     int32_t pitch;
+    int32_t joint[2];  // sizes of the two tables of sums
 };
 constexpr int kGroupEntries = 4096;  // table entries of one key head's query heads (16 KB of LDS)
 constexpr int kTableEntries = 64;  // entries whose gradients one launch forms

@@ -173,6 +173,8 @@ static fpstok_status check_bias(const fpstok_rel_bias* r, const fpstok_attn_para
         b.entries += r->buckets[i];
     }
     b.count = b.entries;
+    for (int i = 0; i < b.axes; i += 2)
+        b.joint[i / 2] = r->buckets[i] * (i + 1 < b.axes ? r->buckets[i + 1] : 1);
     if ((int64_t)(p->num_heads / p->num_kv_heads) * b.entries > kGroupEntries)
         return fail(FPSTOK_EUNSUPPORTED, "query heads per key head times buckets > %d",
                     kGroupEntries);
@@ -198,8 +200,13 @@ static size_t lay_out(const fpstok_seqs* qs, const fpstok_seqs* ks, bool backwar
     char* at = (char*)ws;
     if (!backward) plan = plan_attention(a, likely_len(qs), likely_len(ks));
     if (b && (b->pitch = plan_plane(a, *b, !backward && plan.few, likely_len(ks))) > 0) {
+        const size_t bytes = align256((size_t)qs->num_rows * b->pitch * sizeof(uint32_t));
         b->plane = (uint32_t*)at;
-        at += align256((size_t)qs->num_rows * b->pitch * sizeof(uint32_t));
+        at += bytes;
+        if (backward) {
+            b->bytes = (uint32_t*)at;
+            at += bytes;
+        }
     }
     const size_t plane = (size_t)(at - (char*)ws);
     if (backward) {

@@ -398,33 +398,48 @@ __device__ __forceinline__ float log_sum(float mc, float l) {
 // What a workgroup needs to form its scores' bias: the group's tables in LDS
 // (behind the kernel's own, in what the launch adds to it) and the positions of the
 // walk's next tile.
-template <BiasFrom BIAS, int ROWS, int THREADS = 256>
+// JOINT: the tables are of the sums of two axes' values (one load of LDS for both).
+template <BiasFrom BIAS, int ROWS, int THREADS = 256, bool JOINT = false>
 struct BiasTile {
     const FPSTOK_LDS float* table;  // of head `head` of the group
     bool planed;                    // the sequence's entries are in the plane
     PosStage<ROWS, THREADS> stage;
-    const float* from;  // the group's tables, and how many values they are
-    int size;
-    float first;  // this thread's value of the first 256
+    const float* from;  // the group's tables
+    int size;           // values of them in LDS
+    float2 first;       // what this thread's first one is made of
     __device__ __forceinline__ BiasTile(const BiasArgs& b, int hk, int G, int head, int tk, int tid)
         : planed(BIAS == kPlane && tk <= b.pitch), stage(b, tid % THREADS) {
-        table = (const FPSTOK_LDS float*)bias_lds() + head * b.entries;
+        table = (const FPSTOK_LDS float*)bias_lds() + head * table_size(b, JOINT);
         from = b.table + (int64_t)hk * G * b.entries;
-        size = G * b.entries;
-        first = from[tid < size ? tid : 0];
+        size = G * table_size(b, JOINT);
+        first = value(b, tid < size ? tid : 0);
+    }
+    // The one or two table values that make the i-th value in LDS.
+    __device__ __forceinline__ float2 value(const BiasArgs& b, int i) const {
+        if constexpr (!JOINT) return make_float2(from[i], 0.0f);
+        const int per = table_size(b, true), g = (int)((uint32_t)i / (uint32_t)per);
+        int x = i - g * per;
+        const int behind = x >= b.joint[0];
+        x -= behind ? b.joint[0] : 0;
+        const int a = 2 * behind, n = a + 1 < b.axes ? (behind ? b.top[3] : b.top[1]) + 1 : 1;
+        const int b0 = (int)((uint32_t)x / (uint32_t)n), b1 = x - b0 * n;
+        const float* t = from + g * b.entries;
+        const int at0 = behind ? b.first[2] : 0, at1 = behind ? b.first[3] : b.first[1];
+        return make_float2(t[at0 + b0], a + 1 < b.axes ? t[at1 + b1] : 0.0f);
     }
     // Writes the tables to LDS, in units of log2; -1e30 and less hides a pair.
     // (Their load is on its way since the constructor.)
-    __device__ __forceinline__ void finish(int tid) const {
+    __device__ __forceinline__ void finish(const BiasArgs& b, int tid) const {
         float* lds = bias_lds();
         for (int i = tid; i < size; i += 256) {
-            const float x = i < 256 ? first : from[i];
-            lds[i] = x <= -1e30f ? -INFINITY : x * kLog2e;
+            const float2 x = i < 256 ? first : value(b, i);
+            const float y = x.x <= -1e30f ? -INFINITY : x.x * kLog2e;
+            lds[i] = JOINT ? y + (x.y <= -1e30f ? -INFINITY : x.y * kLog2e) : y;
         }
     }
 };
-template <int ROWS, int THREADS>
-struct BiasTile<kNoBias, ROWS, THREADS> {
+template <int ROWS, int THREADS, bool JOINT>
+struct BiasTile<kNoBias, ROWS, THREADS, JOINT> {
     __device__ __forceinline__ BiasTile(const NoBias&, int, int, int, int, int) {}
 };
 
@@ -453,11 +468,11 @@ struct EntryWalk {
         next = load_entries(row + j);
     }
     // Of the keys j .. j + 31; then_j: the block that may come next.
-    template <int BN>
+    template <bool JOINT, int BN>
     __device__ __forceinline__ u32x16 take(const BiasArgs& b, bool planed, int j, int then_j,
                                            const FPSTOK_LDS uint32_t* own,
                                            const FPSTOK_LDS uint32_t* tile) {
-        if (!planed) return find_entries<false, 128, BN>(b, own, tile);
+        if (!planed) return find_entries<JOINT, false, 128, BN>(b, own, tile);
         if (j != at) next = load_entries(row + j);
         const u32x16 now = next;
         at = then_j <= last ? then_j : last;
@@ -655,7 +670,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     q.load<T, STEPS>(qf, a.q, a.D, half);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
-    BiasTile<BIAS, BN> scores(bias, t.hk, G, q.h - t.hk * G, t.tk, tid);
+    BiasTile<BIAS, BN, 256, BIAS == kPlane> scores(bias, t.hk, G, q.h - t.hk * G, t.tk, tid);
     EntryWalk walk;
     if constexpr (BIAS != kNoBias) {
         if (!scores.planed)
@@ -722,7 +737,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             f32x16 x = 0.0f;
             u32x16 entries;
             if constexpr (BIAS == kPlane)
-                entries = walk.take<BN>(
+                entries = walk.take<true, BN>(
                     bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
                     (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
@@ -733,7 +748,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if constexpr (BIAS != kNoBias) {
                 x *= cs;
                 if constexpr (BIAS == kPlane)
-                    add_entries(x, entries, bias.axes, scores.table);
+                    add_entries<true>(x, entries, bias.axes, scores.table);
                 else
                     add_bias<false, false, 128, BN>(
                         x, nullptr, bias, scores.table,
@@ -760,7 +775,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     __syncthreads();
     if (n > 0) load(0);
     if constexpr (BIAS == kPlane) walk.begin(scores.planed, jn);
-    if constexpr (BIAS != kNoBias) scores.finish(tid);
+    if constexpr (BIAS != kNoBias) scores.finish(bias, tid);
     if (n > 0) arrive(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
@@ -870,7 +885,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const float cs = a.scale * kLog2e, c = BIAS ? 1.0f : cs;
     if (wave < n) load(wave);
     bad.clear(tid);
-    if constexpr (BIAS != kNoBias) scores.finish(tid);
+    if constexpr (BIAS != kNoBias) scores.finish(bias, tid);
     __syncthreads();
     for (int i = wave; i < n; i += 4) {
         const int j0 = kt.tile(i) * BN;
@@ -1055,7 +1070,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if (!scores.planed)
             own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
         if (BIAS == kPlane) {
-            walk.row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+            walk.row = bias.bytes + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
             walk.last = (t.tk - 1) & ~31;
         }
     }
@@ -1133,7 +1148,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if constexpr (BIAS != kNoBias) {
             x *= cs;
             if constexpr (BIAS == kPlane)
-                add_entries(x, walk.take<BN>(
+                add_entries<false>(x, walk.take<false, BN>(
                 bias, scores.planed, j0 + b, j0 + b + 32,
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]), bias.axes, scores.table);
@@ -1155,7 +1170,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
         u32x16 entries;
-        if constexpr (BIAS == kPlane) entries = walk.take<BN>(
+        if constexpr (BIAS == kPlane) entries = walk.take<false, BN>(
                 bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
@@ -1167,7 +1182,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if constexpr (BIAS != kNoBias) {
             x *= cs;
             if constexpr (BIAS == kPlane)
-                add_entries(x, entries, bias.axes, scores.table);
+                add_entries<false>(x, entries, bias.axes, scores.table);
             else
                 add_bias<false, true, 128, BN>(
                     x, &entries, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
@@ -1212,7 +1227,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     __syncthreads();
     if (n > 0) load(0);
     if constexpr (BIAS == kPlane) walk.begin(scores.planed, jn);
-    if constexpr (BIAS != kNoBias) scores.finish(tid);
+    if constexpr (BIAS != kNoBias) scores.finish(bias, tid);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -1353,7 +1368,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const float cs = a.scale * kLog2e;
     BiasTile<BIAS, 32, 64> scores(bias, hk, G, 0, tk, tid);
     if constexpr (BIAS != kNoBias) {
-        scores.finish(tid);
+        scores.finish(bias, tid);
         __syncthreads();
     }
 
@@ -1519,7 +1534,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     if constexpr (!kVLds)
         load_row<T, STEPS>(vf, (const T*)a.v.data + krow * a.v.row + t.hk * a.v.head, live,
                            (const T*)a.v.data, a.D, half);
-    BiasTile<BIAS, BQ> scores(bias, t.hk, G, 0, t.tk, tid);
+    BiasTile<BIAS, BQ, 256, BIAS == kPlane> scores(bias, t.hk, G, 0, t.tk, tid);
     const uint32_t* entry_col = nullptr;
     if constexpr (BIAS != kNoBias) {
         if (!scores.planed) own_positions(bias, pos.own, r, bias.k_pos, krow, live, half);
@@ -1649,7 +1664,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                     entries[e] = entry_col[(int64_t)(i < i1 ? i : i1) * bias.pitch];
                 }
             } else {
-                entries = find_entries<true, 128, BQ>(
+                entries = find_entries<true, true, 128, BQ>(
                     bias, (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
             }
@@ -1668,10 +1683,10 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if constexpr (BIAS != kNoBias) {
             x *= c;
             if constexpr (BIAS == kPlane)
-                add_entries(x, entries, bias.axes, scores.table + head * bias.entries);
+                add_entries<true>(x, entries, bias.axes, scores.table + head * table_size(bias, BIAS == kPlane));
             else
                 add_bias<true, false, 128, BQ>(
-                    x, nullptr, bias, scores.table + head * bias.entries,
+                    x, nullptr, bias, scores.table + head * table_size(bias, BIAS == kPlane),
                     (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
         }
@@ -1713,7 +1728,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         }
         load(0);
     }
-    if constexpr (BIAS != kNoBias) scores.finish(tid);
+    if constexpr (BIAS != kNoBias) scores.finish(bias, tid);
     if (n > 0) arrive(0);
     __syncthreads();
     for (int i = 0; i < n; ++i) {
@@ -1827,7 +1842,7 @@ static hipError_t forward(const AttnArgs& a, const BiasParam<BIAS>& b, const Att
     const int64_t blocks = row_slots(a.qs, a.G, plan.few ? 5 : 7) * a.Hk;
     const dim3 grid((unsigned)(blocks * a.splits));
     size_t lds = 0;
-    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, false);
+    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, BIAS == kPlane, false);
     if (BIAS != kPlane && plan.few) {
         if constexpr (BIAS != kPlane) {  // (few queries have no plane)
             if (a.D <= 64)
@@ -1852,7 +1867,7 @@ static void backward_q(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t 
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
     const bool narrow = k16 && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
     size_t lds = 0;
-    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, b.part != nullptr);
+    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, false, b.part != nullptr);
     if (a.D <= 64) {
         if (narrow)
             attention_dq_kernel<T, 64, BIAS ? 32 : 64, k16, BIAS><<<q, 256, lds, s>>>(a, b);
@@ -1871,14 +1886,17 @@ template <class T, BiasFrom BIAS>
 static void backward_kv(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t s) {
     constexpr bool k16 = sizeof(T) == 2;
     const dim3 k((unsigned)(row_slots(a.ks, 1, 7) * a.Hk * a.k_splits));
-    size_t lds = 0;
-    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, false);
+    size_t lds = 0, lds_sink = 0;
+    if constexpr (BIAS != kNoBias) {
+        lds = bias_lds_bytes(b, a.G, BIAS == kPlane, false);
+        lds_sink = bias_lds_bytes(b, a.G, false, false);
+    }
     if (a.sink_part && a.qs.rows > 0) {
         const dim3 c((unsigned)(row_slots(a.qs, 1, a.sink_shift) * a.Hk));
         if (a.D <= 64)
-            attention_sink_kernel<T, 64, BIAS><<<c, 256, lds, s>>>(a, b);
+            attention_sink_kernel<T, 64, BIAS><<<c, 256, lds_sink, s>>>(a, b);
         else
-            attention_sink_kernel<T, 128, BIAS><<<c, 256, lds, s>>>(a, b);
+            attention_sink_kernel<T, 128, BIAS><<<c, 256, lds_sink, s>>>(a, b);
     }
     if (a.ks.rows > 0) {
         if (a.D <= 64)

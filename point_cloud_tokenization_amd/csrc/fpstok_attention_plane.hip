@@ -31,17 +31,6 @@ __global__ __launch_bounds__(256) void bias_plane_kernel(AttnArgs a, BiasArgs b)
     const int rows = left < 16 ? (int)left : 16;
     const int64_t row0 = q0 + (tile << 4);
     const int keys = (tk + 31) & ~31;
-    uint32_t key[kMaxAxes];
-    auto load_key = [&](int j) {
-#pragma unroll
-        for (int axis = 0; axis < kMaxAxes; ++axis) {
-            if (axis >= b.axes) break;
-            const uint32_t x =
-                ((const uint32_t*)b.k_pos)[(k0 + (j < tk ? j : tk - 1)) * b.axes + axis];
-            key[axis] = b.ints ? x : __float_as_uint(__uint_as_float(x) * b.rate[axis]);
-        }
-    };
-    load_key(tid);
     if (tid < 16 * kMaxAxes) {
         const int r = tid & 15, axis = tid >> 4;
         if (axis < b.axes && r < rows) {
@@ -51,27 +40,39 @@ __global__ __launch_bounds__(256) void bias_plane_kernel(AttnArgs a, BiasArgs b)
         }
     }
     __syncthreads();
-    for (int j = tid; j < keys; j += 256) {
-        if (j != tid) load_key(j);
-#pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 4) {
-            uint32_t entries[4] = {0, 0, 0, 0};
+    // 4 rows and every 64th key a wave
+    const int r0 = tid >> 6 << 2;
+    if (r0 >= rows) return;
+    const uint32_t joint_base = entry_base<true>(b), bytes_base = entry_base<false>(b);
+    for (int j = tid & 63; j < keys; j += 64) {
+        uint32_t joint[4], bytes[4];
 #pragma unroll
-            for (int axis = 0; axis < kMaxAxes; ++axis) {
-                if (axis >= b.axes) break;
-                by_kind(b.ints, b.log_shift[axis] >= 0, [&](auto ints, auto log) {
+        for (int r = 0; r < 4; ++r) joint[r] = joint_base, bytes[r] = bytes_base;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
-                            key[axis], own[axis][r0 + r], b.rate[axis], b.shift[axis], b.top[axis],
-                            b.log_shift[axis]);
-                        entries[r] |= (uint32_t)(b.first[axis] + bucket) << (8 * axis + 2);
-                    }
-                });
-            }
+        for (int axis = 0; axis < kMaxAxes; ++axis) {
+            if (axis >= b.axes) break;
+            const uint32_t x =
+                ((const uint32_t*)b.k_pos)[(k0 + (j < tk ? j : tk - 1)) * b.axes + axis];
+            const uint32_t key =
+                b.ints ? x : __float_as_uint(__uint_as_float(x) * b.rate[axis]);
+            const uint32_t unit = entry_unit<true>(b, axis);
+            by_kind(b.ints, b.log_shift[axis] >= 0, [&](auto ints, auto log) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (r0 + r < rows) b.plane[(row0 + r0 + r) * b.pitch + j] = entries[r];
+                for (int r = 0; r < 4; ++r) {
+                    const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                        key, own[axis][r0 + r], b.rate[axis], b.shift[axis], b.top[axis],
+                        b.log_shift[axis]);
+                    joint[r] += (uint32_t)bucket * unit;
+                    bytes[r] += (uint32_t)bucket * entry_unit<false>(b, axis);
+                }
+            });
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (r0 + r >= rows) break;
+            const int64_t at = (row0 + r0 + r) * b.pitch + j;
+            b.plane[at] = joint[r];
+            if (b.bytes) b.bytes[at] = bytes[r];
         }
     }
 }
@@ -83,6 +84,7 @@ static void fill_plane(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
 
 int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len) {
     if (few || b.entries > kTableEntries || a.H < 4 || k_len > 1024) return 0;
+    if ((int64_t)a.G * table_size(b, true) > kGroupEntries) return 0;
     // a window that hides most pairs of the plane
     if (a.left >= 0 && a.right >= 0 && 4 * ((int64_t)a.left + a.right + 1) < k_len) return 0;
     return (k_len + 31) & ~31;

@@ -99,8 +99,12 @@ __device__ __forceinline__ float* bias_lds() {
 __host__ __device__ inline int table_slots(const BiasArgs& b) {
     return b.count + (b.count != b.entries);
 }
-inline size_t bias_lds_bytes(const BiasArgs& b, int G, bool sums) {
-    const size_t table = ((size_t)G * b.entries + 63) & ~(size_t)63;
+// Values of one head's tables: an entry each, or (JOINT) two axes' sums.
+__host__ __device__ inline int table_size(const BiasArgs& b, bool joint) {
+    return joint ? b.joint[0] + b.joint[1] : b.entries;
+}
+inline size_t bias_lds_bytes(const BiasArgs& b, int G, bool joint, bool sums) {
+    const size_t table = ((size_t)G * table_size(b, joint) + 63) & ~(size_t)63;
     return (table + (sums ? (size_t)4 * table_slots(b) * 64 : 0)) * sizeof(float);
 }
 
@@ -142,28 +146,56 @@ __device__ __forceinline__ void by_kind(bool ints, bool log, F f) {
     }
 }
 
-// The same from the pairs' entries as they are in the plane.
+// The same from the pairs' entries as they are in the plane (JOINT) or its bytes.
+template <bool JOINT>
 __device__ __forceinline__ void add_entries(f32x16& s, const u32x16& entries, int axes,
                                             const FPSTOK_LDS float* table) {
-#pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a) {
-        if (a >= axes) break;
+    const FPSTOK_LDS char* at = (const FPSTOK_LDS char*)table;
+    if constexpr (JOINT) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            s[e] += *(const FPSTOK_LDS float*)((const FPSTOK_LDS char*)table +
-                                               (entries[e] >> 8 * a & 255u));
+            s[e] += *(const FPSTOK_LDS float*)(at + (entries[e] & 0xffffu));
+        if (axes <= 2) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            s[e] += *(const FPSTOK_LDS float*)(at + (entries[e] >> 16));
+    } else {
+#pragma unroll
+        for (int a = 0; a < kMaxAxes; ++a) {
+            if (a >= axes) break;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                s[e] += *(const FPSTOK_LDS float*)(at + (entries[e] >> 8 * a & 255u));
+        }
     }
 }
 
+// What bucket 1 of axis a adds to a pair's word, and what a word begins with.
+template <bool JOINT>
+__device__ __forceinline__ uint32_t entry_unit(const BiasArgs& b, int a) {
+    if (!JOINT) return 4u << 8 * a;
+    // (the first of two axes: as many as the second has)
+    const uint32_t n = (a & 1) == 0 && a + 1 < b.axes ? (uint32_t)pick(b.top, a + 1) + 1 : 1u;
+    return 4 * n << 16 * (a >> 1);
+}
+template <bool JOINT>
+__device__ __forceinline__ uint32_t entry_base(const BiasArgs& b) {
+    if (JOINT) return b.axes > 2 ? (uint32_t)b.joint[0] << 18 : 0;
+    uint32_t x = 0;
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) x += a < b.axes ? (uint32_t)b.first[a] << (8 * a + 2) : 0;
+    return x;
+}
+
 // Entries of a block's pairs as the plane would hold them (places as for add_bias).
-template <bool KEY, int OWN, int ROWS>
+template <bool JOINT, bool KEY, int OWN, int ROWS>
 __device__ __forceinline__ u32x16 find_entries(const BiasArgs& b, const FPSTOK_LDS uint32_t* own,
                                                const FPSTOK_LDS uint32_t* tile) {
-    u32x16 entries = 0;
+    u32x16 entries = entry_base<JOINT>(b);
 #pragma unroll 1
     for (int a = 0; a < b.axes; ++a) {
-        const uint32_t mine = own[a * OWN];
-        const int first = pick(b.first, a), top = pick(b.top, a), shift = pick(b.log_shift, a);
+        const uint32_t mine = own[a * OWN], unit = entry_unit<JOINT>(b, a);
+        const int top = pick(b.top, a), shift = pick(b.log_shift, a);
         const float rate = pick(b.rate, a), zero = pick(b.shift, a);
         by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
 #pragma unroll
@@ -171,7 +203,7 @@ __device__ __forceinline__ u32x16 find_entries(const BiasArgs& b, const FPSTOK_L
                 const uint32_t other = tile[a * ROWS + (e >> 2) * 8 + (e & 3)];
                 const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
                     KEY ? mine : other, KEY ? other : mine, rate, zero, top, shift);
-                entries[e] |= (uint32_t)(first + bucket) << (8 * a + 2);
+                entries[e] += (uint32_t)bucket * unit;
             }
         });
     }
