@@ -503,7 +503,7 @@ struct TableSums {
         on = b.part != nullptr;
         if (!on) return;
         slots = table_slots(b);
-        all = (u64*)(bias_lds() + ((G * b.entries + 63) & ~63));
+        all = (u64*)(bias_lds() + ((G * table_size(b, BIAS == kPlane) + 63) & ~63));
         lane_sums = (FPSTOK_LDS u64*)all + wave * slots * 32 + (lane & 31);
         for (int i = tid; i < 4 * slots * 32; i += 256) all[i] = 0;
     }
@@ -723,6 +723,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     };
 
     Softmax<T, DB> sm;
+    const int share = query_share(G);
     // (with a bias the scores are in units of log2 already)
     const float cs = a.scale * kLog2e, c = BIAS ? 1.0f : cs;
     constexpr int NB = DP == 64 || BN == 32 ? 1 : 2;
@@ -751,7 +752,7 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                     add_entries<true>(x, entries, bias.axes, scores.table);
                 else
                     add_bias<false, false, 128, BN>(
-                        x, nullptr, bias, scores.table,
+                        x, nullptr, bias, share, scores.table,
                         (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                         (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
             }
@@ -882,6 +883,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 
     const View<BN> all(a, q.pa, q.pb, t.tk);
     Softmax<T, DB> sm;
+    constexpr int share = 1;  // (what the sharing needs does not fit in its registers)
     const float cs = a.scale * kLog2e, c = BIAS ? 1.0f : cs;
     if (wave < n) load(wave);
     bad.clear(tid);
@@ -913,7 +915,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if constexpr (BIAS != kNoBias) {
                 x *= cs;
                 add_bias<false, false, BM, BN>(
-                    x, nullptr, bias, scores.table,
+                    x, nullptr, bias, share, scores.table,
                     (const FPSTOK_LDS uint32_t*)&pos[wave].own[0][q.r],
                     (const FPSTOK_LDS uint32_t*)&pos[wave].tile[0][0][b * 32 + half * 4]);
             }
@@ -1063,14 +1065,16 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const QueryRows q(a, t, wave * 32, lane);
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     const bool wave_live = wave * 32 < t.rows;
-    BiasTile<BIAS, BN> scores(bias, t.hk, a.G, q.h - t.hk * a.G, t.tk, tid);
+    BiasTile<BIAS, BN, 256, BIAS == kPlane> scores(bias, t.hk, a.G, q.h - t.hk * a.G, t.tk, tid);
     TableSums<BIAS> sums(bias, a.G, wave, lane, tid);
     EntryWalk walk;
+    const uint32_t* byte_row = nullptr;
     if constexpr (BIAS != kNoBias) {
         if (!scores.planed)
             own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
         if (BIAS == kPlane) {
-            walk.row = bias.bytes + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+            byte_row = bias.bytes + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
+            walk.row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
             walk.last = (t.tk - 1) & ~31;
         }
     }
@@ -1127,6 +1131,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     for (int db = 0; db < DB; ++db) dq[db] = 0.0f;
     const float cs = a.scale * kLog2e, c = BIAS ? 1.0f : cs;
     float delta = 0.0f, lse2 = 0.0f, off_by = 0.0f;
+    const int share = query_share(a.G);
     // tile i may hold keys that lost elements
     auto lost_in = [&](int i) { return __builtin_amdgcn_readfirstlane(bad.tiles) >> (i & 31) & 1; };
     // the scores of such keys, of 32 from row b of tile i on
@@ -1148,13 +1153,13 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if constexpr (BIAS != kNoBias) {
             x *= cs;
             if constexpr (BIAS == kPlane)
-                add_entries<false>(x, walk.take<false, BN>(
+                add_entries<true>(x, walk.take<true, BN>(
                 bias, scores.planed, j0 + b, j0 + b + 32,
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]), bias.axes, scores.table);
             else
                 add_bias<false, false, 128, BN>(
-                    x, nullptr, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    x, nullptr, bias, share, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]);
         }
         if (holes) hide_lost(x, b, i);
@@ -1170,10 +1175,20 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         const FPSTOK_LDS char* vbuf = kbuf + BN * Tl::kPitch;
         f32x16 x = 0.0f, y = 0.0f;
         u32x16 entries;
-        if constexpr (BIAS == kPlane) entries = walk.take<false, BN>(
+        u32x16 joint;
+        if constexpr (BIAS == kPlane) {
+            if (sums.on)
+                entries = scores.planed
+                              ? load_entries(byte_row + j0 + b * 32)
+                              : find_entries<false, false, 128, BN>(
+                                    bias, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                                    (const FPSTOK_LDS uint32_t*)&pos
+                                        .tile[i & 1][0][b * 32 + half * 4]);
+            joint = walk.take<true, BN>(
                 bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
+        }
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
@@ -1182,10 +1197,10 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         if constexpr (BIAS != kNoBias) {
             x *= cs;
             if constexpr (BIAS == kPlane)
-                add_entries<false>(x, entries, bias.axes, scores.table);
+                add_entries<true>(x, joint, bias.axes, scores.table);
             else
                 add_bias<false, true, 128, BN>(
-                    x, &entries, bias, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    x, &entries, bias, share, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
         }
         if (holes) hide_lost(x, b * 32, i);
@@ -1366,6 +1381,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     FPSTOK_LDS char* qbuf = lds + wave * kWaveBytes;
     FPSTOK_LDS char* gbuf = qbuf + kTile;
     const float cs = a.scale * kLog2e;
+    constexpr int share = 1;  // (the lanes hold keys)
     BiasTile<BIAS, 32, 64> scores(bias, hk, G, 0, tk, tid);
     if constexpr (BIAS != kNoBias) {
         scores.finish(bias, tid);
@@ -1427,7 +1443,7 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if constexpr (BIAS != kNoBias) {
                 s *= cs;
                 add_bias<true, false, 32, 32>(
-                    s, nullptr, bias, scores.table + head * bias.entries,
+                    s, nullptr, bias, share, scores.table + head * bias.entries,
                     (const FPSTOK_LDS uint32_t*)&pos[wave].own[0][lane & 31],
                     (const FPSTOK_LDS uint32_t*)&pos[wave].tile[0][0][half * 4]);
             }
@@ -1650,6 +1666,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
     const float c = a.scale * kLog2e;
+    constexpr int share = 1;  // (the lanes hold keys)
     // (turn, head: the tile's buffer and its head of the group)
     auto block = [&](const FPSTOK_LDS char* qbuf, const float (*stat)[64], int b, int x0,
                      bool mask, int turn, int head) {
@@ -1686,7 +1703,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                 add_entries<true>(x, entries, bias.axes, scores.table + head * table_size(bias, BIAS == kPlane));
             else
                 add_bias<true, false, 128, BQ>(
-                    x, nullptr, bias, scores.table + head * table_size(bias, BIAS == kPlane),
+                    x, nullptr, bias, share, scores.table + head * table_size(bias, BIAS == kPlane),
                     (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
         }
@@ -1867,7 +1884,7 @@ static void backward_q(const AttnArgs& a, const BiasParam<BIAS>& b, hipStream_t 
     const dim3 q((unsigned)(row_slots(a.qs, a.G, 7) * a.Hk));
     const bool narrow = k16 && a.left >= 0 && a.right >= 0 && a.left + a.right < 32 - a.sinks;
     size_t lds = 0;
-    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, false, b.part != nullptr);
+    if constexpr (BIAS != kNoBias) lds = bias_lds_bytes(b, a.G, BIAS == kPlane, b.part != nullptr);
     if (a.D <= 64) {
         if (narrow)
             attention_dq_kernel<T, 64, BIAS ? 32 : 64, k16, BIAS><<<q, 256, lds, s>>>(a, b);

@@ -83,7 +83,9 @@ static void fill_plane(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
 }
 
 int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len) {
-    if (few || b.entries > kTableEntries || a.H < 4 || k_len > 1024) return 0;
+    // (64 padded float32 events of up to 128 tokens, 8 heads, 2 axes: 37 us without, 40
+    // with it; 64 events, 12 heads, 4 axes: 34.7 and 31.8)
+    if (few || b.entries > kTableEntries || a.H * b.axes < 24 || k_len > 1024) return 0;
     if ((int64_t)a.G * table_size(b, true) > kGroupEntries) return 0;
     // a window that hides most pairs of the plane
     if (a.left >= 0 && a.right >= 0 && 4 * ((int64_t)a.left + a.right + 1) < k_len) return 0;

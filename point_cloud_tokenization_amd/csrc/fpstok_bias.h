@@ -210,37 +210,88 @@ __device__ __forceinline__ u32x16 find_entries(const BiasArgs& b, const FPSTOK_L
     return entries;
 }
 
+// Lane FROM of every four lanes' value, in all four (SHARE 4), or that of lane FROM
+// of every two (SHARE 2).
+template <int SHARE, int FROM>
+__device__ __forceinline__ uint32_t from_lane(uint32_t x) {
+    constexpr int kPerm = SHARE == 4 ? FROM * 0x55 : SHARE == 2 ? (FROM ? 0xf5 : 0xa0) : 0xe4;
+    if (SHARE == 1) return x;
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kPerm, 0xf, 0xf, true);
+}
+
 // Adds the bias of a block of 32 x 32 pairs to its scores (in units of log2): a
 // lane's own row against the block's rows in its registers.  own: this lane's
 // place in own[0], tile: that of the block's row 4 half in tile[0].
 // KEY: the own row is the key.  PACK: entries, byte a of a pair's: the entry of
 // axis a.
-template <bool KEY, bool PACK, int OWN, int ROWS>
-__device__ __forceinline__ void add_bias(f32x16& s, u32x16* entries, const BiasArgs& b,
-                                         const FPSTOK_LDS float* table,
-                                         const FPSTOK_LDS uint32_t* own,
-                                         const FPSTOK_LDS uint32_t* tile) {
-    if constexpr (PACK) *entries = 0;
+// SHARE: that many lanes after one another hold one query (in heads of a group): each
+// finds a part of the pairs' buckets for all of them.  (8192 + 5000 rows, causal, 16
+// heads on 4 of 128: SHARE_US with one in four, 884 with all.)
+template <bool KEY, bool PACK, int SHARE, int OWN, int ROWS>
+__device__ __forceinline__ void add_bias_shared(f32x16& s, u32x16* entries, const BiasArgs& b,
+                                                const FPSTOK_LDS float* table,
+                                                const FPSTOK_LDS uint32_t* own,
+                                                const FPSTOK_LDS uint32_t* tile) {
+    constexpr int kGroups = 4 / SHARE;  // of 4 adjacent rows that this lane looks at
+    const int part = SHARE > 1 ? (int)(threadIdx.x & (SHARE - 1)) : 0;
 #pragma unroll 1
     for (int a = 0; a < b.axes; ++a) {
         const uint32_t mine = own[a * OWN];
         const int first = pick(b.first, a), top = pick(b.top, a), shift = pick(b.log_shift, a);
         const float rate = pick(b.rate, a), zero = pick(b.shift, a);
-        const FPSTOK_LDS float* tab = table + first;
+        uint32_t found[kGroups * 4];
         by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const u32x4 other = *(const FPSTOK_LDS u32x4*)(tile + a * ROWS + g * 8);
+            for (int g = 0; g < kGroups; ++g) {
+                const u32x4 other =
+                    *(const FPSTOK_LDS u32x4*)(tile + a * ROWS + (part * kGroups + g) * 8);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int bucket = bucket_of<decltype(ints)::value, decltype(log)::value>(
-                        KEY ? mine : other[e], KEY ? other[e] : mine, rate, zero, top, shift);
-                    s[g * 4 + e] += tab[bucket];
-                    if constexpr (PACK) (*entries)[g * 4 + e] += (uint32_t)(first + bucket) << 8 * a;
-                }
+                for (int e = 0; e < 4; ++e)
+                    found[g * 4 + e] =
+                        (uint32_t)(first +
+                                   bucket_of<decltype(ints)::value, decltype(log)::value>(
+                                       KEY ? mine : other[e], KEY ? other[e] : mine, rate, zero,
+                                       top, shift))
+                        << 2;
             }
         });
+        auto add = [&](auto lane, int to) {
+#pragma unroll
+            for (int e = 0; e < kGroups * 4; ++e) {
+                const uint32_t at = from_lane<SHARE, decltype(lane)::value>(found[e]);
+                s[to + e] += *(const FPSTOK_LDS float*)((const FPSTOK_LDS char*)table + at);
+                if constexpr (PACK) (*entries)[to + e] += at >> 2 << 8 * a;
+            }
+        };
+        add(std::integral_constant<int, 0>{}, 0);
+        if constexpr (SHARE > 1) add(std::integral_constant<int, 1>{}, kGroups * 4);
+        if constexpr (SHARE > 2) {
+            add(std::integral_constant<int, 2>{}, kGroups * 8);
+            add(std::integral_constant<int, 3>{}, kGroups * 12);
+        }
     }
+}
+
+// share: 4, 2 or 1, the same in all lanes (query_share of the group).
+template <bool KEY, bool PACK, int OWN, int ROWS>
+__device__ __forceinline__ void add_bias(f32x16& s, u32x16* entries, const BiasArgs& b, int share,
+                                         const FPSTOK_LDS float* table,
+                                         const FPSTOK_LDS uint32_t* own,
+                                         const FPSTOK_LDS uint32_t* tile) {
+    if constexpr (PACK) *entries = 0;
+    if constexpr (!KEY) {
+        if (share == 4)
+            return add_bias_shared<KEY, PACK, 4, OWN, ROWS>(s, entries, b, table, own, tile);
+        if (share == 2)
+            return add_bias_shared<KEY, PACK, 2, OWN, ROWS>(s, entries, b, table, own, tile);
+    }
+    add_bias_shared<KEY, PACK, 1, OWN, ROWS>(s, entries, b, table, own, tile);
+}
+
+// Lanes after one another that hold one query: tiles begin at a multiple of 32 rows,
+// so rows of a group of 4 n heads come in fours.
+__device__ __forceinline__ int query_share(int G) {
+    return (G & 3) == 0 ? 4 : (G & 1) == 0 ? 2 : 1;
 }
 
 }  // namespace fpstok
