@@ -62,6 +62,7 @@ struct BiasArgs {
     int32_t first[kMaxAxes], top[kMaxAxes];  // an axis's first entry and its last bucket
     int32_t log_shift[kMaxAxes];             // bits below a step of a log axis, -1: linear
     float rate[kMaxAxes], shift[kMaxAxes];
+    int32_t spans;  // look for blocks of pairs in one bucket
     // gradient: the entries from .. from + count - 1 (all there are, or a part of
     // many), and the workgroups' parts, [row tiles][Hk][G][count]
     int32_t from, count;

@@ -181,8 +181,11 @@ static fpstok_status check_bias(const fpstok_rel_bias* r, const fpstok_attn_para
     return FPSTOK_OK;
 }
 
-static fpstok_status check_bias_data(const fpstok_seqs* qs, const fpstok_seqs* ks, BiasArgs& b) {
+static fpstok_status check_bias_data(const fpstok_seqs* qs, const fpstok_seqs* ks,
+                                     const fpstok_attn_params* p, BiasArgs& b) {
     if (!b.k_pos && qs == ks) b.k_pos = b.q_pos;
+    b.spans = p->window_left < 0 || p->window_right < 0 ||
+              (int64_t)p->window_left + p->window_right >= 1024;
     if (!b.table) return fail(FPSTOK_EINVAL, "table is NULL");
     if ((qs->num_rows > 0 && !b.q_pos) || (ks->num_rows > 0 && !b.k_pos))
         return fail(FPSTOK_EINVAL, "q_positions or k_positions is NULL");
@@ -299,7 +302,7 @@ static fpstok_status attend(const fpstok_seqs* qs, const fpstok_seqs* ks,
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
     BiasArgs b{};
     if (biased && ((st = check_bias(r, p, b)) != FPSTOK_OK ||
-                   (st = check_bias_data(qs, ks, b)) != FPSTOK_OK))
+                   (st = check_bias_data(qs, ks, p, b)) != FPSTOK_OK))
         return st;
     AttnArgs a = attn_args(qs, ks, p);
     AttnPlan plan;
@@ -343,7 +346,7 @@ static fpstok_status attend_backward(
     if (((uintptr_t)lse & 3u) != 0) return fail(FPSTOK_EINVAL, "lse must be 4-byte aligned");
     BiasArgs b{};
     if (biased && ((st = check_bias(r, p, b)) != FPSTOK_OK ||
-                   (st = check_bias_data(qs, ks, b)) != FPSTOK_OK))
+                   (st = check_bias_data(qs, ks, p, b)) != FPSTOK_OK))
         return st;
     if (((uintptr_t)grad_table & 3u) != 0)
         return fail(FPSTOK_EINVAL, "grad_table must be 4-byte aligned");

@@ -509,8 +509,10 @@ struct TableSums {
     }
     // 16 pairs of this lane's row: t = dP - delta, weights w (both 0 where hidden)
     // and dS = w t.
-    __device__ __forceinline__ void add(const BiasArgs& b, const u32x16& entries, const f32x16& t,
-                                        const f32x16& w, const f32x16& ds, bool counts, int half) {
+    // same: bit a: this lane's pairs have one entry of axis a.
+    __device__ __forceinline__ void add(const BiasArgs& b, const u32x16& entries, uint32_t same,
+                                        const f32x16& t, const f32x16& w, const f32x16& ds,
+                                        bool counts, int half) {
         float top = 0.0f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(t[e]));
@@ -530,10 +532,19 @@ struct TableSums {
             x[e] = (u64)__builtin_amdgcn_alignbit(hi, lo, 32 - kWeightBits) << 32 |
                    ((lo << kWeightBits) + weight);
         }
+        u64 total = 0;
+        if (BIAS == kPositions && same != 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) total += x[e];
+        }
         if (b.count == b.entries) {
 #pragma unroll
             for (int a = 0; a < kMaxAxes; ++a) {
                 if (a >= b.axes) break;
+                if (BIAS == kPositions && (same >> a & 1)) {
+                    put(entries[0] >> 8 * a & 255u, 8, total);
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     put(entries[e] >> 8 * a & 255u, BIAS == kPlane ? 6 : 8, x[e]);
@@ -674,7 +685,8 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     EntryWalk walk;
     if constexpr (BIAS != kNoBias) {
         if (!scores.planed)
-            own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
+            own_positions(bias, pos.own, pos.span[wave], q.r, bias.q_pos, q.row, q.live,
+                          half);
         if (BIAS == kPlane) {
             walk.row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
             walk.last = (t.tk - 1) & ~31;
@@ -736,27 +748,33 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             f32x16 x = 0.0f;
-            u32x16 entries;
-            if constexpr (BIAS == kPlane)
-                entries = walk.take<true, BN>(
-                    bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
-                    (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
-                    (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
 #pragma unroll
             for (int st = 0; st < STEPS; ++st)
                 if (sizeof(T) == 2 || st * 16 < a.D)  // (float32: a step is 8 instructions)
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
-            if constexpr (BIAS != kNoBias) {
-                x *= cs;
-                if constexpr (BIAS == kPlane)
-                    add_entries<true>(x, entries, bias.axes, scores.table);
-                else
-                    add_bias<false, false, 128, BN>(
-                        x, nullptr, bias, share, scores.table,
-                        (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
-                        (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
-            }
             s[b] = x;
+        }
+        if constexpr (BIAS != kNoBias) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                f32x16 sum = 0.0f;  // (by itself: it need not wait for the products)
+                if constexpr (BIAS == kPlane)
+                    add_entries<true>(
+                        sum,
+                        walk.take<true, BN>(bias, scores.planed, j0 + b * 32, j0 + b * 32 + 32,
+                                            (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                                            (const FPSTOK_LDS uint32_t*)&pos
+                                                .tile[turn][0][from + b * 32 + half * 4]),
+                        bias.axes, scores.table);
+                else
+                    add_bias<false, false, true, 128, BN>(
+                        sum, nullptr, bias, share, scores.table,
+                        (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                        (const FPSTOK_LDS uint32_t*)&pos.span[wave],
+                        (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][from + b * 32 + half * 4]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[b][e] = __builtin_fmaf(s[b][e], cs, sum[e]);
+            }
         }
         if (v0 != 2) win.mask(s[0], j0, half, a.sinks, -INFINITY);
         if (NB == 2 && v1 != 2) win.mask(s[NB - 1], j0 + 32, half, a.sinks, -INFINITY);
@@ -865,7 +883,7 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const Window win(a, q.qi + t.tk - t.tq, t.tk);
     BiasTile<BIAS, BN, 64> scores(bias, t.hk, G, q.h - t.hk * G, t.tk, tid);
     if constexpr (BIAS != kNoBias)
-        own_positions(bias, pos[wave].own, q.r, bias.q_pos, q.row, q.live, half);
+        own_positions(bias, pos[wave].own, pos[wave].span[0], q.r, bias.q_pos, q.row, q.live, half);
 
     KeyTiles<BN> kt(a, q.pa, q.pb, t.tk);
     const int n = t.rows > 0 ? kt.part(t.part, a.splits) : 0;
@@ -914,9 +932,10 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                     x = Elem<T>::mma(Tl::row_frag(kbuf, b * 32 + (lane & 31), st, half), qf[st], x);
             if constexpr (BIAS != kNoBias) {
                 x *= cs;
-                add_bias<false, false, BM, BN>(
+                add_bias<false, false, false, BM, BN>(
                     x, nullptr, bias, share, scores.table,
                     (const FPSTOK_LDS uint32_t*)&pos[wave].own[0][q.r],
+                    (const FPSTOK_LDS uint32_t*)&pos[wave].span[0],
                     (const FPSTOK_LDS uint32_t*)&pos[wave].tile[0][0][b * 32 + half * 4]);
             }
             s[b] = x;
@@ -1071,7 +1090,8 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     const uint32_t* byte_row = nullptr;
     if constexpr (BIAS != kNoBias) {
         if (!scores.planed)
-            own_positions(bias, pos.own, q.r, bias.q_pos, q.row, q.live, half);
+            own_positions(bias, pos.own, pos.span[wave], q.r, bias.q_pos, q.row, q.live,
+                          half);
         if (BIAS == kPlane) {
             byte_row = bias.bytes + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
             walk.row = bias.plane + (q.live ? q.row : t.q0) * bias.pitch + half * 4;
@@ -1158,8 +1178,10 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
                 (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
                 (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]), bias.axes, scores.table);
             else
-                add_bias<false, false, 128, BN>(
-                    x, nullptr, bias, share, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                add_bias<false, false, true, 128, BN>(
+                    x, nullptr, bias, share, scores.table,
+                    (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    (const FPSTOK_LDS uint32_t*)&pos.span[wave],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b + half * 4]);
         }
         if (holes) hide_lost(x, b, i);
@@ -1176,6 +1198,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         f32x16 x = 0.0f, y = 0.0f;
         u32x16 entries;
         u32x16 joint;
+        uint32_t same = 0;
         if constexpr (BIAS == kPlane) {
             if (sums.on)
                 entries = scores.planed
@@ -1199,8 +1222,10 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if constexpr (BIAS == kPlane)
                 add_entries<true>(x, joint, bias.axes, scores.table);
             else
-                add_bias<false, true, 128, BN>(
-                    x, &entries, bias, share, scores.table, (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                same = add_bias<false, true, true, 128, BN>(
+                    x, &entries, bias, share, scores.table,
+                    (const FPSTOK_LDS uint32_t*)&pos.own[0][q.r],
+                    (const FPSTOK_LDS uint32_t*)&pos.span[wave],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[i & 1][0][b * 32 + half * 4]);
         }
         if (holes) hide_lost(x, b * 32, i);
@@ -1220,7 +1245,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if (sums.on) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) off_by += ds[e];
-                sums.add(bias, entries, y, x, ds, counts, half);
+                sums.add(bias, entries, same, y, x, ds, counts, half);
             }
         } else {
 #pragma unroll
@@ -1397,7 +1422,8 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
         load_row<T, STEPS>(vf, (const T*)a.v.data + (k0 + j) * a.v.row + hk * a.v.head, live,
                            (const T*)a.v.data, a.D, half);
         if constexpr (BIAS != kNoBias)
-            own_positions(bias, pos[wave].own, lane & 31, bias.k_pos, k0 + j, live, half);
+            own_positions(bias, pos[wave].own, pos[wave].span[0], lane & 31, bias.k_pos, k0 + j,
+                          live, half);
         f32x16 dk[DB], dv[DB];
 #pragma unroll
         for (int db = 0; db < DB; ++db) dk[db] = 0.0f, dv[db] = 0.0f;
@@ -1442,9 +1468,10 @@ void attention_sink_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             f32x16 w, ds;
             if constexpr (BIAS != kNoBias) {
                 s *= cs;
-                add_bias<true, false, 32, 32>(
+                add_bias<true, false, true, 32, 32>(
                     s, nullptr, bias, share, scores.table + head * bias.entries,
                     (const FPSTOK_LDS uint32_t*)&pos[wave].own[0][lane & 31],
+                    (const FPSTOK_LDS uint32_t*)&pos[wave].span[0],
                     (const FPSTOK_LDS uint32_t*)&pos[wave].tile[0][0][half * 4]);
             }
 #pragma unroll
@@ -1553,7 +1580,7 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
     BiasTile<BIAS, BQ, 256, BIAS == kPlane> scores(bias, t.hk, G, 0, t.tk, tid);
     const uint32_t* entry_col = nullptr;
     if constexpr (BIAS != kNoBias) {
-        if (!scores.planed) own_positions(bias, pos.own, r, bias.k_pos, krow, live, half);
+        if (!scores.planed) own_positions(bias, pos.own, pos.span[wave], r, bias.k_pos, krow, live, half);
         if (BIAS == kPlane)
             entry_col = bias.plane + t.q0 * bias.pitch + (live ? t.row0 + r : 0);
     }
@@ -1702,9 +1729,10 @@ void attention_dkv_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if constexpr (BIAS == kPlane)
                 add_entries<true>(x, entries, bias.axes, scores.table + head * table_size(bias, BIAS == kPlane));
             else
-                add_bias<true, false, 128, BQ>(
+                add_bias<true, false, true, 128, BQ>(
                     x, nullptr, bias, share, scores.table + head * table_size(bias, BIAS == kPlane),
                     (const FPSTOK_LDS uint32_t*)&pos.own[0][r],
+                    (const FPSTOK_LDS uint32_t*)&pos.span[wave],
                     (const FPSTOK_LDS uint32_t*)&pos.tile[turn][0][b * 32 + half * 4]);
         }
 #pragma unroll

@@ -26,11 +26,13 @@ template <BiasFrom BIAS>
 using BiasParam = std::conditional_t<BIAS != kNoBias, BiasArgs, NoBias>;
 
 // Positions of a tile's rows in LDS, and of the rows across the lanes: float32
-// times the axis's rate, or the int32 as they are.  [axis][row]
+// times the axis's rate, or the int32 as they are.  [axis][row]; `span`: the least
+// and the greatest of a wave's own 32 rows.
 template <BiasFrom BIAS, int OWN, int ROWS>
 struct BiasPos {
     uint32_t own[kMaxAxes][OWN];
     uint32_t tile[2][kMaxAxes][ROWS];
+    uint32_t span[OWN / 32][kMaxAxes][2];
 };
 template <int OWN, int ROWS>
 struct BiasPos<kNoBias, OWN, ROWS> {};
@@ -76,17 +78,51 @@ struct PosStage {
     }
 };
 
+// A position as a whole number of the same order, and back.
+__device__ __forceinline__ int ordered(uint32_t x, bool ints) {
+    return ints ? (int)x : (int)(x ^ ((uint32_t)((int)x >> 31) & 0x7fffffffu));
+}
+__device__ __forceinline__ uint32_t position(int x, bool ints) {
+    return (uint32_t)ordered((uint32_t)x, ints);
+}
+
+// The least and the greatest over 32 lanes, the two halves of a wave alike.
+__device__ __forceinline__ void span_of(int x, int& least, int& most) {
+    least = most = x;
+    auto step = [&](auto ctrl) {
+        constexpr int kCtrl = decltype(ctrl)::value;
+        const int a = __builtin_amdgcn_update_dpp(0, least, kCtrl, 0xf, 0xf, true);
+        const int b = __builtin_amdgcn_update_dpp(0, most, kCtrl, 0xf, 0xf, true);
+        least = a < least ? a : least;
+        most = b > most ? b : most;
+    };
+    step(std::integral_constant<int, 0xb1>{});   // lanes l ^ 1
+    step(std::integral_constant<int, 0x4e>{});   // l ^ 2
+    step(std::integral_constant<int, 0x141>{});  // 7 - l % 8
+    step(std::integral_constant<int, 0x140>{});  // 15 - l % 16
+    const auto a = __builtin_amdgcn_permlane16_swap(least, least, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(most, most, false, false);
+    least = (int)a[0] < (int)a[1] ? (int)a[0] : (int)a[1];
+    most = (int)b[0] > (int)b[1] ? (int)b[0] : (int)b[1];
+}
+
 // Positions of the rows across a wave's lanes (lanes 0-31 write): row `row` of
-// the buffer, or, not `live`, one that exists.
+// the buffer, or, not `live`, the first lane's (if that is not either, row 0).
 template <int OWN>
-__device__ __forceinline__ void own_positions(const BiasArgs& b, uint32_t (*own)[OWN], int at,
-                                              const void* pos, int64_t row, bool live, int half) {
+__device__ __forceinline__ void own_positions(const BiasArgs& b, uint32_t (*own)[OWN],
+                                              uint32_t (*span)[2], int at, const void* pos,
+                                              int64_t row, bool live, int half) {
+    const int first = __builtin_amdgcn_readfirstlane(live ? (int)row : 0);
 #pragma unroll
     for (int a = 0; a < kMaxAxes; ++a) {
         if (a >= b.axes) break;
-        const uint32_t x = ((const uint32_t*)pos)[(live ? row : 0) * b.axes + a];
-        if (half == 0)
-            own[a][at] = b.ints ? x : __float_as_uint(__uint_as_float(x) * b.rate[a]);
+        uint32_t x = ((const uint32_t*)pos)[(live ? row : first) * b.axes + a];
+        if (!b.ints) x = __float_as_uint(__uint_as_float(x) * b.rate[a]);
+        if (half == 0) own[a][at] = x;
+        int least, most;
+        span_of(ordered(x, b.ints), least, most);
+        if ((threadIdx.x & 63) == 0)
+            span[a][0] = position(least, b.ints), span[a][1] = position(most, b.ints);
     }
 }
 
@@ -223,15 +259,27 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t x) {
 // lane's own row against the block's rows in its registers.  own: this lane's
 // place in own[0], tile: that of the block's row 4 half in tile[0].
 // KEY: the own row is the key.  PACK: entries, byte a of a pair's: the entry of
-// axis a.
+// axis a; bit a of `same`: it is one for all of the block's pairs.
 // SHARE: that many lanes after one another hold one query (in heads of a group): each
 // finds a part of the pairs' buckets for all of them.  (8192 + 5000 rows, causal, 16
-// heads on 4 of 128: SHARE_US with one in four, 884 with all.)
-template <bool KEY, bool PACK, int SHARE, int OWN, int ROWS>
-__device__ __forceinline__ void add_bias_shared(f32x16& s, u32x16* entries, const BiasArgs& b,
-                                                const FPSTOK_LDS float* table,
-                                                const FPSTOK_LDS uint32_t* own,
-                                                const FPSTOK_LDS uint32_t* tile) {
+// heads on 4 of 128: 788 us with one in four, 884 with all.)
+//
+// Rows in order (of time, of their place) and buckets that grow with the distance, or
+// end, leave most blocks of a long walk in one bucket.  It grows or falls with the
+// distance, so it is one for the block if the least key less the greatest query and the
+// greatest less the least fall into the same: then a lane needs one value, not 16
+// loads of LDS (the same rows: 703 us, 788 without).  Where a window hides the far keys this
+// would be looked for in vain (b.spans; 6000 + 2500 + 333 pulses, window of 256: a
+// training step 369 us with it, 344 without).
+template <bool KEY, bool PACK, bool SPANS, int SHARE, int OWN, int ROWS>
+__device__ __forceinline__ uint32_t add_bias_shared(f32x16& s, u32x16* entries,
+                                                    const BiasArgs& b,
+                                                    const FPSTOK_LDS float* table,
+                                                    const FPSTOK_LDS uint32_t* own,
+                                                    const FPSTOK_LDS uint32_t* span,
+                                                    const FPSTOK_LDS uint32_t* tile) {
+    const int lane = threadIdx.x & 63;
+    uint32_t same = 0;
     constexpr int kGroups = 4 / SHARE;  // of 4 adjacent rows that this lane looks at
     const int part = SHARE > 1 ? (int)(threadIdx.x & (SHARE - 1)) : 0;
 #pragma unroll 1
@@ -239,6 +287,39 @@ __device__ __forceinline__ void add_bias_shared(f32x16& s, u32x16* entries, cons
         const uint32_t mine = own[a * OWN];
         const int first = pick(b.first, a), top = pick(b.top, a), shift = pick(b.log_shift, a);
         const float rate = pick(b.rate, a), zero = pick(b.shift, a);
+        if (SPANS && b.spans) {
+            int least, most, one = 0, other_end = 0;
+            // (tile is at row 4 half)
+            span_of(ordered(tile[a * ROWS + (lane & 31) - (lane >> 5) * 4], b.ints), least, most);
+            by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
+                const uint32_t lo = position(least, b.ints), hi = position(most, b.ints);
+                const uint32_t own_lo = span[a * 2], own_hi = span[a * 2 + 1];
+                one = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                    KEY ? own_lo : lo, KEY ? hi : own_hi, rate, zero, top, shift);
+                other_end = bucket_of<decltype(ints)::value, decltype(log)::value>(
+                    KEY ? own_hi : hi, KEY ? lo : own_lo, rate, zero, top, shift);
+                // (an end that is not a number says nothing of what lies between)
+                if constexpr (!decltype(ints)::value) {
+                    const float from = KEY ? __uint_as_float(own_lo) - __uint_as_float(hi)
+                                           : __uint_as_float(lo) - __uint_as_float(own_hi);
+                    const float to = KEY ? __uint_as_float(own_hi) - __uint_as_float(lo)
+                                         : __uint_as_float(hi) - __uint_as_float(own_lo);
+                    if (!(from <= to)) other_end = -1;
+                }
+            });
+            if (__builtin_amdgcn_readfirstlane(one) == __builtin_amdgcn_readfirstlane(other_end)) {
+                const float value = table[first + one];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] += value;
+                if constexpr (PACK) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        (*entries)[e] += (uint32_t)(first + one) << 8 * a;
+                    same |= 1u << a;
+                }
+                continue;
+            }
+        }
         uint32_t found[kGroups * 4];
         by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
 #pragma unroll
@@ -270,22 +351,27 @@ __device__ __forceinline__ void add_bias_shared(f32x16& s, u32x16* entries, cons
             add(std::integral_constant<int, 3>{}, kGroups * 12);
         }
     }
+    return same;
 }
 
-// share: 4, 2 or 1, the same in all lanes (query_share of the group).
-template <bool KEY, bool PACK, int OWN, int ROWS>
-__device__ __forceinline__ void add_bias(f32x16& s, u32x16* entries, const BiasArgs& b, int share,
-                                         const FPSTOK_LDS float* table,
-                                         const FPSTOK_LDS uint32_t* own,
-                                         const FPSTOK_LDS uint32_t* tile) {
+// share: 4, 2 or 1, the same in all lanes (query_share of the group).  Returns `same`.
+template <bool KEY, bool PACK, bool SPANS, int OWN, int ROWS>
+__device__ __forceinline__ uint32_t add_bias(f32x16& s, u32x16* entries, const BiasArgs& b,
+                                             int share, const FPSTOK_LDS float* table,
+                                             const FPSTOK_LDS uint32_t* own,
+                                             const FPSTOK_LDS uint32_t* span,
+                                             const FPSTOK_LDS uint32_t* tile) {
     if constexpr (PACK) *entries = 0;
     if constexpr (!KEY) {
         if (share == 4)
-            return add_bias_shared<KEY, PACK, 4, OWN, ROWS>(s, entries, b, table, own, tile);
+            return add_bias_shared<KEY, PACK, SPANS, 4, OWN, ROWS>(s, entries, b, table, own, span,
+                                                                  tile);
         if (share == 2)
-            return add_bias_shared<KEY, PACK, 2, OWN, ROWS>(s, entries, b, table, own, tile);
+            return add_bias_shared<KEY, PACK, SPANS, 2, OWN, ROWS>(s, entries, b, table, own, span,
+                                                                  tile);
     }
-    add_bias_shared<KEY, PACK, 1, OWN, ROWS>(s, entries, b, table, own, tile);
+    return add_bias_shared<KEY, PACK, SPANS, 1, OWN, ROWS>(s, entries, b, table, own, span,
+                                                                  tile);
 }
 
 // Lanes after one another that hold one query: tiles begin at a multiple of 32 rows,

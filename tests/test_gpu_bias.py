@@ -183,6 +183,37 @@ def test_far_positions(dev):
         assert bool(got[name].isfinite().all())
 
 
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2), (4, 1), (8, 1), (3, 1)])
+@pytest.mark.parametrize("dt,D", [(BF, 64), (HF, 128), (FL, 64)])
+@pytest.mark.parametrize("spec", ["i 12:0.25:4:11", "f 9:0.05 6:1:1", "f 20:-0.5:2"])
+def test_rows_in_order(dev, H, Hk, dt, D, spec):
+    """Positions that grow along the sequence: most blocks of pairs fall into one
+    bucket, the ones near the diagonal do not."""
+    c = Case(dev, [260, 1, 140], None, H, Hk, D, dt, spec, 100, 40, 3)
+    n = c.k_pos.shape[0]
+    step = torch.arange(n)[:, None] * (3 if c.kind == "i" else 0.7)
+    c.k_pos[:, :1] = (step + (2000000000 if c.kind == "i" else -90)).to(c.k_pos.dtype)
+    c.run()
+
+
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 1)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("spec", ["f 9:0.05", "f 12:0.5:2", "f 12:1:1:11"])
+def test_position_that_is_not_finite_reaches_who_sees_it(dev, H, Hk, bad, spec):
+    """Causal, positions in order: queries before the row do not see it, and their
+    results do not change, though they share blocks of pairs with it."""
+    for sign in (1, -1):
+        c = Case(dev, [300], None, H, Hk, 64, BF, spec, right=0)
+        c.k_pos[:, 0] = torch.arange(c.k_pos.shape[0]) * 0.5 * sign
+        want = c.reference()
+        r0 = c.q_seq[0][0]
+        c.k_pos[r0 + 75] = bad
+        c.q_pos = c.k_pos
+        got = dict(zip(NAMES, c.outputs(c.call())))
+        for name in ("out", "lse", "grad_q"):
+            check(got[name][r0:r0 + 75], tuple(x[r0:r0 + 75] for x in want[name]), name)
+
+
 @pytest.mark.parametrize("dt", [BF, FL])
 @pytest.mark.parametrize("low", [float("-inf"), -3.4028234663852886e38, -1e30])
 def test_hidden_by_the_table(dev, dt, low):
