@@ -500,7 +500,8 @@ fpstok_status fpstok_rope(const fpstok_seqs* seqs, const fpstok_rope_params* par
  * float32 operation below is rounded by itself:
  *   FPSTOK_F32 positions: D = fl(x_k - x_q), x = fl(position * rate[a])
  *   FPSTOK_I32 positions: D = fl(fl(p_k - p_q) * rate[a]), the difference taken
- *                         as int32 (it has to fit) and then rounded to float32
+ *                         as int32 and then rounded to float32; of a pair whose
+ *                         difference does not fit the bucket is any of the axis's
  *   log_steps[a] = 0, linear: bucket = floor(fl(D + shift[a])): buckets of one
  *     unit, distance 0 in bucket floor(shift[a])
  *   log_steps[a] = g, a power of two up to 16: bucket = shift[a] + L, or

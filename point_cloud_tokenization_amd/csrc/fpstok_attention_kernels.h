@@ -661,6 +661,14 @@ struct TableSums<kNoBias> {
 // event.  84k pulses, window 257, 8 heads on 2: 0.14 ms; 64 events of at most
 // 128 tokens, 12 heads: 14 us (7 us of bytes).  A third buffer cost 5 %, scores
 // formed one tile ahead 5 to 15 % (and spills at D = 128).
+//
+// With a bias a score is one more sum of LDS values, found by the pair's distance:
+// per pair and axis about 6 instructions of the vector unit and a load of LDS of its
+// own address (32 banks: 5.3 cycles a wave's instruction), which is then the bound.  From the
+// plane it is one load of memory (4 bytes a pair and head) and, for every two axes, one of
+// LDS.  256 events of up to 256 tokens, 12 heads of 64, 4 axes: 147 us and 24 for the
+// plane (without a bias 75); 8192 + 5000 causal rows, 16 heads on 4 of 128, one axis of
+// int32: 703 us (437); pulses, window of 256, one axis: 43 us (21).
 template <class T, int DP, int BN, BiasFrom BIAS>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) - (BIAS && DP * sizeof(T) == 128))
 void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
@@ -856,7 +864,9 @@ void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // for the join: 5.2 TB/s, a large copy's rate.  Tiles of 64 keys leave one
 // workgroup per compute unit: 435 us there.  Sequences of more than 32 rows are
 // slower here (64 events of up to 128 tokens: 30 us against 14), for every 32
-// rows read all keys again.
+// rows read all keys again.  With a bias by one axis of int32 the long ones take 228 us
+// instead of 172: the 8 heads of a group find the same entries, each lane for itself (one lane
+// finding them for four took 306, with spills).
 template <class T, int DP, int BN, BiasFrom BIAS>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) > 3 ? 3 : 512 / (DP * (int)sizeof(T)))
 void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
@@ -1052,7 +1062,10 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // its whole gradient.  So the scores of such keys are set to -infinity, and 0
 // times the lost element, which is not a number, is added after the walk.
 //
-// The bias's gradient is dS summed by the pairs' entries (TableSums).  It is a
+// The bias's gradient is dS summed by the pairs' entries (TableSums).  These sums are
+// the bound: an addition of 64 bits in LDS takes 7 cycles for 64 lanes at best, one per
+// pair and axis.  256 events of up to 256 tokens, 12 heads of 64, 4 axes: 416 us (113
+// without a bias); pulses, window of 256, one axis: 193 us (26).  It is a
 // float32 result of up to all pairs, for which the delta of the rounded out is
 // not good enough; so the weights are summed by entry too, and what dS summed
 // over the keys is off by is taken back at the end: sum over the rows of (sum dS) -
@@ -1360,7 +1373,8 @@ __device__ __forceinline__ int last_by_window(const AttnArgs& a, int tq, int tk)
 // of them, its waves 32 rows in turn; nothing is masked.  Rows without weights,
 // and rows past the last one, have lse2 = infinity (see below).  The chunks' parts
 // are added in order by the kernel below.  (40k + 12k + 2.5k pulses, 4 sinks, 8
-// heads on 4: the walk in one workgroup 4 ms, in chunks 27 us.  At float32 and
+// heads on 4: the walk in one workgroup 4 ms, in chunks 27 us.  6000 + 2500 + 333
+// pulses with a bias: 18 us, 11 without.  At float32 and
 // D > 64 its two results and two operands pass the registers and spill.)
 template <class T, int DP, BiasFrom BIAS>
 __global__ __launch_bounds__(256, DP * (int)sizeof(T) <= 128 ? 2 : 1)
@@ -1538,7 +1552,8 @@ __device__ __forceinline__ int64_t k_part_at(const AttnArgs& a, int split, int h
 // keys, many queries or heads) the walk is split over several, whose parts are
 // added by the kernel below.  4 products: 6000 + 2111 + 64 rows, D = 128: 0.74 ms,
 // 0.90 PFLOP/s (V's operands from LDS, for its registers hold accumulators); at
-// D = 64 the vector unit bounds it: 256 events of up to 256 tokens, 149 us.
+// D = 64 the vector unit bounds it: 256 events of up to 256 tokens, 149 us; with a bias
+// by 4 axes from the plane, whose words it reads again for every head, 214 us.
 //
 // A query whose every visible score is -infinity adds nothing: its lse2 is
 // infinity, so its weights exp2(score - infinity) are 0 as long as its scores

@@ -268,9 +268,10 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t x) {
 // end, leave most blocks of a long walk in one bucket.  It grows or falls with the
 // distance, so it is one for the block if the least key less the greatest query and the
 // greatest less the least fall into the same: then a lane needs one value, not 16
-// loads of LDS (the same rows: 703 us, 788 without).  Where a window hides the far keys this
-// would be looked for in vain (b.spans; 6000 + 2500 + 333 pulses, window of 256: a
-// training step 369 us with it, 344 without).
+// loads of LDS (the same rows: 703 us, 788 without).  Where a window hides the far
+// keys, or there are few, this would be looked for in vain (b.spans; 6000 + 2500 + 333
+// pulses, window of 256: a training step 369 us with it, 344 without; 64 events of up
+// to 128 tokens, float32: 39 and 37).
 template <bool KEY, bool PACK, bool SPANS, int SHARE, int OWN, int ROWS>
 __device__ __forceinline__ uint32_t add_bias_shared(f32x16& s, u32x16* entries,
                                                     const BiasArgs& b,
@@ -293,18 +294,23 @@ __device__ __forceinline__ uint32_t add_bias_shared(f32x16& s, u32x16* entries,
             span_of(ordered(tile[a * ROWS + (lane & 31) - (lane >> 5) * 4], b.ints), least, most);
             by_kind(b.ints, shift >= 0, [&](auto ints, auto log) {
                 const uint32_t lo = position(least, b.ints), hi = position(most, b.ints);
-                const uint32_t own_lo = span[a * 2], own_hi = span[a * 2 + 1];
-                one = bucket_of<decltype(ints)::value, decltype(log)::value>(
-                    KEY ? own_lo : lo, KEY ? hi : own_hi, rate, zero, top, shift);
+                const uint32_t k0 = KEY ? span[a * 2] : lo, k1 = KEY ? span[a * 2 + 1] : hi;
+                const uint32_t q0 = KEY ? lo : span[a * 2], q1 = KEY ? hi : span[a * 2 + 1];
+                one = bucket_of<decltype(ints)::value, decltype(log)::value>(k0, q1, rate, zero,
+                                                                             top, shift);
                 other_end = bucket_of<decltype(ints)::value, decltype(log)::value>(
-                    KEY ? own_hi : hi, KEY ? lo : own_lo, rate, zero, top, shift);
-                // (an end that is not a number says nothing of what lies between)
-                if constexpr (!decltype(ints)::value) {
-                    const float from = KEY ? __uint_as_float(own_lo) - __uint_as_float(hi)
-                                           : __uint_as_float(lo) - __uint_as_float(own_hi);
-                    const float to = KEY ? __uint_as_float(own_hi) - __uint_as_float(lo)
-                                         : __uint_as_float(hi) - __uint_as_float(own_lo);
-                    if (!(from <= to)) other_end = -1;
+                    k1, q0, rate, zero, top, shift);
+                // (a distance that does not fit, or is not a number, says nothing of what
+                // lies between)
+                if constexpr (decltype(ints)::value) {
+                    int d;
+                    if (__builtin_sub_overflow((int)k0, (int)q1, &d) ||
+                        __builtin_sub_overflow((int)k1, (int)q0, &d))
+                        other_end = -1;
+                } else {
+                    if (!(__uint_as_float(k0) - __uint_as_float(q1) <=
+                          __uint_as_float(k1) - __uint_as_float(q0)))
+                        other_end = -1;
                 }
             });
             if (__builtin_amdgcn_readfirstlane(one) == __builtin_amdgcn_readfirstlane(other_end)) {

