@@ -184,8 +184,9 @@ static fpstok_status check_bias(const fpstok_rel_bias* r, const fpstok_attn_para
 static fpstok_status check_bias_data(const fpstok_seqs* qs, const fpstok_seqs* ks,
                                      const fpstok_attn_params* p, BiasArgs& b) {
     if (!b.k_pos && qs == ks) b.k_pos = b.q_pos;
-    b.spans = likely_len(ks) > 256 && (p->window_left < 0 || p->window_right < 0 ||
-                                       (int64_t)p->window_left + p->window_right >= 1024);
+    b.spans = b.axes == 1 && likely_len(ks) > 256 &&
+              (p->window_left < 0 || p->window_right < 0 ||
+               (int64_t)p->window_left + p->window_right >= 1024);
     if (!b.table) return fail(FPSTOK_EINVAL, "table is NULL");
     if ((qs->num_rows > 0 && !b.q_pos) || (ks->num_rows > 0 && !b.k_pos))
         return fail(FPSTOK_EINVAL, "q_positions or k_positions is NULL");

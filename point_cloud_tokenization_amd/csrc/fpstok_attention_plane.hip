@@ -89,7 +89,12 @@ static void fill_plane(const AttnArgs& a, const BiasArgs& b, hipStream_t s) {
 int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len) {
     // (64 padded float32 events of up to 128 tokens, 8 heads, 2 axes: 37 us without, 40
     // with it; 64 events, 12 heads, 4 axes: 34.7 and 31.8)
-    if (few || b.entries > kTableEntries || a.H * b.axes < 24 || k_len > 1024) return 0;
+    if (few || b.entries > kTableEntries || a.H * b.axes < 24) return 0;
+    // Longer sequences: two axes or more, planes of up to 1 GiB.  (2 of 2500 rows, 12 heads
+    // of 64, 4 axes, a training step: 1104 us, by positions 1853; 6000 + 2111 + 64 rows, 16
+    // heads on 8 of 128: 6.6 and 9.7 ms; one axis in order, 4000 causal rows, 24 heads on 8
+    // of 128: 1765 and 1371)
+    if (k_len > (b.axes > 1 ? 8192 : 1024) || a.qs.rows * ((k_len + 31) & ~31) > 1 << 28) return 0;
     if ((int64_t)a.G * table_size(b, true) > kGroupEntries) return 0;
     // a window that hides most pairs of the plane
     if (a.left >= 0 && a.right >= 0 && 4 * ((int64_t)a.left + a.right + 1) < k_len) return 0;

@@ -183,6 +183,16 @@ def test_far_positions(dev):
         assert bool(got[name].isfinite().all())
 
 
+@pytest.mark.parametrize("dt,D,H,Hk", [(BF, 64, 12, 12), (HF, 128, 12, 6), (FL, 64, 12, 4)])
+@pytest.mark.parametrize("window", [(-1, -1, 0), (-1, 0, 0), (500, 10, 5)])
+@pytest.mark.parametrize("form", ["packed", "padded"])
+def test_longer_sequences_of_several_heads(dev, dt, D, H, Hk, window, form):
+    """(Padded, the plan's length is that of a slot; packed, it is the mean, which
+    two sequences pass.)"""
+    Case(dev, [5, 1311, 0, 1100, 1], None, H, Hk, D, dt, "f 9:0.3 12:1:2", *window,
+         form=form).run()
+
+
 @pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2), (4, 1), (8, 1), (3, 1)])
 @pytest.mark.parametrize("dt,D", [(BF, 64), (HF, 128), (FL, 64)])
 @pytest.mark.parametrize("spec", ["i 12:0.25:4:11", "f 9:0.05 6:1:1", "f 20:-0.5:2"])
