@@ -651,7 +651,8 @@ fpstok_status fpstok_residual(const fpstok_seqs* seqs, const fpstok_residual_par
  * grad_gate of FPSTOK_GATE_SEQUENCE is summed over the sequence's rows.  Sums are
  * held in float32 or float64 in a fixed order (no floating-point atomics).
  *   x, y, gate, stats   as given to, and written by, the forward call (stats
- *                       may be NULL if there is no norm)
+ *                       may be NULL if there is no norm; x and y as they were
+ *                       before it: a call in place has no gradients)
  *   grad_x_out          [rows][C] in, stream_dtype, or NULL (x_out was not used)
  *   grad_h              [rows][C] in, branch_dtype, or NULL (h was not used)
  *   grad_x              [rows][C] out, or NULL; may be grad_x_out itself

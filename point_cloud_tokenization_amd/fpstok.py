@@ -878,7 +878,8 @@ class Residual(_DeviceCall):
     "none", "sigmoid" or "silu"; the weights [C] float32 or None.  A call takes
     what the tensors hold by then; it returns (x_out, h), the same buffers each
     time (h None without pre_norm); rows behind the last packed sequence keep
-    what they held (0 after construction).  x_out=x and h=y work in place."""
+    what they held (0 after construction).  x_out=x and h=y work in place (not
+    with training=True, whose gradients read x and y)."""
 
     def __init__(self, x, y, seqs, gate=None, gate_per="none", activation="none",
                  post_norm="none", pre_norm="rms", post_weight=None, post_bias=None, scale=None,
@@ -901,6 +902,9 @@ class Residual(_DeviceCall):
         yr = None if y is None else make_rows(y, "y", n, C, bd, dev)
         if (gate is None) != (gate_per == "none"):
             raise ValueError("give gate with gate_per, or neither")
+        inputs = [t.data_ptr() for t in (x, y, gate) if t is not None and n > 0]
+        if training and any(t is not None and t.data_ptr() in inputs for t in (x_out, h)):
+            raise ValueError("training=True reads x and y again: give x_out and h of their own")
         gate_rows = n if gate_per == "row" else seqs.num_seqs
         gr = None if gate is None else make_rows(gate, "gate", gate_rows, C, bd, dev)
         weights = dict(post_weight=post_weight, post_bias=post_bias, scale=scale,

@@ -200,6 +200,17 @@ def test_in_place(dev, C):
     check(y, want["h"], "h")
 
 
+def test_no_training_in_place(dev):
+    """The gradients read x and y again, which a call in place has written over."""
+    from point_cloud_tokenization_amd import fpstok as F
+
+    _, rows, s = _layout([50, 14], "packed", 0, 5, dev)
+    x, y = torch.ones((rows, 64), device=dev), torch.ones((rows, 64), device=dev)
+    for kw in (dict(x_out=x), dict(h=y), dict(x_out=x, h=y)):
+        with pytest.raises(ValueError, match="training"):
+            F.Residual(x, y, s, training=True, **kw)
+
+
 def test_gradient_in_place(dev):
     """grad_x in the place of grad_x_out."""
     seq, rows, s = _layout([50, 14], "packed", 0, 5, dev)
