@@ -444,7 +444,7 @@ struct BiasTile<kNoBias, ROWS, THREADS, JOINT> {
 };
 
 // A block's entries from the plane: the keys p + 8 g + 0 .. 3 of one query.
-__device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
+__host__ __device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
     u32x16 x;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -457,27 +457,32 @@ __device__ __forceinline__ u32x16 load_entries(const uint32_t* p) {
 
 // The entries of a walk's blocks, each called for one block ahead (a load and its
 // use in one block would wait for memory every time); of a sequence that is longer
-// than the plane they are found where they are used.
+// than the plane they are found where they are used.  Where two blocks are taken
+// at a time the second one may lie past the sequence, and past the plane's row: it
+// gets the last block's entries, and its pairs are masked.
 struct EntryWalk {
     const uint32_t* row;  // key 4 half of the query
     u32x16 next;
     int at = -1, last = 0;  // the block called for, and the last there is
-    __device__ __forceinline__ void begin(bool planed, int j) {
+    __host__ __device__ __forceinline__ void begin(bool planed, int j) {
         if (!planed || j > last) return;
         at = j;
         next = load_entries(row + j);
     }
-    // Of the keys j .. j + 31; then_j: the block that may come next.
-    template <bool JOINT, int BN>
-    __device__ __forceinline__ u32x16 take(const BiasArgs& b, bool planed, int j, int then_j,
-                                           const FPSTOK_LDS uint32_t* own,
-                                           const FPSTOK_LDS uint32_t* tile) {
-        if (!planed) return find_entries<JOINT, false, 128, BN>(b, own, tile);
+    // Of the keys j .. j + 31, from the plane; then_j: the block that may come next.
+    __host__ __device__ __forceinline__ u32x16 planed_block(int j, int then_j) {
+        j = j <= last ? j : last;
         if (j != at) next = load_entries(row + j);
         const u32x16 now = next;
         at = then_j <= last ? then_j : last;
         next = load_entries(row + at);
         return now;
+    }
+    template <bool JOINT, int BN>
+    __device__ __forceinline__ u32x16 take(const BiasArgs& b, bool planed, int j, int then_j,
+                                           const FPSTOK_LDS uint32_t* own,
+                                           const FPSTOK_LDS uint32_t* tile) {
+        return planed ? planed_block(j, then_j) : find_entries<JOINT, false, 128, BN>(b, own, tile);
     }
 };
 
