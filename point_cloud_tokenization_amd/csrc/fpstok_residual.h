@@ -33,6 +33,23 @@ struct ResidualArgs {
     float* gate_part;
 };
 
+// The parts of a sequence's gate gradient: the rows start .. start + len - 1 of
+// sequence b among rows first .. last - 1, shared out in runs of `per` adjacent
+// ones.  In range whatever the boundaries are: sequences that run backwards may
+// begin before the first one or end behind the last.
+struct GateParts {
+    int64_t first;
+    int n;
+};
+__host__ __device__ inline GateParts gate_parts(int64_t start, int len, int64_t first,
+                                                int64_t last, int per, int b) {
+    const int64_t lo = start > first ? start : first;
+    const int64_t hi = start + len < last ? start + len : last;
+    if (lo >= hi) return GateParts{0, 0};
+    const uint32_t run = (uint32_t)per, from = (uint32_t)(lo - first) / run;
+    return GateParts{(int64_t)from + b, (int)((uint32_t)(hi - 1 - first) / run - from) + 1};
+}
+
 void plan_residual(ResidualArgs& a, bool backward);
 int64_t residual_blocks(const ResidualArgs& a);  // workgroups
 hipError_t launch_residual(const ResidualArgs& a, hipStream_t s);

@@ -661,15 +661,11 @@ __global__ __launch_bounds__(256) void residual_gates_kernel(ResidualArgs a) {
         int64_t start;
         int len;
         seq_rows(a.seqs, b, start, len);
+        const GateParts parts = gate_parts(start, len, runs.first, runs.last, runs.rows, b);
+        const float* part = a.gate_part + parts.first * a.C + (c < a.C ? c : 0);
         float sum = 0.0f;
-        if (len > 0) {
-            const uint32_t from = (uint32_t)(start - runs.first), run = (uint32_t)runs.rows;
-            const int64_t first = (int64_t)(from / run) + b;
-            const int n = (int)((from + (uint32_t)len - 1) / run - from / run) + 1;
-            const float* part = a.gate_part + first * a.C + (c < a.C ? c : 0);
 #pragma unroll 4
-            for (int i = turn; i < n; i += 8) sum += part[(int64_t)i * a.C];
-        }
+        for (int i = turn; i < parts.n; i += 8) sum += part[(int64_t)i * a.C];
         sums[turn][lane] = sum;
         __syncthreads();
         if (turn == 0 && c < a.C) {

@@ -23,3 +23,9 @@ def test_walk_over_the_plane(tmp_path):
     """Sequences that end in the first half of a tile of 64 keys, in the plane's last
     row: the second block of a pair is not loaded from behind the plane."""
     assert "walks ok" in _run(tmp_path, "plane_walk_main")
+
+
+def test_parts_of_the_gates(tmp_path):
+    """The parts of a gate's gradient, for boundaries in order (each part of a
+    sequence, once) and for ones that run backwards (none outside the parts)."""
+    assert "parts ok" in _run(tmp_path, "gate_parts_main")
