@@ -486,123 +486,121 @@ struct EntryWalk {
     }
 };
 
-// The sums of dS and of the weights of a row by entry: [wave][entry][lane & 31]
-// behind the tables in LDS; one entry more takes those that are another launch's.
-// A place holds both as whole numbers: dS in units of 2^-35 of the row's `cap` in
-// the upper 38 bits, the weights in units of 2^-25 in the lower 26.  Whole numbers
-// add up to the same in any order, and by LDS's integer atomics (7 cycles for
-// the 64 lanes' 8 bytes; float32 ones take 3 cycles a lane, 192).  The cap is
-// a power of two that |dP - delta| stays below, so a sum does too, its weights
-// adding up to 1; where it grows, by more than a factor of 4 over what came
-// before, the sums are shifted.
+// The value of a lane of the lower half of a wave, and that of the lane 32 above
+// it, in both.
+__device__ __forceinline__ void both_halves(uint32_t x, uint32_t& lower, uint32_t& upper) {
+    const auto s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    lower = s[0];
+    upper = s[1];
+}
+
+// The sums of dS and of the weights of a row by entry, in float32: [wave][entry]
+// [lane & 31] behind the tables in LDS, and one place more for what is another
+// launch's or no half's.  A row's two lanes hold its pairs with 16 keys each; they
+// pass them on to one another, and each adds all 32 for every other axis (the lower
+// half for axes 0 and 2, the upper for 1 and 3).  The axes' entries differ, so no
+// two lanes add to one place and a place is read, added to and written back in
+// turn: the order is fixed, and nothing is rounded but the float32 sums.  (Float32
+// atomics in LDS take 3 cycles a lane, 192.)  Two keys at a time, the second from the
+// first's sum if they share a place.  (With one axis the upper half has nothing to add;
+// each half its own 16 instead, joined where both lanes have one entry, took as long:
+// the reads' latency is the bound.)
 template <BiasFrom BIAS>
 struct TableSums {
-    using u64 = unsigned long long;
-    static constexpr int kWeightBits = 26;
-    FPSTOK_LDS u64* lane_sums;
-    u64* all;
+    using f2 = float __attribute__((ext_vector_type(2)));  // of dS, of weights
+    static constexpr int kShift = BIAS == kPlane ? 6 : 8;  // (the plane's bytes are 4 entries)
+    f2* all;
+    FPSTOK_LDS char* sums;  // this lane's place of entry 0
     int slots;
-    uint32_t cap = 0x0d800000u;  // 2^-100
+    // of the two axes this lane adds for: the bits of a word that hold the entry, and
+    // where entry 0 is (no bits, and the place that nobody reads: no such axis)
+    int bits[2];
+    FPSTOK_LDS char* base[2];
     bool on;
     __device__ __forceinline__ TableSums(const BiasArgs& b, int G, int wave, int lane, int tid) {
         on = b.part != nullptr;
         if (!on) return;
         slots = table_slots(b);
-        all = (u64*)(bias_lds() + ((G * table_size(b, BIAS == kPlane) + 63) & ~63));
-        lane_sums = (FPSTOK_LDS u64*)all + wave * slots * 32 + (lane & 31);
-        for (int i = tid; i < 4 * slots * 32; i += 256) all[i] = 0;
-    }
-    // 16 pairs of this lane's row: t = dP - delta, weights w (both 0 where hidden)
-    // and dS = w t.
-    // same: bit a: this lane's pairs have one entry of axis a.
-    __device__ __forceinline__ void add(const BiasArgs& b, const u32x16& entries, uint32_t same,
-                                        const f32x16& t, const f32x16& w, const f32x16& ds,
-                                        bool counts, int half) {
-        float top = 0.0f;
+        all = (f2*)(bias_lds() + ((G * table_size(b, BIAS == kPlane) + 63) & ~63));
+        sums = (FPSTOK_LDS char*)((FPSTOK_LDS f2*)all + wave * slots * 32 + (lane & 31));
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(t[e]));
-        top = pair_max(counts ? top : 0.0f);  // (both lanes of a row keep one cap)
-        if (__any(top > __uint_as_float(cap))) grow(top, half);
-        if (!counts) return;
-        // 2^35 / cap, and what makes a double's last bit 1
-        const double units =
-            __builtin_bit_cast(double, (u64)(uint32_t)(1023 + 35 + 127 - (cap >> 23)) << 52);
-        constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52
-        u64 x[16];
+        for (int k = 0; k < 2; ++k) {
+            const bool has = 2 * k + (lane >> 5) < b.axes;
+            bits[k] = has ? 8 : 0;
+            base[k] = sums + (has ? 0 : b.count << 8);
+        }
+        for (int i = tid; i < 4 * slots * 32; i += 256) all[i] = 0.0f;
+    }
+    __device__ __forceinline__ FPSTOK_LDS f2* place(const BiasArgs& b, uint32_t word, int k,
+                                                    int half) const {
+        uint32_t at = __builtin_amdgcn_ubfe(word, 16 * k + 8 * half, bits[k]);
+        if (BIAS == kPositions && b.count != b.entries && bits[k] != 0) {
+            at -= (uint32_t)b.from;
+            at = at < (uint32_t)b.count ? at : (uint32_t)b.count;
+        }
+        return (FPSTOK_LDS f2*)(base[k] + (at << kShift));
+    }
+    // 16 pairs of this lane's row: weights w and dS (both 0 where hidden).
+    // same: bit a: the block's pairs have one entry of axis a (looked for with one
+    // axis only).
+    __device__ __forceinline__ void add(const BiasArgs& b, const u32x16& entries, uint32_t same,
+                                        const f32x16& w, const f32x16& ds, bool counts, int half) {
+        if (!counts) return;  // (a row's two lanes alike)
+        if (BIAS == kPositions && same != 0) {
+            f2 sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum += f2{ds[e], w[e]};
+            sum = f2{pair_sum(sum[0]), pair_sum(sum[1])};
+            FPSTOK_LDS f2* p = place(b, entries[0], 0, half);
+            *p += sum;
+            return;
+        }
+        if (b.axes > 2)
+            add_axes<2>(b, entries, w, ds, half);
+        else
+            add_axes<1>(b, entries, w, ds, half);
+    }
+    template <int AXES>
+    __device__ __forceinline__ void add_axes(const BiasArgs& b, const u32x16& entries,
+                                             const f32x16& w, const f32x16& ds, int half) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const u64 bits = __builtin_bit_cast(u64, __builtin_fma((double)ds[e], units, kWhole));
-            const uint32_t lo = (uint32_t)bits, hi = (uint32_t)(bits >> 32) - 0x43380000u;
-            const uint32_t weight = (uint32_t)(w[e] * 33554432.0f);
-            x[e] = (u64)__builtin_amdgcn_alignbit(hi, lo, 32 - kWeightBits) << 32 |
-                   ((lo << kWeightBits) + weight);
-        }
-        u64 total = 0;
-        if (BIAS == kPositions && same != 0) {
+            uint32_t words[2], x[2], y[2];
+            both_halves(entries[e], words[0], words[1]);
+            both_halves(__float_as_uint(ds[e]), x[0], x[1]);
+            both_halves(__float_as_uint(w[e]), y[0], y[1]);
+            FPSTOK_LDS f2* at[AXES][2];
+            f2 sum[AXES][2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) total += x[e];
-        }
-        if (b.count == b.entries) {
+            for (int k = 0; k < AXES; ++k)
 #pragma unroll
-            for (int a = 0; a < kMaxAxes; ++a) {
-                if (a >= b.axes) break;
-                if (BIAS == kPositions && (same >> a & 1)) {
-                    put(entries[0] >> 8 * a & 255u, 8, total);
-                    continue;
+                for (int i = 0; i < 2; ++i) {
+                    at[k][i] = place(b, words[i], k, half);
+                    sum[k][i] = *at[k][i];
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    put(entries[e] >> 8 * a & 255u, BIAS == kPlane ? 6 : 8, x[e]);
-            }
-        } else {
-#pragma unroll 1
-            for (int a = 0; a < b.axes; ++a) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint32_t at = (entries[e] >> 8 * a & 255u) - (uint32_t)b.from;
-                    put(at < (uint32_t)b.count ? at : (uint32_t)b.count, 8, x[e]);
-                }
+            for (int k = 0; k < AXES; ++k) {
+                const bool one = at[k][0] == at[k][1];
+                sum[k][0] += f2{__uint_as_float(x[0]), __uint_as_float(y[0])};
+                sum[k][1] = f2{one ? sum[k][0][0] : sum[k][1][0],
+                               one ? sum[k][0][1] : sum[k][1][1]};
+                sum[k][1] += f2{__uint_as_float(x[1]), __uint_as_float(y[1])};
+                *at[k][0] = sum[k][0];
+                *at[k][1] = sum[k][1];
             }
         }
-    }
-    __device__ __forceinline__ void put(uint32_t at, int shift, u64 x) const {
-        __hip_atomic_fetch_add((FPSTOK_LDS u64*)((FPSTOK_LDS char*)lane_sums + (at << shift)), x,
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
-    }
-    // A cap of 4 times `top` or more; the row's first lane shifts its sums.
-    __device__ __forceinline__ void grow(float top, int half) {
-        const bool more = top > __uint_as_float(cap);
-        uint32_t to = (__float_as_uint(top) & 0x7f800000u) + (3u << 23);
-        to = to < 0x7f000000u ? to : 0x7f000000u;
-        const int by = more ? (int)((to - cap) >> 23) : 0;
-        const bool started = cap != 0x0d800000u;
-        cap = more ? to : cap;
-        if (!__any(more && started)) return;
-        if (half == 0 && by > 0) {
-            const int n = by < 63 ? by : 63;
-#pragma unroll 1
-            for (int i = 0; i < slots; ++i) {
-                FPSTOK_LDS u64* p = lane_sums + i * 32;
-                const u64 x = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
-                const long long sum = ((long long)x >> kWeightBits) >> n;
-                __hip_atomic_store(p, ((u64)sum << kWeightBits) | (x & ((1u << kWeightBits) - 1)),
-                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
-            }
-        }
-        wave_sync();
     }
     // The workgroup's part: per head of the group and entry, the rows' sums of dS
     // less `off` (what dS of all the row's keys is off 0 by) times its weights'.  As many
     // threads to an entry as there are, each with every so manieth row of it, from one
     // that is elsewhere in every thread on (threads of one entry after another would all
-    // read one bank): the order is fixed.  A row whose dS is not finite has an `off` that
-    // is not: nor are the entries it adds to.
+    // read one bank): the order is fixed.  An entry that none of a row's pairs has adds
+    // nothing, also where the row's `off` is not a number.
     __device__ __forceinline__ void store(const BiasArgs& b, int G, const RowTile& t, float off,
                                           int row, int half, int tid) const {
-        __shared__ float2 rows[128];  // off and cap, in the units of the sums
+        __shared__ float rows[128];  // off
         __shared__ float parts[256];
-        if (half == 0)
-            rows[row] = make_float2(off * 0x1p-25f, __uint_as_float(cap) * 0x1p-35f);
+        if (half == 0) rows[row] = off;
         __syncthreads();
         const uint32_t all_entries = (uint32_t)(G * b.count);
         const uint32_t share = all_entries < 256u ? 256u / all_entries : 1u;
@@ -621,15 +619,9 @@ struct TableSums {
 #pragma unroll 4
                 for (int k = 0; k < n; ++k) {
                     const int r = first + ((int)p + x * (int)share) * G;
-                    const u64 s = all[((r >> 5) * slots + e) * 32 + (r & 31)];
-                    const float2 is = rows[r];
-                    // (38 bits: 32 and 6, joined in one rounding)
-                    const float value =
-                        __builtin_fmaf((float)(int)(s >> 32), 64.0f,
-                                       (float)((uint32_t)s >> kWeightBits));
-                    const float weight = (float)((uint32_t)s & ((1u << kWeightBits) - 1));
-                    const float term = __builtin_fmaf(-is.x, weight, value * is.y);
-                    sum += s != 0 ? term : 0.0f;
+                    const f2 s = all[((r >> 5) * slots + e) * 32 + (r & 31)];
+                    const float term = __builtin_fmaf(-rows[r], s[1], s[0]);
+                    sum += s[0] != 0.0f || s[1] != 0.0f ? term : 0.0f;
                     if (++x == n) x = 0;
                 }
             }
@@ -1067,12 +1059,12 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // its whole gradient.  So the scores of such keys are set to -infinity, and 0
 // times the lost element, which is not a number, is added after the walk.
 //
-// The bias's gradient is dS summed by the pairs' entries (TableSums).  An
-// addition of 64 bits in LDS takes 7 cycles for 64 lanes (of 32 bits of float: 3 cycles
-// a lane), one per pair and axis.  256 events of up to 256 tokens, 12 heads of 64, 4
-// axes: 416 us (113 without a bias), the vector unit busy for 41 % of it, LDS for 22 %:
-// two workgroups a compute unit, whose registers allow no third, leave latency;
-// pulses, window of 256, one axis: 193 us (26).  The table's gradient is a
+// The bias's gradient is dS summed by the pairs' entries (TableSums): per two keys and
+// axis a read and a write of LDS and the wait between them.  256 events of up to 256
+// tokens, 12 heads of 64, 4 axes: 492 us (113 without a bias): two workgroups a compute
+// unit, whose registers (217) allow no third, leave latency; pulses, window of 256, one
+// axis: 200 us (26).  (64-bit whole numbers by LDS's integer atomics took 416 and 193,
+// but lose what is small beside the row's largest term.)  The table's gradient is a
 // float32 result of up to all pairs, for which the delta of the rounded out is
 // not good enough; so the weights are summed by entry too, and what dS summed
 // over the keys is off by is taken back at the end: sum over the rows of (sum dS) -
@@ -1265,7 +1257,7 @@ void attention_dq_kernel(AttnArgs a, BiasParam<BIAS> bias) {
             if (sums.on) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) off_by += ds[e];
-                sums.add(bias, entries, same, y, x, ds, counts, half);
+                sums.add(bias, entries, same, x, ds, counts, half);
             }
         } else {
 #pragma unroll

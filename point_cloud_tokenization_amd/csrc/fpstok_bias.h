@@ -132,8 +132,10 @@ __device__ __forceinline__ float* bias_lds() {
     extern __shared__ __attribute__((aligned(256))) float fpstok_bias_lds[];
     return fpstok_bias_lds;
 }
+// Places of a row's sums: an entry each, and one that nobody reads for entries of
+// another launch and for the half of a wave that has no axis.
 __host__ __device__ inline int table_slots(const BiasArgs& b) {
-    return b.count + (b.count != b.entries);
+    return b.count + (b.count != b.entries || (b.axes & 1) != 0);
 }
 // Values of one head's tables: an entry each, or (JOINT) two axes' sums.
 __host__ __device__ inline int table_size(const BiasArgs& b, bool joint) {
