@@ -630,8 +630,8 @@ typedef struct {
  *   stats  [rows][4] f32 out, 16-byte aligned, for the gradients: mean and
  *          1/std of the post norm, then of the pre norm; or NULL
  * Rows behind the last packed sequence (and ahead of the first) are left as they
- * were; the free slots of padded ones get 0.  No other output may overlap
- * an input.  Errors: EINVAL, EUNSUPPORTED, EHIP. */
+ * were; the free slots of padded ones get 0.  No output may overlap an input in
+ * part, or another output (EINVAL).  Errors: EINVAL, EUNSUPPORTED, EHIP. */
 fpstok_status fpstok_residual(const fpstok_seqs* seqs, const fpstok_residual_params* params,
                               const fpstok_residual_weights* weights, const fpstok_rows* x,
                               const fpstok_rows* y, const fpstok_rows* gate,
@@ -659,8 +659,9 @@ fpstok_status fpstok_residual(const fpstok_seqs* seqs, const fpstok_residual_par
  *   grad_y, grad_gate   out, as y and gate, or NULL
  *   grads               the weights' gradients, or NULL
  *   ws  fpstok_residual_workspace_size(seqs, params) bytes, 256-byte aligned
- * Rows of no sequence as in the forward call; a sequence without rows gets a
- * gate gradient of 0.  Errors: EINVAL, EWORKSPACE, EUNSUPPORTED, EHIP. */
+ * Rows of no sequence as in the forward call, and overlaps; a sequence without
+ * rows gets a gate gradient of 0.  Errors: EINVAL, EWORKSPACE, EUNSUPPORTED,
+ * EHIP. */
 fpstok_status fpstok_residual_backward(
     const fpstok_seqs* seqs, const fpstok_residual_params* params,
     const fpstok_residual_weights* weights, const fpstok_rows* x, const fpstok_rows* y,

@@ -48,6 +48,58 @@ static fpstok_status check_rows(const fpstok_rows* v, const char* what, int64_t 
     return FPSTOK_OK;
 }
 
+// A view's rows in bytes, for the check of overlaps.
+struct Span {
+    const char* name;
+    const char* data;
+    int64_t rows, step, width;
+    Span(const char* name, const RowsArg& v, int64_t rows, int C, int dtype)
+        : name(name), data((const char*)v.data), rows(v.data ? rows : 0),
+          step(v.row * elem_bytes(dtype)), width((int64_t)C * elem_bytes(dtype)) {
+        if (step == 0 && this->rows > 1) this->rows = 1;  // (the same row again)
+    }
+    int64_t end() const { return (rows - 1) * step + width; }
+};
+
+// Whether two views share a byte.  Views of one stride may lie beside each other
+// in wider rows; of two strides, every row of the one with fewer is looked at.
+static bool overlap(const Span& a, const Span& b) {
+    if (a.rows == 0 || b.rows == 0) return false;
+    const int64_t d = b.data - a.data;  // (addresses, not one array's elements)
+    if (d >= a.end() || -d >= b.end()) return false;
+    if (a.rows > b.rows) return overlap(b, a);
+    if (b.rows == 1) return true;
+    if (a.rows == 1 || a.step == b.step) {
+        // where a's row begins within b's step
+        const int64_t at = ((-d) % b.step + b.step) % b.step;
+        return !(at >= b.width && at + a.width <= b.step);
+    }
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const int64_t from = i * a.step - d;  // from b's first byte on
+        // b's first row that ends behind it
+        const int64_t k = from < b.width ? 0 : (from - b.width) / b.step + 1;
+        if (k < b.rows && k * b.step < from + a.width) return true;
+    }
+    return false;
+}
+
+// Outputs may take an input's place row for row, and not overlap one, or one
+// another, in any other way.
+static fpstok_status check_overlaps(const Span* out, int outs, const Span* in, int ins) {
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < ins; ++j) {
+            const bool same = out[i].data == in[j].data && out[i].step == in[j].step &&
+                              out[i].rows == in[j].rows && out[i].width == in[j].width;
+            if (!same && overlap(out[i], in[j]))
+                return fail(FPSTOK_EINVAL, "%s overlaps %s", out[i].name, in[j].name);
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return fail(FPSTOK_EINVAL, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return FPSTOK_OK;
+}
+
 static fpstok_status check_weight(const float* w, const char* what, bool fits) {
     if (w && !fits) return fail(FPSTOK_EINVAL, "%s without what it belongs to", what);
     if (((uintptr_t)w & 3u) != 0) return fail(FPSTOK_EINVAL, "%s must be 4-byte aligned", what);
@@ -153,6 +205,12 @@ FPSTOK_API fpstok_status fpstok_residual(const fpstok_seqs* s, const fpstok_resi
             return fail(FPSTOK_EINVAL, "%s in place needs the same stride", i ? "h" : "x_out");
     if (((uintptr_t)stats & 15u) != 0)
         return fail(FPSTOK_EINVAL, "stats must be 16-byte aligned");
+    const int64_t gate_rows = a.gate_per == FPSTOK_GATE_SEQUENCE ? s->num_seqs : n;
+    const Span ins[] = {{"x", a.x, n, a.C, a.stream},
+                        {"y", a.y, n, a.C, a.branch},
+                        {"gate", a.gate, gate_rows, a.C, a.branch}};
+    const Span outs[] = {{"x_out", a.x_out, n, a.C, a.stream}, {"h", a.h, n, a.C, a.branch}};
+    if ((st = check_overlaps(outs, 2, ins, 3)) != FPSTOK_OK) return st;
     if (s->num_seqs == 0 || n == 0) return ok();
     a.stats = stats;
     plan_residual(a, false);
@@ -221,6 +279,15 @@ FPSTOK_API fpstok_status fpstok_residual_backward(
     const bool gates = a.gate_per == FPSTOK_GATE_SEQUENCE;
     const size_t need = lay_out(a, kResidualWeights, gates, ws);
     if ((st = check_ws(need, ws, ws_bytes)) != FPSTOK_OK) return st;
+    const Span ins[] = {{"x", a.x, n, a.C, a.stream},
+                        {"y", a.y, n, a.C, a.branch},
+                        {"gate", a.gate, gate_rows, a.C, a.branch},
+                        {"grad_x_out", a.grad_x_out, n, a.C, a.stream},
+                        {"grad_h", a.grad_h, n, a.C, a.branch}};
+    const Span outs[] = {{"grad_x", a.grad_x, n, a.C, a.stream},
+                         {"grad_y", a.grad_y, n, a.C, a.branch},
+                         {"grad_gate", a.grad_gate, gate_rows, a.C, a.branch}};
+    if ((st = check_overlaps(outs, 3, ins, 5)) != FPSTOK_OK) return st;
     lay_out(a, given, gates, ws);
     if (s->num_seqs == 0) a.runs = 0;  // no row is one of a sequence: zeros
     const hipError_t e = launch_residual_backward(a, (hipStream_t)stream);

@@ -868,6 +868,29 @@ def make_rows(t, name, rows=None, width=None, dtype=None, device=None):
     return Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0)
 
 
+def _rows_overlap(a, b):
+    """Whether two [rows, C] views (any row stride, adjacent elements) share a byte."""
+    def span(t):
+        n, step = t.shape[0], (t.stride(0) if t.shape[0] > 1 else 0) * t.element_size()
+        return t.data_ptr(), (n if step else min(n, 1)), step, t.shape[1] * t.element_size()
+
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (pa, na, sa, wa), (pb, nb, sb, wb) = sorted((span(a), span(b)), key=lambda x: x[1])
+    if pb >= pa + (na - 1) * sa + wa or pa >= pb + (nb - 1) * sb + wb:
+        return False
+    if nb == 1:
+        return True
+    if na == 1 or sa == sb:  # side by side in wider rows
+        at = (pa - pb) % sb
+        return not (at >= wb and at + wa <= sb)
+    for start in range(pa - pb, pa - pb + na * sa, sa):
+        k = 0 if start < wb else (start - wb) // sb + 1  # the first row that ends behind it
+        if k < nb and k * sb < start + wa:
+            return True
+    return False
+
+
 class Residual(_DeviceCall):
     """fpstok_residual on given tensors, with its outputs allocated once, and
     with training=True fpstok_residual_backward.
@@ -902,11 +925,13 @@ class Residual(_DeviceCall):
         yr = None if y is None else make_rows(y, "y", n, C, bd, dev)
         if (gate is None) != (gate_per == "none"):
             raise ValueError("give gate with gate_per, or neither")
-        inputs = [t.data_ptr() for t in (x, y, gate) if t is not None and n > 0]
-        if training and any(t is not None and t.data_ptr() in inputs for t in (x_out, h)):
-            raise ValueError("training=True reads x and y again: give x_out and h of their own")
         gate_rows = n if gate_per == "row" else seqs.num_seqs
         gr = None if gate is None else make_rows(gate, "gate", gate_rows, C, bd, dev)
+        for name, t in (("x_out", x_out), ("h", h)):
+            if training and t is not None and t.dim() == 2 and \
+                    any(i is not None and _rows_overlap(t, i) for i in (x, y, gate)):
+                raise ValueError("training=True reads x, y and gate again: give %s rows of its own"
+                                 % name)
         weights = dict(post_weight=post_weight, post_bias=post_bias, scale=scale,
                        pre_weight=pre_weight, pre_bias=pre_bias)
         for name, w in weights.items():
