@@ -665,7 +665,7 @@ struct TableSums<kNoBias> {
 // plane it is one load of memory (4 bytes a pair and head) and, for every two axes, one of
 // LDS.  256 events of up to 256 tokens, 12 heads of 64, 4 axes: 147 us and 24 for the
 // plane (without a bias 75); 8192 + 5000 causal rows, 16 heads on 4 of 128, one axis of
-// int32: 703 us (437); pulses, window of 256, one axis: 43 us (21).
+// int32: 703 us (437); pulses, window of 256, two axes: 44 us (21).
 template <class T, int DP, int BN, BiasFrom BIAS>
 __global__ __launch_bounds__(256, 512 / (DP * (int)sizeof(T)) - (BIAS && DP * sizeof(T) == 128))
 void attention_kernel(AttnArgs a, BiasParam<BIAS> bias) {
@@ -1062,8 +1062,8 @@ void attention_few_kernel(AttnArgs a, BiasParam<BIAS> bias) {
 // The bias's gradient is dS summed by the pairs' entries (TableSums): per two keys and
 // axis a read and a write of LDS and the wait between them.  256 events of up to 256
 // tokens, 12 heads of 64, 4 axes: 492 us (113 without a bias): two workgroups a compute
-// unit, whose registers (217) allow no third, leave latency; pulses, window of 256, one
-// axis: 200 us (26).  (64-bit whole numbers by LDS's integer atomics took 416 and 193,
+// unit, whose registers (217) allow no third, leave latency; pulses, window of 256, two
+// axes: 200 us (26).  (64-bit whole numbers by LDS's integer atomics took 416 and 193,
 // but lose what is small beside the row's largest term.)  The table's gradient is a
 // float32 result of up to all pairs, for which the delta of the rounded out is
 // not good enough; so the weights are summed by entry too, and what dS summed

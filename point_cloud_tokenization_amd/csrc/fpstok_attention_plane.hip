@@ -90,10 +90,13 @@ int32_t plan_plane(const AttnArgs& a, const BiasArgs& b, bool few, int32_t k_len
     // (64 padded float32 events of up to 128 tokens, 8 heads, 2 axes: 37 us without, 40
     // with it; 64 events, 12 heads, 4 axes: 34.7 and 31.8)
     if (few || b.entries > kTableEntries || a.H * b.axes < 24) return 0;
-    // Longer sequences: two axes or more, planes of up to 1 GiB.  (2 of 2500 rows, 12 heads
-    // of 64, 4 axes, a training step: 1104 us, by positions 1853; 6000 + 2111 + 64 rows, 16
-    // heads on 8 of 128: 6.6 and 9.7 ms; one axis in order, 4000 causal rows, 24 heads on 8
-    // of 128: 1765 and 1371)
+    // Longer sequences: two axes or more, planes of up to 1 GiB.  In bfloat16, with the
+    // plane and by positions, us: 2 of 2500 rows, 12 heads of 64, 4 axes 224 and 352, a
+    // training step 917 and 1455; 2 axes 197 and 227, 792 and 932; causal, whose plane is
+    // half hidden, 177 and 203, 740 and 891.  6000 + 2111 + 64 rows, 16 heads on 8 of 128, 4
+    // axes 1060 and 1476, 7.1 and 10.4 ms; 2 axes 968 and 920 (the one form that loses;
+    // causal 548 and 488), 6.4 and 7.1 ms.  (One axis in order, 4000 causal rows, 24 heads
+    // on 8 of 128: 1765 and 1371.)
     if (k_len > (b.axes > 1 ? 8192 : 1024) || a.qs.rows * ((k_len + 31) & ~31) > 1 << 28) return 0;
     if ((int64_t)a.G * table_size(b, true) > kGroupEntries) return 0;
     // a window that hides most pairs of the plane
